@@ -13,7 +13,20 @@ from typing import Optional
 
 from . import _lib
 
-__all__ = ["chunk_fwd", "chunk_fwd_noalloc", "Context", "get_context", "workspace_bytes", "KDAError"]
+__all__ = ["chunk_fwd", "chunk_fwd_noalloc", "Context", "get_context", "workspace_bytes", "KDAError",
+           "linear_fwd", "linear_step", "rotary", "rotary_frequencies"]
+
+# Linear attention and rotary positions (linear.py), loaded on first use: importing the package
+# does not import torch.
+_LINEAR = ("linear_fwd", "linear_step", "rotary", "rotary_frequencies", "make_linear_args", "make_rotary_args")
+
+
+def __getattr__(name):
+    if name in _LINEAR:
+        from . import linear
+        globals().update({n: getattr(linear, n) for n in _LINEAR})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class KDAError(RuntimeError):

@@ -52,6 +52,36 @@ class FwdArgs(Structure):
     ]
 
 
+class LinearArgs(Structure):
+    _fields_ = [
+        ("T", c_int32), ("N", c_int32), ("H", c_int32), ("H_qk", c_int32), ("K", c_int32), ("V", c_int32),
+        ("scale", c_float),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("out", c_void_p),
+        ("q_stride_t", c_int64), ("q_stride_h", c_int64), ("k_stride_t", c_int64), ("k_stride_h", c_int64),
+        ("v_stride_t", c_int64), ("v_stride_h", c_int64), ("out_stride_t", c_int64), ("out_stride_h", c_int64),
+        ("g", c_void_p), ("g_dtype", c_int), ("g_per_token", c_int32),
+        ("cu_seqlens", c_void_p), ("cu_seqlens_host", c_void_p),
+        ("state_dtype", c_int),
+        ("initial_state", c_void_p), ("final_state", c_void_p), ("state_cache", c_void_p),
+        ("num_slots", c_int64), ("state_cache_stride0", c_int64),
+        ("state_indices", c_void_p), ("has_initial_state", c_void_p), ("state_k_first", c_int32),
+        ("rot_dim", c_int32), ("inv_freq", c_void_p), ("positions", c_void_p),
+        ("positions_i64", c_int32), ("interleaved", c_int32), ("rot_factor", c_float),
+        ("seg_len", c_int32),
+    ]
+
+
+class RotaryArgs(Structure):
+    _fields_ = [
+        ("T", c_int32), ("H_q", c_int32), ("H_k", c_int32), ("D", c_int32), ("rot_dim", c_int32), ("dtype", c_int),
+        ("q", c_void_p), ("k", c_void_p), ("out_q", c_void_p), ("out_k", c_void_p),
+        ("q_stride_t", c_int64), ("q_stride_h", c_int64), ("k_stride_t", c_int64), ("k_stride_h", c_int64),
+        ("out_q_stride_t", c_int64), ("out_q_stride_h", c_int64), ("out_k_stride_t", c_int64), ("out_k_stride_h", c_int64),
+        ("positions", c_void_p), ("positions_i64", c_int32), ("inv_freq", c_void_p), ("factor", c_float),
+        ("interleaved", c_int32), ("inverse", c_int32),
+    ]
+
+
 class Stats(Structure):
     _fields_ = [
         ("calls", c_uint64), ("cache_hits", c_uint64), ("cache_misses", c_uint64),
@@ -155,6 +185,29 @@ def load() -> ctypes.CDLL:
     lib.kda_stats_size.argtypes = []
     if lib.kda_stats_size() != ctypes.sizeof(Stats):
         raise ImportError("kda_stats layout mismatch between include/kda.h and the binding")
+    for name in ("kda_linear_fwd_validate", "kda_linear_step_validate"):
+        getattr(lib, name).restype = c_int
+        getattr(lib, name).argtypes = [POINTER(LinearArgs)]
+    lib.kda_linear_fwd_workspace_bytes.restype = c_size_t
+    lib.kda_linear_fwd_workspace_bytes.argtypes = [POINTER(LinearArgs)]
+    lib.kda_linear_seg_len.restype = c_int32
+    lib.kda_linear_seg_len.argtypes = [POINTER(LinearArgs)]
+    lib.kda_linear_fwd.restype = c_int
+    lib.kda_linear_fwd.argtypes = [P, POINTER(LinearArgs), P, c_size_t, P]
+    lib.kda_linear_step.restype = c_int
+    lib.kda_linear_step.argtypes = [P, POINTER(LinearArgs), P]
+    lib.kda_rotary.restype = c_int
+    lib.kda_rotary.argtypes = [P, POINTER(RotaryArgs), P]
+    lib.kda_rotary_validate.restype = c_int
+    lib.kda_rotary_validate.argtypes = [POINTER(RotaryArgs)]
+    lib.kda_linear_args_size.restype = c_size_t
+    lib.kda_linear_args_size.argtypes = []
+    lib.kda_rotary_args_size.restype = c_size_t
+    lib.kda_rotary_args_size.argtypes = []
+    if lib.kda_linear_args_size() != ctypes.sizeof(LinearArgs):
+        raise ImportError("kda_linear_args layout mismatch between include/kda.h and the binding")
+    if lib.kda_rotary_args_size() != ctypes.sizeof(RotaryArgs):
+        raise ImportError("kda_rotary_args layout mismatch between include/kda.h and the binding")
     _lib = lib
     return lib
 
@@ -172,4 +225,7 @@ EXPORTS = [
     "kda_stats_size",
     "kda_status_str", "kda_get_stats", "kda_reset_stats", "kda_profile_enable", "kda_profile_read",
     "kda_profile_calls",
+    "kda_linear_fwd", "kda_linear_fwd_validate", "kda_linear_fwd_workspace_bytes", "kda_linear_seg_len",
+    "kda_linear_step", "kda_linear_step_validate", "kda_rotary", "kda_rotary_validate",
+    "kda_linear_args_size", "kda_rotary_args_size",
 ]

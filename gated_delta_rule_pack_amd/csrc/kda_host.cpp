@@ -24,6 +24,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_linear.h"
 
 using kda::kChunk;
 using kda::kHead;
@@ -65,6 +66,13 @@ int rt_host_free(void*, void* p) { return (int)hipHostFree(p); }
 int rt_dev_alloc(void*, void** p, size_t n) { return (int)hipMalloc(p, n); }
 int rt_dev_free(void*, void* p) { return (int)hipFree(p); }
 int rt_launch(void*, int kernel, const void* plan, void* s, void* start, void* stop) {
+  switch (kernel) {  // kernels with launch data of their own
+    case 5: return kda::launch_linear_maps(*reinterpret_cast<const kda::LinearPlan*>(plan), s);
+    case 6: return kda::launch_linear_combine(*reinterpret_cast<const kda::LinearPlan*>(plan), s);
+    case 7: return kda::launch_linear_output(*reinterpret_cast<const kda::LinearPlan*>(plan), s);
+    case 8: return kda::launch_linear_step(*reinterpret_cast<const kda::LinearPlan*>(plan), s);
+    case 9: return kda::launch_rotary(*reinterpret_cast<const kda::RotaryPlan*>(plan), s);
+  }
   const kda::Plan& p = *reinterpret_cast<const kda::Plan*>(plan);
   switch (kernel) {
     case 0: return kda::launch_prep(p, s, start, stop);
@@ -360,6 +368,10 @@ struct kda_ctx {
   uint64_t tick = 0;
   kda_stats stats{};
 };
+
+namespace kda {
+const kda_runtime& context_runtime(kda_ctx* ctx) { return ctx->rt; }
+}  // namespace kda
 
 namespace {
 

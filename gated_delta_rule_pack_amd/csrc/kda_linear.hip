@@ -1,0 +1,513 @@
+// Linear attention with a decay for each head, chunked form for prompts.
+//
+// Per sequence and value head, S_t = e^{g_t} S_{t-1} + v_t k_t^T and o_t = scale S_t q_t. A chunk
+// of 64 tokens with G the inclusive cumsum of g in it and S0 the state before it gives
+//
+//   P[t, s] = scale (q_t . k_s) e^{G_t - G_s}  (s <= t)
+//   O = P V + diag(scale e^G) Q S0^T
+//   S = e^{G_C} S0 + (diag(e^{G_C - G}) V)^T K
+//
+// Every factor is the exponential of a sum of log decays over a run of tokens, taken of the
+// difference of 64-bit prefix sums: nothing is divided, so no decay is too steep, and the
+// factors keep fp32 accuracy however long the run is.
+//
+// Split. The tokens of all sequences lie on one axis (LinearPlan) that is cut into equal
+// segments; a workgroup walks one segment of one value head. With more than one segment,
+// linear_maps walks the part of each segment whose sequence crosses the segment's end, for the
+// state there; linear_combine chains those states along each sequence; linear_output walks
+// every segment with its true start states. Nothing but the bounds' own values decides which
+// tokens a workgroup takes, so a call needs no host tables.
+//
+// A workgroup is four waves; wave w holds the V/4 state rows from w V/4 in fp32 MFMA
+// accumulators, S^T[k][v], for the whole walk. Lanes (l, g = l / 16): accumulator tiles of
+// K^T U hold column v = l % 16, rows k = 4g + i, which is an operand of Q S^T whose contraction
+// order is (4g + i, 16 + 4g + i); q is read from LDS in that order, and P, made as K Q^T, meets V
+// the same way, so neither the state nor P is ever transposed.
+#include <hip/hip_runtime.h>
+
+#include "kda_device.h"
+#include "kda_linear.h"
+
+namespace kda {
+namespace {
+
+constexpr int kC = kLinChunk;
+constexpr int kThreads = 256;
+constexpr float kMinLogDecay = -120.f;  // e^-120 is 0 in fp32; keeps -inf out of the differences
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+// LDS tile of 64 rows of D bf16, 16-byte units. Unit c of row r sits at c ^ swizzle(r): the 16
+// rows a 16-byte operand read touches, and the 8 rows of a half-wave's transposing read, fall on
+// different banks (256 B hold all of them: one row of 128 channels, or two of 64).
+template <int D>
+__device__ __forceinline__ int unit_at(int row, int c) {
+  if constexpr (D == 128) {
+    return row * 256 + ((c ^ (((row & 7) << 1) | ((row >> 3) & 1))) << 4);
+  } else {
+    const int r = row >> 1;
+    return row * 128 + ((c ^ (((r & 3) << 1) | ((r >> 2) & 1))) << 4);
+  }
+}
+
+// Row `row`, elements 8 c .. 8 c + 7.
+template <int D>
+__device__ __forceinline__ bf16x8 read_row(const char* tile, int row, int c) {
+  return *reinterpret_cast<const bf16x8*>(tile + unit_at<D>(row, c));
+}
+// Row `row`, elements 32 m + 4 g + i and 32 m + 16 + 4 g + i: the accumulators' order.
+template <int D>
+__device__ __forceinline__ bf16x8 read_row_acc(const char* tile, int row, int m, int g) {
+  const int half = (g & 1) * 8;
+  const bf16x4 a = *reinterpret_cast<const bf16x4*>(tile + unit_at<D>(row, 4 * m + (g >> 1)) + half);
+  const bf16x4 b = *reinterpret_cast<const bf16x4*>(tile + unit_at<D>(row, 4 * m + 2 + (g >> 1)) + half);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// Column 16 c + l % 16 of rows t0 + 4 g + i and t0 + 16 + 4 g + i, by two transposing reads: 16
+// lanes give the addresses of a 4 x 16 block, lane j of row j / 4 and columns 4 (j % 4).
+template <int D>
+__device__ __forceinline__ bf16x8 read_col(const char* tile, int t0, int c, int lane) {
+  const int row = t0 + 4 * (lane >> 4) + ((lane & 15) >> 2);
+  const int unit = 2 * c + ((lane & 3) >> 1), half = (lane & 1) * 8;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + unit_at<D>(row, unit) + half));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + unit_at<D>(row + 16, unit) + half));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Token bounds of sequence n inside [0, T], whatever the device bounds hold.
+struct Seq {
+  int begin, len;
+};
+__device__ __forceinline__ int bound(const LinearPlan& p, int n) { return min(max(p.cu[n], 0), p.T); }
+__device__ __forceinline__ Seq sequence(const LinearPlan& p, int n) {
+  const int b = bound(p, n);
+  return Seq{b, max(bound(p, n + 1) - b, 0)};
+}
+// Where sequence n's tokens start on the axis, and the first place that is its own: an empty
+// sequence takes that place (in the stretch that stands for its state).
+__device__ __forceinline__ int64_t axis_start(const LinearPlan& p, int n) { return bound(p, n) + (int64_t)n * p.head_cost; }
+__device__ __forceinline__ int64_t axis_own(const LinearPlan& p, int n) { return axis_start(p, n) - (n > 0); }
+
+// The last sequence whose own place is at or before x: every wave probes 64 places at a time.
+__device__ __forceinline__ int find_sequence(const LinearPlan& p, int64_t x, int lane) {
+  int lo = 0, hi = p.N;  // own(lo) <= x; own(hi) > x or hi == N
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) >> 6;
+    const int at = lo + lane * step;
+    const bool before = at < hi && axis_own(p, at) <= x;
+    const uint64_t mask = __ballot(before) | 1;
+    const int last = __builtin_amdgcn_readfirstlane(63 - __builtin_clzll(mask));
+    lo += last * step;
+    hi = min(lo + step, hi);
+  }
+  return lo;
+}
+
+// Plane of sequence n and head h to start from / to leave the final state in; null: none.
+__device__ __forceinline__ int64_t slot_of(const LinearPlan& p, int mode, int n) {
+  if (mode == kStateDense) return n;
+  if (mode != kStatePaged) return -1;
+  const int64_t s = p.indices[n];
+  return s >= 0 && s < p.num_slots ? s : -1;
+}
+__device__ __forceinline__ int64_t plane_at(const LinearPlan& p, int64_t slot, int h) {
+  return slot * p.stride0 + (int64_t)h * p.K * p.V;
+}
+__device__ __forceinline__ int64_t initial_slot(const LinearPlan& p, int n) {
+  if (p.in_mode == kStatePaged && !p.flags[n]) return -1;
+  return slot_of(p, p.in_mode, n);
+}
+
+__device__ __forceinline__ float load_state(const LinearPlan& p, const void* base, int64_t at) {
+  if (p.state_dtype == kF32) return reinterpret_cast<const float*>(base)[at];
+  if (p.state_dtype == kF16) return (float)reinterpret_cast<const _Float16*>(base)[at];
+  return (float)reinterpret_cast<const __bf16*>(base)[at];
+}
+__device__ __forceinline__ void store_state(const LinearPlan& p, void* base, int64_t at, float x) {
+  if (p.state_dtype == kF32) reinterpret_cast<float*>(base)[at] = x;
+  else if (p.state_dtype == kF16) reinterpret_cast<_Float16*>(base)[at] = (_Float16)x;
+  else reinterpret_cast<__bf16*>(base)[at] = to_bf16(x);
+}
+
+// The walk's state registers: S[vt][kt] holds v = 16 vt + l % 16 of the wave's rows and
+// k = 16 kt + 4 g + i.
+template <int K, int V>
+struct Walk {
+  static constexpr int VT = V / 64;  // 16-row tiles of V per wave
+  static constexpr int KT = K / 16;
+  f32x4 S[VT][KT];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) S[vt][kt] = zero4();
+  }
+  // Plain workspace planes: register order, 1 KB per tile.
+  __device__ __forceinline__ void load(const float* plane, int wave, int lane) {
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+        S[vt][kt] = *reinterpret_cast<const f32x4*>(plane + (((wave * VT + vt) * KT + kt) * 64 + lane) * 4);
+  }
+  __device__ __forceinline__ void store(float* plane, int wave, int lane) const {
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+        *reinterpret_cast<f32x4*>(plane + (((wave * VT + vt) * KT + kt) * 64 + lane) * 4) = S[vt][kt];
+  }
+  // The caller's planes, [V][K] or [K][V].
+  __device__ __forceinline__ void load_plane(const LinearPlan& p, int64_t at, int wave, int lane) {
+    const int g = lane >> 4;
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const int v = (wave * VT + vt) * 16 + (lane & 15), k = kt * 16 + 4 * g;
+        if (!p.kfirst) {
+          const size_t off = (size_t)(at + (int64_t)v * K + k);
+          if (p.state_dtype == kF32) S[vt][kt] = load_state4<kF32>(p.state_in, off);
+          else if (p.state_dtype == kF16) S[vt][kt] = load_state4<kF16>(p.state_in, off);
+          else S[vt][kt] = load_state4<kBF16>(p.state_in, off);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[vt][kt][i] = load_state(p, p.state_in, at + (int64_t)(k + i) * V + v);
+        }
+      }
+  }
+  __device__ __forceinline__ void store_plane(const LinearPlan& p, int64_t at, int wave, int lane) const {
+    const int g = lane >> 4;
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const int v = (wave * VT + vt) * 16 + (lane & 15), k = kt * 16 + 4 * g;
+        if (!p.kfirst) {
+          const size_t off = (size_t)(at + (int64_t)v * K + k);
+          if (p.state_dtype == kF32) store_state4<kF32>(p.state_out, off, S[vt][kt]);
+          else if (p.state_dtype == kF16) store_state4<kF16>(p.state_out, off, S[vt][kt]);
+          else store_state4<kBF16>(p.state_out, off, S[vt][kt]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store_state(p, p.state_out, at + (int64_t)(k + i) * V + v, S[vt][kt][i]);
+        }
+      }
+  }
+};
+
+// 64 rows of D bf16 on their way from memory to an LDS tile: loaded a chunk ahead into
+// registers, rows past the chunk's end as zeros.
+template <int D>
+struct Rows {
+  static constexpr int kUnits = D / 8;             // 16-byte units of a row
+  static constexpr int kRows = kThreads / kUnits;  // rows per pass
+  static constexpr int kPasses = kC / kRows;
+  uint4 w[kPasses];
+  __device__ __forceinline__ void load(const void* base, int64_t stride, int64_t first, int count, int tid) {
+    const __bf16* at = reinterpret_cast<const __bf16*>(base) + first * stride + (tid % kUnits) * 8;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int row = tid / kUnits + i * kRows;
+      w[i] = uint4{0, 0, 0, 0};
+      if (row < count) w[i] = *reinterpret_cast<const uint4*>(at + row * stride);
+    }
+  }
+  __device__ __forceinline__ void put(char* tile, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      *reinterpret_cast<uint4*>(tile + unit_at<D>(tid / kUnits + i * kRows, tid % kUnits)) = w[i];
+  }
+};
+
+template <int K, int V, bool kOut>
+struct Shared {
+  alignas(16) char k[kC * K * 2];
+  alignas(16) char v[kC * V * 2];
+  alignas(16) char q[kOut ? kC * K * 2 : 16];
+  alignas(16) char p[kOut ? 8 * 1024 : 16];  // P fragments (token tile of 16, block of 32 sources)
+  double G[kC];                              // inclusive cumsum of g
+  alignas(16) float c[kC];                   // e^{G_C - G}
+  float e[kC];                               // scale e^G
+  float total;                               // e^{G_C}
+};
+
+// Sum over lanes 0 .. l.
+__device__ __forceinline__ double prefix_sum(double x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// One chunk of `count` tokens: P and the outputs (kOut), then the state.
+template <int K, int V, bool kOut>
+__device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& sh, Walk<K, V>& walk, int64_t first,
+                                      int count, int h, int wave, int lane) {
+  constexpr int VT = Walk<K, V>::VT, KT = Walk<K, V>::KT, KB = K / 32;
+  const int g = lane >> 4, l16 = lane & 15;
+  f32x4 acc[VT][4];
+  if constexpr (kOut) {
+    // P^T tiles of the wave's 16 tokens: rows s = 4 g + i, column t.
+    const int t = 16 * wave + l16;
+    const double Gt = sh.G[t];
+    bf16x8 qf[KB];
+#pragma unroll
+    for (int m = 0; m < KB; ++m) qf[m] = read_row<K>(sh.q, t, 4 * m + g);
+    for (int st = 0; st <= (wave | 1); ++st) {
+      f32x4 d = zero4();
+      if (st <= wave) {
+#pragma unroll
+        for (int m = 0; m < KB; ++m) d = mfma(read_row<K>(sh.k, 16 * st + l16, 4 * m + g), qf[m], d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int s = 16 * st + 4 * g + i;
+          d[i] = s <= t ? d[i] * p.scale * __expf((float)(Gt - sh.G[s])) : 0.f;
+        }
+      }
+      // Rounded to bf16 once: the product with V is a bf16 MFMA with fp32 sums.
+      const bf16x4 b = {to_bf16(d[0]), to_bf16(d[1]), to_bf16(d[2]), to_bf16(d[3])};
+      *reinterpret_cast<bf16x4*>(sh.p + (wave * 2 + (st >> 1)) * 1024 + lane * 16 + (st & 1) * 8) = b;
+    }
+    // Q S^T, transposed: rows v = 4 g + i, column t. The state is rounded to bf16 for it.
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) acc[vt][tt] = zero4();
+#pragma unroll
+    for (int m = 0; m < KB; ++m) {
+      bf16x8 sb[VT];
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) sb[vt] = pack8(walk.S[vt][2 * m], walk.S[vt][2 * m + 1]);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const bf16x8 b = read_row_acc<K>(sh.q, 16 * tt + l16, m, g);
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(sb[vt], b, acc[vt][tt]);
+      }
+    }
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      const float e = sh.e[16 * tt + l16];
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) acc[vt][tt] *= e;
+    }
+  }
+  // State. The decayed values go in as three bf16 terms, exact to 2^-25 of each, against the
+  // stored keys, which are bf16: the state keeps fp32 accuracy. (Two terms leave 3e-6.)
+  bf16x8 raw[2][VT];
+  const float total = sh.total;
+#pragma unroll
+  for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) walk.S[vt][kt] *= total;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    bf16x8 hi[VT], mid[VT], lo[VT];
+    const f32x4 c0 = *reinterpret_cast<const f32x4*>(&sh.c[32 * b + 4 * g]);
+    const f32x4 c1 = *reinterpret_cast<const f32x4*>(&sh.c[32 * b + 16 + 4 * g]);
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt) {
+      raw[b][vt] = read_col<V>(sh.v, 32 * b, wave * VT + vt, lane);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = from_bf16(raw[b][vt][i]) * (i < 4 ? c0[i & 3] : c1[i & 3]);
+        hi[vt][i] = to_bf16(x);
+        const float r = x - from_bf16(hi[vt][i]);
+        mid[vt][i] = to_bf16(r);
+        lo[vt][i] = to_bf16(r - from_bf16(mid[vt][i]));
+      }
+    }
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      const bf16x8 kf = read_col<K>(sh.k, 32 * b, kt, lane);
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        walk.S[vt][kt] = mfma(kf, lo[vt], walk.S[vt][kt]);
+        walk.S[vt][kt] = mfma(kf, mid[vt], walk.S[vt][kt]);
+        walk.S[vt][kt] = mfma(kf, hi[vt], walk.S[vt][kt]);
+      }
+    }
+  }
+  if constexpr (kOut) {
+    __syncthreads();  // P
+    __bf16* out = reinterpret_cast<__bf16*>(p.out) + (int64_t)h * p.o_h;
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+      for (int b = 0; b <= tt / 2; ++b) {
+        const bf16x8 pf = *reinterpret_cast<const bf16x8*>(sh.p + (tt * 2 + b) * 1024 + lane * 16);
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(raw[b][vt], pf, acc[vt][tt]);
+      }
+      const int t = 16 * tt + l16;
+      if (t < count) {
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          const f32x4 o = acc[vt][tt];
+          const bf16x4 b = {to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])};
+          *reinterpret_cast<bf16x4*>(out + (first + t) * p.o_t + (wave * VT + vt) * 16 + 4 * g) = b;
+        }
+      }
+    }
+  }
+}
+
+// Walks segment `seg` of head h. kOut: every token, with outputs and final states; else only
+// the sequence that crosses the segment's end, for its map.
+template <int K, int V, bool kOut>
+__global__ __launch_bounds__(kThreads, 2) void linear_walk(const LinearPlan p) {
+  __shared__ Shared<K, V, kOut> sh;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  const int64_t a = (int64_t)seg * p.seg_len, b = a + p.seg_len;
+  const int64_t plane = (int64_t)K * V;
+  const int64_t border = ((int64_t)seg * p.H + h) * plane;  // this segment's entry in maps and initials
+  const __bf16* q = reinterpret_cast<const __bf16*>(p.q) + (h / p.group) * p.q_h;
+  const __bf16* k = reinterpret_cast<const __bf16*>(p.k) + (h / p.group) * p.k_h;
+  const __bf16* v = reinterpret_cast<const __bf16*>(p.v) + h * p.v_h;
+
+  int n = find_sequence(p, kOut ? a : b - 1, lane);
+  if constexpr (!kOut) {
+    const Seq s = sequence(p, n);
+    const int64_t start = axis_start(p, n);
+    const bool crosses = s.len > 0 && start < b && start + s.len > b;
+    if (h == 0 && tid == 0) p.spans[seg] = crosses ? (start >= a ? 1 : 2) : 0;
+    if (!crosses) return;
+  }
+  Walk<K, V> walk;
+  Rows<K> rq, rk;
+  Rows<V> rv;
+  float g_next = 0.f;  // this lane's token of the next chunk
+  auto fetch = [&](int64_t first, int count) {
+    if constexpr (kOut) rq.load(q, p.q_t, first, count, tid);
+    rk.load(k, p.k_t, first, count, tid);
+    rv.load(v, p.v_t, first, count, tid);
+    g_next = 0.f;
+    if (wave == 0 && p.g && lane < count) {
+      const int64_t at = p.g_per_token ? (first + lane) * p.H + h : h;
+      g_next = p.g_bf16 ? (float)reinterpret_cast<const __bf16*>(p.g)[at] : reinterpret_cast<const float*>(p.g)[at];
+    }
+  };
+  do {
+    const Seq s = sequence(p, n);
+    const int64_t start = axis_start(p, n);
+    if (s.len == 0) {
+      if constexpr (kOut) {
+        const int64_t own = axis_own(p, n);
+        const int64_t to = slot_of(p, p.out_mode, n);
+        if (own >= a && own < b && to >= 0) {
+          const int64_t from = initial_slot(p, n);
+          walk.zero();
+          if (from >= 0) walk.load_plane(p, plane_at(p, from, h), wave, lane);
+          walk.store_plane(p, plane_at(p, to, h), wave, lane);
+        }
+      }
+      continue;
+    }
+    const int t0 = (int)max((int64_t)0, a - start), t1 = (int)min((int64_t)s.len, b - start);
+    if (t0 >= t1) continue;
+    int64_t first = (int64_t)s.begin + t0;
+    int left = t1 - t0;
+    fetch(first, min(left, kC));
+    // Start state. A sequence that goes on after this segment leaves its final state from
+    // another workgroup, perhaps in the plane it starts from: the output walk starts it from
+    // the copy that the map walk made.
+    walk.zero();
+    if (t0 == 0) {
+      const int64_t from = initial_slot(p, n);
+      if (from >= 0) {
+        if (kOut && t1 < s.len) {
+          walk.load(p.initials + border, wave, lane);
+        } else {
+          walk.load_plane(p, plane_at(p, from, h), wave, lane);
+          if (!kOut) walk.store(p.initials + border, wave, lane);
+        }
+      }
+    } else if (kOut) {
+      walk.load(p.maps + border - p.H * plane, wave, lane);
+    }
+    float decay = 1.f;
+    while (left > 0) {
+      const int count = min(left, kC);
+      if constexpr (kOut) rq.put(sh.q, tid);
+      rk.put(sh.k, tid);
+      rv.put(sh.v, tid);
+      if (wave == 0) {
+        const double G = prefix_sum((double)fmaxf(g_next, kMinLogDecay), lane);
+        const double end = __shfl(G, 63);
+        sh.G[lane] = G;
+        sh.c[lane] = __expf((float)(end - G));
+        sh.e[lane] = p.scale * __expf((float)G);
+        if (lane == 0) sh.total = __expf((float)end);
+      }
+      __syncthreads();
+      const int64_t here = first;
+      first += count;
+      left -= count;
+      if (left > 0) fetch(first, min(left, kC));
+      chunk<K, V, kOut>(p, sh, walk, here, count, h, wave, lane);
+      decay *= sh.total;
+      __syncthreads();
+    }
+    if constexpr (kOut) {
+      if (t1 == s.len) {
+        const int64_t to = slot_of(p, p.out_mode, n);
+        if (to >= 0) walk.store_plane(p, plane_at(p, to, h), wave, lane);
+      }
+    } else {
+      walk.store(p.maps + border, wave, lane);
+      if (tid == 0) p.decays[(int64_t)seg * p.H + h] = decay;
+    }
+  } while (kOut && ++n < p.N && axis_own(p, n) < b);
+}
+
+// Chains the segments' states: map s becomes the true state at the end of segment s. The chain
+// runs along each element by itself, so every thread owns four and only loads wait on nothing.
+__global__ __launch_bounds__(kThreads) void linear_combine(const LinearPlan p) {
+  const int per_head = p.K * p.V / (4 * kThreads);
+  const int h = blockIdx.x / per_head;
+  const int64_t plane = (int64_t)p.K * p.V;
+  const int64_t e = (int64_t)(blockIdx.x % per_head) * 4 * kThreads + threadIdx.x * 4;
+  f32x4 cur = zero4();
+#pragma unroll 4
+  for (int s = 0; s < p.n_seg - 1; ++s) {
+    f32x4* at = reinterpret_cast<f32x4*>(p.maps + ((int64_t)s * p.H + h) * plane + e);
+    const f32x4 m = *at;
+    const float d = p.decays[(int64_t)s * p.H + h];
+    const int span = p.spans[s];
+    if (span == 1) {
+      cur = m;
+    } else if (span == 2) {
+      cur = m + cur * d;
+      *at = cur;
+    }
+  }
+}
+
+template <bool kOut>
+int launch_walk(const LinearPlan& p, int segments, void* stream) {
+  const dim3 grid((unsigned)((int64_t)segments * p.H));
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (p.K == 128 && p.V == 128) linear_walk<128, 128, kOut><<<grid, kThreads, 0, s>>>(p);
+  else if (p.K == 128) linear_walk<128, 64, kOut><<<grid, kThreads, 0, s>>>(p);
+  else if (p.V == 128) linear_walk<64, 128, kOut><<<grid, kThreads, 0, s>>>(p);
+  else linear_walk<64, 64, kOut><<<grid, kThreads, 0, s>>>(p);
+  return (int)hipGetLastError();
+}
+
+}  // namespace
+
+int launch_linear_maps(const LinearPlan& p, void* stream) { return launch_walk<false>(p, p.n_seg - 1, stream); }
+int launch_linear_output(const LinearPlan& p, void* stream) { return launch_walk<true>(p, p.n_seg, stream); }
+int launch_linear_combine(const LinearPlan& p, void* stream) {
+  const dim3 grid((unsigned)((int64_t)p.H * (p.K * p.V / (4 * kThreads))));
+  linear_combine<<<grid, kThreads, 0, reinterpret_cast<hipStream_t>(stream)>>>(p);
+  return (int)hipGetLastError();
+}
+
+}  // namespace kda

@@ -169,7 +169,9 @@ typedef struct kda_runtime {
   int (*device_free)(void* user, void* ptr);
   /* kernel: 0 = prep (only when the call has chunks), 1 = scan, 2 = segment maps,
    * 3 = segment combine (2 and 3 only for a segmented call, between prep and scan),
-   * 4 = decode (alone, when no sequence of the call has more than one token). plan
+   * 4 = decode (alone, when no sequence of the call has more than one token); 5 = linear
+   * state maps, 6 = linear combine (5 and 6 only with several segments, before 7),
+   * 7 = linear output, 8 = linear step, 9 = rotary. plan
    * is internal launch data, opaque to the runtime. start and stop, when not NULL, are
    * events the launch itself records when the kernel starts and when it completes
    * (hipExtLaunchKernel), with no separate marker in the stream. */
@@ -325,6 +327,144 @@ const char* kda_status_str(kda_status status);
  * pointers. kda_reset_stats zeroes every counter except the arena sizes. */
 kda_status kda_get_stats(const kda_ctx* ctx, kda_stats* out);
 kda_status kda_reset_stats(kda_ctx* ctx);
+
+/* ---- Linear attention with a decay for each head. ---------------------------------
+ * For every token t of sequence n and value head h, with the V-first state S in R^{V x K}
+ * and the log decay g of the head (constant, or one for each token):
+ *
+ *     S = e^g S + v k^T,      o = scale * S q
+ *
+ * (no normalisation, no delta rule: kda_chunk_fwd has those). It serves beside
+ * kda_chunk_fwd with the same conventions: packed sequences, the same state pool and slots,
+ * grouped value heads, and the caller's stream and workspace. It builds no host metadata:
+ * every workgroup finds its tokens from the device bounds, so no call reads anything back,
+ * needs host bounds or a metadata cache, and a captured call can be replayed with other
+ * bounds in the same memory.
+ *
+ * K and V are 64 or 128 each. Token tensors are bf16 rows of K (or V) adjacent elements;
+ * *_stride_t and *_stride_h are the elements between tokens and between heads, multiples of
+ * 8 (both 0: dense [T, H, D]), so q, k and v may be parts of one projection's output.
+ * g <= 0 in use; -inf (forget everything before this token) is allowed, and anything below
+ * -120 counts as -inf (e^-120 is 0 in fp32). Every exponential the kernels take is of a sum
+ * of log decays over a run of tokens. q, k, v and flagged states must be finite: a row that
+ * is not can reach the rows of up to 63 tokens before it in its own sequence and head.
+ *
+ * With rotary positions (inv_freq not null) q and k are rotated first, as kda_rotary does,
+ * into the workspace, in bf16. */
+typedef struct kda_linear_args {
+  int32_t T;     /* rows of the token tensors; may be 0, at most INT32_MAX - 2^20 */
+  int32_t N;     /* sequences (kda_linear_step: rows), >= 1 */
+  int32_t H;     /* value heads, >= 1 */
+  int32_t H_qk;  /* q/k heads, dividing H; 0 means H. Value head h reads q/k head h / (H / H_qk) */
+  int32_t K, V;  /* head sizes, 64 or 128 */
+  float scale;   /* read-out scale, finite */
+
+  const void* q; /* bf16 [T, H_qk, K] */
+  const void* k; /* bf16 [T, H_qk, K] */
+  const void* v; /* bf16 [T, H, V] */
+  void* out;     /* bf16 [T, H, V]; its byte range must not overlap those of q, k and v */
+  int64_t q_stride_t, q_stride_h;
+  int64_t k_stride_t, k_stride_h;
+  int64_t v_stride_t, v_stride_h;
+  int64_t out_stride_t, out_stride_h;
+
+  const void* g;       /* log decays: [T, H] when g_per_token, else [H]; null: no decay */
+  kda_dtype g_dtype;   /* KDA_F32 or KDA_BF16 */
+  int32_t g_per_token; /* 0 or 1 */
+
+  /* kda_linear_fwd only: device bounds [N+1], cu[0] = 0, never decreasing, cu[N] <= T (rows
+   * from cu[N] on belong to no sequence and are left as they were). The optional host copy
+   * is only checked. Device bounds that break these rules give wrong results, but every
+   * access stays inside the T rows. */
+  const int32_t* cu_seqlens;
+  const int32_t* cu_seqlens_host;
+
+  /* State, as in kda_fwd_args: none, dense (initial_state and/or final_state [N, H, V, K],
+   * the same memory allowed) or a paged pool updated in place. An empty sequence's final
+   * state is its initial state. A sequence whose index is outside [0, num_slots) has no slot:
+   * it starts from zero and its final state is not stored. No slot may serve two sequences. */
+  kda_dtype state_dtype;
+  const void* initial_state;
+  void* final_state;
+  void* state_cache;
+  int64_t num_slots;
+  int64_t state_cache_stride0;
+  const int32_t* state_indices;     /* kda_linear_step: null means row n is slot n */
+  const uint8_t* has_initial_state; /* kda_linear_step: null means every slot holds a state */
+  int32_t state_k_first;
+
+  /* Rotary positions of q and k, null inv_freq for none (see kda_rotary_args). */
+  int32_t rot_dim;
+  const double* inv_freq;
+  const void* positions;
+  int32_t positions_i64;
+  int32_t interleaved;
+  float rot_factor;
+
+  /* kda_linear_fwd only: tokens per segment of the parallel walk, 0 = the policy
+   * (kda_linear_seg_len); otherwise a positive multiple of 64. */
+  int32_t seg_len;
+} kda_linear_args;
+
+/* Prompts: every sequence walks in chunks of 64 tokens, the packed tokens cut into segments
+ * of equal cost that run in parallel (state maps of the segments, a combine over them, the
+ * outputs; one kernel alone when there is one segment). Enqueues on stream and returns; a
+ * failed call enqueues nothing. Errors as kda_chunk_fwd, with KDA_ERR_ALIAS also for out over
+ * q or k, and for an initial_state that overlaps final_state without being the same memory. */
+kda_status kda_linear_fwd(kda_ctx* ctx, const kda_linear_args* args, void* workspace, size_t workspace_bytes,
+                          void* stream);
+/* Host-only, pure: every argument check of kda_linear_fwd. */
+kda_status kda_linear_fwd_validate(const kda_linear_args* args);
+/* Host-only, pure: bytes of caller workspace (256-byte aligned) the call needs, from shapes,
+ * types and seg_len alone; 0 for one segment without rotary positions, and for invalid
+ * arguments. */
+size_t kda_linear_fwd_workspace_bytes(const kda_linear_args* args);
+/* Host-only, pure: the policy's segment length for these shapes; 0 for invalid arguments. */
+int32_t kda_linear_seg_len(const kda_linear_args* args);
+
+/* Single tokens: row n of q, k, v, out is one token of the request in slot
+ * state_indices[n] of state_cache (dense tensors go in as a pool of N slots), and T must equal
+ * N. A row whose index is outside [0, num_slots) is padding: its state and its row of out are
+ * left as they were. No workspace; nothing is read back or allocated; capturable. One kernel,
+ * which also rotates q and k, in fp32. */
+kda_status kda_linear_step(kda_ctx* ctx, const kda_linear_args* args, void* stream);
+kda_status kda_linear_step_validate(const kda_linear_args* args);
+
+/* ---- Rotary positions. -------------------------------------------------------------
+ * With theta = positions[t] * inv_freq[i] (64-bit) and c = factor cos theta,
+ * s = factor sin theta, the pair (a, b) of channels (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * when interleaved, becomes (a c - b s, a s + b c) for i < rot_dim / 2, in fp32, rounded once.
+ * Channels from rot_dim on pass through. inverse negates s: the transposed rotation, which is
+ * the gradient. Scaled contexts are a matter of inv_freq and factor. */
+typedef struct kda_rotary_args {
+  int32_t T;         /* tokens, may be 0 */
+  int32_t H_q, H_k;  /* heads of q (>= 1) and of k (0: no k) */
+  int32_t D;         /* head size, 1..1024 */
+  int32_t rot_dim;   /* even, 2..D */
+  kda_dtype dtype;   /* of q, k and the results: KDA_BF16, KDA_F16 or KDA_F32 */
+  const void* q;     /* [T, H_q, D], element strides below; the D elements adjacent */
+  const void* k;     /* [T, H_k, D] or null */
+  void* out_q;       /* as q; the same memory with the same strides (in place), or disjoint */
+  void* out_k;
+  int64_t q_stride_t, q_stride_h; /* each pair: 0, 0 means dense */
+  int64_t k_stride_t, k_stride_h;
+  int64_t out_q_stride_t, out_q_stride_h;
+  int64_t out_k_stride_t, out_k_stride_h;
+  const void* positions;  /* device [T], int32 or int64 */
+  int32_t positions_i64;  /* 0: int32, 1: int64 */
+  const double* inv_freq; /* device [rot_dim / 2], radians per position */
+  float factor;           /* finite; 1 unless the scaling asks for more */
+  int32_t interleaved;
+  int32_t inverse;
+} kda_rotary_args;
+
+/* Enqueues the rotation of q and k as one kernel; a failed call enqueues nothing. */
+kda_status kda_rotary(kda_ctx* ctx, const kda_rotary_args* args, void* stream);
+kda_status kda_rotary_validate(const kda_rotary_args* args);
+
+/* sizeof the two structs, so a binding can check its mirrors. */
+size_t kda_linear_args_size(void);
+size_t kda_rotary_args_size(void);
 
 #ifdef __cplusplus
 }

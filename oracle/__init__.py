@@ -7,3 +7,4 @@ does, and shares no code with it.
 from .kda_oracle import (  # noqa: F401
     L2_EPS, chunk_indices, kda_forward, kda_sequence, l2_normalize, sigmoid,
 )
+from .linear_oracle import linear_forward, rotate  # noqa: F401
