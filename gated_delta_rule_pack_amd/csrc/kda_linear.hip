@@ -38,6 +38,13 @@ constexpr float kMinLogDecay = -120.f;  // e^-120 is 0 in fp32; keeps -inf out o
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
+// Keeps what is derived from x inside the loop it is used in: left to itself the compiler makes all
+// the walk's LDS and state addresses once, and then spills them around every chunk.
+__device__ __forceinline__ int local_copy(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // LDS tile of 64 rows of D bf16, 16-byte units. Unit c of row r sits at c ^ swizzle(r): the 16
 // rows a 16-byte operand read touches, and the 8 rows of a half-wave's transposing read, fall on
 // different banks (256 B hold all of them: one row of 128 channels, or two of 64).
@@ -160,8 +167,8 @@ struct Walk {
         *reinterpret_cast<f32x4*>(plane + (((wave * VT + vt) * KT + kt) * 64 + lane) * 4) = S[vt][kt];
   }
   // The caller's planes, [V][K] or [K][V].
-  __device__ __forceinline__ void load_plane(const LinearPlan& p, int64_t at, int wave, int lane) {
-    const int g = lane >> 4;
+  __device__ __forceinline__ void load_plane(const LinearPlan& p, int64_t at, int wave, int lane_) {
+    const int lane = local_copy(lane_), g = lane >> 4;
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -178,8 +185,8 @@ struct Walk {
         }
       }
   }
-  __device__ __forceinline__ void store_plane(const LinearPlan& p, int64_t at, int wave, int lane) const {
-    const int g = lane >> 4;
+  __device__ __forceinline__ void store_plane(const LinearPlan& p, int64_t at, int wave, int lane_) const {
+    const int lane = local_copy(lane_), g = lane >> 4;
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -198,6 +205,14 @@ struct Walk {
   }
 };
 
+// Buffer over `count` rows of D bf16, `stride` elements apart, from row `first` of a tensor: a row
+// behind them is out of range (rows do not overlap), so loads of it give zeros and stores are dropped.
+template <int D>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const __bf16* base, int64_t first, int64_t stride, int count) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<__bf16*>(base + first * stride), (short)0,
+                                           ((count - 1) * (int)stride + D) * 2, kBufWord3);
+}
+
 // 64 rows of D bf16 on their way from memory to an LDS tile: loaded a chunk ahead into
 // registers, rows past the chunk's end as zeros.
 template <int D>
@@ -205,20 +220,18 @@ struct Rows {
   static constexpr int kUnits = D / 8;             // 16-byte units of a row
   static constexpr int kRows = kThreads / kUnits;  // rows per pass
   static constexpr int kPasses = kC / kRows;
-  uint4 w[kPasses];
-  __device__ __forceinline__ void load(const void* base, int64_t stride, int64_t first, int count, int tid) {
-    const __bf16* at = reinterpret_cast<const __bf16*>(base) + first * stride + (tid % kUnits) * 8;
+  u32x4 w[kPasses];
+  __device__ __forceinline__ void load(const __bf16* base, int64_t stride, int64_t first, int count, int tid) {
+    const __amdgpu_buffer_rsrc_t r = rows_buffer<D>(base, first, stride, count);
+    const int at = (tid / kUnits) * (int)stride * 2 + (tid % kUnits) * 16;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int row = tid / kUnits + i * kRows;
-      w[i] = uint4{0, 0, 0, 0};
-      if (row < count) w[i] = *reinterpret_cast<const uint4*>(at + row * stride);
-    }
+    for (int i = 0; i < kPasses; ++i)
+      w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRows * (int)stride * 2, 0, 0));
   }
   __device__ __forceinline__ void put(char* tile, int tid) const {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
-      *reinterpret_cast<uint4*>(tile + unit_at<D>(tid / kUnits + i * kRows, tid % kUnits)) = w[i];
+      *reinterpret_cast<u32x4*>(tile + unit_at<D>(tid / kUnits + i * kRows, tid % kUnits)) = w[i];
   }
 };
 
@@ -228,52 +241,77 @@ struct Shared {
   alignas(16) char v[kC * V * 2];
   alignas(16) char q[kOut ? kC * K * 2 : 16];
   alignas(16) char p[kOut ? 8 * 1024 : 16];  // P fragments (token tile of 16, block of 32 sources)
-  double G[kC];                              // inclusive cumsum of g
-  alignas(16) float c[kC];                   // e^{G_C - G}
-  float e[kC];                               // scale e^G
-  float total;                               // e^{G_C}
+  struct Decays {
+    double G[kC];             // inclusive cumsum of g
+    alignas(16) float c[kC];  // e^{G_C - G}
+    float e[kC];              // scale e^G
+    float total;              // e^{G_C}
+  } decays[2];                // of this chunk and the next
 };
 
-// Sum over lanes 0 .. l.
-__device__ __forceinline__ double prefix_sum(double x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+// Sum over lanes 0 .. l: row shifts inside 16 lanes, then the rows' last lanes broadcast on.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_dpp(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xf, false);
+  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double prefix_sum(double x) {
+  x = add_dpp<0x111, 0xf>(x);  // row_shr:1, 2, 4, 8; lanes without a source add 0
+  x = add_dpp<0x112, 0xf>(x);
+  x = add_dpp<0x114, 0xf>(x);
+  x = add_dpp<0x118, 0xf>(x);
+  x = add_dpp<0x142, 0xa>(x);  // row_bcast:15 into rows 1 and 3
+  x = add_dpp<0x143, 0xc>(x);  // row_bcast:31 into rows 2 and 3
   return x;
+}
+template <typename D>
+__device__ __forceinline__ void put_decays(D& d, float g, float scale, int lane) {
+  const double G = prefix_sum((double)fmaxf(g, kMinLogDecay));
+  const uint64_t u = __builtin_bit_cast(uint64_t, G);
+  const double end = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
+                                                    (uint32_t)__builtin_amdgcn_readlane((int)u, 63));
+  d.G[lane] = G;
+  d.c[lane] = __expf((float)(end - G));
+  d.e[lane] = scale * __expf((float)G);
+  if (lane == 0) d.total = __expf((float)end);
 }
 
 // One chunk of `count` tokens: P and the outputs (kOut), then the state.
 template <int K, int V, bool kOut>
-__device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& sh, Walk<K, V>& walk, int64_t first,
-                                      int count, int h, int wave, int lane) {
+__device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& sh, const typename Shared<K, V, kOut>::Decays& dec,
+                                      Walk<K, V>& walk, int64_t first, int count, int h, int wave, int lane_) {
+  const int lane = local_copy(lane_);
   constexpr int VT = Walk<K, V>::VT, KT = Walk<K, V>::KT, KB = K / 32;
   const int g = lane >> 4, l16 = lane & 15;
-  f32x4 acc[VT][4];
+  bf16x8 raw[2][VT];
   if constexpr (kOut) {
-    // P^T tiles of the wave's 16 tokens: rows s = 4 g + i, column t.
-    const int t = 16 * wave + l16;
-    const double Gt = sh.G[t];
-    bf16x8 qf[KB];
+    // P^T tiles (token tile tt, source tile st <= tt), rows s = 4 g + i, column t. The ten tiles are
+    // dealt out three or two to a wave: waves 0 and 1 share row 3 and take (0, 0) and (1, 0),
+    // waves 2 and 3 share row 2, and wave 3 has (1, 1).
 #pragma unroll
-    for (int m = 0; m < KB; ++m) qf[m] = read_row<K>(sh.q, t, 4 * m + g);
-    for (int st = 0; st <= (wave | 1); ++st) {
+    for (int j = 0; j < 3; ++j) {
+      const int tt = j < 2 ? (wave < 2 ? 3 : (wave == 3 && j == 1 ? 1 : 2)) : wave;
+      const int st = j < 2 ? (wave < 2 ? 2 * wave + j : (wave == 2 ? j : 2 - j)) : 0;
+      if (j == 2 && wave >= 2) break;
+      const int t = 16 * tt + l16;
       f32x4 d = zero4();
-      if (st <= wave) {
 #pragma unroll
-        for (int m = 0; m < KB; ++m) d = mfma(read_row<K>(sh.k, 16 * st + l16, 4 * m + g), qf[m], d);
+      for (int m = 0; m < KB; ++m)
+        d = mfma(read_row<K>(sh.k, 16 * st + l16, 4 * m + g), read_row<K>(sh.q, t, 4 * m + g), d);
+      const double Gt = dec.G[t];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int s = 16 * st + 4 * g + i;
-          d[i] = s <= t ? d[i] * p.scale * __expf((float)(Gt - sh.G[s])) : 0.f;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int s = 16 * st + 4 * g + i;
+        d[i] = s <= t ? d[i] * p.scale * __expf((float)(Gt - dec.G[s])) : 0.f;
       }
       // Rounded to bf16 once: the product with V is a bf16 MFMA with fp32 sums.
       const bf16x4 b = {to_bf16(d[0]), to_bf16(d[1]), to_bf16(d[2]), to_bf16(d[3])};
-      *reinterpret_cast<bf16x4*>(sh.p + (wave * 2 + (st >> 1)) * 1024 + lane * 16 + (st & 1) * 8) = b;
+      *reinterpret_cast<bf16x4*>(sh.p + (tt * 2 + (st >> 1)) * 1024 + lane * 16 + (st & 1) * 8) = b;
     }
     // Q S^T, transposed: rows v = 4 g + i, column t. The state is rounded to bf16 for it.
+    f32x4 acc[VT][4];
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -292,15 +330,46 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
     }
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
-      const float e = sh.e[16 * tt + l16];
+      const float e = dec.e[16 * tt + l16];
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) acc[vt][tt] *= e;
     }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, 32 * b, wave * VT + vt, lane);
+    __syncthreads();  // P
+    const __amdgpu_buffer_rsrc_t out = rows_buffer<V>(reinterpret_cast<const __bf16*>(p.out) + h * p.o_h, first, p.o_t, count);
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+      for (int b = 0; b <= tt / 2; ++b) {
+        bf16x8 pf = *reinterpret_cast<const bf16x8*>(sh.p + (tt * 2 + b) * 1024 + lane * 16);
+        if (tt == 2 * b) {  // the tile past the diagonal is not made
+#pragma unroll
+          for (int i = 4; i < 8; ++i) pf[i] = (__bf16)0.f;
+        }
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(raw[b][vt], pf, acc[vt][tt]);
+      }
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        const f32x4 o = acc[vt][tt];
+        const bf16x4 b = {to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])};
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), out,
+                                              (16 * tt + l16) * (int)p.o_t * 2 + ((wave * VT + vt) * 16 + 4 * g) * 2, 0, 0);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, 32 * b, wave * VT + vt, lane);
   }
   // State. The decayed values go in as three bf16 terms, exact to 2^-25 of each, against the
   // stored keys, which are bf16: the state keeps fp32 accuracy. (Two terms leave 3e-6.)
-  bf16x8 raw[2][VT];
-  const float total = sh.total;
+  const float total = dec.total;
 #pragma unroll
   for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -308,11 +377,10 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     bf16x8 hi[VT], mid[VT], lo[VT];
-    const f32x4 c0 = *reinterpret_cast<const f32x4*>(&sh.c[32 * b + 4 * g]);
-    const f32x4 c1 = *reinterpret_cast<const f32x4*>(&sh.c[32 * b + 16 + 4 * g]);
+    const f32x4 c0 = *reinterpret_cast<const f32x4*>(&dec.c[32 * b + 4 * g]);
+    const f32x4 c1 = *reinterpret_cast<const f32x4*>(&dec.c[32 * b + 16 + 4 * g]);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt) {
-      raw[b][vt] = read_col<V>(sh.v, 32 * b, wave * VT + vt, lane);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float x = from_bf16(raw[b][vt][i]) * (i < 4 ? c0[i & 3] : c1[i & 3]);
@@ -330,28 +398,6 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
         walk.S[vt][kt] = mfma(kf, lo[vt], walk.S[vt][kt]);
         walk.S[vt][kt] = mfma(kf, mid[vt], walk.S[vt][kt]);
         walk.S[vt][kt] = mfma(kf, hi[vt], walk.S[vt][kt]);
-      }
-    }
-  }
-  if constexpr (kOut) {
-    __syncthreads();  // P
-    __bf16* out = reinterpret_cast<__bf16*>(p.out) + (int64_t)h * p.o_h;
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-      for (int b = 0; b <= tt / 2; ++b) {
-        const bf16x8 pf = *reinterpret_cast<const bf16x8*>(sh.p + (tt * 2 + b) * 1024 + lane * 16);
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(raw[b][vt], pf, acc[vt][tt]);
-      }
-      const int t = 16 * tt + l16;
-      if (t < count) {
-#pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          const f32x4 o = acc[vt][tt];
-          const bf16x4 b = {to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])};
-          *reinterpret_cast<bf16x4*>(out + (first + t) * p.o_t + (wave * VT + vt) * 16 + 4 * g) = b;
-        }
       }
     }
   }
@@ -384,14 +430,14 @@ __global__ __launch_bounds__(kThreads, 2) void linear_walk(const LinearPlan p) {
   Rows<V> rv;
   float g_next = 0.f;  // this lane's token of the next chunk
   auto fetch = [&](int64_t first, int count) {
-    if constexpr (kOut) rq.load(q, p.q_t, first, count, tid);
-    rk.load(k, p.k_t, first, count, tid);
-    rv.load(v, p.v_t, first, count, tid);
     g_next = 0.f;
-    if (wave == 0 && p.g && lane < count) {
+    if (wave == 3 && p.g && lane < count) {
       const int64_t at = p.g_per_token ? (first + lane) * p.H + h : h;
       g_next = p.g_bf16 ? (float)reinterpret_cast<const __bf16*>(p.g)[at] : reinterpret_cast<const float*>(p.g)[at];
     }
+    if constexpr (kOut) rq.load(q, p.q_t, first, count, tid);
+    rk.load(k, p.k_t, first, count, tid);
+    rv.load(v, p.v_t, first, count, tid);
   };
   do {
     const Seq s = sequence(p, n);
@@ -432,26 +478,23 @@ __global__ __launch_bounds__(kThreads, 2) void linear_walk(const LinearPlan p) {
       walk.load(p.maps + border - p.H * plane, wave, lane);
     }
     float decay = 1.f;
+    int turn = 0;
+    if (wave == 3) put_decays(sh.decays[0], g_next, p.scale, lane);
     while (left > 0) {
       const int count = min(left, kC);
       if constexpr (kOut) rq.put(sh.q, tid);
       rk.put(sh.k, tid);
       rv.put(sh.v, tid);
-      if (wave == 0) {
-        const double G = prefix_sum((double)fmaxf(g_next, kMinLogDecay), lane);
-        const double end = __shfl(G, 63);
-        sh.G[lane] = G;
-        sh.c[lane] = __expf((float)(end - G));
-        sh.e[lane] = p.scale * __expf((float)G);
-        if (lane == 0) sh.total = __expf((float)end);
-      }
       __syncthreads();
       const int64_t here = first;
       first += count;
       left -= count;
       if (left > 0) fetch(first, min(left, kC));
-      chunk<K, V, kOut>(p, sh, walk, here, count, h, wave, lane);
-      decay *= sh.total;
+      chunk<K, V, kOut>(p, sh, sh.decays[turn], walk, here, count, h, wave, lane);
+      decay *= sh.decays[turn].total;
+      turn ^= 1;
+      // Wave 3 has the fewest tiles of P.
+      if (wave == 3 && left > 0) put_decays(sh.decays[turn], g_next, p.scale, lane);
       __syncthreads();
     }
     if constexpr (kOut) {

@@ -38,6 +38,7 @@ Strides strides_of(int64_t t, int64_t h, int64_t H, int64_t D) {
 }
 // Largest stride: far above any real row, and far below what would overflow 64-bit offsets.
 constexpr int64_t kMaxStride = int64_t(1) << 31;
+constexpr int64_t kMaxTokenStride = int64_t(1) << 23;
 bool stride_ok(Strides s) { return s.t >= 0 && s.h >= 0 && s.t <= kMaxStride && s.h <= kMaxStride; }
 // No two rows of an output overlap: heads inside tokens, or tokens inside heads.
 bool distinct_rows(Strides s, int64_t T, int64_t H, int64_t D) {
@@ -125,8 +126,14 @@ kda_status check_linear(const kda_linear_args* a) {
   const Strides sk = strides_of(a->k_stride_t, a->k_stride_h, H_qk, a->K);
   const Strides sv = strides_of(a->v_stride_t, a->v_stride_h, a->H, a->V);
   const Strides so = strides_of(a->out_stride_t, a->out_stride_h, a->H, a->V);
-  for (const Strides& s : {sq, sk, sv, so})
-    if (!stride_ok(s) || s.t % 8 != 0 || s.h % 8 != 0) return KDA_ERR_INVALID_ARG;
+  // The kernels hold a chunk's 64 rows in 32-bit byte offsets, and rows do not overlap.
+  const int64_t least[4] = {a->K, a->K, a->V, a->V};
+  int i = 0;
+  for (const Strides& s : {sq, sk, sv, so}) {
+    if (!stride_ok(s) || s.t % 8 != 0 || s.h % 8 != 0 || s.t > kMaxTokenStride) return KDA_ERR_INVALID_ARG;
+    if (a->T > 1 && s.t < least[i]) return KDA_ERR_INVALID_ARG;
+    ++i;
+  }
   if (!distinct_rows(so, a->T, a->H, a->V)) return KDA_ERR_ALIAS;
   if (a->T > 0) {
     if (!a->q || !a->k || !a->v || !a->out) return KDA_ERR_INVALID_ARG;

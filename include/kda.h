@@ -343,7 +343,8 @@ kda_status kda_reset_stats(kda_ctx* ctx);
  *
  * K and V are 64 or 128 each. Token tensors are bf16 rows of K (or V) adjacent elements;
  * *_stride_t and *_stride_h are the elements between tokens and between heads, multiples of
- * 8 (both 0: dense [T, H, D]), so q, k and v may be parts of one projection's output.
+ * 8 (both 0: dense [T, H, D]), so q, k and v may be parts of one projection's output; tokens are
+ * at least one row and at most 2^23 elements apart.
  * g <= 0 in use; -inf (forget everything before this token) is allowed, and anything below
  * -120 counts as -inf (e^-120 is 0 in fp32). Every exponential the kernels take is of a sum
  * of log decays over a run of tokens. q, k, v and flagged states must be finite: a row that
