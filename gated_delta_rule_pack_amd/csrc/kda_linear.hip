@@ -32,7 +32,9 @@ namespace kda {
 namespace {
 
 constexpr int kC = kLinChunk;
-constexpr int kThreads = 256;
+// Waves of a walk's workgroup; each has V / (16 waves) tiles of 16 state rows.
+template <int V>
+constexpr int kWavesOf = V / 16 >= 8 ? 8 : 4;
 constexpr float kMinLogDecay = -120.f;  // e^-120 is 0 in fp32; keeps -inf out of the differences
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -45,40 +47,46 @@ __device__ __forceinline__ int local_copy(int x) {
   return x;
 }
 
-// LDS tile of 64 rows of D bf16, 16-byte units. Unit c of row r sits at c ^ swizzle(r): the 16
-// rows a 16-byte operand read touches, and the 8 rows of a half-wave's transposing read, fall on
-// different banks (256 B hold all of them: one row of 128 channels, or two of 64).
-template <int D>
-__device__ __forceinline__ int unit_at(int row, int c) {
-  if constexpr (D == 128) {
-    return row * 256 + ((c ^ (((row & 7) << 1) | ((row >> 3) & 1))) << 4);
-  } else {
-    const int r = row >> 1;
-    return row * 128 + ((c ^ (((r & 3) << 1) | ((r >> 2) & 1))) << 4);
-  }
+// bf16 is the upper half of fp32: the upper halves of a and b, a below.
+constexpr uint32_t kTop = 0xffff0000u;
+__device__ __forceinline__ uint32_t top_halves(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
 }
 
-// Row `row`, elements 8 c .. 8 c + 7.
+// LDS tile of 64 rows of D bf16. A row takes 16 bytes more than its elements, and inside 16 rows
+// row r stands at place 2 (r % 8) + r / 8: the 16 rows of an operand read then fall on all 64 banks
+// (places 4 banks apart), and so do the 8 rows of half a transposing read (every other place). Every
+// read is a lane's own place and a constant offset.
 template <int D>
-__device__ __forceinline__ bf16x8 read_row(const char* tile, int row, int c) {
-  return *reinterpret_cast<const bf16x8*>(tile + unit_at<D>(row, c));
+constexpr int kRowBytes = 2 * D + 16;
+template <int D>
+__device__ __forceinline__ int row_at(int row) {
+  return ((row & ~15) | ((row & 7) << 1) | ((row >> 3) & 1)) * kRowBytes<D>;
 }
-// Row `row`, elements 32 m + 4 g + i and 32 m + 16 + 4 g + i: the accumulators' order.
+// Operand rows: row r0 + l % 16 (r0 a multiple of 16), elements 32 m + 4 g + i and
+// 32 m + 16 + 4 g + i: the accumulators' order, in which q and k meet each other too.
 template <int D>
-__device__ __forceinline__ bf16x8 read_row_acc(const char* tile, int row, int m, int g) {
-  const int half = (g & 1) * 8;
-  const bf16x4 a = *reinterpret_cast<const bf16x4*>(tile + unit_at<D>(row, 4 * m + (g >> 1)) + half);
-  const bf16x4 b = *reinterpret_cast<const bf16x4*>(tile + unit_at<D>(row, 4 * m + 2 + (g >> 1)) + half);
+__device__ __forceinline__ int row_lane(int lane) {
+  return row_at<D>(lane & 15) + (lane >> 4) * 8;
+}
+template <int D>
+__device__ __forceinline__ bf16x8 read_row(const char* tile, int at, int r0, int m) {
+  const char* p = tile + r0 * kRowBytes<D> + m * 64 + at;
+  const bf16x4 a = *reinterpret_cast<const bf16x4*>(p), b = *reinterpret_cast<const bf16x4*>(p + 32);
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-// Column 16 c + l % 16 of rows t0 + 4 g + i and t0 + 16 + 4 g + i, by two transposing reads: 16
-// lanes give the addresses of a 4 x 16 block, lane j of row j / 4 and columns 4 (j % 4).
+// Operand columns: column 16 c + l % 16 of rows t0 + 4 g + i and t0 + 16 + 4 g + i (t0 a multiple of
+// 32), by two transposing reads: 16 lanes give the addresses of a 4 x 16 block, lane j of row j / 4 and
+// columns 4 (j % 4).
 template <int D>
-__device__ __forceinline__ bf16x8 read_col(const char* tile, int t0, int c, int lane) {
-  const int row = t0 + 4 * (lane >> 4) + ((lane & 15) >> 2);
-  const int unit = 2 * c + ((lane & 3) >> 1), half = (lane & 1) * 8;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + unit_at<D>(row, unit) + half));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(tile + unit_at<D>(row + 16, unit) + half));
+__device__ __forceinline__ int col_lane(int lane) {
+  return row_at<D>(4 * (lane >> 4) + ((lane & 15) >> 2)) + (lane & 3) * 8;
+}
+template <int D>
+__device__ __forceinline__ bf16x8 read_col(const char* tile, int at, int t0, int c) {
+  const char* p = tile + t0 * kRowBytes<D> + c * 32 + at;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 16 * kRowBytes<D>));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -141,7 +149,7 @@ __device__ __forceinline__ void store_state(const LinearPlan& p, void* base, int
 // k = 16 kt + 4 g + i.
 template <int K, int V>
 struct Walk {
-  static constexpr int VT = V / 64;  // 16-row tiles of V per wave
+  static constexpr int VT = V / (16 * kWavesOf<V>);  // 16-row tiles of V per wave
   static constexpr int KT = K / 16;
   f32x4 S[VT][KT];
 
@@ -215,7 +223,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const __bf16* base
 
 // 64 rows of D bf16 on their way from memory to an LDS tile: loaded a chunk ahead into
 // registers, rows past the chunk's end as zeros.
-template <int D>
+template <int D, int kThreads>
 struct Rows {
   static constexpr int kUnits = D / 8;             // 16-byte units of a row
   static constexpr int kRows = kThreads / kUnits;  // rows per pass
@@ -231,15 +239,15 @@ struct Rows {
   __device__ __forceinline__ void put(char* tile, int tid) const {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
-      *reinterpret_cast<u32x4*>(tile + unit_at<D>(tid / kUnits + i * kRows, tid % kUnits)) = w[i];
+      *reinterpret_cast<u32x4*>(tile + row_at<D>(tid / kUnits + i * kRows) + (tid % kUnits) * 16) = w[i];
   }
 };
 
 template <int K, int V, bool kOut>
 struct Shared {
-  alignas(16) char k[kC * K * 2];
-  alignas(16) char v[kC * V * 2];
-  alignas(16) char q[kOut ? kC * K * 2 : 16];
+  alignas(16) char k[kC * kRowBytes<K>];
+  alignas(16) char v[kC * kRowBytes<V>];
+  alignas(16) char q[kOut ? kC * kRowBytes<K> : 16];
   alignas(16) char p[kOut ? 8 * 1024 : 16];  // P fragments (token tile of 16, block of 32 sources)
   struct Decays {
     double G[kC];             // inclusive cumsum of g
@@ -285,26 +293,27 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
   const int lane = local_copy(lane_);
   constexpr int VT = Walk<K, V>::VT, KT = Walk<K, V>::KT, KB = K / 32;
   const int g = lane >> 4, l16 = lane & 15;
+  const int row = row_lane<K>(lane), col_k = col_lane<K>(lane), col_v = col_lane<V>(lane);
   bf16x8 raw[2][VT];
   if constexpr (kOut) {
-    // P^T tiles (token tile tt, source tile st <= tt), rows s = 4 g + i, column t. The ten tiles are
-    // dealt out three or two to a wave: waves 0 and 1 share row 3 and take (0, 0) and (1, 0),
-    // waves 2 and 3 share row 2, and wave 3 has (1, 1).
+    // P^T tiles (token tile tt, source tile st <= tt), rows s = 4 g + i, column t: ten, dealt out
+    // over the waves.
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      const int tt = j < 2 ? (wave < 2 ? 3 : (wave == 3 && j == 1 ? 1 : 2)) : wave;
-      const int st = j < 2 ? (wave < 2 ? 2 * wave + j : (wave == 2 ? j : 2 - j)) : 0;
-      if (j == 2 && wave >= 2) break;
+    for (int j = 0; j < 10; j += kWavesOf<V>) {
+      const int tile = j + wave;
+      if (tile >= 10) break;
+      const int tt = (0x0112223333ull >> (4 * tile)) & 15, st = (0x0102103210ull >> (4 * tile)) & 15;
       const int t = 16 * tt + l16;
       f32x4 d = zero4();
 #pragma unroll
       for (int m = 0; m < KB; ++m)
-        d = mfma(read_row<K>(sh.k, 16 * st + l16, 4 * m + g), read_row<K>(sh.q, t, 4 * m + g), d);
+        d = mfma(read_row<K>(sh.k, row, 16 * st, m), read_row<K>(sh.q, row, 16 * tt, m), d);
       const double Gt = dec.G[t];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int s = 16 * st + 4 * g + i;
-        d[i] = s <= t ? d[i] * p.scale * __expf((float)(Gt - dec.G[s])) : 0.f;
+        const float x = (float)(Gt - dec.G[s]);
+        d[i] *= p.scale * __expf(s <= t ? x : -INFINITY);
       }
       // Rounded to bf16 once: the product with V is a bf16 MFMA with fp32 sums.
       const bf16x4 b = {to_bf16(d[0]), to_bf16(d[1]), to_bf16(d[2]), to_bf16(d[3])};
@@ -323,7 +332,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       for (int vt = 0; vt < VT; ++vt) sb[vt] = pack8(walk.S[vt][2 * m], walk.S[vt][2 * m + 1]);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const bf16x8 b = read_row_acc<K>(sh.q, 16 * tt + l16, m, g);
+        const bf16x8 b = read_row<K>(sh.q, row, 16 * tt, m);
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(sb[vt], b, acc[vt][tt]);
       }
@@ -337,7 +346,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, 32 * b, wave * VT + vt, lane);
+      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, col_v, 32 * b, wave * VT + vt);
     __syncthreads();  // P
     const __amdgpu_buffer_rsrc_t out = rows_buffer<V>(reinterpret_cast<const __bf16*>(p.out) + h * p.o_h, first, p.o_t, count);
 #pragma unroll
@@ -365,10 +374,11 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, 32 * b, wave * VT + vt, lane);
+      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, col_v, 32 * b, wave * VT + vt);
   }
-  // State. The decayed values go in as three bf16 terms, exact to 2^-25 of each, against the
-  // stored keys, which are bf16: the state keeps fp32 accuracy. (Two terms leave 3e-6.)
+  // State. The decayed values x (fp32) go in as three bf16 terms of 8 bits each, cut off rather
+  // than rounded, so that x = hi + mid + lo exactly, against the stored keys, which are bf16: the
+  // state keeps fp32 accuracy. (Two rounded terms leave 3e-6.)
   const float total = dec.total;
 #pragma unroll
   for (int vt = 0; vt < VT; ++vt)
@@ -381,23 +391,32 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
     const f32x4 c1 = *reinterpret_cast<const f32x4*>(&dec.c[32 * b + 16 + 4 * g]);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt) {
+      const u32x4 w = __builtin_bit_cast(u32x4, raw[b][vt]);
+      u32x4 h, m, l;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = from_bf16(raw[b][vt][i]) * (i < 4 ? c0[i & 3] : c1[i & 3]);
-        hi[vt][i] = to_bf16(x);
-        const float r = x - from_bf16(hi[vt][i]);
-        mid[vt][i] = to_bf16(r);
-        lo[vt][i] = to_bf16(r - from_bf16(mid[vt][i]));
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 c = i < 2 ? c0 : c1;
+        const float x0 = __uint_as_float(w[i] << 16) * c[2 * i & 3], x1 = __uint_as_float(w[i] & kTop) * c[(2 * i + 1) & 3];
+        const float r0 = x0 - __uint_as_float(__float_as_uint(x0) & kTop), r1 = x1 - __uint_as_float(__float_as_uint(x1) & kTop);
+        const float s0 = r0 - __uint_as_float(__float_as_uint(r0) & kTop), s1 = r1 - __uint_as_float(__float_as_uint(r1) & kTop);
+        h[i] = top_halves(x0, x1);
+        m[i] = top_halves(r0, r1);
+        l[i] = top_halves(s0, s1);
       }
+      hi[vt] = __builtin_bit_cast(bf16x8, h), mid[vt] = __builtin_bit_cast(bf16x8, m), lo[vt] = __builtin_bit_cast(bf16x8, l);
     }
+    // Two tiles of K at a time, term by term: no product waits for the one before it.
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const bf16x8 kf = read_col<K>(sh.k, 32 * b, kt, lane);
+    for (int kt = 0; kt < KT; kt += 2) {
+      const bf16x8 k0 = read_col<K>(sh.k, col_k, 32 * b, kt), k1 = read_col<K>(sh.k, col_k, 32 * b, kt + 1);
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) {
-        walk.S[vt][kt] = mfma(kf, lo[vt], walk.S[vt][kt]);
-        walk.S[vt][kt] = mfma(kf, mid[vt], walk.S[vt][kt]);
-        walk.S[vt][kt] = mfma(kf, hi[vt], walk.S[vt][kt]);
+      for (int term = 0; term < 3; ++term) {
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          const bf16x8 u = term == 0 ? lo[vt] : (term == 1 ? mid[vt] : hi[vt]);
+          walk.S[vt][kt] = mfma(k0, u, walk.S[vt][kt]);
+          walk.S[vt][kt + 1] = mfma(k1, u, walk.S[vt][kt + 1]);
+        }
       }
     }
   }
@@ -406,7 +425,8 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 // Walks segment `seg` of head h. kOut: every token, with outputs and final states; else only
 // the sequence that crosses the segment's end, for its map.
 template <int K, int V, bool kOut>
-__global__ __launch_bounds__(kThreads, 2) void linear_walk(const LinearPlan p) {
+__global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 && kWavesOf<V> == 8 ? 4 : 2) void linear_walk(const LinearPlan p) {
+  constexpr int kThreads = 64 * kWavesOf<V>;
   __shared__ Shared<K, V, kOut> sh;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
@@ -426,8 +446,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_walk(const LinearPlan p) {
     if (!crosses) return;
   }
   Walk<K, V> walk;
-  Rows<K> rq, rk;
-  Rows<V> rv;
+  Rows<K, kThreads> rq, rk;
+  Rows<V, kThreads> rv;
   float g_next = 0.f;  // this lane's token of the next chunk
   auto fetch = [&](int64_t first, int count) {
     g_next = 0.f;
@@ -509,13 +529,15 @@ __global__ __launch_bounds__(kThreads, 2) void linear_walk(const LinearPlan p) {
   } while (kOut && ++n < p.N && axis_own(p, n) < b);
 }
 
+constexpr int kCombineThreads = 256;
+
 // Chains the segments' states: map s becomes the true state at the end of segment s. The chain
 // runs along each element by itself, so every thread owns four and only loads wait on nothing.
-__global__ __launch_bounds__(kThreads) void linear_combine(const LinearPlan p) {
-  const int per_head = p.K * p.V / (4 * kThreads);
+__global__ __launch_bounds__(kCombineThreads) void linear_combine(const LinearPlan p) {
+  const int per_head = p.K * p.V / (4 * kCombineThreads);
   const int h = blockIdx.x / per_head;
   const int64_t plane = (int64_t)p.K * p.V;
-  const int64_t e = (int64_t)(blockIdx.x % per_head) * 4 * kThreads + threadIdx.x * 4;
+  const int64_t e = (int64_t)(blockIdx.x % per_head) * 4 * kCombineThreads + threadIdx.x * 4;
   f32x4 cur = zero4();
 #pragma unroll 4
   for (int s = 0; s < p.n_seg - 1; ++s) {
@@ -536,10 +558,11 @@ template <bool kOut>
 int launch_walk(const LinearPlan& p, int segments, void* stream) {
   const dim3 grid((unsigned)((int64_t)segments * p.H));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (p.K == 128 && p.V == 128) linear_walk<128, 128, kOut><<<grid, kThreads, 0, s>>>(p);
-  else if (p.K == 128) linear_walk<128, 64, kOut><<<grid, kThreads, 0, s>>>(p);
-  else if (p.V == 128) linear_walk<64, 128, kOut><<<grid, kThreads, 0, s>>>(p);
-  else linear_walk<64, 64, kOut><<<grid, kThreads, 0, s>>>(p);
+  const dim3 threads(64 * (p.V == 128 ? kWavesOf<128> : kWavesOf<64>));
+  if (p.K == 128 && p.V == 128) linear_walk<128, 128, kOut><<<grid, threads, 0, s>>>(p);
+  else if (p.K == 128) linear_walk<128, 64, kOut><<<grid, threads, 0, s>>>(p);
+  else if (p.V == 128) linear_walk<64, 128, kOut><<<grid, threads, 0, s>>>(p);
+  else linear_walk<64, 64, kOut><<<grid, threads, 0, s>>>(p);
   return (int)hipGetLastError();
 }
 
@@ -548,8 +571,8 @@ int launch_walk(const LinearPlan& p, int segments, void* stream) {
 int launch_linear_maps(const LinearPlan& p, void* stream) { return launch_walk<false>(p, p.n_seg - 1, stream); }
 int launch_linear_output(const LinearPlan& p, void* stream) { return launch_walk<true>(p, p.n_seg, stream); }
 int launch_linear_combine(const LinearPlan& p, void* stream) {
-  const dim3 grid((unsigned)((int64_t)p.H * (p.K * p.V / (4 * kThreads))));
-  linear_combine<<<grid, kThreads, 0, reinterpret_cast<hipStream_t>(stream)>>>(p);
+  const dim3 grid((unsigned)((int64_t)p.H * (p.K * p.V / (4 * kCombineThreads))));
+  linear_combine<<<grid, kCombineThreads, 0, reinterpret_cast<hipStream_t>(stream)>>>(p);
   return (int)hipGetLastError();
 }
 
