@@ -37,6 +37,7 @@ template <int V>
 constexpr int kWavesOf = V / 16 >= 8 ? 8 : 4;
 constexpr float kMinLogDecay = -120.f;  // e^-120 is 0 in fp32; keeps -inf out of the differences
 
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
@@ -54,24 +55,23 @@ __device__ __forceinline__ uint32_t top_halves(float a, float b) {
 }
 
 // LDS tile of 64 rows of D bf16. A row takes 16 bytes more than its elements, and inside 16 rows
-// row r stands at place 2 (r % 8) + r / 8: the 16 rows of an operand read then fall on all 64 banks
-// (places 4 banks apart), and so do the 8 rows of half a transposing read (every other place). Every
-// read is a lane's own place and a constant offset.
+// row r stands at place 2 (r % 8) + r / 8: the 16 rows of an operand read then start on different
+// banks, and the 8 rows of half a transposing read do not meet. Every read is a lane's own place and
+// a constant offset. q, which every wave reads as operand rows, holds each 32 elements in the
+// accumulators' order (unit g of 16 bytes has elements 4 g + i and 16 + 4 g + i), so that an operand
+// is one 16-byte read of 9 cycles; k and v, read by columns, keep their order, and k's few reads as
+// rows take two 8-byte pieces, 16 cycles.
 template <int D>
 constexpr int kRowBytes = 2 * D + 16;
 template <int D>
 __device__ __forceinline__ int row_at(int row) {
   return ((row & ~15) | ((row & 7) << 1) | ((row >> 3) & 1)) * kRowBytes<D>;
 }
-// Operand rows: row r0 + l % 16 (r0 a multiple of 16), elements 32 m + 4 g + i and
-// 32 m + 16 + 4 g + i: the accumulators' order, in which q and k meet each other too.
-template <int D>
-__device__ __forceinline__ int row_lane(int lane) {
-  return row_at<D>(lane & 15) + (lane >> 4) * 8;
-}
-template <int D>
-__device__ __forceinline__ bf16x8 read_row(const char* tile, int at, int r0, int m) {
-  const char* p = tile + r0 * kRowBytes<D> + m * 64 + at;
+// Operand rows: row r0 + l % 16 (r0 a multiple of 16), elements 32 m + 4 g + i, 32 m + 16 + 4 g + i.
+template <int D, bool kOrdered>
+__device__ __forceinline__ bf16x8 read_row(const char* tile, int lane, int r0, int m) {
+  const char* p = tile + r0 * kRowBytes<D> + m * 64 + row_at<D>(lane & 15) + (lane >> 4) * (kOrdered ? 16 : 8);
+  if constexpr (kOrdered) return *reinterpret_cast<const bf16x8*>(p);
   const bf16x4 a = *reinterpret_cast<const bf16x4*>(p), b = *reinterpret_cast<const bf16x4*>(p + 32);
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
@@ -79,12 +79,8 @@ __device__ __forceinline__ bf16x8 read_row(const char* tile, int at, int r0, int
 // 32), by two transposing reads: 16 lanes give the addresses of a 4 x 16 block, lane j of row j / 4 and
 // columns 4 (j % 4).
 template <int D>
-__device__ __forceinline__ int col_lane(int lane) {
-  return row_at<D>(4 * (lane >> 4) + ((lane & 15) >> 2)) + (lane & 3) * 8;
-}
-template <int D>
-__device__ __forceinline__ bf16x8 read_col(const char* tile, int at, int t0, int c) {
-  const char* p = tile + t0 * kRowBytes<D> + c * 32 + at;
+__device__ __forceinline__ bf16x8 read_col(const char* tile, int lane, int t0, int c) {
+  const char* p = tile + t0 * kRowBytes<D> + c * 32 + row_at<D>(4 * (lane >> 4) + ((lane & 15) >> 2)) + (lane & 3) * 8;
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 16 * kRowBytes<D>));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -231,15 +227,29 @@ struct Rows {
   u32x4 w[kPasses];
   __device__ __forceinline__ void load(const __bf16* base, int64_t stride, int64_t first, int count, int tid) {
     const __amdgpu_buffer_rsrc_t r = rows_buffer<D>(base, first, stride, count);
+    tid = local_copy(tid);
     const int at = (tid / kUnits) * (int)stride * 2 + (tid % kUnits) * 16;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
       w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRows * (int)stride * 2, 0, 0));
   }
+  // kOrdered: the 8 elements of unit u of four go to units 2 (u % 2) and 2 (u % 2) + 1, half u / 2.
+  template <bool kOrdered>
   __device__ __forceinline__ void put(char* tile, int tid) const {
+    tid = local_copy(tid);
+    const int u = tid % kUnits;
+    static_assert(kRows % 16 == 0, "whole groups of rows");
+    char* at = tile + row_at<D>(tid / kUnits) + (kOrdered ? (u >> 2) * 64 + (u & 1) * 32 + ((u >> 1) & 1) * 8 : u * 16);
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      *reinterpret_cast<u32x4*>(tile + row_at<D>(tid / kUnits + i * kRows) + (tid % kUnits) * 16) = w[i];
+    for (int i = 0; i < kPasses; ++i) {
+      char* to = at + i * kRows * kRowBytes<D>;
+      if constexpr (kOrdered) {
+        *reinterpret_cast<u32x2*>(to) = u32x2{w[i][0], w[i][1]};
+        *reinterpret_cast<u32x2*>(to + 16) = u32x2{w[i][2], w[i][3]};
+      } else {
+        *reinterpret_cast<u32x4*>(to) = w[i];
+      }
+    }
   }
 };
 
@@ -276,6 +286,7 @@ __device__ __forceinline__ double prefix_sum(double x) {
 }
 template <typename D>
 __device__ __forceinline__ void put_decays(D& d, float g, float scale, int lane) {
+  lane = local_copy(lane);
   const double G = prefix_sum((double)fmaxf(g, kMinLogDecay));
   const uint64_t u = __builtin_bit_cast(uint64_t, G);
   const double end = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
@@ -293,7 +304,6 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
   const int lane = local_copy(lane_);
   constexpr int VT = Walk<K, V>::VT, KT = Walk<K, V>::KT, KB = K / 32;
   const int g = lane >> 4, l16 = lane & 15;
-  const int row = row_lane<K>(lane), col_k = col_lane<K>(lane), col_v = col_lane<V>(lane);
   bf16x8 raw[2][VT];
   if constexpr (kOut) {
     // P^T tiles (token tile tt, source tile st <= tt), rows s = 4 g + i, column t: ten, dealt out
@@ -307,7 +317,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       f32x4 d = zero4();
 #pragma unroll
       for (int m = 0; m < KB; ++m)
-        d = mfma(read_row<K>(sh.k, row, 16 * st, m), read_row<K>(sh.q, row, 16 * tt, m), d);
+        d = mfma(read_row<K, false>(sh.k, lane, 16 * st, m), read_row<K, true>(sh.q, lane, 16 * tt, m), d);
       const double Gt = dec.G[t];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -332,7 +342,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       for (int vt = 0; vt < VT; ++vt) sb[vt] = pack8(walk.S[vt][2 * m], walk.S[vt][2 * m + 1]);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const bf16x8 b = read_row<K>(sh.q, row, 16 * tt, m);
+        const bf16x8 b = read_row<K, true>(sh.q, lane, 16 * tt, m);
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(sb[vt], b, acc[vt][tt]);
       }
@@ -346,8 +356,8 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, col_v, 32 * b, wave * VT + vt);
-    __syncthreads();  // P
+      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, lane, 32 * b, wave * VT + vt);
+    barrier_lds();  // P
     const __amdgpu_buffer_rsrc_t out = rows_buffer<V>(reinterpret_cast<const __bf16*>(p.out) + h * p.o_h, first, p.o_t, count);
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
@@ -365,7 +375,6 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       for (int vt = 0; vt < VT; ++vt) {
         const f32x4 o = acc[vt][tt];
         const bf16x4 b = {to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])};
-        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), out,
                                               (16 * tt + l16) * (int)p.o_t * 2 + ((wave * VT + vt) * 16 + 4 * g) * 2, 0, 0);
       }
@@ -374,7 +383,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, col_v, 32 * b, wave * VT + vt);
+      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, lane, 32 * b, wave * VT + vt);
   }
   // State. The decayed values x (fp32) go in as three bf16 terms of 8 bits each, cut off rather
   // than rounded, so that x = hi + mid + lo exactly, against the stored keys, which are bf16: the
@@ -408,7 +417,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
     // Two tiles of K at a time, term by term: no product waits for the one before it.
 #pragma unroll
     for (int kt = 0; kt < KT; kt += 2) {
-      const bf16x8 k0 = read_col<K>(sh.k, col_k, 32 * b, kt), k1 = read_col<K>(sh.k, col_k, 32 * b, kt + 1);
+      const bf16x8 k0 = read_col<K>(sh.k, lane, 32 * b, kt), k1 = read_col<K>(sh.k, lane, 32 * b, kt + 1);
 #pragma unroll
       for (int term = 0; term < 3; ++term) {
 #pragma unroll
@@ -502,10 +511,10 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 && kWavesOf<V> == 8 ? 4 
     if (wave == 3) put_decays(sh.decays[0], g_next, p.scale, lane);
     while (left > 0) {
       const int count = min(left, kC);
-      if constexpr (kOut) rq.put(sh.q, tid);
-      rk.put(sh.k, tid);
-      rv.put(sh.v, tid);
-      __syncthreads();
+      if constexpr (kOut) rq.template put<true>(sh.q, tid);
+      rk.template put<false>(sh.k, tid);
+      rv.template put<false>(sh.v, tid);
+      barrier_lds();
       const int64_t here = first;
       first += count;
       left -= count;
@@ -515,7 +524,7 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 && kWavesOf<V> == 8 ? 4 
       turn ^= 1;
       // Wave 3 has the fewest tiles of P.
       if (wave == 3 && left > 0) put_decays(sh.decays[turn], g_next, p.scale, lane);
-      __syncthreads();
+      barrier_lds();
     }
     if constexpr (kOut) {
       if (t1 == s.len) {
@@ -532,24 +541,35 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 && kWavesOf<V> == 8 ? 4 
 constexpr int kCombineThreads = 256;
 
 // Chains the segments' states: map s becomes the true state at the end of segment s. The chain
-// runs along each element by itself, so every thread owns four and only loads wait on nothing.
+// runs along each element by itself: a thread owns four, and loads kAhead segments at a time, so
+// that it waits for memory once for each kAhead.
+constexpr int kAhead = 16;
 __global__ __launch_bounds__(kCombineThreads) void linear_combine(const LinearPlan p) {
   const int per_head = p.K * p.V / (4 * kCombineThreads);
   const int h = blockIdx.x / per_head;
-  const int64_t plane = (int64_t)p.K * p.V;
-  const int64_t e = (int64_t)(blockIdx.x % per_head) * 4 * kCombineThreads + threadIdx.x * 4;
+  const int64_t plane = (int64_t)p.K * p.V, step = p.H * plane;
+  float* at = p.maps + h * plane + (int64_t)(blockIdx.x % per_head) * 4 * kCombineThreads + threadIdx.x * 4;
+  const int n = p.n_seg - 1;
   f32x4 cur = zero4();
-#pragma unroll 4
-  for (int s = 0; s < p.n_seg - 1; ++s) {
-    f32x4* at = reinterpret_cast<f32x4*>(p.maps + ((int64_t)s * p.H + h) * plane + e);
-    const f32x4 m = *at;
-    const float d = p.decays[(int64_t)s * p.H + h];
-    const int span = p.spans[s];
-    if (span == 1) {
-      cur = m;
-    } else if (span == 2) {
-      cur = m + cur * d;
-      *at = cur;
+  for (int s0 = 0; s0 < n; s0 += kAhead) {
+    f32x4 m[kAhead];
+    float d[kAhead];
+    int span[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int s = min(s0 + j, n - 1);
+      m[j] = *reinterpret_cast<const f32x4*>(at + s * step);
+      d[j] = p.decays[(int64_t)s * p.H + h];
+      span[j] = p.spans[s];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (s0 + j >= n) break;
+      if (span[j] == 1) cur = m[j];
+      if (span[j] == 2) {
+        cur = m[j] + cur * d[j];
+        *reinterpret_cast<f32x4*>(at + (s0 + j) * step) = cur;
+      }
     }
   }
 }
