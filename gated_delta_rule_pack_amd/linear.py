@@ -19,25 +19,26 @@ __all__ = ["linear_fwd", "linear_step", "rotary", "rotary_frequencies"]
 _STATE_DT = {torch.float32: _lib.KDA_F32, torch.float16: _lib.KDA_F16, torch.bfloat16: _lib.KDA_BF16}
 
 
-def _need(cond, msg, exc=ValueError):
-    if not cond:
-        raise exc(msg)
+# The calls are made once for each layer and token, where a kernel of a few microseconds waits for
+# them: every check is a plain condition, and a message is made only when it fails.
 
 
 def _packed(name, t):
     """[T, H, D] of a [T, H, D] or [1, T, H, D] tensor."""
-    if t.dim() == 4 and t.shape[0] == 1:
-        t = t[0]
-    _need(t.dim() == 3, f"{name} must be [T, H, D] (or [1, T, H, D]), got {tuple(t.shape)}")
-    return t
+    n = t.dim()
+    if n == 3:
+        return t
+    if n == 4 and t.shape[0] == 1:
+        return t[0]
+    raise ValueError(f"{name} must be [T, H, D] (or [1, T, H, D]), got {tuple(t.shape)}")
 
 
-def _strides(name, t):
+def _strides(name, t, T, H, D):
     """Element strides between tokens and between heads; dense ones stand in where the tensor has
     a single token or head (torch leaves those arbitrary)."""
-    T, H, D = t.shape
     st, sh, sd = t.stride()
-    _need(sd == 1 or D == 1, f"{name} must have adjacent elements along its last dimension")
+    if sd != 1 and D != 1:
+        raise ValueError(f"{name} must have adjacent elements along its last dimension")
     if H == 1:
         sh = D
     if T <= 1:
@@ -45,29 +46,42 @@ def _strides(name, t):
     return st, sh
 
 
-def _on(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _on(index, names, *tensors):
+    for i, t in enumerate(tensors):
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{names.split()[i]} must be on cuda:{index}, got {t.device}")
 
 
-def _fill_rotation(a, T, limit, positions, inv_freq, interleaved, factor):
+def _vector(name, t, n, dtypes):
+    """A contiguous vector of n elements of one of the dtypes."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+_I32 = (torch.int32,)
+_INTS = (torch.int32, torch.int64)
+_BOOLS = (torch.bool, torch.uint8)
+_BF16 = torch.bfloat16
+
+
+def _fill_rotation(a, T, limit, positions, inv_freq, interleaved):
     """The rotary fields of either argument struct."""
-    _need(positions is not None and inv_freq is not None, "rotary positions need both positions and inv_freq")
-    _need(inv_freq.dtype == torch.float64, f"inv_freq must be fp64, got {inv_freq.dtype}", TypeError)
-    _need(inv_freq.dim() == 1 and inv_freq.is_contiguous() and 1 <= inv_freq.numel() <= limit // 2,
-          f"inv_freq must be a contiguous vector of 1 to {limit // 2} frequencies")
-    _need(positions.dtype in (torch.int32, torch.int64), f"positions must be int32 or int64, got {positions.dtype}", TypeError)
+    if positions is None or inv_freq is None:
+        raise ValueError("rotary positions need both positions and inv_freq")
+    if inv_freq.dtype != torch.float64:
+        raise TypeError(f"inv_freq must be fp64, got {inv_freq.dtype}")
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not 1 <= inv_freq.shape[0] <= limit // 2:
+        raise ValueError(f"inv_freq must be a contiguous vector of 1 to {limit // 2} frequencies")
     if positions.dim() == 2 and positions.shape[0] == 1:
         positions = positions[0]
-    _need(positions.dim() == 1 and positions.is_contiguous() and positions.numel() == T,
-          f"positions must be a contiguous vector of T = {T} elements")
-    a.rot_dim = 2 * inv_freq.numel()
+    a.positions = _vector("positions", positions, T, _INTS)
+    a.positions_i64 = positions.dtype == torch.int64
+    a.rot_dim = 2 * inv_freq.shape[0]
     a.inv_freq = inv_freq.data_ptr()
-    a.positions = positions.data_ptr()
-    a.positions_i64 = 1 if positions.dtype == torch.int64 else 0
-    a.interleaved = 1 if interleaved else 0
-    return float(factor)
+    a.interleaved = bool(interleaved)
 
 
 def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None, scale=None, initial_state=None,
@@ -78,130 +92,160 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
     cannot see: dtypes, shapes, strides and element counts."""
     q, k, v = _packed("q", q), _packed("k", k), _packed("v", v)
     T, H_qk, K = q.shape
-    H, V = v.shape[1], v.shape[2]
-    _need(k.shape == q.shape, "q and k must have the same shape")
-    _need(v.shape[0] == T, "v must have q's token count")
-    _need(0 < H_qk <= H and H % H_qk == 0, f"q/k heads ({H_qk}) must divide v heads ({H})")
+    Tv, H, V = v.shape
+    if k.shape != q.shape:
+        raise ValueError("q and k must have the same shape")
+    if Tv != T:
+        raise ValueError("v must have q's token count")
+    if H_qk < 1 or H % H_qk != 0 or H < 1:
+        raise ValueError(f"q/k heads ({H_qk}) must divide v heads ({H})")
+    if q.dtype != _BF16 or k.dtype != _BF16 or v.dtype != _BF16:
+        raise TypeError(f"q, k and v must be bf16, got {q.dtype}, {k.dtype}, {v.dtype}")
     a = _lib.LinearArgs()
     if cu_seqlens is not None:
-        _need(cu_seqlens.dtype == torch.int32, "cu_seqlens must be int32", TypeError)
-        _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2 and cu_seqlens.is_contiguous(),
-              "cu_seqlens must be a contiguous [N+1] vector with N >= 1")
         N = cu_seqlens.numel() - 1
-        a.cu_seqlens = cu_seqlens.data_ptr()
+        if N < 1:
+            raise ValueError("cu_seqlens must be an [N+1] vector with N >= 1")
+        a.cu_seqlens = _vector("cu_seqlens", cu_seqlens, N + 1, _I32)
         if cu_seqlens_cpu is not None:
-            _need(cu_seqlens_cpu.device.type == "cpu" and cu_seqlens_cpu.dtype == torch.int32,
-                  "cu_seqlens_cpu must be a CPU int32 tensor", TypeError)
-            _need(cu_seqlens_cpu.is_contiguous() and cu_seqlens_cpu.numel() == N + 1,
-                  "cu_seqlens_cpu must be contiguous with N+1 elements, like cu_seqlens")
-            a.cu_seqlens_host = cu_seqlens_cpu.data_ptr()
+            if cu_seqlens_cpu.device.type != "cpu":
+                raise TypeError("cu_seqlens_cpu must be a CPU int32 tensor")
+            a.cu_seqlens_host = _vector("cu_seqlens_cpu", cu_seqlens_cpu, N + 1, _I32)
     a.T, a.N, a.H, a.H_qk, a.K, a.V = T, N, H, H_qk, K, V
-    a.scale = 1.0 / math.sqrt(K) if scale is None else float(scale)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t.dtype == torch.bfloat16, f"{name} must be bf16, got {t.dtype}", TypeError)
+    a.scale = 1.0 / math.sqrt(K) if scale is None else scale
     a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    a.q_stride_t, a.q_stride_h = _strides("q", q)
-    a.k_stride_t, a.k_stride_h = _strides("k", k)
-    a.v_stride_t, a.v_stride_h = _strides("v", v)
+    a.q_stride_t, a.q_stride_h = _strides("q", q, T, H_qk, K)
+    a.k_stride_t, a.k_stride_h = _strides("k", k, T, H_qk, K)
+    a.v_stride_t, a.v_stride_h = _strides("v", v, T, H, V)
     if out is not None:
         out = _packed("out", out)
-        _need(out.dtype == torch.bfloat16, f"out must be bf16, got {out.dtype}", TypeError)
-        _need(out.shape == v.shape, f"out must have v's shape {tuple(v.shape)}, got {tuple(out.shape)}")
+        if out.dtype != _BF16:
+            raise TypeError(f"out must be bf16, got {out.dtype}")
+        if out.shape != v.shape:
+            raise ValueError(f"out must have v's shape {tuple(v.shape)}, got {tuple(out.shape)}")
         a.out = out.data_ptr()
-        a.out_stride_t, a.out_stride_h = _strides("out", out)
+        a.out_stride_t, a.out_stride_h = _strides("out", out, T, H, V)
     if g is not None:
-        _need(g.dtype in (torch.float32, torch.bfloat16), f"g must be fp32 or bf16, got {g.dtype}", TypeError)
-        if g.dim() == 3 and g.shape[0] == 1:
-            g = g[0]
-        per_token = g.dim() == 2
-        _need(tuple(g.shape) == ((T, H) if per_token else (H,)),
-              f"g must be [H] = {(H,)} or [T, H] = {(T, H)}, got {tuple(g.shape)}")
-        _need(g.is_contiguous(), "g must be contiguous")
+        n = g.dim()
+        if n == 3 and g.shape[0] == 1:
+            g, n = g[0], 2
+        if g.dtype == torch.float32:
+            a.g_dtype = _lib.KDA_F32
+        elif g.dtype == _BF16:
+            a.g_dtype = _lib.KDA_BF16
+        else:
+            raise TypeError(f"g must be fp32 or bf16, got {g.dtype}")
+        if g.shape != ((T, H) if n == 2 else (H,)) or not g.is_contiguous():
+            raise ValueError(f"g must be a contiguous [H] = {(H,)} or [T, H] = {(T, H)}, got {tuple(g.shape)}")
         a.g = g.data_ptr()
-        a.g_dtype = _STATE_DT[g.dtype]
-        a.g_per_token = 1 if per_token else 0
-    plane = (H, K, V) if state_k_first else (H, V, K)
-    for name, st in (("initial_state", initial_state), ("final_state", final_state)):
-        if st is None:
-            continue
-        _need(st.dtype in _STATE_DT, f"{name} must be fp32, fp16 or bf16", TypeError)
-        _need(tuple(st.shape) == (N, *plane), f"{name} must be {(N, *plane)}, got {tuple(st.shape)}")
-        _need(st.is_contiguous(), f"{name} must be contiguous")
-        a.state_dtype = _STATE_DT[st.dtype]
-    if initial_state is not None and final_state is not None:
-        _need(initial_state.dtype == final_state.dtype, "final_state must have initial_state's dtype", TypeError)
-    a.initial_state = None if initial_state is None else initial_state.data_ptr()
-    a.final_state = None if final_state is None else final_state.data_ptr()
+        a.g_per_token = n == 2
     if state_cache is not None:
-        _need(state_cache.dtype in _STATE_DT, "state_cache must be fp32, fp16 or bf16", TypeError)
-        _need(state_cache.dim() == 4 and tuple(state_cache.shape[1:]) == plane and state_cache.shape[0] >= 1,
-              f"state_cache must be [slots, {', '.join(map(str, plane))}] with at least one slot")
-        sizes, strides = state_cache.shape, state_cache.stride()
-        _need((H == 1 or strides[1] == K * V) and strides[2:] == (sizes[3], 1), "each state_cache slot plane must be dense")
-        stride0 = H * K * V if sizes[0] == 1 else strides[0]
-        _need(stride0 >= H * K * V, "state_cache stride(0) must be at least one H*V*K plane")
+        if state_cache.dtype not in _STATE_DT:
+            raise TypeError("state_cache must be fp32, fp16 or bf16")
+        rows, cols = (K, V) if state_k_first else (V, K)
+        sizes = state_cache.shape
+        if sizes[1:] != (H, rows, cols) or sizes[0] < 1:
+            raise ValueError(f"state_cache must be [slots, {H}, {rows}, {cols}] with at least one slot")
+        s0, s1, s2, s3 = state_cache.stride()
+        plane = H * K * V
+        if (H != 1 and s1 != K * V) or s2 != cols or s3 != 1:
+            raise ValueError("each state_cache slot plane must be dense")
+        if sizes[0] == 1:
+            s0 = plane
+        if s0 < plane:
+            raise ValueError("state_cache stride(0) must be at least one H*V*K plane")
         a.state_dtype = _STATE_DT[state_cache.dtype]
-        a.state_cache, a.num_slots, a.state_cache_stride0 = state_cache.data_ptr(), sizes[0], stride0
+        a.state_cache, a.num_slots, a.state_cache_stride0 = state_cache.data_ptr(), sizes[0], s0
         if state_indices is not None:
-            _need(state_indices.dtype == torch.int32, f"state_indices must be int32, got {state_indices.dtype}", TypeError)
-            _need(state_indices.dim() == 1 and state_indices.is_contiguous() and state_indices.numel() == N,
-                  f"state_indices must be a contiguous vector of N = {N} elements")
-            a.state_indices = state_indices.data_ptr()
+            a.state_indices = _vector("state_indices", state_indices, N, _I32)
         if has_initial_state is not None:
-            _need(has_initial_state.dtype in (torch.bool, torch.uint8),
-                  f"has_initial_state must be bool or uint8, got {has_initial_state.dtype}", TypeError)
-            _need(has_initial_state.dim() == 1 and has_initial_state.is_contiguous() and has_initial_state.numel() == N,
-                  f"has_initial_state must be a contiguous vector of N = {N} elements")
-            a.has_initial_state = has_initial_state.data_ptr()
-    else:
-        _need(state_indices is None and has_initial_state is None, "state_indices and has_initial_state belong to a state_cache")
-    a.state_k_first = 1 if state_k_first else 0
+            a.has_initial_state = _vector("has_initial_state", has_initial_state, N, _BOOLS)
+    elif state_indices is not None or has_initial_state is not None:
+        raise ValueError("state_indices and has_initial_state belong to a state_cache")
+    if initial_state is not None or final_state is not None:
+        shape = (N, H, K, V) if state_k_first else (N, H, V, K)
+        for name, st in (("initial_state", initial_state), ("final_state", final_state)):
+            if st is None:
+                continue
+            if st.dtype not in _STATE_DT:
+                raise TypeError(f"{name} must be fp32, fp16 or bf16")
+            if st.shape != shape or not st.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {shape}, got {tuple(st.shape)}")
+            a.state_dtype = _STATE_DT[st.dtype]
+        if initial_state is not None:
+            a.initial_state = initial_state.data_ptr()
+        if final_state is not None:
+            a.final_state = final_state.data_ptr()
+            if initial_state is not None and initial_state.dtype != final_state.dtype:
+                raise TypeError("final_state must have initial_state's dtype")
+    if state_k_first:
+        a.state_k_first = 1
     if positions is not None or inv_freq is not None:
-        a.rot_factor = _fill_rotation(a, T, K, positions, inv_freq, interleaved, rotary_factor)
-    a.seg_len = int(seg_len)
+        _fill_rotation(a, T, K, positions, inv_freq, interleaved)
+        a.rot_factor = rotary_factor
+    if seg_len:
+        a.seg_len = seg_len
     return a
 
 
-def _enter(q, stream):
-    """(device index, stream handle) of a call on q's device."""
-    device = q.device
-    if device.type != "cuda":
-        raise ValueError("inputs must be on a GPU")
-    return device.index, (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-
-def _context(context, index):
-    if context is not None:
-        _need(context.device == index, f"the context is device {context.device}'s, the tensors are on {index}")
-        return context.ptr
-    from . import get_context
-    return get_context(torch.device("cuda", index)).ptr
-
-
 def _check(rc, where):
-    if rc != _lib.KDA_OK:
+    if rc:
         from . import KDAError
         raise KDAError(rc, where)
 
 
-class _On:
-    """The call's device current, and its allocations on its stream (entered only where that differs
-    from what is current already: the guards cost more than a small kernel)."""
+_contexts = {}  # device index -> the device's shared context
 
-    def __init__(self, index, stream):
-        self.guards = []
-        if torch.cuda.current_device() != index:
-            self.guards.append(torch.cuda.device(index))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
+
+def _context(context, index):
+    if context is None:
+        context = _contexts.get(index)
+        if context is None:
+            from . import get_context
+            context = _contexts[index] = get_context(torch.device("cuda", index))
+    elif context.device != index:
+        raise ValueError(f"the context is device {context.device}'s, the tensors are on {index}")
+    return context.ptr
+
+
+# The current stream's handle; torch.cuda.current_stream makes an object of it in 2 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+class _Call:
+    """The call's device current and its allocations on its stream. The guards cost more than a
+    small kernel, so they are entered only where they change something."""
+
+    __slots__ = ("device", "index", "handle", "guards")
+
+    def __init__(self, q, stream):
+        device = q.device
+        if device.type != "cuda":
+            raise ValueError("inputs must be on a GPU")
+        self.device, self.index, self.guards = device, q.get_device(), ()
+        if torch.cuda.current_device() != self.index:
+            self.guards += (torch.cuda.device(self.index),)
+        if stream is None:
+            self.handle = _raw_stream(self.index)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream must be on {device}, got {stream.device}")
+            self.guards += (torch.cuda.stream(stream),)
+            self.handle = stream.cuda_stream
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
+        return self
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
+
+
+def _like(t):
+    """A dense tensor of t's shape, whatever t's strides."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def linear_fwd(q, k, v, g, cu_seqlens, *, cu_seqlens_cpu=None, scale=None, initial_state=None,
@@ -225,14 +269,14 @@ def linear_fwd(q, k, v, g, cu_seqlens, *, cu_seqlens_cpu=None, scale=None, initi
     rotated first, in bf16, by the kernel of :func:`rotary`. ``seg_len`` overrides the segment
     length policy (a multiple of 64). Returns ``(out, final_state)``, final_state None unless dense
     and asked for."""
-    index, handle = _enter(q, stream)
-    _on(q.device, k=k, v=v, g=g, cu_seqlens=cu_seqlens, initial_state=initial_state, state_cache=state_cache,
-        state_indices=state_indices, has_initial_state=has_initial_state, out=out, workspace=workspace,
-        positions=positions, inv_freq=inv_freq)
-    _need(cu_seqlens is not None, "cu_seqlens is required")
-    with _On(index, stream):
+    with _Call(q, stream) as call:
+        _on(call.index, "k v g cu_seqlens initial_state state_cache state_indices has_initial_state out workspace positions "
+            "inv_freq", k, v, g, cu_seqlens, initial_state, state_cache, state_indices, has_initial_state, out, workspace,
+            positions, inv_freq)
+        if cu_seqlens is None:
+            raise ValueError("cu_seqlens is required")
         if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            out = _like(v)
         final_state = None
         if output_final_state and state_cache is None:
             H, V, K = v.shape[-2], v.shape[-1], q.shape[-1]
@@ -246,15 +290,13 @@ def linear_fwd(q, k, v, g, cu_seqlens, *, cu_seqlens_cpu=None, scale=None, initi
                              interleaved=interleaved, rotary_factor=rotary_factor, seg_len=seg_len)
         lib = _lib.load()
         ref = ctypes.byref(a)
-        _check(lib.kda_linear_fwd_validate(ref), "kda_linear_fwd_validate")
-        need = lib.kda_linear_fwd_workspace_bytes(ref)
-        if workspace is not None:
-            _need(workspace.dtype == torch.uint8 and workspace.is_contiguous(),
-                  "workspace must be a contiguous uint8 tensor", TypeError)
+        need = lib.kda_linear_fwd_workspace_bytes(ref)  # 0 for a refused call too: the call says why
+        if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+            raise TypeError("workspace must be a contiguous uint8 tensor")
         if need and (workspace is None or workspace.numel() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ptr, size = (workspace.data_ptr(), workspace.numel()) if need else (None, 0)
-        _check(lib.kda_linear_fwd(_context(context, index), ref, ptr, size, handle), "kda_linear_fwd")
+            workspace = torch.empty(need, dtype=torch.uint8, device=call.device)
+        _check(lib.kda_linear_fwd(_context(context, call.index), ref, workspace.data_ptr() if need else None, need, call.handle),
+               "kda_linear_fwd")
     return out, final_state
 
 
@@ -268,46 +310,53 @@ def linear_step(q, k, v, g, *, state_cache, state_indices=None, has_initial_stat
     updated in place; a row whose index is outside the pool is padding, its row of ``out`` and every
     state left as they were. ``has_initial_state`` false: the slot is taken as zero and not read.
     With ``positions`` and ``inv_freq`` the kernel rotates q and k itself, in fp32. Returns out."""
-    index, handle = _enter(q, stream)
-    _on(q.device, k=k, v=v, g=g, state_cache=state_cache, state_indices=state_indices,
-        has_initial_state=has_initial_state, out=out, positions=positions, inv_freq=inv_freq)
-    with _On(index, stream):
+    with _Call(q, stream) as call:
+        _on(call.index, "k v g state_cache state_indices has_initial_state out positions inv_freq",
+            k, v, g, state_cache, state_indices, has_initial_state, out, positions, inv_freq)
         if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            out = _like(v)
         a = make_linear_args(q, k, v, g, N=q.shape[-3], scale=scale, state_cache=state_cache,
                              state_indices=state_indices, has_initial_state=has_initial_state, out=out,
                              state_k_first=state_k_first, positions=positions, inv_freq=inv_freq,
                              interleaved=interleaved, rotary_factor=rotary_factor)
-        _check(_lib.load().kda_linear_step(_context(context, index), ctypes.byref(a), handle), "kda_linear_step")
+        _check(_lib.load().kda_linear_step(_context(context, call.index), ctypes.byref(a), call.handle), "kda_linear_step")
     return out
-
-
-_ROTARY_DT = _STATE_DT
 
 
 def make_rotary_args(q, k, positions, inv_freq, out_q, out_k, *, interleaved=False, factor=1.0, inverse=False) -> "_lib.RotaryArgs":
     """Fill a ``kda_rotary_args`` from tensors (no allocation), checking what the C side cannot see."""
     q, out_q = _packed("q", q), _packed("out_q", out_q)
     T, H, D = q.shape
+    dtype = q.dtype
     a = _lib.RotaryArgs()
-    _need(q.dtype in _ROTARY_DT, f"q must be fp32, fp16 or bf16, got {q.dtype}", TypeError)
-    _need(H >= 1 and D >= 2, "q must have heads and at least two channels")
-    _need((k is None) == (out_k is None), "out_k goes with k")
-    _need(out_q.dtype == q.dtype and out_q.shape == q.shape, "out_q must have q's shape and dtype")
-    a.T, a.H_q, a.D, a.dtype = T, H, D, _ROTARY_DT[q.dtype]
+    if dtype not in _STATE_DT:
+        raise TypeError(f"q must be fp32, fp16 or bf16, got {dtype}")
+    if H < 1 or D < 2:
+        raise ValueError("q must have heads and at least two channels")
+    if (k is None) != (out_k is None):
+        raise ValueError("out_k goes with k")
+    if out_q.dtype != dtype or out_q.shape != q.shape:
+        raise ValueError("out_q must have q's shape and dtype")
+    a.T, a.H_q, a.D, a.dtype = T, H, D, _STATE_DT[dtype]
     a.q, a.out_q = q.data_ptr(), out_q.data_ptr()
-    a.q_stride_t, a.q_stride_h = _strides("q", q)
-    a.out_q_stride_t, a.out_q_stride_h = _strides("out_q", out_q)
+    a.q_stride_t, a.q_stride_h = _strides("q", q, T, H, D)
+    a.out_q_stride_t, a.out_q_stride_h = _strides("out_q", out_q, T, H, D)
     if k is not None:
         k, out_k = _packed("k", k), _packed("out_k", out_k)
-        _need(k.dtype == q.dtype, "q and k must have the same dtype", TypeError)
-        _need(k.shape[0] == T and k.shape[2] == D, "k must have q's token count and head size")
-        _need(out_k.dtype == k.dtype and out_k.shape == k.shape, "out_k must have k's shape and dtype")
-        a.H_k, a.k, a.out_k = k.shape[1], k.data_ptr(), out_k.data_ptr()
-        a.k_stride_t, a.k_stride_h = _strides("k", k)
-        a.out_k_stride_t, a.out_k_stride_h = _strides("out_k", out_k)
-    a.factor = _fill_rotation(a, T, D, positions, inv_freq, interleaved, factor)
-    a.inverse = 1 if inverse else 0
+        Tk, Hk, Dk = k.shape
+        if k.dtype != dtype:
+            raise TypeError("q and k must have the same dtype")
+        if Tk != T or Dk != D:
+            raise ValueError("k must have q's token count and head size")
+        if out_k.dtype != dtype or out_k.shape != k.shape:
+            raise ValueError("out_k must have k's shape and dtype")
+        a.H_k, a.k, a.out_k = Hk, k.data_ptr(), out_k.data_ptr()
+        a.k_stride_t, a.k_stride_h = _strides("k", k, T, Hk, D)
+        a.out_k_stride_t, a.out_k_stride_h = _strides("out_k", out_k, T, Hk, D)
+    _fill_rotation(a, T, D, positions, inv_freq, interleaved)
+    a.factor = factor
+    if inverse:
+        a.inverse = 1
     return a
 
 
@@ -322,16 +371,20 @@ def rotary(q, k, positions, inv_freq, *, interleaved=False, factor=1.0, inverse=
     ``factor`` scales the rotated channels. ``inverse`` applies the transposed rotation: the gradient
     with respect to q and k, given the results' gradients. ``out_q`` / ``out_k`` may be q / k
     themselves (in place). Returns ``(out_q, out_k)``."""
-    index, handle = _enter(q, stream)
-    _on(q.device, k=k, positions=positions, inv_freq=inv_freq, out_q=out_q, out_k=out_k)
-    with _On(index, stream):
+    with _Call(q, stream) as call:
+        _on(call.index, "k positions inv_freq out_q out_k", k, positions, inv_freq, out_q, out_k)
         if out_q is None:
-            out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out_q = _like(q)
         if out_k is None and k is not None:
-            out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            out_k = _like(k)
         a = make_rotary_args(q, k, positions, inv_freq, out_q, out_k, interleaved=interleaved, factor=factor, inverse=inverse)
-        _check(_lib.load().kda_rotary(_context(context, index), ctypes.byref(a), handle), "kda_rotary")
+        _check(_lib.load().kda_rotary(_context(context, call.index), ctypes.byref(a), call.handle), "kda_rotary")
     return out_q, out_k
+
+
+def _need(cond, msg):
+    if not cond:
+        raise ValueError(msg)
 
 
 def rotary_frequencies(rot_dim, *, base=10000.0, scaling=None, scale=1.0, original_length=None, beta_fast=32.0,
