@@ -52,10 +52,11 @@ struct LinearPlan {
   const int32_t* indices;
   const uint8_t* flags;
   int seg_len, head_cost, n_seg;
-  float* maps;      // [n_seg - 1][H][V * K]: state at the end of segment s, as if its start were
+  int slices;       // workgroups that share a segment of a head, V / slices state rows each
+  float* maps;      // [n_seg - 1][H][slices][V / slices * K]: state at the end of segment s, as if its start were
                     // zero; after the combine the true state. Register order of the walk.
-  float* initials;  // [n_seg - 1][H][V * K]: copy of the initial state of a sequence that
-                    // starts in segment s and crosses its end, in the same order
+  float* initials;  // as maps: copy of the initial state of a sequence that
+                    // starts in segment s and crosses its end
   float* decays;    // [n_seg - 1][H]: e^{sum of g} over the crossing sequence's part of s
   int32_t* spans;   // [n_seg - 1]: 0 nothing crosses the end of s, 1 a sequence that starts in
                     // s, 2 one that came from before

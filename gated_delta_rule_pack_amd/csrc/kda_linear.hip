@@ -18,8 +18,8 @@
 // every segment with its true start states. Nothing but the bounds' own values decides which
 // tokens a workgroup takes, so a call needs no host tables.
 //
-// A workgroup is four waves; wave w holds the V/4 state rows from w V/4 in fp32 MFMA
-// accumulators, S^T[k][v], for the whole walk. Lanes (l, g = l / 16): accumulator tiles of
+// A workgroup takes all V state rows, or a slice of 64 of them where there are few segments and
+// heads. Each wave holds 16 of its rows in fp32 MFMA accumulators, S^T[k][v], for the whole walk. Lanes (l, g = l / 16): accumulator tiles of
 // K^T U hold column v = l % 16, rows k = 4g + i, which is an operand of Q S^T whose contraction
 // order is (4g + i, 16 + 4g + i); q is read from LDS in that order, and P, made as K Q^T, meets V
 // the same way, so neither the state nor P is ever transposed.
@@ -32,9 +32,9 @@ namespace kda {
 namespace {
 
 constexpr int kC = kLinChunk;
-// Waves of a walk's workgroup; each has V / (16 waves) tiles of 16 state rows.
+// Waves of a walk's workgroup, 16 state rows each.
 template <int V>
-constexpr int kWavesOf = V / 16 >= 8 ? 8 : 4;
+constexpr int kWavesOf = V / 16;
 constexpr float kMinLogDecay = -120.f;  // e^-120 is 0 in fp32; keeps -inf out of the differences
 
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
@@ -86,15 +86,8 @@ __device__ __forceinline__ bf16x8 read_col(const char* tile, int lane, int t0, i
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Token bounds of sequence n inside [0, T], whatever the device bounds hold.
-struct Seq {
-  int begin, len;
-};
+// Token bound n inside [0, T], whatever the device bounds hold.
 __device__ __forceinline__ int bound(const LinearPlan& p, int n) { return min(max(p.cu[n], 0), p.T); }
-__device__ __forceinline__ Seq sequence(const LinearPlan& p, int n) {
-  const int b = bound(p, n);
-  return Seq{b, max(bound(p, n + 1) - b, 0)};
-}
 // Where sequence n's tokens start on the axis, and the first place that is its own: an empty
 // sequence takes that place (in the stretch that stands for its state).
 __device__ __forceinline__ int64_t axis_start(const LinearPlan& p, int n) { return bound(p, n) + (int64_t)n * p.head_cost; }
@@ -115,19 +108,18 @@ __device__ __forceinline__ int find_sequence(const LinearPlan& p, int64_t x, int
   return lo;
 }
 
-// Plane of sequence n and head h to start from / to leave the final state in; null: none.
-__device__ __forceinline__ int64_t slot_of(const LinearPlan& p, int mode, int n) {
-  if (mode == kStateDense) return n;
-  if (mode != kStatePaged) return -1;
-  const int64_t s = p.indices[n];
-  return s >= 0 && s < p.num_slots ? s : -1;
+// Slots that sequence n starts from and leaves its final state in; -1: none.
+struct Slots {
+  int from, to;
+};
+__device__ __forceinline__ Slots slots_of(const LinearPlan& p, int n) {
+  if (p.in_mode != kStatePaged) return Slots{p.in_mode == kStateDense ? n : -1, p.out_mode == kStateDense ? n : -1};
+  const int s = p.indices[n];
+  const bool old = p.flags[n], inside = s >= 0 && s < p.num_slots;
+  return Slots{inside && old ? s : -1, inside ? s : -1};
 }
-__device__ __forceinline__ int64_t plane_at(const LinearPlan& p, int64_t slot, int h) {
+__device__ __forceinline__ int64_t plane_at(const LinearPlan& p, int slot, int h) {
   return slot * p.stride0 + (int64_t)h * p.K * p.V;
-}
-__device__ __forceinline__ int64_t initial_slot(const LinearPlan& p, int n) {
-  if (p.in_mode == kStatePaged && !p.flags[n]) return -1;
-  return slot_of(p, p.in_mode, n);
 }
 
 __device__ __forceinline__ float load_state(const LinearPlan& p, const void* base, int64_t at) {
@@ -170,14 +162,14 @@ struct Walk {
       for (int kt = 0; kt < KT; ++kt)
         *reinterpret_cast<f32x4*>(plane + (((wave * VT + vt) * KT + kt) * 64 + lane) * 4) = S[vt][kt];
   }
-  // The caller's planes, [V][K] or [K][V].
-  __device__ __forceinline__ void load_plane(const LinearPlan& p, int64_t at, int wave, int lane_) {
+  // The caller's planes, [V][K] or [K][V], from row (column) v0 on.
+  __device__ __forceinline__ void load_plane(const LinearPlan& p, int64_t at, int v0, int wave, int lane_) {
     const int lane = local_copy(lane_), g = lane >> 4;
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const int v = (wave * VT + vt) * 16 + (lane & 15), k = kt * 16 + 4 * g;
+        const int v = v0 + (wave * VT + vt) * 16 + (lane & 15), k = kt * 16 + 4 * g;
         if (!p.kfirst) {
           const size_t off = (size_t)(at + (int64_t)v * K + k);
           if (p.state_dtype == kF32) S[vt][kt] = load_state4<kF32>(p.state_in, off);
@@ -185,17 +177,17 @@ struct Walk {
           else S[vt][kt] = load_state4<kBF16>(p.state_in, off);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[vt][kt][i] = load_state(p, p.state_in, at + (int64_t)(k + i) * V + v);
+          for (int i = 0; i < 4; ++i) S[vt][kt][i] = load_state(p, p.state_in, at + (int64_t)(k + i) * p.V + v);
         }
       }
   }
-  __device__ __forceinline__ void store_plane(const LinearPlan& p, int64_t at, int wave, int lane_) const {
+  __device__ __forceinline__ void store_plane(const LinearPlan& p, int64_t at, int v0, int wave, int lane_) const {
     const int lane = local_copy(lane_), g = lane >> 4;
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const int v = (wave * VT + vt) * 16 + (lane & 15), k = kt * 16 + 4 * g;
+        const int v = v0 + (wave * VT + vt) * 16 + (lane & 15), k = kt * 16 + 4 * g;
         if (!p.kfirst) {
           const size_t off = (size_t)(at + (int64_t)v * K + k);
           if (p.state_dtype == kF32) store_state4<kF32>(p.state_out, off, S[vt][kt]);
@@ -203,7 +195,7 @@ struct Walk {
           else store_state4<kBF16>(p.state_out, off, S[vt][kt]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) store_state(p, p.state_out, at + (int64_t)(k + i) * V + v, S[vt][kt][i]);
+          for (int i = 0; i < 4; ++i) store_state(p, p.state_out, at + (int64_t)(k + i) * p.V + v, S[vt][kt][i]);
         }
       }
   }
@@ -258,7 +250,7 @@ struct Shared {
   alignas(16) char k[kC * kRowBytes<K>];
   alignas(16) char v[kC * kRowBytes<V>];
   alignas(16) char q[kOut ? kC * kRowBytes<K> : 16];
-  alignas(16) char p[kOut ? 8 * 1024 : 16];  // P fragments (token tile of 16, block of 32 sources)
+  alignas(16) char p[kOut ? 6 * 1024 : 16];  // P fragments (token tile of 16, block of 32 sources)
   struct Decays {
     double G[kC];             // inclusive cumsum of g
     alignas(16) float c[kC];  // e^{G_C - G}
@@ -297,10 +289,13 @@ __device__ __forceinline__ void put_decays(D& d, float g, float scale, int lane)
   if (lane == 0) d.total = __expf((float)end);
 }
 
+// Fragment of P with token tile tt and sources 32 b .. 32 b + 31: the causal ones alone.
+__device__ __forceinline__ int fragment(int tt, int b) { return tt + (tt == 3) + b; }
+
 // One chunk of `count` tokens: P and the outputs (kOut), then the state.
 template <int K, int V, bool kOut>
 __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& sh, const typename Shared<K, V, kOut>::Decays& dec,
-                                      Walk<K, V>& walk, int64_t first, int count, int h, int wave, int lane_) {
+                                      Walk<K, V>& walk, const __bf16* out_rows, int64_t first, int count, int wave, int lane_) {
   const int lane = local_copy(lane_);
   constexpr int VT = Walk<K, V>::VT, KT = Walk<K, V>::KT, KB = K / 32;
   const int g = lane >> 4, l16 = lane & 15;
@@ -327,7 +322,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       }
       // Rounded to bf16 once: the product with V is a bf16 MFMA with fp32 sums.
       const bf16x4 b = {to_bf16(d[0]), to_bf16(d[1]), to_bf16(d[2]), to_bf16(d[3])};
-      *reinterpret_cast<bf16x4*>(sh.p + (tt * 2 + (st >> 1)) * 1024 + lane * 16 + (st & 1) * 8) = b;
+      *reinterpret_cast<bf16x4*>(sh.p + fragment(tt, st >> 1) * 1024 + lane * 16 + (st & 1) * 8) = b;
     }
     // Q S^T, transposed: rows v = 4 g + i, column t. The state is rounded to bf16 for it.
     f32x4 acc[VT][4];
@@ -358,12 +353,12 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, lane, 32 * b, wave * VT + vt);
     barrier_lds();  // P
-    const __amdgpu_buffer_rsrc_t out = rows_buffer<V>(reinterpret_cast<const __bf16*>(p.out) + h * p.o_h, first, p.o_t, count);
+    const __amdgpu_buffer_rsrc_t out = rows_buffer<V>(out_rows, first, p.o_t, count);
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
 #pragma unroll
       for (int b = 0; b <= tt / 2; ++b) {
-        bf16x8 pf = *reinterpret_cast<const bf16x8*>(sh.p + (tt * 2 + b) * 1024 + lane * 16);
+        bf16x8 pf = *reinterpret_cast<const bf16x8*>(sh.p + fragment(tt, b) * 1024 + lane * 16);
         if (tt == 2 * b) {  // the tile past the diagonal is not made
 #pragma unroll
           for (int i = 4; i < 8; ++i) pf[i] = (__bf16)0.f;
@@ -431,27 +426,65 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
   }
 }
 
+// A sequence of one token: the recurrent step on the walk's registers, in fp32. No wave waits for
+// another, so a batch's single tokens run as 8 KB of state in flight for every wave.
+template <int K, int V>
+__device__ __forceinline__ void single(const LinearPlan& p, Walk<K, V>& walk, const __bf16* q, const __bf16* k, const __bf16* v,
+                                       __bf16* out, int64_t token, int h, int wave, int lane_) {
+  constexpr int VT = Walk<K, V>::VT, KT = Walk<K, V>::KT;
+  const int lane = local_copy(lane_), g = lane >> 4, row = wave * VT * 16 + (lane & 15);
+  float decay = 1.f;
+  if (p.g) {
+    const int64_t at = p.g_per_token ? token * p.H + h : h;
+    decay = __expf(p.g_bf16 ? (float)reinterpret_cast<const __bf16*>(p.g)[at] : reinterpret_cast<const float*>(p.g)[at]);
+  }
+  float x[VT], o[VT];
+#pragma unroll
+  for (int vt = 0; vt < VT; ++vt) x[vt] = from_bf16(v[token * p.v_t + row + 16 * vt]), o[vt] = 0.f;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    const bf16x4 kk = *reinterpret_cast<const bf16x4*>(k + token * p.k_t + 16 * kt + 4 * g);
+    const bf16x4 qq = *reinterpret_cast<const bf16x4*>(q + token * p.q_t + 16 * kt + 4 * g);
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        walk.S[vt][kt][i] = walk.S[vt][kt][i] * decay + x[vt] * (float)kk[i];
+        o[vt] += walk.S[vt][kt][i] * (float)qq[i];
+      }
+  }
+#pragma unroll
+  for (int vt = 0; vt < VT; ++vt) {
+    o[vt] += __shfl_xor(o[vt], 16);
+    o[vt] += __shfl_xor(o[vt], 32);
+    if (g == 0) out[token * p.o_t + row + 16 * vt] = to_bf16(p.scale * o[vt]);
+  }
+}
+
 // Walks segment `seg` of head h. kOut: every token, with outputs and final states; else only
 // the sequence that crosses the segment's end, for its map.
 template <int K, int V, bool kOut>
-__global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 && kWavesOf<V> == 8 ? 4 : 2) void linear_walk(const LinearPlan p) {
+__global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 ? 4 : 3) void linear_walk(const LinearPlan p) {
   constexpr int kThreads = 64 * kWavesOf<V>;
   __shared__ Shared<K, V, kOut> sh;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int seg = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  const int slice = blockIdx.x % p.slices, unit = blockIdx.x / p.slices;
+  const int seg = unit / p.H, h = unit % p.H, v0 = slice * V;
   const int64_t a = (int64_t)seg * p.seg_len, b = a + p.seg_len;
-  const int64_t plane = (int64_t)K * V;
-  const int64_t border = ((int64_t)seg * p.H + h) * plane;  // this segment's entry in maps and initials
+  const int64_t plane = (int64_t)K * V;  // of the slice
+  const int64_t border = ((int64_t)unit * p.slices + slice) * plane;  // this segment's entry in maps and initials
   const __bf16* q = reinterpret_cast<const __bf16*>(p.q) + (h / p.group) * p.q_h;
   const __bf16* k = reinterpret_cast<const __bf16*>(p.k) + (h / p.group) * p.k_h;
-  const __bf16* v = reinterpret_cast<const __bf16*>(p.v) + h * p.v_h;
+  const __bf16* v = reinterpret_cast<const __bf16*>(p.v) + h * p.v_h + v0;
+  __bf16* out = reinterpret_cast<__bf16*>(p.out) + h * p.o_h + v0;
 
   int n = find_sequence(p, kOut ? a : b - 1, lane);
+  int begin = bound(p, n), end = bound(p, n + 1);
+  Slots slots = slots_of(p, n);
   if constexpr (!kOut) {
-    const Seq s = sequence(p, n);
-    const int64_t start = axis_start(p, n);
-    const bool crosses = s.len > 0 && start < b && start + s.len > b;
-    if (h == 0 && tid == 0) p.spans[seg] = crosses ? (start >= a ? 1 : 2) : 0;
+    const int64_t start = begin + (int64_t)n * p.head_cost;
+    const bool crosses = end > begin && start < b && start + (end - begin) > b;
+    if (h == 0 && slice == 0 && tid == 0) p.spans[seg] = crosses ? (start >= a ? 1 : 2) : 0;
     if (!crosses) return;
   }
   Walk<K, V> walk;
@@ -468,74 +501,75 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 && kWavesOf<V> == 8 ? 4 
     rk.load(k, p.k_t, first, count, tid);
     rv.load(v, p.v_t, first, count, tid);
   };
-  do {
-    const Seq s = sequence(p, n);
-    const int64_t start = axis_start(p, n);
-    if (s.len == 0) {
+  while (true) {
+    // The next sequence's bound and slots are on their way while this one is walked.
+    const bool last = !kOut || n + 1 >= p.N;
+    const int next_end = last ? end : bound(p, n + 2);
+    const Slots next_slots = last ? slots : slots_of(p, n + 1);
+    const int len = max(end - begin, 0);
+    const int64_t start = begin + (int64_t)n * p.head_cost;
+    const int t0 = (int)max((int64_t)0, a - start), t1 = (int)min((int64_t)len, b - start);
+    if (kOut && len <= 1) {
+      // An empty sequence stands in the stretch before its place, from which find_sequence finds it.
+      const int64_t place = start - (len == 0 && n > 0);
+      if (place >= a && place < b) {
+        walk.zero();
+        if (slots.from >= 0) walk.load_plane(p, plane_at(p, slots.from, h), v0, wave, lane);
+        if (len == 1) single<K, V>(p, walk, q, k, v, out, begin, h, wave, lane);
+        if (slots.to >= 0) walk.store_plane(p, plane_at(p, slots.to, h), v0, wave, lane);
+      }
+    } else if (t0 < t1) {
+      int64_t first = (int64_t)begin + t0;
+      int left = t1 - t0;
+      fetch(first, min(left, kC));
+      // Start state. A sequence that goes on after this segment leaves its final state from
+      // another workgroup, perhaps in the plane it starts from: the output walk starts it from
+      // the copy that the map walk made.
+      walk.zero();
+      if (t0 == 0) {
+        if (slots.from >= 0) {
+          if (kOut && t1 < len) {
+            walk.load(p.initials + border, wave, lane);
+          } else {
+            walk.load_plane(p, plane_at(p, slots.from, h), v0, wave, lane);
+            if (!kOut) walk.store(p.initials + border, wave, lane);
+          }
+        }
+      } else if (kOut) {
+        walk.load(p.maps + border - p.H * p.slices * plane, wave, lane);
+      }
+      float decay = 1.f;
+      int turn = 0;
+      if (wave == 3) put_decays(sh.decays[0], g_next, p.scale, lane);
+      while (left > 0) {
+        const int count = min(left, kC);
+        if constexpr (kOut) rq.template put<true>(sh.q, tid);
+        rk.template put<false>(sh.k, tid);
+        rv.template put<false>(sh.v, tid);
+        barrier_lds();
+        const int64_t here = first;
+        first += count;
+        left -= count;
+        if (left > 0) fetch(first, min(left, kC));
+        chunk<K, V, kOut>(p, sh, sh.decays[turn], walk, out, here, count, wave, lane);
+        decay *= sh.decays[turn].total;
+        turn ^= 1;
+        // Wave 3 has few tiles of P.
+        if (wave == 3 && left > 0) put_decays(sh.decays[turn], g_next, p.scale, lane);
+        barrier_lds();
+      }
       if constexpr (kOut) {
-        const int64_t own = axis_own(p, n);
-        const int64_t to = slot_of(p, p.out_mode, n);
-        if (own >= a && own < b && to >= 0) {
-          const int64_t from = initial_slot(p, n);
-          walk.zero();
-          if (from >= 0) walk.load_plane(p, plane_at(p, from, h), wave, lane);
-          walk.store_plane(p, plane_at(p, to, h), wave, lane);
-        }
+        if (t1 == len && slots.to >= 0) walk.store_plane(p, plane_at(p, slots.to, h), v0, wave, lane);
+      } else {
+        walk.store(p.maps + border, wave, lane);
+        if (slice == 0 && tid == 0) p.decays[(int64_t)seg * p.H + h] = decay;
       }
-      continue;
     }
-    const int t0 = (int)max((int64_t)0, a - start), t1 = (int)min((int64_t)s.len, b - start);
-    if (t0 >= t1) continue;
-    int64_t first = (int64_t)s.begin + t0;
-    int left = t1 - t0;
-    fetch(first, min(left, kC));
-    // Start state. A sequence that goes on after this segment leaves its final state from
-    // another workgroup, perhaps in the plane it starts from: the output walk starts it from
-    // the copy that the map walk made.
-    walk.zero();
-    if (t0 == 0) {
-      const int64_t from = initial_slot(p, n);
-      if (from >= 0) {
-        if (kOut && t1 < s.len) {
-          walk.load(p.initials + border, wave, lane);
-        } else {
-          walk.load_plane(p, plane_at(p, from, h), wave, lane);
-          if (!kOut) walk.store(p.initials + border, wave, lane);
-        }
-      }
-    } else if (kOut) {
-      walk.load(p.maps + border - p.H * plane, wave, lane);
-    }
-    float decay = 1.f;
-    int turn = 0;
-    if (wave == 3) put_decays(sh.decays[0], g_next, p.scale, lane);
-    while (left > 0) {
-      const int count = min(left, kC);
-      if constexpr (kOut) rq.template put<true>(sh.q, tid);
-      rk.template put<false>(sh.k, tid);
-      rv.template put<false>(sh.v, tid);
-      barrier_lds();
-      const int64_t here = first;
-      first += count;
-      left -= count;
-      if (left > 0) fetch(first, min(left, kC));
-      chunk<K, V, kOut>(p, sh, sh.decays[turn], walk, here, count, h, wave, lane);
-      decay *= sh.decays[turn].total;
-      turn ^= 1;
-      // Wave 3 has the fewest tiles of P.
-      if (wave == 3 && left > 0) put_decays(sh.decays[turn], g_next, p.scale, lane);
-      barrier_lds();
-    }
-    if constexpr (kOut) {
-      if (t1 == s.len) {
-        const int64_t to = slot_of(p, p.out_mode, n);
-        if (to >= 0) walk.store_plane(p, plane_at(p, to, h), wave, lane);
-      }
-    } else {
-      walk.store(p.maps + border, wave, lane);
-      if (tid == 0) p.decays[(int64_t)seg * p.H + h] = decay;
-    }
-  } while (kOut && ++n < p.N && axis_own(p, n) < b);
+    if (last) break;
+    ++n;
+    begin = end, end = next_end, slots = next_slots;
+    if (begin + (int64_t)n * p.head_cost - 1 >= b) break;
+  }
 }
 
 constexpr int kCombineThreads = 256;
@@ -576,12 +610,12 @@ __global__ __launch_bounds__(kCombineThreads) void linear_combine(const LinearPl
 
 template <bool kOut>
 int launch_walk(const LinearPlan& p, int segments, void* stream) {
-  const dim3 grid((unsigned)((int64_t)segments * p.H));
+  const int V = p.V / p.slices;
+  const dim3 grid((unsigned)((int64_t)segments * p.H * p.slices)), threads(64 * (V == 128 ? kWavesOf<128> : kWavesOf<64>));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 threads(64 * (p.V == 128 ? kWavesOf<128> : kWavesOf<64>));
-  if (p.K == 128 && p.V == 128) linear_walk<128, 128, kOut><<<grid, threads, 0, s>>>(p);
+  if (p.K == 128 && V == 128) linear_walk<128, 128, kOut><<<grid, threads, 0, s>>>(p);
   else if (p.K == 128) linear_walk<128, 64, kOut><<<grid, threads, 0, s>>>(p);
-  else if (p.V == 128) linear_walk<64, 128, kOut><<<grid, threads, 0, s>>>(p);
+  else if (V == 128) linear_walk<64, 128, kOut><<<grid, threads, 0, s>>>(p);
   else linear_walk<64, 64, kOut><<<grid, threads, 0, s>>>(p);
   return (int)hipGetLastError();
 }

@@ -61,14 +61,22 @@ int64_t axis_of(const kda_linear_args* a) {
   return std::max<int64_t>(a->T, 1) + (int64_t)head_cost_of(a) * (a->N - 1);
 }
 
-// Segments: as few as fill the chip, since all but the last are walked twice (once for their
-// map) and every border costs maps of V * K floats.
-constexpr int64_t kLinUnits = 512;  // two workgroups for each of 256 compute units
+// Segment length. A long segment costs its own walk (5 us for each 64 tokens of K = V = 128, map and
+// output, one workgroup on a compute unit); every segment costs states of K V floats, written, chained
+// and read back. The sum is least at a length that grows with the root of the work: measured best at
+// H = 12 for 1024 tokens 128, 4096 tokens 192 (41.9 us; 128: 47.4, 384: 49.7), 8192 tokens 384, and at
+// H = 32 for 1536 tokens 192, 6144 tokens 384. Work for more workgroups than the chip holds at once
+// (two of 128 state rows on a compute unit, three of 64) takes as many: 32768 tokens at H = 32, 2048
+// (399 us; 1024: 425). Little work takes one segment and one kernel: 128 tokens 11.2 us, 14.9 in two
+// segments; 16 sequences of 16 tokens 17.2 us, 26.7 in segments.
 int32_t seg_len_of(const kda_linear_args* a) {
   if (a->seg_len > 0) return a->seg_len;
-  const int64_t segs = std::max<int64_t>(1, kLinUnits / a->H);
-  const int64_t len = (axis_of(a) + segs - 1) / segs;
-  return (int32_t)((len + kda::kLinChunk - 1) / kda::kLinChunk * kda::kLinChunk);
+  const int64_t axis = axis_of(a), units = a->V == 64 ? 768 : 512;
+  const int64_t fit = std::max<int64_t>(1, units / a->H), fill = (axis + fit - 1) / fit;
+  const int64_t root = (int64_t)std::sqrt(0.75 * (double)axis * a->H * a->K * a->V / (128 * 128));
+  const int64_t len = a->T <= 256 && a->N <= 16 ? axis : std::max(fill, root);
+  const int64_t whole = (std::max<int64_t>(len, 1) + kda::kLinChunk - 1) / kda::kLinChunk * kda::kLinChunk;
+  return (int32_t)std::min<int64_t>(whole, 1 << 30);
 }
 int32_t segments_of(const kda_linear_args* a) {
   const int64_t L = seg_len_of(a);
@@ -258,6 +266,9 @@ kda_status kda_linear_fwd(kda_ctx* ctx, const kda_linear_args* a, void* ws, size
   p.seg_len = seg_len_of(a);
   p.head_cost = head_cost_of(a);
   p.n_seg = segments_of(a);
+  // Slices of 64 state rows where they still get a compute unit each: 37 tokens at H = 12 take 8.0
+  // instead of 10.0 us; 4096 tokens (252 units) would take 45.8 instead of 43.2.
+  p.slices = a->V == 128 && (int64_t)p.n_seg * a->H <= 128 ? 2 : 1;
   p.maps = reinterpret_cast<float*>(base + w.maps);
   p.initials = reinterpret_cast<float*>(base + w.initials);
   p.decays = reinterpret_cast<float*>(base + w.decays);
