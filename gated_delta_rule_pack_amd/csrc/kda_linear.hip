@@ -54,6 +54,13 @@ __device__ __forceinline__ uint32_t top_halves(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
 }
 
+// Both rounded to nearest, a below.
+__device__ __forceinline__ uint32_t both_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 r = {to_bf16(a), to_bf16(b)};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
 // LDS tile of 64 rows of D bf16. A row takes 16 bytes more than its elements, and inside 16 rows
 // row r stands at place 2 (r % 8) + r / 8: the 16 rows of an operand read then start on different
 // banks, and the 8 rows of half a transposing read do not meet. Every read is a lane's own place and
@@ -293,7 +300,7 @@ __device__ __forceinline__ void put_decays(D& d, float g, float scale, int lane)
 __device__ __forceinline__ int fragment(int tt, int b) { return tt + (tt == 3) + b; }
 
 // One chunk of `count` tokens: P and the outputs (kOut), then the state.
-template <int K, int V, bool kOut>
+template <int K, int V, bool kOut, int kTerms>
 __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& sh, const typename Shared<K, V, kOut>::Decays& dec,
                                       Walk<K, V>& walk, const __bf16* out_rows, int64_t first, int count, int wave, int lane_) {
   const int lane = local_copy(lane_);
@@ -380,9 +387,10 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, lane, 32 * b, wave * VT + vt);
   }
-  // State. The decayed values x (fp32) go in as three bf16 terms of 8 bits each, cut off rather
-  // than rounded, so that x = hi + mid + lo exactly, against the stored keys, which are bf16: the
-  // state keeps fp32 accuracy. (Two rounded terms leave 3e-6.)
+  // State. The decayed values x (fp32) go in as bf16 terms against the stored keys, which are bf16.
+  // Three terms of 8 bits each, cut off rather than rounded, are x exactly: the state keeps fp32
+  // accuracy. Two rounded terms leave 3e-6 of x, which serves where the state is stored in 16 bits or
+  // not at all.
   const float total = dec.total;
 #pragma unroll
   for (int vt = 0; vt < VT; ++vt)
@@ -390,36 +398,41 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
     for (int kt = 0; kt < KT; ++kt) walk.S[vt][kt] *= total;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    bf16x8 hi[VT], mid[VT], lo[VT];
+    bf16x8 term[kTerms][VT];  // the largest last
     const f32x4 c0 = *reinterpret_cast<const f32x4*>(&dec.c[32 * b + 4 * g]);
     const f32x4 c1 = *reinterpret_cast<const f32x4*>(&dec.c[32 * b + 16 + 4 * g]);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt) {
       const u32x4 w = __builtin_bit_cast(u32x4, raw[b][vt]);
-      u32x4 h, m, l;
+      u32x4 t[kTerms];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f32x4 c = i < 2 ? c0 : c1;
         const float x0 = __uint_as_float(w[i] << 16) * c[2 * i & 3], x1 = __uint_as_float(w[i] & kTop) * c[(2 * i + 1) & 3];
-        const float r0 = x0 - __uint_as_float(__float_as_uint(x0) & kTop), r1 = x1 - __uint_as_float(__float_as_uint(x1) & kTop);
-        const float s0 = r0 - __uint_as_float(__float_as_uint(r0) & kTop), s1 = r1 - __uint_as_float(__float_as_uint(r1) & kTop);
-        h[i] = top_halves(x0, x1);
-        m[i] = top_halves(r0, r1);
-        l[i] = top_halves(s0, s1);
+        if constexpr (kTerms == 3) {
+          const float r0 = x0 - __uint_as_float(__float_as_uint(x0) & kTop), r1 = x1 - __uint_as_float(__float_as_uint(x1) & kTop);
+          const float s0 = r0 - __uint_as_float(__float_as_uint(r0) & kTop), s1 = r1 - __uint_as_float(__float_as_uint(r1) & kTop);
+          t[2][i] = top_halves(x0, x1);
+          t[1][i] = top_halves(r0, r1);
+          t[0][i] = top_halves(s0, s1);
+        } else {
+          t[1][i] = both_bf16(x0, x1);
+          t[0][i] = both_bf16(x0 - __uint_as_float(t[1][i] << 16), x1 - __uint_as_float(t[1][i] & kTop));
+        }
       }
-      hi[vt] = __builtin_bit_cast(bf16x8, h), mid[vt] = __builtin_bit_cast(bf16x8, m), lo[vt] = __builtin_bit_cast(bf16x8, l);
+#pragma unroll
+      for (int j = 0; j < kTerms; ++j) term[j][vt] = __builtin_bit_cast(bf16x8, t[j]);
     }
     // Two tiles of K at a time, term by term: no product waits for the one before it.
 #pragma unroll
     for (int kt = 0; kt < KT; kt += 2) {
       const bf16x8 k0 = read_col<K>(sh.k, lane, 32 * b, kt), k1 = read_col<K>(sh.k, lane, 32 * b, kt + 1);
 #pragma unroll
-      for (int term = 0; term < 3; ++term) {
+      for (int j = 0; j < kTerms; ++j) {
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
-          const bf16x8 u = term == 0 ? lo[vt] : (term == 1 ? mid[vt] : hi[vt]);
-          walk.S[vt][kt] = mfma(k0, u, walk.S[vt][kt]);
-          walk.S[vt][kt + 1] = mfma(k1, u, walk.S[vt][kt + 1]);
+          walk.S[vt][kt] = mfma(k0, term[j][vt], walk.S[vt][kt]);
+          walk.S[vt][kt + 1] = mfma(k1, term[j][vt], walk.S[vt][kt + 1]);
         }
       }
     }
@@ -463,7 +476,7 @@ __device__ __forceinline__ void single(const LinearPlan& p, Walk<K, V>& walk, co
 
 // Walks segment `seg` of head h. kOut: every token, with outputs and final states; else only
 // the sequence that crosses the segment's end, for its map.
-template <int K, int V, bool kOut>
+template <int K, int V, bool kOut, int kTerms>
 __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 ? 4 : 3) void linear_walk(const LinearPlan p) {
   constexpr int kThreads = 64 * kWavesOf<V>;
   __shared__ Shared<K, V, kOut> sh;
@@ -551,7 +564,7 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 ? 4 : 3) void linear_wal
         first += count;
         left -= count;
         if (left > 0) fetch(first, min(left, kC));
-        chunk<K, V, kOut>(p, sh, sh.decays[turn], walk, out, here, count, wave, lane);
+        chunk<K, V, kOut, kTerms>(p, sh, sh.decays[turn], walk, out, here, count, wave, lane);
         decay *= sh.decays[turn].total;
         turn ^= 1;
         // Wave 3 has few tiles of P.
@@ -608,16 +621,21 @@ __global__ __launch_bounds__(kCombineThreads) void linear_combine(const LinearPl
   }
 }
 
-template <bool kOut>
-int launch_walk(const LinearPlan& p, int segments, void* stream) {
+template <bool kOut, int kTerms>
+int launch_walk(const LinearPlan& p, int segments, hipStream_t s) {
   const int V = p.V / p.slices;
   const dim3 grid((unsigned)((int64_t)segments * p.H * p.slices)), threads(64 * (V == 128 ? kWavesOf<128> : kWavesOf<64>));
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (p.K == 128 && V == 128) linear_walk<128, 128, kOut><<<grid, threads, 0, s>>>(p);
-  else if (p.K == 128) linear_walk<128, 64, kOut><<<grid, threads, 0, s>>>(p);
-  else if (V == 128) linear_walk<64, 128, kOut><<<grid, threads, 0, s>>>(p);
-  else linear_walk<64, 64, kOut><<<grid, threads, 0, s>>>(p);
+  if (p.K == 128 && V == 128) linear_walk<128, 128, kOut, kTerms><<<grid, threads, 0, s>>>(p);
+  else if (p.K == 128) linear_walk<128, 64, kOut, kTerms><<<grid, threads, 0, s>>>(p);
+  else if (V == 128) linear_walk<64, 128, kOut, kTerms><<<grid, threads, 0, s>>>(p);
+  else linear_walk<64, 64, kOut, kTerms><<<grid, threads, 0, s>>>(p);
   return (int)hipGetLastError();
+}
+template <bool kOut>
+int launch_walk(const LinearPlan& p, int segments, void* stream) {
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const bool exact = p.out_mode != kStateNone && p.state_dtype == kF32;
+  return exact ? launch_walk<kOut, 3>(p, segments, s) : launch_walk<kOut, 2>(p, segments, s);
 }
 
 }  // namespace
