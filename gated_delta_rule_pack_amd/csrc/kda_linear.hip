@@ -232,6 +232,20 @@ struct Rows {
     for (int i = 0; i < kPasses; ++i)
       w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRows * (int)stride * 2, 0, 0));
   }
+  // Rows of a tile that is not ordered to memory, `count` of them, whole rows to a wave (parts of rows
+  // leave their merging to L2: 32768 tokens at H = 32 take 405 us so, 379 here) and past the caches, which
+  // have no use for them (385 us without the hint). A thread reads the bytes that its own put writes
+  // next, so no barrier stands between.
+  static __device__ __forceinline__ void store(const char* tile, __bf16* base, int64_t stride, int64_t first, int count, int tid) {
+    const __amdgpu_buffer_rsrc_t r = rows_buffer<D>(base, first, stride, count);
+    tid = local_copy(tid);
+    const int at = (tid / kUnits) * (int)stride * 2 + (tid % kUnits) * 16;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(tile + row_at<D>(tid / kUnits) + i * kRows * kRowBytes<D> + (tid % kUnits) * 16);
+      __builtin_amdgcn_raw_buffer_store_b128(x, r, at + i * kRows * (int)stride * 2, 0, kStreamLoad);
+    }
+  }
   // kOrdered: the 8 elements of unit u of four go to units 2 (u % 2) and 2 (u % 2) + 1, half u / 2.
   template <bool kOrdered>
   __device__ __forceinline__ void put(char* tile, int tid) const {
@@ -255,7 +269,7 @@ struct Rows {
 template <int K, int V, bool kOut>
 struct Shared {
   alignas(16) char k[kC * kRowBytes<K>];
-  alignas(16) char v[kC * kRowBytes<V>];
+  alignas(16) char v[kC * kRowBytes<V>];  // then, once every wave has its columns, the outputs
   alignas(16) char q[kOut ? kC * kRowBytes<K> : 16];
   alignas(16) char p[kOut ? 6 * 1024 : 16];  // P fragments (token tile of 16, block of 32 sources)
   struct Decays {
@@ -302,7 +316,7 @@ __device__ __forceinline__ int fragment(int tt, int b) { return tt + (tt == 3) +
 // One chunk of `count` tokens: P and the outputs (kOut), then the state.
 template <int K, int V, bool kOut, int kTerms>
 __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& sh, const typename Shared<K, V, kOut>::Decays& dec,
-                                      Walk<K, V>& walk, const __bf16* out_rows, int64_t first, int count, int wave, int lane_) {
+                                      Walk<K, V>& walk, int wave, int lane_) {
   const int lane = local_copy(lane_);
   constexpr int VT = Walk<K, V>::VT, KT = Walk<K, V>::KT, KB = K / 32;
   const int g = lane >> 4, l16 = lane & 15;
@@ -360,7 +374,6 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, lane, 32 * b, wave * VT + vt);
     barrier_lds();  // P
-    const __amdgpu_buffer_rsrc_t out = rows_buffer<V>(out_rows, first, p.o_t, count);
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
 #pragma unroll
@@ -377,8 +390,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       for (int vt = 0; vt < VT; ++vt) {
         const f32x4 o = acc[vt][tt];
         const bf16x4 b = {to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])};
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), out,
-                                              (16 * tt + l16) * (int)p.o_t * 2 + ((wave * VT + vt) * 16 + 4 * g) * 2, 0, 0);
+        *reinterpret_cast<bf16x4*>(sh.v + row_at<V>(16 * tt + l16) + ((wave * VT + vt) * 16 + 4 * g) * 2) = b;
       }
     }
   } else {
@@ -564,12 +576,13 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 ? 4 : 3) void linear_wal
         first += count;
         left -= count;
         if (left > 0) fetch(first, min(left, kC));
-        chunk<K, V, kOut, kTerms>(p, sh, sh.decays[turn], walk, out, here, count, wave, lane);
+        chunk<K, V, kOut, kTerms>(p, sh, sh.decays[turn], walk, wave, lane);
         decay *= sh.decays[turn].total;
         turn ^= 1;
         // Wave 3 has few tiles of P.
         if (wave == 3 && left > 0) put_decays(sh.decays[turn], g_next, p.scale, lane);
         barrier_lds();
+        if constexpr (kOut) Rows<V, kThreads>::store(sh.v, out, p.o_t, here, count, tid);
       }
       if constexpr (kOut) {
         if (t1 == len && slots.to >= 0) walk.store_plane(p, plane_at(p, slots.to, h), v0, wave, lane);
