@@ -65,6 +65,8 @@ class Case:
             self.g = None
         elif decay == "head":
             self.g = -torch.exp(randn(H) - 2)
+        elif decay == "growth":
+            self.g = 0.05 * randn(T, H)
         else:
             self.g = -torch.exp(randn(T, H) - 2)
             if decay == "resets":

@@ -41,6 +41,9 @@ PROMPTS = {
     "f16_pool_kfirst": dict(lengths=[90, 0, 65], state_dtype="f16", k_first=True, pad=8),
     "f32_pool_kfirst_v64": dict(lengths=[90, 0, 65], V=64, k_first=True),
     "rows_behind": dict(lengths=[33, 40], extra_rows=9),
+    "growth": dict(lengths=[130, 1], decay="growth"),
+    "singles_among_prompts": dict(lengths=[1, 70, 1, 0, 1, 1, 2, 1, 130], H=4, H_qk=2, state_dtype="f16", k_first=True),
+    "singles_no_state": dict(lengths=[1, 1, 3, 1], state="none", decay="none"),
 }
 
 
@@ -401,6 +404,116 @@ def test_two_captured_calls_share_a_workspace():
         torch.cuda.synchronize()
         check(a, oa, da, None)
         check(b, ob, db, None)
+
+
+# ------------------------------------------------------------------------------ at the edges of the call
+def test_offsets_past_32_bits():
+    """Slots and rows whose element offsets pass 2^31: a pool with wide padding, rows far apart."""
+    H, n = 2, 300
+    case = Case([n - 80, 80], H=H, seed=90, flags="all", slots=4, state_dtype="bf16")
+    case.indices = torch.tensor([3, 2], dtype=torch.int32)
+    d = case.device()
+    wide = 1 << 30  # elements between slots
+    big = torch.empty(3 * wide + H * 128 * 128, dtype=torch.bfloat16, device="cuda")
+    cache = big.as_strided((4, H, 128, 128), (wide, 128 * 128, 128, 1))
+    cache.copy_(d["cache"])
+    rows = torch.empty(n << 23, dtype=torch.bfloat16, device="cuda")  # 5 GB, 2^23 elements between tokens
+    apart = rows.as_strided((n, H, 128), (1 << 23, 128, 1))
+    apart.copy_(d["q"])
+    d["cache"], d["q"] = cache, apart
+    out, _ = case.forward(d, seg_len=64)
+    torch.cuda.synchronize()
+    d["store"].copy_(cache.reshape(4, -1))
+    check(case, out, d, None)
+    step = kda.linear_step(apart[:2], d["k"][:2], d["v"][:2], d["g"][:2], state_cache=cache, state_indices=d["indices"])
+    ref = kda.linear_step(apart[:2].contiguous(), d["k"][:2], d["v"][:2], d["g"][:2], state_cache=case.planes(d["store"]),
+                          state_indices=d["indices"])
+    torch.cuda.synchronize()
+    assert same_bits(step, ref) and same_bits(cache.reshape(4, -1), d["store"])
+
+
+@pytest.mark.parametrize("bounds", [[0, 50, 20, 200], [0, -7, 90, 2 ** 31 - 1], [60, 60, 60, 60], [0, 0, -2 ** 31, 130]])
+def test_bounds_that_break_the_rules_stay_inside(bounds):
+    """Without host bounds nothing can refuse them; every access stays inside the rows and the slots."""
+    case = Case([60, 40, 30], H=2, seed=91, flags="all", pad=64)
+    d = case.device()
+    d["cu"] = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    before = d["store"].clone()
+    guard = torch.full((case.T + 128, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    case.forward(d, out=guard[64:-64], seg_len=64)
+    torch.cuda.synchronize()
+    assert torch.all(guard[:64] == 7.0) and torch.all(guard[-64:] == 7.0)
+    used = set(case.indices.tolist())
+    for s in range(case.slots):
+        if s not in used:
+            assert same_bits(d["store"][s], before[s])
+        assert same_bits(d["store"][s, 2 * 128 * 128:], before[s, 2 * 128 * 128:])
+
+
+def test_non_finite_rows_stay_in_their_head_and_sequence():
+    case = Case([100, 70, 1], H=3, seed=92, state="dense")
+    d = case.device()
+    clean, final = case.forward(d, seg_len=64)
+    d["v"][30, 1] = float("nan")
+    d["k"][120, 2] = float("inf")
+    out, bad = case.forward(d, seg_len=64)
+    torch.cuda.synchronize()
+    keep = torch.ones(171, 3, dtype=torch.bool, device="cuda")
+    keep[:100, 1] = False
+    keep[100:170, 2] = False
+    assert same_bits(out[keep], clean[keep])
+    ok = torch.ones(3, 3, dtype=torch.bool, device="cuda")
+    ok[0, 1] = ok[1, 2] = False
+    assert same_bits(bad[ok], final[ok])
+    assert torch.isnan(out[31:100, 1].float()).all()
+
+
+def test_calls_from_two_threads_on_two_streams():
+    import threading
+    cases = [Case([150, 90], H=2, seed=93 + i) for i in range(2)]
+    data = [c.device() for c in cases]
+    outs, errors = [None, None], []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            store = data[i]["store"].clone()
+            torch.cuda.synchronize()
+            for _ in range(20):
+                with torch.cuda.stream(s):
+                    data[i]["store"].copy_(store)
+                outs[i], _ = cases[i].forward(data[i], stream=s, seg_len=64)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    torch.cuda.synchronize()
+    for c, d, o in zip(cases, data, outs):
+        check(c, o, d, None)
+
+
+def test_refused_calls_on_the_device():
+    case = Case([20, 30], H=2, seed=95)
+    d = case.device()
+    with pytest.raises(ValueError):
+        case.forward(d, workspace=torch.empty(8, dtype=torch.uint8))  # another device
+    with pytest.raises(TypeError):
+        case.forward(d, workspace=torch.empty(8, device="cuda"))
+    with pytest.raises(kda.KDAError):
+        case.forward(d, out=d["v"])
+    with pytest.raises(kda.KDAError):
+        case.forward(d, cu_seqlens_cpu=torch.tensor([0, 60, 50], dtype=torch.int32))
+    with pytest.raises(kda.KDAError):
+        case.forward(d, seg_len=100)
+    with pytest.raises(ValueError):
+        kda.linear_fwd(d["q"], d["k"], d["v"], d["g"], case.cu)  # bounds on the CPU
 
 
 # ------------------------------------------------------------------------------ larger, random

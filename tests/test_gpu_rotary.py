@@ -166,6 +166,18 @@ def test_captured_rotation_replays():
         assert same_bits(oq, rq) and same_bits(ok, rk)
 
 
+def test_offsets_past_32_bits():
+    """Rows whose element offsets pass 2^31, on both access paths."""
+    for D, far in ((64, 1 << 30), (60, (1 << 30) + 2)):
+        q, _, pos = _inputs(4, 2, 0, D, torch.bfloat16, 40)
+        inv, _ = kda.rotary_frequencies(D)
+        rows = torch.empty(3 * far + 2 * D, dtype=torch.bfloat16, device="cuda").as_strided((4, 2, D), (far, D, 1))
+        rows.copy_(q)
+        kda.rotary(rows, None, pos.cuda(), inv.cuda(), out_q=rows)
+        torch.cuda.synchronize()
+        _within("q", rows, q, pos, inv, torch.bfloat16)
+
+
 def test_other_stream():
     q, k, pos = _inputs(50, 4, 2, 128, torch.bfloat16, 31)
     inv, _ = kda.rotary_frequencies(128)
