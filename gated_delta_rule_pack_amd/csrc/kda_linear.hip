@@ -314,13 +314,16 @@ __device__ __forceinline__ void put_decays(D& d, float g, float scale, int lane)
 __device__ __forceinline__ int fragment(int tt, int b) { return tt + (tt == 3) + b; }
 
 // One chunk of `count` tokens: P and the outputs (kOut), then the state.
-template <int K, int V, bool kOut, int kTerms>
+// next(i) issues the loads of part i of the next chunk (0: k, 1: v, 2: q), spread over the work: issued
+// at once they hold every wave for the 48 KB to pass.
+template <int K, int V, bool kOut, int kTerms, typename Next>
 __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& sh, const typename Shared<K, V, kOut>::Decays& dec,
-                                      Walk<K, V>& walk, int wave, int lane_) {
+                                      Walk<K, V>& walk, int wave, int lane_, Next next) {
   const int lane = local_copy(lane_);
   constexpr int VT = Walk<K, V>::VT, KT = Walk<K, V>::KT, KB = K / 32;
   const int g = lane >> 4, l16 = lane & 15;
   bf16x8 raw[2][VT];
+  next(0);
   if constexpr (kOut) {
     // P^T tiles (token tile tt, source tile st <= tt), rows s = 4 g + i, column t: ten, dealt out
     // over the waves.
@@ -345,6 +348,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       const bf16x4 b = {to_bf16(d[0]), to_bf16(d[1]), to_bf16(d[2]), to_bf16(d[3])};
       *reinterpret_cast<bf16x4*>(sh.p + fragment(tt, st >> 1) * 1024 + lane * 16 + (st & 1) * 8) = b;
     }
+    next(1);
     // Q S^T, transposed: rows v = 4 g + i, column t. The state is rounded to bf16 for it.
     f32x4 acc[VT][4];
 #pragma unroll
@@ -373,6 +377,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, lane, 32 * b, wave * VT + vt);
+    next(2);
     barrier_lds();  // P
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
@@ -394,6 +399,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       }
     }
   } else {
+    next(1);
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -516,15 +522,19 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 ? 4 : 3) void linear_wal
   Rows<K, kThreads> rq, rk;
   Rows<V, kThreads> rv;
   float g_next = 0.f;  // this lane's token of the next chunk
-  auto fetch = [&](int64_t first, int count) {
-    g_next = 0.f;
-    if (wave == 3 && p.g && lane < count) {
-      const int64_t at = p.g_per_token ? (first + lane) * p.H + h : h;
-      g_next = p.g_bf16 ? (float)reinterpret_cast<const __bf16*>(p.g)[at] : reinterpret_cast<const float*>(p.g)[at];
+  auto fetch = [&](int part, int64_t first, int count) {
+    if (part == 0) {
+      g_next = 0.f;
+      if (wave == 3 && p.g && lane < count) {
+        const int64_t at = p.g_per_token ? (first + lane) * p.H + h : h;
+        g_next = p.g_bf16 ? (float)reinterpret_cast<const __bf16*>(p.g)[at] : reinterpret_cast<const float*>(p.g)[at];
+      }
+      rk.load(k, p.k_t, first, count, tid);
+    } else if (part == 1) {
+      rv.load(v, p.v_t, first, count, tid);
+    } else if constexpr (kOut) {
+      rq.load(q, p.q_t, first, count, tid);
     }
-    if constexpr (kOut) rq.load(q, p.q_t, first, count, tid);
-    rk.load(k, p.k_t, first, count, tid);
-    rv.load(v, p.v_t, first, count, tid);
   };
   while (true) {
     // The next sequence's bound and slots are on their way while this one is walked.
@@ -546,7 +556,7 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 ? 4 : 3) void linear_wal
     } else if (t0 < t1) {
       int64_t first = (int64_t)begin + t0;
       int left = t1 - t0;
-      fetch(first, min(left, kC));
+      for (int part = 0; part < 3; ++part) fetch(part, first, min(left, kC));
       // Start state. A sequence that goes on after this segment leaves its final state from
       // another workgroup, perhaps in the plane it starts from: the output walk starts it from
       // the copy that the map walk made.
@@ -575,8 +585,9 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 ? 4 : 3) void linear_wal
         const int64_t here = first;
         first += count;
         left -= count;
-        if (left > 0) fetch(first, min(left, kC));
-        chunk<K, V, kOut, kTerms>(p, sh, sh.decays[turn], walk, wave, lane);
+        chunk<K, V, kOut, kTerms>(p, sh, sh.decays[turn], walk, wave, lane, [&](int part) {
+          if (left > 0) fetch(part, first, min(left, kC));
+        });
         decay *= sh.decays[turn].total;
         turn ^= 1;
         // Wave 3 has few tiles of P.
