@@ -302,7 +302,7 @@ kda_status kda_linear_step_validate(const kda_linear_args* a) {
   if (kda_status st = check_linear(a)) return st;
   if (a->T != a->N || !a->state_cache) return KDA_ERR_INVALID_ARG;
   if (!a->state_indices && a->num_slots < a->N) return KDA_ERR_INVALID_ARG;
-  if ((int64_t)a->N * a->H > INT32_MAX / 8) return KDA_ERR_UNSUPPORTED;  // workgroups of one launch
+  if ((int64_t)a->N * a->H > INT32_MAX) return KDA_ERR_UNSUPPORTED;  // workgroups of one launch
   return KDA_OK;
 }
 

@@ -456,16 +456,32 @@ def test_non_finite_rows_stay_in_their_head_and_sequence():
     clean, final = case.forward(d, seg_len=64)
     d["v"][30, 1] = float("nan")
     d["k"][120, 2] = float("inf")
+    d["g"][170, 0] = float("nan")
     out, bad = case.forward(d, seg_len=64)
     torch.cuda.synchronize()
     keep = torch.ones(171, 3, dtype=torch.bool, device="cuda")
     keep[:100, 1] = False
     keep[100:170, 2] = False
+    keep[170, 0] = False
     assert same_bits(out[keep], clean[keep])
     ok = torch.ones(3, 3, dtype=torch.bool, device="cuda")
-    ok[0, 1] = ok[1, 2] = False
+    ok[0, 1] = ok[1, 2] = ok[2, 0] = False
     assert same_bits(bad[ok], final[ok])
-    assert torch.isnan(out[31:100, 1].float()).all()
+    assert torch.isnan(out[31:100, 1].float()).all() and torch.isnan(out[170, 0].float()).all()
+
+
+def test_large_keys_do_not_reach_earlier_rows():
+    """q . k of later tokens may overflow fp32: those pairs are left out, not multiplied by 0."""
+    case = Case([60], H=1, seed=94, state="none")
+    d = case.device()
+    clean, _ = case.forward(d)
+    d["k"][40:] = 3e38
+    d["q"] = d["q"] * 1e3
+    out, _ = case.forward(d)
+    torch.cuda.synchronize()
+    ref, _ = case.forward(dict(d, k=torch.where(torch.arange(60, device="cuda")[:, None, None] < 40, d["k"], 0)))
+    torch.cuda.synchronize()
+    assert torch.isfinite(out[:40]).all() and same_bits(out[:40], ref[:40])
 
 
 def test_calls_from_two_threads_on_two_streams():
