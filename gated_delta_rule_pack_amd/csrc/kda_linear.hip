@@ -20,9 +20,11 @@
 //
 // A workgroup takes all V state rows, or a slice of 64 of them where there are few segments and
 // heads. Each wave holds 16 of its rows in fp32 MFMA accumulators, S^T[k][v], for the whole walk.
-// Lanes (l, g = l / 16): accumulator tiles of K^T U hold column v = l % 16, rows k = 4g + i, which is
-// an operand of Q S^T whose contraction order is (4g + i, 16 + 4g + i); q is read from LDS in that
-// order, and P, made as K Q^T, meets V the same way, so neither the state nor P is ever transposed.
+// Lanes (l, g = l / 16): an accumulator tile of K^T U holds column l % 16 (v), rows 4g + i. Tile 2m is
+// made of channels 32m + 8g + i and tile 2m + 1 of 32m + 8g + 4 + i (i < 4), so that a lane's two
+// tiles are eight channels in a row: an operand of Q S^T as it stands, and 16 or 32 bytes of a stored
+// state. P, made as K Q^T, meets V in the order (4g + i, 16 + 4g + i) of its tiles. Neither the state
+// nor P is ever transposed.
 //
 // What bounds it. A long prompt reads k and v twice (map and output), q once, and writes the outputs:
 // 1 x 32768 tokens at H = 32, fp32 state, move 1.6 GB in 380 us (map 125, combine 11, output 240),
@@ -71,30 +73,25 @@ __device__ __forceinline__ uint32_t both_bf16(float a, float b) {
 // LDS tile of 64 rows of D bf16. A row takes 16 bytes more than its elements, and inside 16 rows
 // row r stands at place 2 (r % 8) + r / 8: the 16 rows of an operand read then start on different
 // banks, and the 8 rows of half a transposing read do not meet. Every read is a lane's own place and
-// a constant offset. q, which every wave reads as operand rows, holds each 32 elements in the
-// accumulators' order (unit g of 16 bytes has elements 4 g + i and 16 + 4 g + i), so that an operand
-// is one 16-byte read of 9 cycles; k and v, read by columns, keep their order, and k's few reads as
-// rows take two 8-byte pieces, 16 cycles.
+// a constant offset, and takes 9 cycles a wave (a transposing read moves half as much in them).
 template <int D>
 constexpr int kRowBytes = 2 * D + 16;
 template <int D>
 __device__ __forceinline__ int row_at(int row) {
   return ((row & ~15) | ((row & 7) << 1) | ((row >> 3) & 1)) * kRowBytes<D>;
 }
-// Operand rows: row r0 + l % 16 (r0 a multiple of 16), elements 32 m + 4 g + i, 32 m + 16 + 4 g + i.
-template <int D, bool kOrdered>
-__device__ __forceinline__ bf16x8 read_row(const char* tile, int lane, int r0, int m) {
-  const char* p = tile + r0 * kRowBytes<D> + m * 64 + row_at<D>(lane & 15) + (lane >> 4) * (kOrdered ? 16 : 8);
-  if constexpr (kOrdered) return *reinterpret_cast<const bf16x8*>(p);
-  const bf16x4 a = *reinterpret_cast<const bf16x4*>(p), b = *reinterpret_cast<const bf16x4*>(p + 32);
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-// Operand columns: column 16 c + l % 16 of rows t0 + 4 g + i and t0 + 16 + 4 g + i (t0 a multiple of
-// 32), by two transposing reads: 16 lanes give the addresses of a 4 x 16 block, lane j of row j / 4 and
-// columns 4 (j % 4).
+// Operand rows: row r0 + l % 16 (r0 a multiple of 16), elements 32 m + 8 g + j.
 template <int D>
+__device__ __forceinline__ bf16x8 read_row(const char* tile, int lane, int r0, int m) {
+  return *reinterpret_cast<const bf16x8*>(tile + r0 * kRowBytes<D> + m * 64 + row_at<D>(lane & 15) + (lane >> 4) * 16);
+}
+// Operand columns: of rows t0 + 4 g + i and t0 + 16 + 4 g + i (t0 a multiple of 32), by two transposing
+// reads: 16 lanes give the addresses of four groups of four columns in four rows, lane j of row j / 4
+// and group j % 4. Plain: columns 16 c + l % 16. Spread (k): the channels of state tile c.
+template <int D, bool kSpread>
 __device__ __forceinline__ bf16x8 read_col(const char* tile, int lane, int t0, int c) {
-  const char* p = tile + t0 * kRowBytes<D> + c * 32 + row_at<D>(4 * (lane >> 4) + ((lane & 15) >> 2)) + (lane & 3) * 8;
+  const char* p = tile + t0 * kRowBytes<D> + (kSpread ? (c >> 1) * 64 + (c & 1) * 8 : c * 32) +
+                  row_at<D>(4 * (lane >> 4) + ((lane & 15) >> 2)) + (lane & 3) * (kSpread ? 16 : 8);
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 16 * kRowBytes<D>));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -147,8 +144,20 @@ __device__ __forceinline__ void store_state(const LinearPlan& p, void* base, int
   else reinterpret_cast<__bf16*>(base)[at] = to_bf16(x);
 }
 
-// The walk's state registers: S[vt][kt] holds v = 16 vt + l % 16 of the wave's rows and
-// k = 16 kt + 4 g + i.
+// Eight elements of a state in a row.
+template <int SDT>
+__device__ __forceinline__ void load8(const void* base, size_t at, f32x4& a, f32x4& b) {
+  a = load_state4<SDT>(base, at);
+  b = load_state4<SDT>(base, at + 4);
+}
+template <int SDT>
+__device__ __forceinline__ void store8(void* base, size_t at, f32x4 a, f32x4 b) {
+  store_state4<SDT>(base, at, a);
+  store_state4<SDT>(base, at + 4, b);
+}
+
+// The walk's state registers: S[vt][2 m + h] holds v = 16 vt + l % 16 of the wave's rows and
+// k = 32 m + 8 g + 4 h + i.
 template <int K, int V>
 struct Walk {
   static constexpr int VT = V / (16 * kWavesOf<V>);  // 16-row tiles of V per wave
@@ -182,16 +191,20 @@ struct Walk {
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const int v = v0 + (wave * VT + vt) * 16 + (lane & 15), k = kt * 16 + 4 * g;
+      for (int m = 0; m < KT / 2; ++m) {
+        const int v = v0 + (wave * VT + vt) * 16 + (lane & 15), k = m * 32 + 8 * g;
+        f32x4 &a = S[vt][2 * m], &b = S[vt][2 * m + 1];
         if (!p.kfirst) {
           const size_t off = (size_t)(at + (int64_t)v * K + k);
-          if (p.state_dtype == kF32) S[vt][kt] = load_state4<kF32>(p.state_in, off);
-          else if (p.state_dtype == kF16) S[vt][kt] = load_state4<kF16>(p.state_in, off);
-          else S[vt][kt] = load_state4<kBF16>(p.state_in, off);
+          if (p.state_dtype == kF32) load8<kF32>(p.state_in, off, a, b);
+          else if (p.state_dtype == kF16) load8<kF16>(p.state_in, off, a, b);
+          else load8<kBF16>(p.state_in, off, a, b);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) S[vt][kt][i] = load_state(p, p.state_in, at + (int64_t)(k + i) * p.V + v);
+          for (int i = 0; i < 4; ++i) {
+            a[i] = load_state(p, p.state_in, at + (int64_t)(k + i) * p.V + v);
+            b[i] = load_state(p, p.state_in, at + (int64_t)(k + 4 + i) * p.V + v);
+          }
         }
       }
   }
@@ -200,16 +213,20 @@ struct Walk {
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const int v = v0 + (wave * VT + vt) * 16 + (lane & 15), k = kt * 16 + 4 * g;
+      for (int m = 0; m < KT / 2; ++m) {
+        const int v = v0 + (wave * VT + vt) * 16 + (lane & 15), k = m * 32 + 8 * g;
+        const f32x4 a = S[vt][2 * m], b = S[vt][2 * m + 1];
         if (!p.kfirst) {
           const size_t off = (size_t)(at + (int64_t)v * K + k);
-          if (p.state_dtype == kF32) store_state4<kF32>(p.state_out, off, S[vt][kt]);
-          else if (p.state_dtype == kF16) store_state4<kF16>(p.state_out, off, S[vt][kt]);
-          else store_state4<kBF16>(p.state_out, off, S[vt][kt]);
+          if (p.state_dtype == kF32) store8<kF32>(p.state_out, off, a, b);
+          else if (p.state_dtype == kF16) store8<kF16>(p.state_out, off, a, b);
+          else store8<kBF16>(p.state_out, off, a, b);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) store_state(p, p.state_out, at + (int64_t)(k + i) * p.V + v, S[vt][kt][i]);
+          for (int i = 0; i < 4; ++i) {
+            store_state(p, p.state_out, at + (int64_t)(k + i) * p.V + v, a[i]);
+            store_state(p, p.state_out, at + (int64_t)(k + 4 + i) * p.V + v, b[i]);
+          }
         }
       }
   }
@@ -239,7 +256,7 @@ struct Rows {
     for (int i = 0; i < kPasses; ++i)
       w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRows * (int)stride * 2, 0, 0));
   }
-  // Rows of a tile that is not ordered to memory, `count` of them, whole rows to a wave (parts of rows
+  // Rows of a tile to memory, `count` of them, whole rows to a wave (parts of rows
   // leave their merging to L2: 32768 tokens at H = 32 take 405 us so, 379 here) and past the caches, which
   // have no use for them (385 us without the hint). A thread reads the bytes that its own put writes
   // next, so no barrier stands between.
@@ -253,23 +270,12 @@ struct Rows {
       __builtin_amdgcn_raw_buffer_store_b128(x, r, at + i * kRows * (int)stride * 2, 0, kStreamLoad);
     }
   }
-  // kOrdered: the 8 elements of unit u of four go to units 2 (u % 2) and 2 (u % 2) + 1, half u / 2.
-  template <bool kOrdered>
   __device__ __forceinline__ void put(char* tile, int tid) const {
     tid = local_copy(tid);
-    const int u = tid % kUnits;
     static_assert(kRows % 16 == 0, "whole groups of rows");
-    char* at = tile + row_at<D>(tid / kUnits) + (kOrdered ? (u >> 2) * 64 + (u & 1) * 32 + ((u >> 1) & 1) * 8 : u * 16);
+    char* at = tile + row_at<D>(tid / kUnits) + (tid % kUnits) * 16;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      char* to = at + i * kRows * kRowBytes<D>;
-      if constexpr (kOrdered) {
-        *reinterpret_cast<u32x2*>(to) = u32x2{w[i][0], w[i][1]};
-        *reinterpret_cast<u32x2*>(to + 16) = u32x2{w[i][2], w[i][3]};
-      } else {
-        *reinterpret_cast<u32x4*>(to) = w[i];
-      }
-    }
+    for (int i = 0; i < kPasses; ++i) *reinterpret_cast<u32x4*>(at + i * kRows * kRowBytes<D>) = w[i];
   }
 };
 
@@ -343,7 +349,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       f32x4 d = zero4();
 #pragma unroll
       for (int m = 0; m < KB; ++m)
-        d = mfma(read_row<K, false>(sh.k, lane, 16 * st, m), read_row<K, true>(sh.q, lane, 16 * tt, m), d);
+        d = mfma(read_row<K>(sh.k, lane, 16 * st, m), read_row<K>(sh.q, lane, 16 * tt, m), d);
       const double Gt = dec.G[t];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -370,7 +376,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       for (int vt = 0; vt < VT; ++vt) sb[vt] = pack8(walk.S[vt][2 * m], walk.S[vt][2 * m + 1]);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const bf16x8 b = read_row<K, true>(sh.q, lane, 16 * tt, m);
+        const bf16x8 b = read_row<K>(sh.q, lane, 16 * tt, m);
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(sb[vt], b, acc[vt][tt]);
       }
@@ -384,7 +390,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, lane, 32 * b, wave * VT + vt);
+      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V, false>(sh.v, lane, 32 * b, wave * VT + vt);
     next(2);
     barrier_lds();  // P
 #pragma unroll
@@ -411,7 +417,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V>(sh.v, lane, 32 * b, wave * VT + vt);
+      for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V, false>(sh.v, lane, 32 * b, wave * VT + vt);
   }
   // State. The decayed values x (fp32) go in as bf16 terms against the stored keys, which are bf16.
   // Three terms of 8 bits each, cut off rather than rounded, are x exactly: the state keeps fp32
@@ -452,7 +458,7 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
     // Two tiles of K at a time, term by term: no product waits for the one before it.
 #pragma unroll
     for (int kt = 0; kt < KT; kt += 2) {
-      const bf16x8 k0 = read_col<K>(sh.k, lane, 32 * b, kt), k1 = read_col<K>(sh.k, lane, 32 * b, kt + 1);
+      const bf16x8 k0 = read_col<K, true>(sh.k, lane, 32 * b, kt), k1 = read_col<K, true>(sh.k, lane, 32 * b, kt + 1);
 #pragma unroll
       for (int j = 0; j < kTerms; ++j) {
 #pragma unroll
@@ -481,15 +487,16 @@ __device__ __forceinline__ void single(const LinearPlan& p, Walk<K, V>& walk, co
 #pragma unroll
   for (int vt = 0; vt < VT; ++vt) x[vt] = from_bf16(v[token * p.v_t + row + 16 * vt]), o[vt] = 0.f;
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt) {
-    const bf16x4 kk = *reinterpret_cast<const bf16x4*>(k + token * p.k_t + 16 * kt + 4 * g);
-    const bf16x4 qq = *reinterpret_cast<const bf16x4*>(q + token * p.q_t + 16 * kt + 4 * g);
+  for (int m = 0; m < KT / 2; ++m) {
+    const bf16x8 kk = *reinterpret_cast<const bf16x8*>(k + token * p.k_t + 32 * m + 8 * g);
+    const bf16x8 qq = *reinterpret_cast<const bf16x8*>(q + token * p.q_t + 32 * m + 8 * g);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        walk.S[vt][kt][i] = walk.S[vt][kt][i] * decay + x[vt] * (float)kk[i];
-        o[vt] += walk.S[vt][kt][i] * (float)qq[i];
+      for (int j = 0; j < 8; ++j) {
+        f32x4& S = walk.S[vt][2 * m + j / 4];
+        S[j % 4] = S[j % 4] * decay + x[vt] * (float)kk[j];
+        o[vt] += S[j % 4] * (float)qq[j];
       }
   }
 #pragma unroll
@@ -586,9 +593,9 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, V == 128 ? 4 : 3) void linear_wal
       if (wave == 3) put_decays(sh.decays[0], g_next, p.scale, lane);
       while (left > 0) {
         const int count = min(left, kC);
-        if constexpr (kOut) rq.template put<true>(sh.q, tid);
-        rk.template put<false>(sh.k, tid);
-        rv.template put<false>(sh.v, tid);
+        if constexpr (kOut) rq.put(sh.q, tid);
+        rk.put(sh.k, tid);
+        rv.put(sh.v, tid);
         barrier_lds();
         const int64_t here = first;
         first += count;
