@@ -62,21 +62,23 @@ int64_t axis_of(const kda_linear_args* a) {
 }
 
 // Segment length. A long segment costs its own walk (5 us for each 64 tokens of K = V = 128, map and
-// output, one workgroup on a compute unit); every segment costs states of K V floats, written, chained
-// and read back. The sum is least at a length that grows with the root of the work: measured best at
-// H = 12 for 1024 tokens 128, 4096 tokens 192 (41.9 us; 128: 47.4, 384: 49.7), 8192 tokens 384, and at
-// H = 32 for 1536 tokens 192, 6144 tokens 384. Work for more workgroups than the chip holds at once
-// (two of 128 state rows on a compute unit, three of 64) takes as many: 32768 tokens at H = 32, 2048
-// (399 us; 1024: 425). Little work takes one segment and one kernel: 128 tokens 11.2 us, 14.9 in two
-// segments; 16 sequences of 16 tokens 17.2 us, 26.7 in segments.
+// output, one workgroup on a compute unit); every segment costs a step of the combine's chain (0.06 us)
+// and, for each head, a state that is written, chained and read back (0.059 us at K = V = 128). The sum
+// is least at a length that grows with the root of the tokens: measured best at H = 12 for 1024 tokens
+// 128, 4096 tokens 192 (41.0 us; 128: 47.2, 384: 47.8), 8192 tokens 384; at H = 32 for 1536 tokens 192,
+// 6144 tokens 384; at H = 1 for 168 K tokens (V = 64) 384 to 768 (91 us; 256: 108). Work for more
+// workgroups than the chip holds at once (two of 128 state rows on a compute unit, three of 64) takes
+// as many: 32768 tokens at H = 32, 2048 (399 us; 1024: 425). Little work takes one segment and one
+// kernel: 128 tokens 11.2 us, 14.9 in two segments; 16 sequences of 16 tokens 17.2 us, 26.7 in segments.
 int32_t seg_len_of(const kda_linear_args* a) {
   if (a->seg_len > 0) return a->seg_len;
+  constexpr int64_t C = kda::kLinChunk;
   const int64_t axis = axis_of(a), units = a->V == 64 ? 768 : 512;
   const int64_t fit = std::max<int64_t>(1, units / a->H), fill = (axis + fit - 1) / fit;
-  const int64_t root = (int64_t)std::sqrt(0.75 * (double)axis * a->H * a->K * a->V / (128 * 128));
+  const double per_segment = 0.06 + 0.059 * a->H * a->K * a->V / (128 * 128), per_token = 5.0 / C;
+  const int64_t root = (int64_t)(std::sqrt(per_segment * (double)axis / per_token) / C + 0.5) * C;
   const int64_t len = a->T <= 256 && a->N <= 16 ? axis : std::max(fill, root);
-  const int64_t whole = (std::max<int64_t>(len, 1) + kda::kLinChunk - 1) / kda::kLinChunk * kda::kLinChunk;
-  return (int32_t)std::min<int64_t>(whole, 1 << 30);
+  return (int32_t)std::min<int64_t>((std::max<int64_t>(len, 1) + C - 1) / C * C, 1 << 30);
 }
 int32_t segments_of(const kda_linear_args* a) {
   const int64_t L = seg_len_of(a);
