@@ -69,7 +69,8 @@ int64_t axis_of(const kda_linear_args* a) {
 // 6144 tokens 384; at H = 1 for 168 K tokens (V = 64) 384 to 768 (91 us; 256: 108). Work for more
 // workgroups than the chip holds at once (two of 128 state rows on a compute unit, three of 64) takes
 // as many: 32768 tokens at H = 32, 2048 (399 us; 1024: 425). Little work takes one segment and one
-// kernel: 128 tokens 11.2 us, 14.9 in two segments; 16 sequences of 16 tokens 17.2 us, 26.7 in segments.
+// kernel: 128 tokens 12.6 us, 16.4 in two segments; 192 tokens 16.1 and 16.8, 256 tokens 19.5 and 17.0;
+// two sequences of 10 tokens 15.0 and 15.2, three 20.8 and 15.0.
 int32_t seg_len_of(const kda_linear_args* a) {
   if (a->seg_len > 0) return a->seg_len;
   constexpr int64_t C = kda::kLinChunk;
@@ -77,7 +78,11 @@ int32_t seg_len_of(const kda_linear_args* a) {
   const int64_t fit = std::max<int64_t>(1, units / a->H), fill = (axis + fit - 1) / fit;
   const double per_segment = 0.06 + 0.059 * a->H * a->K * a->V / (128 * 128), per_token = 5.0 / C;
   const int64_t root = (int64_t)(std::sqrt(per_segment * (double)axis / per_token) / C + 0.5) * C;
-  const int64_t len = a->T <= 256 && a->N <= 16 ? axis : std::max(fill, root);
+  int64_t len = a->T + 128 * ((int64_t)a->N - 1) <= 224 ? axis : std::max(fill, root);
+  // Between one workgroup and two for each of 256 compute units the second ones decide the time: one
+  // for each it is (65536 tokens at H = 2, 256 workgroups 74.7 us, 342: 85.5).
+  const int64_t work = (axis + len - 1) / len * a->H;
+  if (work > 264 && work < 500) len = axis * a->H / 256;
   return (int32_t)std::min<int64_t>((std::max<int64_t>(len, 1) + C - 1) / C * C, 1 << 30);
 }
 int32_t segments_of(const kda_linear_args* a) {
