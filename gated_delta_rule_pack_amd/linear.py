@@ -35,14 +35,17 @@ def _packed(name, t):
 
 def _strides(name, t, T, H, D):
     """Element strides between tokens and between heads; dense ones stand in where the tensor has
-    a single token or head (torch leaves those arbitrary)."""
+    a single token or head (torch leaves those arbitrary). A stride of 0 shows one row as several;
+    both 0 would mean dense to the library."""
     st, sh, sd = t.stride()
     if sd != 1 and D != 1:
         raise ValueError(f"{name} must have adjacent elements along its last dimension")
     if H == 1:
         sh = D
     if T <= 1:
-        st = H * sh
+        st = H * (sh or D)
+    if st == 0 and sh == 0:
+        raise ValueError(f"{name} must not be broadcast over both tokens and heads")
     return st, sh
 
 

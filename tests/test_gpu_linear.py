@@ -163,6 +163,23 @@ def test_broadcast_rows():
     check(case, out, d, None)
 
 
+@pytest.mark.parametrize("entry", ["prompt", "step"])
+def test_broadcast_row_of_one_token(entry):
+    """One token whose q and k heads are one row (all strides 0)."""
+    case = Case([1], H=3, H_qk=1, seed=61, flags="all")
+    shared = {n: getattr(case, n).cuda().expand(-1, 3, -1) for n in "qk"}
+    outs = []
+    for q, k in ((case.q.cuda(), case.k.cuda()), (shared["q"], shared["k"])):
+        d = dict(case.device(), q=q, k=k)
+        if entry == "prompt":
+            out, _ = case.forward(d)
+        else:
+            out = kda.linear_step(q, k, d["v"], d["g"], state_cache=d["cache"], state_indices=d["indices"])
+        outs.append((out, d["store"]))
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
 def test_prompts_with_rotary_positions():
     case = Case([150, 40], H=4, H_qk=2, K=128, seed=12, state="dense")
     d = case.device()

@@ -296,6 +296,28 @@ def test_binding_fills_strides_and_types():
     assert a.scale == pytest.approx(128 ** -0.5)
 
 
+def test_binding_of_broadcast_rows():
+    # Strides 0, 0 mean dense to the library: a broadcast row must not be passed as such.
+    t, kw = _tensors()
+    one, many = torch.zeros(1, 1, 128, dtype=BF), torch.zeros(20, 1, 128, dtype=BF)
+    a = kda.make_linear_args(t["q"], many.expand(-1, 2, -1), t["v"], t["g"], **kw)
+    assert (a.k_stride_t, a.k_stride_h) == (128, 0)
+    with pytest.raises(ValueError, match="broadcast"):
+        kda.make_linear_args(t["q"], one.expand(20, 2, -1), t["v"], t["g"], **kw)
+    step = dict(N=1, state_cache=kw["state_cache"], out=torch.zeros(1, 4, 64, dtype=BF))
+    a = kda.make_linear_args(one.expand(-1, 2, -1), one.expand(-1, 2, -1), t["v"][:1], t["g"][:1], **step)
+    assert a.q_stride_h == a.k_stride_h == 0 and a.q_stride_t == a.k_stride_t == 256
+    pos, inv = torch.zeros(20, dtype=torch.int32), torch.ones(8, dtype=torch.float64)
+    with pytest.raises(ValueError, match="broadcast"):
+        kda.make_rotary_args(one.expand(20, 3, -1), None, pos, inv, torch.zeros(20, 3, 128, dtype=BF), None)
+    with pytest.raises(ValueError, match="broadcast"):
+        kda.make_rotary_args(torch.zeros(20, 3, 128, dtype=BF), None, pos, inv, one.expand(20, 3, -1), None)
+    a = kda.make_rotary_args(one.expand(1, 3, -1), None, pos[:1], inv, torch.zeros(1, 3, 128, dtype=BF), None)
+    assert (a.q_stride_t, a.q_stride_h) == (384, 0)
+    a = kda.make_rotary_args(torch.zeros(1, 3, 128, dtype=BF).expand(20, -1, -1), None, pos, inv, torch.zeros(20, 3, 128, dtype=BF), None)
+    assert (a.q_stride_t, a.q_stride_h) == (0, 128)
+
+
 def _m(name, value):
     return lambda t, kw: (t if name in t else kw).__setitem__(name, value)
 
