@@ -39,6 +39,8 @@ Strides strides_of(int64_t t, int64_t h, int64_t H, int64_t D) {
 // Largest stride: far above any real row, and far below what would overflow 64-bit offsets.
 constexpr int64_t kMaxStride = int64_t(1) << 31;
 constexpr int64_t kMaxTokenStride = int64_t(1) << 23;
+// Workgroups of 256 threads in one launch: its work-items are counted in 32 bits.
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
 bool stride_ok(Strides s) { return s.t >= 0 && s.h >= 0 && s.t <= kMaxStride && s.h <= kMaxStride; }
 // No two rows of an output overlap: heads inside tokens, or tokens inside heads.
 bool distinct_rows(Strides s, int64_t T, int64_t H, int64_t D) {
@@ -246,7 +248,7 @@ kda_status kda_linear_fwd_validate(const kda_linear_args* a) {
   if (a->seg_len < 0 || a->seg_len % kda::kLinChunk != 0 || a->seg_len > (1 << 30)) return KDA_ERR_INVALID_ARG;
   if (a->state_cache && (!a->state_indices || !a->has_initial_state)) return KDA_ERR_INVALID_ARG;
   if (axis_of(a) > INT32_MAX - (1 << 20)) return KDA_ERR_UNSUPPORTED;
-  if ((int64_t)segments_of(a) * a->H > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)segments_of(a) * a->H > kMaxGroups / 2) return KDA_ERR_UNSUPPORTED;  // of 512 threads
   if (const int32_t* cu = a->cu_seqlens_host) {
     if (cu[0] != 0 || cu[a->N] > a->T) return KDA_ERR_INVALID_ARG;
     for (int i = 0; i < a->N; ++i)
@@ -309,7 +311,7 @@ kda_status kda_linear_step_validate(const kda_linear_args* a) {
   if (kda_status st = check_linear(a)) return st;
   if (a->T != a->N || !a->state_cache) return KDA_ERR_INVALID_ARG;
   if (!a->state_indices && a->num_slots < a->N) return KDA_ERR_INVALID_ARG;
-  if ((int64_t)a->N * a->H > INT32_MAX) return KDA_ERR_UNSUPPORTED;  // workgroups of one launch
+  if ((int64_t)a->N * a->H > kMaxGroups) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 

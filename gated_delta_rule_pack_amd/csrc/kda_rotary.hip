@@ -187,11 +187,24 @@ int launch_dt(const RotaryPlan& p, hipStream_t s) {
 
 }  // namespace
 
-int launch_rotary(const RotaryPlan& p, void* stream) {
+// A launch counts its work-items in 32 bits, so it takes 2^22 tokens at most.
+int launch_rotary(const RotaryPlan& whole, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (p.dtype == kF32) return launch_dt<kF32>(p, s);
-  if (p.dtype == kF16) return launch_dt<kF16>(p, s);
-  return launch_dt<kBF16>(p, s);
+  constexpr int64_t kMost = 1 << 22;
+  const int64_t size = whole.dtype == kF32 ? 4 : 2;
+  for (int64_t first = 0; first < whole.T; first += kMost) {
+    RotaryPlan p = whole;
+    p.T = (int)(whole.T - first < kMost ? whole.T - first : kMost);
+    for (int i = 0; i < 2; ++i) {
+      if (p.H[i] == 0) continue;
+      p.in[i] = static_cast<const char*>(p.in[i]) + first * p.in_t[i] * size;
+      p.out[i] = static_cast<char*>(p.out[i]) + first * p.out_t[i] * size;
+    }
+    p.positions = static_cast<const char*>(p.positions) + first * (p.positions_i64 ? 8 : 4);
+    const int error = p.dtype == kF32 ? launch_dt<kF32>(p, s) : p.dtype == kF16 ? launch_dt<kF16>(p, s) : launch_dt<kBF16>(p, s);
+    if (error) return error;
+  }
+  return 0;
 }
 
 }  // namespace kda

@@ -403,14 +403,14 @@ typedef struct kda_linear_args {
   float rot_factor;
 
   /* kda_linear_fwd only: tokens per segment of the parallel walk, 0 = the policy
-   * (kda_linear_seg_len); otherwise a positive multiple of 64. */
+   * (kda_linear_seg_len); otherwise a positive multiple of 64. Segments times H stay below 2^23. */
   int32_t seg_len;
 } kda_linear_args;
 
 /* Prompts: every sequence walks in chunks of 64 tokens, the packed tokens cut into segments
  * of equal cost that run in parallel (state maps of the segments, a combine over them, the
  * outputs; one kernel alone when there is one segment). Enqueues on stream and returns; a
- * failed call enqueues nothing. Errors as kda_chunk_fwd, with KDA_ERR_ALIAS also for out over
+ * refused call enqueues nothing. Errors as kda_chunk_fwd, with KDA_ERR_ALIAS also for out over
  * q or k, and for an initial_state that overlaps final_state without being the same memory. */
 kda_status kda_linear_fwd(kda_ctx* ctx, const kda_linear_args* args, void* workspace, size_t workspace_bytes,
                           void* stream);
@@ -427,7 +427,7 @@ int32_t kda_linear_seg_len(const kda_linear_args* args);
  * state_indices[n] of state_cache (dense tensors go in as a pool of N slots), and T must equal
  * N. A row whose index is outside [0, num_slots) is padding: its state and its row of out are
  * left as they were. No workspace; nothing is read back or allocated; capturable. One kernel,
- * which also rotates q and k, in fp32. */
+ * which also rotates q and k, in fp32; N * H below 2^24. */
 kda_status kda_linear_step(kda_ctx* ctx, const kda_linear_args* args, void* stream);
 kda_status kda_linear_step_validate(const kda_linear_args* args);
 
@@ -459,7 +459,8 @@ typedef struct kda_rotary_args {
   int32_t inverse;
 } kda_rotary_args;
 
-/* Enqueues the rotation of q and k as one kernel; a failed call enqueues nothing. */
+/* Enqueues the rotation of q and k as one kernel (one for each 2^22 tokens); a refused call enqueues
+ * nothing. */
 kda_status kda_rotary(kda_ctx* ctx, const kda_rotary_args* args, void* stream);
 kda_status kda_rotary_validate(const kda_rotary_args* args);
 

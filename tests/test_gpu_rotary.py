@@ -178,6 +178,22 @@ def test_offsets_past_32_bits():
         _within("q", rows, q, pos, inv, torch.bfloat16)
 
 
+@pytest.mark.parametrize("D, rot", [(6, 4), (16, 16)])
+def test_more_tokens_than_one_launch_takes(D, rot):
+    T = (1 << 22) + 1000
+    inv, _ = kda.rotary_frequencies(rot, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(31)
+    q = torch.randn(T, 1, D, device="cuda", generator=gen).bfloat16()
+    k = torch.randn(T, 1, D, device="cuda", generator=gen).bfloat16()
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    out = kda.rotary(q, k, pos, inv)
+    for first in (0, (1 << 22) - 500, (1 << 22) - 1, 1 << 22, T - 700):  # alone, the same tokens give the same bits
+        part = slice(first, first + 700)
+        want = kda.rotary(q[part], k[part], pos[part], inv)
+        for got, ref in zip(out, want):
+            assert torch.equal(got[part], ref)
+
+
 def test_other_stream():
     q, k, pos = _inputs(50, 4, 2, 128, torch.bfloat16, 31)
     inv, _ = kda.rotary_frequencies(128)

@@ -217,6 +217,30 @@ def test_policy_gives_whole_chunks_and_covers_the_axis(lib):
         assert L > 0 and L % 64 == 0
 
 
+def _sizes_only(a, T, N, H):
+    """Sizes alone change: nothing is read, and the addresses are far apart."""
+    a.T, a.N, a.H, a.H_qk = T, N, H, H
+    a.q, a.k, a.v, a.out = (i << 46 for i in range(1, 5))
+    a.cu_seqlens_host = None
+    a.num_slots, a.state_cache_stride0 = N, H * 128 * 64
+
+
+def test_launches_stay_within_32_bits_of_work_items(lib, fake):
+    b = FakeBufs()
+    for N, H, code in ((1 << 20, 15, _lib.KDA_OK), (1 << 20, 16, UNS), (1 << 18, 63, _lib.KDA_OK), (1 << 12, 1 << 13, UNS)):
+        a = _args(b, T=3, N=3, step=True)
+        _sizes_only(a, N, N, H)
+        assert lib.kda_linear_step_validate(ctypes.byref(a)) == code, (N, H)
+    for T, H, code in ((1 << 22, 127, _lib.KDA_OK), (1 << 22, 128, UNS), (1 << 29, 1, UNS), (1 << 30, 1, UNS)):
+        a = _args(b)
+        _sizes_only(a, T, 1, H)
+        a.seg_len = 64
+        assert lib.kda_linear_fwd_validate(ctypes.byref(a)) == code, (T, H)
+        a.seg_len = 0  # the policy stays far below
+        assert lib.kda_linear_fwd_validate(ctypes.byref(a)) == _lib.KDA_OK
+    assert fake.launches == []
+
+
 # ------------------------------------------------------------------------------ rotary
 def _rotary_args(b, T=10, Hq=4, Hk=2, D=64):
     a = _lib.RotaryArgs()
