@@ -2,7 +2,8 @@
 
 ``chunk_fwd`` marshals torch tensors into the C ABI of ``libkda.so`` (``include/kda.h``)
 and enqueues the HIP kernels on the current torch stream. torch provides device memory
-and streams only; the computation is entirely in the library.
+and streams only; the computation is entirely in the library. ``linear_fwd``, ``linear_step`` and
+``rotary`` (``linear.py``) do the same for linear attention with a decay per head and rotary positions.
 """
 from __future__ import annotations
 

@@ -27,11 +27,11 @@
 // nor P is ever transposed.
 //
 // What bounds it. A long prompt reads k and v twice (map and output), q once, and writes the outputs:
-// 1 x 32768 tokens at H = 32, fp32 state, move 1.6 GB in 380 us (map 125, combine 11, output 240),
+// 1 x 32768 tokens at H = 32, fp32 state, move 1.6 GB in 380 us (map 122, combine 10, output 237),
 // 4.2 TB/s; the output walk without its arithmetic takes 237 us, without its loads 160, so memory
-// bounds both walks. 128 ragged prompts (131 K tokens at H = 12, bf16 pool) take 451 us, 3.7 TB/s. A
+// bounds both walks. 128 ragged prompts (131 K tokens at H = 12, bf16 pool) take 453 us (map 58, output 378). A
 // workgroup alone on a compute unit takes 3 us for a chunk, 2 us in the map walk, by the length of
-// its chain of LDS reads, products and three barriers: 1 x 4096 at H = 12 takes 42 us that way.
+// its chain of LDS reads, products and three barriers: 1 x 4096 at H = 12 takes 38 us that way.
 #include <hip/hip_runtime.h>
 
 #include "kda_device.h"

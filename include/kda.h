@@ -24,6 +24,9 @@
  * call build and upload its metadata without any synchronising call (aiter PR 6912,
  * Changes).
  *
+ * Beside it: linear attention with a decay for each head (kda_linear_fwd, kda_linear_step)
+ * over the same pool, and rotary positions (kda_rotary), at the end of this file.
+ *
  * Conventions for every function below:
  *  - Pointers are device memory owned by the caller unless marked "host".
  *  - The library never allocates or frees caller memory. It owns only its context: a
