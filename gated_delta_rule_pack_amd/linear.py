@@ -34,9 +34,9 @@ def _packed(name, t):
 
 
 def _strides(name, t, T, H, D):
-    """Element strides between tokens and between heads; dense ones stand in where the tensor has
-    a single token or head (torch leaves those arbitrary). A stride of 0 shows one row as several;
-    both 0 would mean dense to the library."""
+    """Element strides between tokens and between heads, for tensors that are not contiguous (a call's
+    fields left 0, 0 mean dense); dense ones stand in where the tensor has a single token or head (torch
+    leaves those arbitrary). One stride of 0 shows a row as several."""
     st, sh, sd = t.stride()
     if sd != 1 and D != 1:
         raise ValueError(f"{name} must have adjacent elements along its last dimension")
@@ -117,9 +117,12 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
     a.T, a.N, a.H, a.H_qk, a.K, a.V = T, N, H, H_qk, K, V
     a.scale = 1.0 / math.sqrt(K) if scale is None else scale
     a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    a.q_stride_t, a.q_stride_h = _strides("q", q, T, H_qk, K)
-    a.k_stride_t, a.k_stride_h = _strides("k", k, T, H_qk, K)
-    a.v_stride_t, a.v_stride_h = _strides("v", v, T, H, V)
+    if not q.is_contiguous():
+        a.q_stride_t, a.q_stride_h = _strides("q", q, T, H_qk, K)
+    if not k.is_contiguous():
+        a.k_stride_t, a.k_stride_h = _strides("k", k, T, H_qk, K)
+    if not v.is_contiguous():
+        a.v_stride_t, a.v_stride_h = _strides("v", v, T, H, V)
     if out is not None:
         out = _packed("out", out)
         if out.dtype != _BF16:
@@ -127,7 +130,8 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
         if out.shape != v.shape:
             raise ValueError(f"out must have v's shape {tuple(v.shape)}, got {tuple(out.shape)}")
         a.out = out.data_ptr()
-        a.out_stride_t, a.out_stride_h = _strides("out", out, T, H, V)
+        if not out.is_contiguous():
+            a.out_stride_t, a.out_stride_h = _strides("out", out, T, H, V)
     if g is not None:
         n = g.dim()
         if n == 3 and g.shape[0] == 1:
@@ -222,10 +226,10 @@ class _Call:
     __slots__ = ("device", "index", "handle", "guards")
 
     def __init__(self, q, stream):
-        device = q.device
-        if device.type != "cuda":
+        if not q.is_cuda:
             raise ValueError("inputs must be on a GPU")
-        self.device, self.index, self.guards = device, q.get_device(), ()
+        self.device = device = q.device
+        self.index, self.guards = device.index, ()
         if torch.cuda.current_device() != self.index:
             self.guards += (torch.cuda.device(self.index),)
         if stream is None:
@@ -342,8 +346,10 @@ def make_rotary_args(q, k, positions, inv_freq, out_q, out_k, *, interleaved=Fal
         raise ValueError("out_q must have q's shape and dtype")
     a.T, a.H_q, a.D, a.dtype = T, H, D, _STATE_DT[dtype]
     a.q, a.out_q = q.data_ptr(), out_q.data_ptr()
-    a.q_stride_t, a.q_stride_h = _strides("q", q, T, H, D)
-    a.out_q_stride_t, a.out_q_stride_h = _strides("out_q", out_q, T, H, D)
+    if not q.is_contiguous():
+        a.q_stride_t, a.q_stride_h = _strides("q", q, T, H, D)
+    if not out_q.is_contiguous():
+        a.out_q_stride_t, a.out_q_stride_h = _strides("out_q", out_q, T, H, D)
     if k is not None:
         k, out_k = _packed("k", k), _packed("out_k", out_k)
         Tk, Hk, Dk = k.shape
@@ -354,8 +360,10 @@ def make_rotary_args(q, k, positions, inv_freq, out_q, out_k, *, interleaved=Fal
         if out_k.dtype != dtype or out_k.shape != k.shape:
             raise ValueError("out_k must have k's shape and dtype")
         a.H_k, a.k, a.out_k = Hk, k.data_ptr(), out_k.data_ptr()
-        a.k_stride_t, a.k_stride_h = _strides("k", k, T, Hk, D)
-        a.out_k_stride_t, a.out_k_stride_h = _strides("out_k", out_k, T, Hk, D)
+        if not k.is_contiguous():
+            a.k_stride_t, a.k_stride_h = _strides("k", k, T, Hk, D)
+        if not out_k.is_contiguous():
+            a.out_k_stride_t, a.out_k_stride_h = _strides("out_k", out_k, T, Hk, D)
     _fill_rotation(a, T, D, positions, inv_freq, interleaved)
     a.factor = factor
     if inverse:
