@@ -354,7 +354,10 @@ kda_status kda_reset_stats(kda_ctx* ctx);
  * is not can reach the rows of up to 63 tokens before it in its own sequence and head.
  *
  * With rotary positions (inv_freq not null) q and k are rotated first, as kda_rotary does,
- * into the workspace, in bf16. */
+ * into the workspace, in bf16.
+ *
+ * The linear and rotary calls use of their context only its runtime and keep nothing in it, so
+ * threads may share one; kda_stats does not count them, and profiling does not time them. */
 typedef struct kda_linear_args {
   int32_t T;     /* rows of the token tensors; may be 0, at most INT32_MAX - 2^20 */
   int32_t N;     /* sequences (kda_linear_step: rows), >= 1 */
