@@ -70,6 +70,16 @@ __device__ __forceinline__ uint32_t both_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
+// a and b in two bf16 terms for a product with bf16 values: the first cut off, the second what that leaves,
+// rounded. The first leaves less than 2^-7 of the value and the second 2^-8 of that: 2^-15 in all. (Both rounded
+// leave 2^-17 and take 407 instead of 403 us for 32768 tokens at H = 32.)
+struct TwoTerms {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ TwoTerms two_terms(float a, float b) {
+  return TwoTerms{top_halves(a, b), both_bf16(a - __uint_as_float(__float_as_uint(a) & kTop), b - __uint_as_float(__float_as_uint(b) & kTop))};
+}
+
 // LDS tile of 64 rows of D bf16. A row takes 16 bytes more than its elements, and inside 16 rows
 // row r stands at place 2 (r % 8) + r / 8: the 16 rows of an operand read then start on different
 // banks, and the 8 rows of half a transposing read do not meet. Every read is a lane's own place and
@@ -300,14 +310,28 @@ struct Rows {
   }
 };
 
+// Where the fragment of P with token tile tt and sources 32 b .. 32 b + 31 stands: the causal ones alone.
+// The two that hold one tile of 16 sources take half as much, and their lanes' other half is zero.
+__device__ __forceinline__ constexpr bool half_fragment(int tt, int b) { return tt == 2 * b; }
+__device__ __forceinline__ constexpr int fragment(int tt, int b) { return 256 * tt * (tt + 1) + 1024 * b; }
+constexpr int kTermP = 5120;  // bytes of one term of P; all first terms stand before the second ones
+// Tile 0 .. 9 of P: token tile and source tile.
+__device__ __forceinline__ int tile_t(int tile) { return (0x0112223333ull >> (4 * tile)) & 15; }
+__device__ __forceinline__ int tile_s(int tile) { return (0x0102103210ull >> (4 * tile)) & 15; }
+
 template <int K, int V, bool kOut>
 struct Shared {
   alignas(16) char k[kC * kRowBytes<K>];
   alignas(16) char v[kC * kRowBytes<V>];  // then, once every wave has its columns, the outputs
   alignas(16) char q[kOut ? kC * kRowBytes<K> : 16];
-  // P fragments (token tile of 16, block of 32 sources); between a sequence's chunks and the next one's,
-  // when no wave reads P, 1 KB of each wave's for its state.
-  alignas(16) char p[1024 * (kOut && kWavesOf<V> < 6 ? 6 : kWavesOf<V>)];
+  // P (terms()), and between a sequence's chunks and the next one's, when no wave reads P, 1 KB of each
+  // wave's for its state. K = 128, V = 64 has P in the q tile, which takes a barrier more and leaves room for a
+  // third workgroup on a compute unit (64 ragged prompts at H = 24 take 354 instead of 383 us; 168 K tokens at
+  // H = 1, which leave one to a unit, 91 instead of 86).
+  static constexpr bool kTermsInQ = kOut && K == 128 && V == 64;
+  static constexpr int kStage = 1024 * kWavesOf<V>;
+  alignas(16) char p[kOut && !kTermsInQ && 2 * kTermP > kStage ? 2 * kTermP : kStage];
+  __device__ __forceinline__ char* terms() { return kTermsInQ ? q : p; }
   struct Decays {
     double G[kC];             // inclusive cumsum of g
     alignas(16) float c[kC];  // e^{G_C - G}
@@ -346,8 +370,12 @@ __device__ __forceinline__ void put_decays(D& d, float g, float scale, int lane)
   if (lane == 0) d.total = __expf((float)end);
 }
 
-// Fragment of P with token tile tt and sources 32 b .. 32 b + 31: the causal ones alone.
-__device__ __forceinline__ int fragment(int tt, int b) { return tt + (tt == 3) + b; }
+// Fragment of one term of P.
+__device__ __forceinline__ bf16x8 read_p(const char* p, int lane, int tt, int b) {
+  if (!half_fragment(tt, b)) return *reinterpret_cast<const bf16x8*>(p + fragment(tt, b) + lane * 16);
+  const u32x2 x = *reinterpret_cast<const u32x2*>(p + fragment(tt, b) + lane * 8);
+  return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], 0u, 0u});  // the tile past the diagonal is not made
+}
 
 // One chunk of `count` tokens: P and the outputs (kOut), then the state.
 // next(i) issues the loads of part i of the next chunk (0: k, 1: v, 2: q), spread over the work: issued
@@ -362,13 +390,20 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
   next(0);
   if constexpr (kOut) {
     // P^T tiles (token tile tt, source tile st <= tt), rows s = 4 g + i, column t: ten, dealt out
-    // over the waves.
+    // over the waves. Two terms each: the product with V is a bf16 MFMA with fp32 sums.
+    constexpr int kDeal = (10 + kWavesOf<V> - 1) / kWavesOf<V>;
+    u32x2 hi[kDeal], lo[kDeal];
+    const auto put_p = [&](int j) {
+      const int tile = j * kWavesOf<V> + wave, tt = tile_t(tile), st = tile_s(tile), b = st >> 1;
+      char* at = sh.terms() + fragment(tt, b) + (half_fragment(tt, b) ? lane * 8 : lane * 16 + (st & 1) * 8);
+      *reinterpret_cast<u32x2*>(at) = hi[j];
+      *reinterpret_cast<u32x2*>(at + kTermP) = lo[j];
+    };
 #pragma unroll
-    for (int j = 0; j < 10; j += kWavesOf<V>) {
-      const int tile = j + wave;
+    for (int j = 0; j < kDeal; ++j) {
+      const int tile = j * kWavesOf<V> + wave;
       if (tile >= 10) break;
-      const int tt = (0x0112223333ull >> (4 * tile)) & 15, st = (0x0102103210ull >> (4 * tile)) & 15;
-      const int t = 16 * tt + l16;
+      const int tt = tile_t(tile), st = tile_s(tile), t = 16 * tt + l16;
       f32x4 d = zero4();
 #pragma unroll
       for (int m = 0; m < KB; ++m)
@@ -381,12 +416,17 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
         asm("" : "+v"(x));  // a select, not a branch around the exponential
         d[i] = s <= t ? x : 0.f;
       }
-      // Rounded to bf16 once: the product with V is a bf16 MFMA with fp32 sums.
-      const bf16x4 b = {to_bf16(d[0]), to_bf16(d[1]), to_bf16(d[2]), to_bf16(d[3])};
-      *reinterpret_cast<bf16x4*>(sh.p + fragment(tt, st >> 1) * 1024 + lane * 16 + (st & 1) * 8) = b;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const TwoTerms w = two_terms(d[2 * i], d[2 * i + 1]);
+        hi[j][i] = w.hi, lo[j][i] = w.lo;
+      }
+      if constexpr (!Shared<K, V, kOut>::kTermsInQ) put_p(j);
     }
     next(1);
-    // Q S^T, transposed: rows v = 4 g + i, column t. The state is rounded to bf16 for it.
+    // Q S^T, transposed: rows v = 4 g + i, column t. The fp32 state goes in as two terms:
+    // with one each for it and P the outputs are off by 2.35e-3 (rel-L2), with two by the 1.66e-3 that their own
+    // rounding to bf16 makes (32768 tokens at H = 32: 378 and 405 us).
     f32x4 acc[VT][4];
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
@@ -394,14 +434,29 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
       for (int tt = 0; tt < 4; ++tt) acc[vt][tt] = zero4();
 #pragma unroll
     for (int m = 0; m < KB; ++m) {
-      bf16x8 sb[VT];
+      bf16x8 hi[VT], lo[VT];
 #pragma unroll
-      for (int vt = 0; vt < VT; ++vt) sb[vt] = pack8(walk.S[vt][2 * m], walk.S[vt][2 * m + 1]);
+      for (int vt = 0; vt < VT; ++vt) {
+        u32x4 h, l;
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const bf16x8 b = read_row<K>(sh.q, lane, 16 * tt, m);
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 x = walk.S[vt][2 * m + i / 2];
+          const TwoTerms w = two_terms(x[2 * i & 3], x[(2 * i + 1) & 3]);
+          h[i] = w.hi, l[i] = w.lo;
+        }
+        hi[vt] = __builtin_bit_cast(bf16x8, h), lo[vt] = __builtin_bit_cast(bf16x8, l);
+      }
+      // Two token tiles at a time, term by term: no product waits for the one before it.
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(sb[vt], b, acc[vt][tt]);
+      for (int tt = 0; tt < 4; tt += 2) {
+        const bf16x8 b0 = read_row<K>(sh.q, lane, 16 * tt, m), b1 = read_row<K>(sh.q, lane, 16 * tt + 16, m);
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          acc[vt][tt] = mfma(lo[vt], b0, acc[vt][tt]);
+          acc[vt][tt + 1] = mfma(lo[vt], b1, acc[vt][tt + 1]);
+          acc[vt][tt] = mfma(hi[vt], b0, acc[vt][tt]);
+          acc[vt][tt + 1] = mfma(hi[vt], b1, acc[vt][tt + 1]);
+        }
       }
     }
 #pragma unroll
@@ -415,18 +470,22 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V, false>(sh.v, lane, 32 * b, wave * VT + vt);
     next(2);
+    if constexpr (Shared<K, V, kOut>::kTermsInQ) {
+      barrier_lds();  // q
+#pragma unroll
+      for (int j = 0; j < kDeal; ++j)
+        if (j * kWavesOf<V> + wave < 10) put_p(j);
+    }
     barrier_lds();  // P
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
 #pragma unroll
       for (int b = 0; b <= tt / 2; ++b) {
-        bf16x8 pf = *reinterpret_cast<const bf16x8*>(sh.p + fragment(tt, b) * 1024 + lane * 16);
-        if (tt == 2 * b) {  // the tile past the diagonal is not made
+        const bf16x8 lo = read_p(sh.terms() + kTermP, lane, tt, b), hi = read_p(sh.terms(), lane, tt, b);
 #pragma unroll
-          for (int i = 4; i < 8; ++i) pf[i] = (__bf16)0.f;
-        }
+        for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(raw[b][vt], lo, acc[vt][tt]);
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(raw[b][vt], pf, acc[vt][tt]);
+        for (int vt = 0; vt < VT; ++vt) acc[vt][tt] = mfma(raw[b][vt], hi, acc[vt][tt]);
       }
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) {
