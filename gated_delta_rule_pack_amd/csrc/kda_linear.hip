@@ -171,6 +171,7 @@ struct Walk {
   }
   // Plain workspace planes: register order, 1 KB per tile.
   __device__ __forceinline__ void load(const float* plane, int wave, int lane) {
+    lane = local_copy(lane);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -178,6 +179,7 @@ struct Walk {
         S[vt][kt] = *reinterpret_cast<const f32x4*>(plane + (((wave * VT + vt) * KT + kt) * 64 + lane) * 4);
   }
   __device__ __forceinline__ void store(float* plane, int wave, int lane) const {
+    lane = local_copy(lane);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -377,6 +379,35 @@ __device__ __forceinline__ bf16x8 read_p(const char* p, int lane, int tt, int b)
   return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], 0u, 0u});  // the tile past the diagonal is not made
 }
 
+// Whether a wave's columns of V are finite, by their largest exponent.
+template <int VT>
+__device__ __forceinline__ bool all_finite(const bf16x8 (&raw)[2][VT]) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 top = {0, 0};
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt) {
+      const u32x4 w = __builtin_bit_cast(u32x4, raw[b][vt]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+    }
+  return __ballot(top[0] >= 0x7f80 || top[1] >= 0x7f80) == 0;
+}
+// Zeros for what is not finite in a column's tokens t0 + i and t0 + 16 + i (i < 4); first: the earliest such token.
+__device__ __forceinline__ void take_finite(bf16x8& x, int t0, int& first) {
+  u32x4 w = __builtin_bit_cast(u32x4, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t half = i & 1 ? kTop : ~kTop;
+    if ((w[i / 2] & half & 0x7f807f80u) == (half & 0x7f807f80u)) {
+      w[i / 2] &= ~half;
+      first = min(first, t0 + (i & 3) + (i & 4) * 4);
+    }
+  }
+  x = __builtin_bit_cast(bf16x8, w);
+}
+
 // One chunk of `count` tokens: P and the outputs (kOut), then the state.
 // next(i) issues the loads of part i of the next chunk (0: k, 1: v, 2: q), spread over the work: issued
 // at once they hold every wave for the 48 KB to pass.
@@ -469,6 +500,29 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) raw[b][vt] = read_col<V, false>(sh.v, lane, 32 * b, wave * VT + vt);
+    if (!all_finite<VT>(raw)) {
+      // The zeros of P would make NaN of such a value in the tokens before it too. Its channel becomes NaN from its
+      // token on and in the state; the products go on with the finite values.
+      const int lane = local_copy(lane_), g = lane >> 4, l16 = lane & 15;
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        int first = kC;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) take_finite(raw[b][vt], 32 * b + 4 * g, first);
+        first = min(first, __shfl_xor(first, 16));
+        first = min(first, __shfl_xor(first, 32));
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+          if (first < kC) walk.S[vt][kt] = zero4() + __builtin_nanf("");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t0 = __shfl(first, 4 * g + i);
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+            if (16 * tt + l16 >= t0) acc[vt][tt][i] = __builtin_nanf("");
+        }
+      }
+    }
     next(2);
     if constexpr (Shared<K, V, kOut>::kTermsInQ) {
       barrier_lds();  // q

@@ -350,8 +350,10 @@ kda_status kda_reset_stats(kda_ctx* ctx);
  * at least one row and at most 2^23 elements apart.
  * g <= 0 in use; -inf (forget everything before this token) is allowed, and anything below
  * -120 counts as -inf (e^-120 is 0 in fp32). Every exponential the kernels take is of a sum
- * of log decays over a run of tokens. q, k, v and flagged states must be finite: a row that
- * is not can reach the rows of up to 63 tokens before it in its own sequence and head.
+ * of log decays over a run of tokens. What is not finite stays causal, in its own
+ * sequence and head: a row of q takes its own output, a row of k or a log decay every output from its token
+ * on and the final state, a value of v or of a state row the same of its own channel (where an Inf may
+ * become NaN).
  *
  * With rotary positions (inv_freq not null) q and k are rotated first, as kda_rotary does,
  * into the workspace, in bf16.

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.linear_harness import HALF, TINY, Case, close, f64
+from tests.linear_harness import HALF, TINY, Case, close, f64, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,57 @@ def test_outputs_are_rounded_once(H, kw):
     out, final = case.forward(d, seg_len=64)
     torch.cuda.synchronize()
     _check_out(case, out)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("H,kw", [(2, dict()), (12, dict()), (2, dict(K=64)), (3, dict(V=64)), (3, dict(K=64, V=64)),
+                                  (2, dict(k_first=True, state_dtype="bf16"))], ids=str)
+def test_values_that_are_not_finite_reach_no_earlier_token(H, kw, bad):
+    """The form is causal: such a value takes its own channel from its own token on, and nothing else."""
+    case = Case([200, 100, 64, 1], H=H, seed=5, flags="all", decay="resets", **kw)
+    _say(f"case H={H} {kw} bad={bad}")
+    begin, end = case.cu[:-1].tolist(), case.cu[1:].tolist()
+    clean = case.device()
+    out, _ = case.forward(clean, seg_len=64)
+    # (sequence, token in it, head, channel): in every token tile and both halves of a tile's rows, in whole and
+    # short chunks, first and later ones.
+    places = [(0, 0, 0, 3), (0, 15, 0, 17), (0, 16, 1, 33), (0, 62, 1, 63), (0, 63, 0, 40), (0, 64, 1, 5), (0, 100, 1, 6),
+              (0, 199, 0, 7), (1, 31, 0, 8), (1, 32, 0, 9), (1, 99, 1, 10), (1, 33, 0, 9), (2, 47, 1, 62), (2, 48, 1, 61), (3, 0, 0, 1)]
+    d = case.device()
+    touched = torch.zeros(case.v.shape, dtype=torch.bool, device="cuda")
+    channels = torch.zeros(case.N, H, case.V, dtype=torch.bool, device="cuda")
+    for n, t, h, c in places:
+        d["v"][begin[n] + t, h, c] = bad
+        touched[begin[n] + t:end[n], h, c] = True
+        channels[n, h, c] = True
+    got, _ = case.forward(d, seg_len=64)
+    torch.cuda.synchronize()
+    assert not torch.isfinite(got[touched].float()).any()
+    assert same_bits(got[~touched], out[~touched])
+    planes, ref = (case.planes(x["store"])[case.indices.long().cuda()] for x in (d, clean))
+    if case.k_first:
+        planes, ref = planes.transpose(-1, -2), ref.transpose(-1, -2)
+    assert not torch.isfinite(planes[channels].float()).any()
+    assert same_bits(planes[~channels], ref[~channels])
+
+
+@pytest.mark.parametrize("name", ["q", "k", "g"])
+@pytest.mark.parametrize("H,V", [(2, 128), (12, 128), (2, 64)])
+def test_rows_that_are_not_finite_reach_no_earlier_token(name, H, V):
+    """A row of q takes its own output, one of k or g everything of its head from its token on."""
+    case = Case([150, 70], H=H, V=V, seed=6, flags="all")
+    clean = case.device()
+    out, _ = case.forward(clean, seg_len=64)
+    d = case.device()
+    touched = torch.zeros(case.T, H, dtype=torch.bool, device="cuda")
+    heads = torch.zeros(case.N, H, dtype=torch.bool, device="cuda")
+    for n, t, end, h in ((0, 70, 150, 0), (1, 150 + 17, 220, 1)):
+        d[name][t, h] = float("nan") if name == "g" else torch.tensor([float("inf"), float("nan")], device="cuda").repeat(64)
+        touched[t:(t + 1 if name == "q" else end), h] = True
+        heads[n, h] = name != "q"
+    got, _ = case.forward(d, seg_len=64)
+    torch.cuda.synchronize()
+    assert torch.isnan(got[touched].float()).all()
+    assert same_bits(got[~touched], out[~touched])
+    planes, ref = (case.planes(x["store"])[case.indices.long().cuda()] for x in (d, clean))
+    assert same_bits(planes[~heads], ref[~heads]) and (name == "q" or not torch.isfinite(planes[heads]).all(-1).any())
