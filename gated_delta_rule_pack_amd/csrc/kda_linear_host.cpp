@@ -80,12 +80,22 @@ int32_t seg_len_of(const kda_linear_args* a) {
   const int64_t fit = std::max<int64_t>(1, units / a->H), fill = (axis + fit - 1) / fit;
   const double per_segment = 0.06 + 0.059 * a->H * a->K * a->V / (128 * 128), per_token = 5.0 / C;
   const int64_t root = (int64_t)(std::sqrt(per_segment * (double)axis / per_token) / C + 0.5) * C;
-  int64_t len = a->T + 128 * ((int64_t)a->N - 1) <= 224 ? axis : std::max(fill, root);
-  // Between one workgroup and two for each of 256 compute units the second ones decide the time: one
-  // for each it is (65536 tokens at H = 2, 256 workgroups 74.7 us, 342: 85.5).
-  const int64_t work = (axis + len - 1) / len * a->H;
-  if (work > 264 && work < 500) len = axis * a->H / 256;
-  return (int32_t)std::min<int64_t>((std::max<int64_t>(len, 1) + C - 1) / C * C, 1 << 30);
+  const auto whole = [](int64_t n) { return (std::max<int64_t>(n, 1) + C - 1) / C * C; };
+  const auto count = [axis](int64_t l) { return (axis + l - 1) / l; };
+  int64_t len = whole(a->T + 128 * ((int64_t)a->N - 1) <= 224 ? axis : std::max(fill, root));
+  // Workgroups for more than one on each of 256 compute units, and for two at most: the units with two decide the
+  // time. As many whole segments as leave one to a unit are taken instead where that is an eighth less by these
+  // costs (3 us for each 64 tokens of a single segment, which has no map). 65536 tokens at H = 2: 342 workgroups 97
+  // us, 256: 85; 16384 at H = 192: 384 in two segments 1183 us, 192 in one 1015; at H = 256: 1397 and 1196. Where the
+  // two ways cost as much, two to a unit run faster, one working while the other waits: 16384 at H = 48: 480
+  // workgroups 349 us, 240: 371; at H = 160: 480 in three segments 966 us, 160 in one 1004.
+  const int64_t n = count(len), most = std::max<int64_t>(1, 256 / a->H), alone = whole((axis + most - 1) / most);
+  if (n * a->H > 264 && n * a->H <= 512 && count(alone) < n) {
+    const double two = 2 * (double)len * per_token + (double)n * per_segment;
+    const double one = (double)alone * (count(alone) == 1 ? 0.6 : 1.0) * per_token + (double)count(alone) * per_segment;
+    if (one < 0.875 * two) len = alone;
+  }
+  return (int32_t)std::min<int64_t>(len, 1 << 30);
 }
 int32_t segments_of(const kda_linear_args* a) {
   const int64_t L = seg_len_of(a);
