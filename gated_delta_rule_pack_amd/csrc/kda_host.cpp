@@ -655,7 +655,7 @@ const char* kda_status_str(kda_status s) {
     case KDA_ERR_UNSUPPORTED: return "unsupported shape, dtype or device";
     case KDA_ERR_STATE_MODE: return "conflicting state arguments (dense vs paged)";
     case KDA_ERR_STRIDE: return "state_cache_stride0 smaller than one H*V*K plane";
-    case KDA_ERR_ALIAS: return "out overlaps v";
+    case KDA_ERR_ALIAS: return "an output overlaps another buffer of the call";
     case KDA_ERR_WORKSPACE: return "workspace missing or too small";
     case KDA_ERR_CAPTURE_MISS: return "metadata cache miss during stream capture";
     case KDA_ERR_HIP: return "HIP runtime error";

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "kda.h"
 #include "kda_linear.h"
@@ -48,6 +49,49 @@ bool distinct_rows(Strides s, int64_t T, int64_t H, int64_t D) {
   const int64_t heads = (H - 1) * s.h + D, tokens = (T - 1) * s.t + D;
   const bool h_ok = H == 1 || s.h >= D, t_ok = T == 1 || s.t >= D;
   return h_ok && t_ok && (T == 1 || H == 1 || s.t >= heads || s.h >= tokens);
+}
+
+// T tokens of H rows of D elements of es bytes at `at`.
+struct Rows {
+  const void* at;
+  int64_t T, H, D;
+  Strides s;
+  size_t es;
+};
+bool overlap(const Rows& a, const Rows& b) {
+  return overlap(range_of(a.at, a.T, a.H, a.D, a.s.t, a.s.h, a.es), range_of(b.at, b.T, b.H, b.D, b.s.t, b.s.h, b.es));
+}
+bool same_rows(const Rows& a, const Rows& b) {
+  return a.at == b.at && a.H == b.H && (a.T == 1 || a.s.t == b.s.t) && (a.H == 1 || a.s.h == b.s.h);
+}
+// Whether no element belongs to both (of equal T, D and es), where their byte ranges may interleave: in the rows of
+// one projection, or of one buffer whose heads hold both in turn. Different token strides are not looked into.
+bool disjoint(const Rows& a, const Rows& b) {
+  if (!overlap(a, b)) return true;
+  if (a.T > 1 && (a.s.t != b.s.t || a.s.t < 1)) return false;
+  const auto mod = [](int64_t x, int64_t m) { return (x % m + m) % m; };
+  const int64_t D = a.D, gap = ((intptr_t)b.at - (intptr_t)a.at) / (intptr_t)a.es;
+  const int64_t wa = (a.H - 1) * a.s.h + D, wb = (b.H - 1) * b.s.h + D;
+  // All heads of one beside those of the other.
+  if (a.T > 1 && mod(gap, a.s.t) >= wa && mod(gap, a.s.t) + wb <= a.s.t) return true;
+  // A head of one beside a head of the other.
+  const int64_t h = a.H > 1 ? a.s.h : b.s.h;
+  if ((a.H == 1 || b.H == 1 || a.s.h == b.s.h) && h > 0 && (a.T == 1 || a.s.t % h == 0) && mod(gap, h) >= D && mod(gap, h) + D <= h)
+    return true;
+  // Each pair of heads: the tokens that come nearest.
+  if (a.H * b.H > 1024) return false;
+  for (int64_t i = 0; i < a.H; ++i)
+    for (int64_t j = 0; j < b.H; ++j) {
+      const int64_t off = gap + j * b.s.h - i * a.s.h;
+      int64_t far = off;
+      if (a.T > 1) {
+        const int64_t k = std::min(std::max(-off / a.s.t, 1 - a.T), a.T - 1);
+        for (int64_t t : {k - 1, k, k + 1})
+          if (std::abs(t) < a.T && std::abs(off + t * a.s.t) < std::abs(far)) far = off + t * a.s.t;
+      }
+      if (std::abs(far) < D) return false;
+    }
+  return true;
 }
 
 int32_t heads_qk(const kda_linear_args* a) { return a->H_qk > 0 ? a->H_qk : a->H; }
@@ -347,28 +391,20 @@ kda_status kda_rotary_validate(const kda_rotary_args* a) {
   const Strides si[2] = {strides_of(a->q_stride_t, a->q_stride_h, a->H_q, a->D), strides_of(a->k_stride_t, a->k_stride_h, a->H_k, a->D)};
   const Strides so[2] = {strides_of(a->out_q_stride_t, a->out_q_stride_h, a->H_q, a->D),
                          strides_of(a->out_k_stride_t, a->out_k_stride_h, a->H_k, a->D)};
-  Range ri[2], ro[2];
+  Rows r[4];  // q, k, and their results
+  int n = 0;
   for (int i = 0; i < 2; ++i) {
     if (H[i] == 0 || a->T == 0) continue;
     if (!in[i] || !out[i] || !aligned(in[i], es) || !aligned(out[i], es)) return KDA_ERR_INVALID_ARG;
     if (!stride_ok(si[i]) || !stride_ok(so[i])) return KDA_ERR_INVALID_ARG;
     if (!distinct_rows(so[i], a->T, H[i], a->D)) return KDA_ERR_ALIAS;
-    ri[i] = range_of(in[i], a->T, H[i], a->D, si[i].t, si[i].h, es);
-    ro[i] = range_of(out[i], a->T, H[i], a->D, so[i].t, so[i].h, es);
+    r[n++] = Rows{in[i], a->T, H[i], a->D, si[i], es};
+    r[n++] = Rows{out[i], a->T, H[i], a->D, so[i], es};
   }
-  for (int i = 0; i < 2; ++i) {
-    const bool in_place = in[i] == out[i] && si[i].t == so[i].t && si[i].h == so[i].h;
-    if (!in_place && overlap(ro[i], ri[i])) return KDA_ERR_ALIAS;
-  }
-  // q's result over k, or k's over q: the two may lie in the rows of one projection (in place),
-  // where their byte ranges interleave without a common element.
-  const auto beside = [&](const Strides& x, const Strides& y) {
-    const int64_t gap = ((intptr_t)a->k - (intptr_t)a->q) / (intptr_t)es;
-    const int64_t wq = (a->H_q - 1) * si[0].h + a->D, wk = (a->H_k - 1) * si[1].h + a->D;
-    return x.t == y.t && (gap >= 0 ? gap >= wq && gap + wk <= x.t : -gap >= wk && -gap + wq <= x.t);
-  };
-  const bool both_in_place = a->q == a->out_q && a->k == a->out_k && beside(si[0], si[1]);
-  if (!both_in_place && (overlap(ro[0], ri[1]) || overlap(ro[1], ri[0]) || overlap(ro[0], ro[1]))) return KDA_ERR_ALIAS;
+  // A result may take its input's place, and share no element with anything else.
+  for (int o = 1; o < n; o += 2)
+    for (int x = 0; x < n; ++x)
+      if (x != o && !(x == o - 1 && same_rows(r[x], r[o])) && !disjoint(r[o], r[x])) return KDA_ERR_ALIAS;
   return KDA_OK;
 }
 

@@ -381,7 +381,7 @@ def rotary(q, k, positions, inv_freq, *, interleaved=False, factor=1.0, inverse=
     ``(i, i + r/2)``, or ``(2i, 2i + 1)`` when ``interleaved``; channels from r on pass through.
     ``factor`` scales the rotated channels. ``inverse`` applies the transposed rotation: the gradient
     with respect to q and k, given the results' gradients. ``out_q`` / ``out_k`` may be q / k
-    themselves (in place). Returns ``(out_q, out_k)``."""
+    themselves (in place) or share no element with either. Returns ``(out_q, out_k)``."""
     with _Call(q, stream) as call:
         _on(call.index, "k positions inv_freq out_q out_k", k, positions, inv_freq, out_q, out_k)
         if out_q is None:

@@ -56,7 +56,7 @@ typedef enum kda_status {
                                H = 1 and a sequence of more than about 15.5 M tokens) */
   KDA_ERR_STATE_MODE = 3,   /* dense and paged state both given, or final_state with a pool */
   KDA_ERR_STRIDE = 4,       /* state_cache_stride0 < H*V*K */
-  KDA_ERR_ALIAS = 5,        /* the byte ranges of out and v overlap */
+  KDA_ERR_ALIAS = 5,        /* an output overlaps another buffer of the call (kda_chunk_fwd: out and v) */
   KDA_ERR_WORKSPACE = 6,    /* workspace null or smaller than kda_chunk_fwd_workspace_bytes() */
   KDA_ERR_CAPTURE_MISS = 7, /* metadata-cache miss while the stream is being captured */
   KDA_ERR_HIP = 8,          /* a HIP runtime call or a kernel launch failed */
@@ -453,8 +453,9 @@ typedef struct kda_rotary_args {
   kda_dtype dtype;   /* of q, k and the results: KDA_BF16, KDA_F16 or KDA_F32 */
   const void* q;     /* [T, H_q, D], element strides below; the D elements adjacent */
   const void* k;     /* [T, H_k, D] or null */
-  void* out_q;       /* as q; the same memory with the same strides (in place), or disjoint */
-  void* out_k;
+  void* out_q;       /* as q; the same memory with the same strides (in place), or no element in common */
+  void* out_k;       /* with it, nor with the other three. Byte ranges may interleave where the token */
+                     /* strides are equal: columns of one projection's rows, heads of q and k in turn */
   int64_t q_stride_t, q_stride_h; /* each pair: 0, 0 means dense */
   int64_t k_stride_t, k_stride_h;
   int64_t out_q_stride_t, out_q_stride_h;

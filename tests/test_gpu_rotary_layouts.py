@@ -1,0 +1,56 @@
+"""Rotary positions in memory whose rows interleave: results beside each other or beside their inputs, one in place."""
+import pytest
+import torch
+
+import gated_delta_rule_pack_amd as kda
+from tests.linear_harness import DT, same_bits
+
+pytestmark = pytest.mark.gpu
+
+T = 37
+
+
+def _call(D, dt):
+    gen = torch.Generator("cpu").manual_seed(D)
+    rows = torch.randn(T, 8, D, generator=gen).to(DT[dt]).cuda()  # 4 heads of q, 2 of k, 2 of v
+    pos = (torch.arange(T) * 7 + 3).cuda()
+    inv, _ = kda.rotary_frequencies(D // 4 * 2, device="cuda")
+    want = kda.rotary(rows[:, :4].contiguous(), rows[:, 4:6].contiguous(), pos, inv)
+    torch.cuda.synchronize()
+    return rows, pos, inv, want
+
+
+@pytest.mark.parametrize("D,dt", [(128, "bf16"), (64, "f32"), (66, "f16")])
+@pytest.mark.parametrize("layout", ["columns", "beside", "q in place", "k in place", "in turn"])
+def test_rows_that_interleave(layout, D, dt):
+    print(f"case {layout} D={D} {dt}", flush=True)
+    rows, pos, inv, want = _call(D, dt)
+    before = rows.clone()
+    q, k, kept = rows[:, :4], rows[:, 4:6], slice(6, 8)
+    if layout == "columns":
+        both = torch.full((T, 7, D), 3.0, dtype=rows.dtype, device="cuda")
+        out = both[:, :4], both[:, 4:6]
+        rest = [(both[:, 6], torch.full_like(both[:, 6], 3.0)), (rows, before)]
+    elif layout == "beside":
+        wide = torch.full((T, 16, D), 3.0, dtype=rows.dtype, device="cuda")
+        wide[:, :8] = rows
+        q, k, out = wide[:, :4], wide[:, 4:6], (wide[:, 8:12], wide[:, 14:16])
+        rest = [(wide[:, :8], before), (wide[:, 12:14], torch.full_like(wide[:, 12:14], 3.0))]
+    elif layout == "q in place":
+        out = q, torch.empty_like(k, memory_format=torch.contiguous_format)
+        rest = [(rows[:, 4:], before[:, 4:])]
+    elif layout == "k in place":
+        out = torch.empty_like(q, memory_format=torch.contiguous_format), k
+        rest = [(rows[:, :4], before[:, :4]), (rows[:, 6:], before[:, 6:])]
+    else:  # heads of q, k and v in turn
+        turn = torch.full((T, 4, 3, D), 3.0, dtype=rows.dtype, device="cuda")
+        turn[:, :, 0], turn[:, :2, 1] = rows[:, :4], rows[:, 4:6]
+        q, k = turn[:, :, 0], turn[:, :2, 1]
+        out = q, k
+        rest = [(turn[:, 2:, 1], torch.full_like(turn[:, 2:, 1], 3.0)), (turn[:, :, 2], torch.full_like(turn[:, :, 2], 3.0))]
+    got = kda.rotary(q, k, pos, inv, out_q=out[0], out_k=out[1])
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert same_bits(a, b)
+    for a, b in rest:
+        assert same_bits(a, b)
