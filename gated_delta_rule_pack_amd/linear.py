@@ -43,7 +43,7 @@ def _strides(name, t, T, H, D):
     if H == 1:
         sh = D
     if T <= 1:
-        st = H * (sh or D)
+        st = H * D
     if st == 0 and sh == 0:
         raise ValueError(f"{name} must not be broadcast over both tokens and heads")
     return st, sh

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import gated_delta_rule_pack_amd as kda
 from tests.linear_harness import HALF, TINY, Case, close, f64, same_bits
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +99,21 @@ def test_rows_that_are_not_finite_reach_no_earlier_token(name, H, V):
     assert same_bits(got[~touched], out[~touched])
     planes, ref = (case.planes(x["store"])[case.indices.long().cuda()] for x in (d, clean))
     assert same_bits(planes[~heads], ref[~heads]) and (name == "q" or not torch.isfinite(planes[heads]).all(-1).any())
+
+
+@pytest.mark.parametrize("entry", ["prompt", "step"])
+def test_one_token_of_heads_that_lie_far_apart(entry):
+    case = Case([1], H=32, seed=7, flags="all")
+    d, e = case.device(), case.device()
+    for n in "qkv":
+        rows = torch.zeros(32, 5000, 128, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+        rows[4321] = e[n][0]
+        e[n] = rows[4321:4322]
+    outs = []
+    for x in (d, e):
+        if entry == "prompt":
+            outs.append(case.forward(x)[0])
+        else:
+            outs.append(kda.linear_step(x["q"], x["k"], x["v"], x["g"], state_cache=x["cache"], state_indices=x["indices"]))
+    torch.cuda.synchronize()
+    assert same_bits(*outs) and same_bits(d["store"], e["store"])
