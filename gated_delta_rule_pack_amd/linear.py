@@ -3,7 +3,8 @@
 ``linear_fwd`` (prompts) and ``linear_step`` (single tokens) serve beside ``chunk_fwd`` with the
 same packed bounds, state pool and slots; ``rotary`` turns q and k by their positions. All three
 marshal tensors into the C ABI of ``libkda.so`` and enqueue its kernels on the current torch
-stream; nothing synchronises and no metadata is built, so every call can be captured.
+stream; nothing synchronises and no metadata is built, so every call can be captured. They record no
+gradient, and refuse inputs that require one while gradients are enabled.
 """
 from __future__ import annotations
 
@@ -64,6 +65,15 @@ def _vector(name, t, n, dtypes):
     return t.data_ptr()
 
 
+def _without_gradient(advice, *tensors):
+    """The calls record nothing for autograd: rather than return results cut off from inputs that ask for a gradient,
+    they refuse."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("an input requires a gradient, and the call records none: use torch.no_grad() or detach()" + advice)
+
+
 _I32 = (torch.int32,)
 _INTS = (torch.int32, torch.int64)
 _BOOLS = (torch.bool, torch.uint8)
@@ -93,6 +103,7 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
                      seg_len=0) -> "_lib.LinearArgs":
     """Fill a ``kda_linear_args`` from tensors (no allocation), checking everything the C side
     cannot see: dtypes, shapes, strides and element counts."""
+    _without_gradient("", q, k, v, g, initial_state, state_cache, out)
     q, k, v = _packed("q", q), _packed("k", k), _packed("v", v)
     T, H_qk, K = q.shape
     Tv, H, V = v.shape
@@ -332,6 +343,7 @@ def linear_step(q, k, v, g, *, state_cache, state_indices=None, has_initial_stat
 
 def make_rotary_args(q, k, positions, inv_freq, out_q, out_k, *, interleaved=False, factor=1.0, inverse=False) -> "_lib.RotaryArgs":
     """Fill a ``kda_rotary_args`` from tensors (no allocation), checking what the C side cannot see."""
+    _without_gradient(" (the gradient is the call with inverse=True)", q, k, out_q, out_k)
     q, out_q = _packed("q", q), _packed("out_q", out_q)
     T, H, D = q.shape
     dtype = q.dtype
@@ -380,7 +392,8 @@ def rotary(q, k, positions, inv_freq, *, interleaved=False, factor=1.0, inverse=
     (radians per position, :func:`rotary_frequencies`); with r twice its length, pair i is channels
     ``(i, i + r/2)``, or ``(2i, 2i + 1)`` when ``interleaved``; channels from r on pass through.
     ``factor`` scales the rotated channels. ``inverse`` applies the transposed rotation: the gradient
-    with respect to q and k, given the results' gradients. ``out_q`` / ``out_k`` may be q / k
+    with respect to q and k, given the results' gradients (the call itself records none, so a training program makes both
+    calls under ``torch.no_grad()``, or in the two halves of an autograd function). ``out_q`` / ``out_k`` may be q / k
     themselves (in place) or share no element with either. Returns ``(out_q, out_k)``."""
     with _Call(q, stream) as call:
         _on(call.index, "k positions inv_freq out_q out_k", k, positions, inv_freq, out_q, out_k)
