@@ -116,6 +116,8 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
     if q.dtype != _BF16 or k.dtype != _BF16 or v.dtype != _BF16:
         raise TypeError(f"q, k and v must be bf16, got {q.dtype}, {k.dtype}, {v.dtype}")
     a = _lib.LinearArgs()
+    if N is None:
+        N = T
     if cu_seqlens is not None:
         N = cu_seqlens.numel() - 1
         if N < 1:
@@ -297,7 +299,7 @@ def linear_fwd(q, k, v, g, cu_seqlens, *, cu_seqlens_cpu=None, scale=None, initi
             out = _like(v)
         final_state = None
         if output_final_state and state_cache is None:
-            H, V, K = v.shape[-2], v.shape[-1], q.shape[-1]
+            H, V, K = *_packed("v", v).shape[1:], _packed("q", q).shape[2]
             dt = initial_state.dtype if initial_state is not None else torch.float32
             planes = (K, V) if state_k_first else (V, K)
             final_state = torch.empty((cu_seqlens.numel() - 1, H, *planes), dtype=dt, device=q.device)
@@ -333,7 +335,7 @@ def linear_step(q, k, v, g, *, state_cache, state_indices=None, has_initial_stat
             k, v, g, state_cache, state_indices, has_initial_state, out, positions, inv_freq)
         if out is None:
             out = _like(v)
-        a = make_linear_args(q, k, v, g, N=q.shape[-3], scale=scale, state_cache=state_cache,
+        a = make_linear_args(q, k, v, g, scale=scale, state_cache=state_cache,
                              state_indices=state_indices, has_initial_state=has_initial_state, out=out,
                              state_k_first=state_k_first, positions=positions, inv_freq=inv_freq,
                              interleaved=interleaved, rotary_factor=rotary_factor)

@@ -264,3 +264,16 @@ def test_slow_decay_over_a_long_prompt(seg_len):
     torch.cuda.synchronize()
     check(case, out, d, final)
     _check_out(case, out)
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_tensors_of_too_few_dimensions_are_refused(name):
+    case = Case([3, 4], H=2, seed=11, state="dense")
+    d = case.device()
+    d[name] = d[name].reshape(-1)
+    with pytest.raises(ValueError, match=name):
+        case.forward(d)
+    with pytest.raises(ValueError, match=name):
+        kda.linear_step(d["q"], d["k"], d["v"], d["g"], state_cache=torch.zeros(7, 2, 128, 128, device="cuda"))
+    with pytest.raises(ValueError):
+        kda.rotary(d["q"].reshape(-1), None, torch.arange(7, device="cuda"), torch.ones(4, dtype=torch.float64, device="cuda"))
