@@ -440,9 +440,10 @@ kda_status kda_linear_step(kda_ctx* ctx, const kda_linear_args* args, void* stre
 kda_status kda_linear_step_validate(const kda_linear_args* args);
 
 /* ---- Rotary positions. -------------------------------------------------------------
- * With theta = positions[t] * inv_freq[i] (64-bit) and c = factor cos theta,
- * s = factor sin theta, the pair (a, b) of channels (i, i + rot_dim / 2), or (2i, 2i + 1)
- * when interleaved, becomes (a c - b s, a s + b c) for i < rot_dim / 2, in fp32, rounded once.
+ * With theta = positions[t] * inv_freq[i] and c = factor cos theta,
+ * s = factor sin theta (all in 64 bits, c and s rounded to fp32), the pair (a, b) of
+ * channels (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved, becomes
+ * (a c - b s, a s + b c) for i < rot_dim / 2, in fp32, rounded once.
  * Channels from rot_dim on pass through. inverse negates s: the transposed rotation, which is
  * the gradient. Scaled contexts are a matter of inv_freq and factor. */
 typedef struct kda_rotary_args {

@@ -85,3 +85,26 @@ def test_gradient_through_an_autograd_function(interleaved):
     (y * w.double()).sum().backward()
     # Two products and a sum of terms no larger than w's, functions within 2 2^-24 of 1, an angle within pi 2^-24.
     assert (leaf.grad.double() - x.grad).abs().max() <= 12 * 2.0 ** -24 * 2 * w.abs().max()
+
+
+@pytest.mark.parametrize("interleaved,inverse,D,rot", [(True, True, 64, 64), (False, False, 64, 64), (False, True, 66, 62)])
+def test_fp32_results_lose_nothing_to_their_angles(interleaved, inverse, D, rot):
+    """cos and sin are rounded to fp32 once, and then two products and their sum are: 2 2^-24 of the terms' sizes, and
+    2^-24 of the result. Against 64 bits, at positions up to 2^20."""
+    gen = torch.Generator("cpu").manual_seed(D + rot)
+    x = torch.randn(3000, 4, D, generator=gen).cuda()
+    pos = torch.randint(0, 1 << 20, (3000,), generator=gen).cuda()
+    inv, _ = kda.rotary_frequencies(rot, device="cuda")
+    factor = 1.25
+    got, _ = kda.rotary(x, None, pos, inv, interleaved=interleaved, inverse=inverse, factor=factor)
+    torch.cuda.synchronize()
+    angle = (pos.double()[:, None] * inv)[:, None] * (-1 if inverse else 1)
+    c, s = factor * angle.cos(), factor * angle.sin()
+    a, b = (x[..., 0:rot:2], x[..., 1:rot:2]) if interleaved else (x[..., :rot // 2], x[..., rot // 2:rot])
+    ya, yb = (got[..., 0:rot:2], got[..., 1:rot:2]) if interleaved else (got[..., :rot // 2], got[..., rot // 2:rot])
+    a, b = a.double(), b.double()
+    for y, u, v in ((ya, a * c, -b * s), (yb, a * s, b * c)):
+        room = 2.0 ** -24 * (2 * (u.abs() + v.abs()) + (u + v).abs()) * 1.001 + 1e-14
+        share = ((y.double() - (u + v)).abs() / room).max().item()
+        print(f"  worst element at {share:.2f} of its bound", flush=True)
+        assert share <= 1.0
