@@ -57,7 +57,8 @@ struct LinearPlan {
                     // zero; after the combine the true state. Register order of the walk.
   float* initials;  // as maps: copy of the initial state of a sequence that
                     // starts in segment s and crosses its end
-  float* decays;    // [n_seg - 1][H]: e^{sum of g} over the crossing sequence's part of s
+  float* decays;    // [n_seg - 1][H]: e^{sum of g} over the crossing sequence's part of s, as the fp32
+                    // product of its chunks' factors
   int32_t* spans;   // [n_seg - 1]: 0 nothing crosses the end of s, 1 a sequence that starts in
                     // s, 2 one that came from before
   RotaryPlan rot;   // step: rotation in the kernel

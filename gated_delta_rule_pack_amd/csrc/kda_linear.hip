@@ -7,9 +7,11 @@
 //   O = P V + diag(scale e^G) Q S0^T
 //   S = e^{G_C} S0 + (diag(e^{G_C - G}) V)^T K
 //
-// Every factor is the exponential of a sum of log decays over a run of tokens, taken of the
-// difference of 64-bit prefix sums: nothing is divided, so no decay is too steep, and the
-// factors keep fp32 accuracy however long the run is.
+// Every factor inside a chunk is the exponential of a sum of log decays over a run of its tokens,
+// taken of the difference of 64-bit prefix sums: nothing is divided, so no decay is too steep. From
+// chunk to chunk the state is an fp32 recurrence: a chunk's product with e^{G_C}, that factor's own
+// rounding and the sum leave at most 3 2^-24 of its terms, which add up where the decay is slow (40000 tokens at
+// g = -1e-5 in one segment, terms of one sign: 1.1e-5 rel-L2, in the policy's segments 2e-6).
 //
 // Split. The tokens of all sequences lie on one axis (LinearPlan) that is cut into equal
 // segments; a workgroup walks one segment of one value head. With more than one segment,
@@ -27,11 +29,12 @@
 // nor P is ever transposed.
 //
 // What bounds it. A long prompt reads k and v twice (map and output), q once, and writes the outputs:
-// 1 x 32768 tokens at H = 32, fp32 state, move 1.6 GB in 380 us (map 122, combine 10, output 237),
-// 4.2 TB/s; the output walk without its arithmetic takes 237 us, without its loads 160, so memory
-// bounds both walks. 128 ragged prompts (131 K tokens at H = 12, bf16 pool) take 453 us (map 58, output 378). A
-// workgroup alone on a compute unit takes 3 us for a chunk, 2 us in the map walk, by the length of
-// its chain of LDS reads, products and three barriers: 1 x 4096 at H = 12 takes 38 us that way.
+// 1 x 32768 tokens at H = 32, fp32 state, move 1.7 GB in 410 us (map 121, combine 10, output 253),
+// 4.1 TB/s. The map walk is bound by memory. The output walk is by both: with one term each for P and the state it took
+// 237 us, as long as without any arithmetic, and their second terms, for which it can not wait less, add 16. 128 ragged
+// prompts (131 K tokens at H = 12, bf16 pool) take 475 us (map 57, output 395). A workgroup alone on a compute
+// unit takes 3 us for a chunk, 2 us in the map walk, by the length of its chain of LDS reads, products and three
+// barriers: 1 x 4096 at H = 12 takes 41 us that way.
 #include <hip/hip_runtime.h>
 
 #include "kda_device.h"
@@ -82,8 +85,11 @@ __device__ __forceinline__ TwoTerms two_terms(float a, float b) {
 
 // LDS tile of 64 rows of D bf16. A row takes 16 bytes more than its elements, and inside 16 rows
 // row r stands at place 2 (r % 8) + r / 8: the 16 rows of an operand read then start on different
-// banks, and the 8 rows of half a transposing read do not meet. Every read is a lane's own place and
-// a constant offset, and takes 9 cycles a wave (a transposing read moves half as much in them).
+// banks, and the 8 rows of half a plain transposing read do not meet. Every read is a lane's own place and
+// a constant offset, and these take 9 cycles a wave (a transposing read moves half as much in them). The
+// spread reads of k do meet: a lane's 8 bytes lie 16 from the next lane's, so rows r and r + 1, 8 banks apart,
+// share every other pair of banks, two lanes to each. SQ_LDS_BANK_CONFLICT is 34 % of SQ_LDS_IDX_ACTIVE in the map walk
+// and 37 % in the output walk of 32768 tokens at H = 32.
 template <int D>
 constexpr int kRowBytes = 2 * D + 16;
 template <int D>
@@ -290,8 +296,8 @@ struct Rows {
       w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRows * (int)stride * 2, 0, 0));
   }
   // Rows of a tile to memory, `count` of them, whole rows to a wave (parts of rows
-  // leave their merging to L2: 32768 tokens at H = 32 take 405 us so, 379 here) and past the caches, which
-  // have no use for them (385 us without the hint). A thread reads the bytes that its own put writes
+  // leave their merging to L2: 32768 tokens at H = 32 took 405 us so when this way took 379) and past the caches,
+  // which have no use for them (385 us without the hint then). A thread reads the bytes that its own put writes
   // next, so no barrier stands between.
   static __device__ __forceinline__ void store(const char* tile, __bf16* base, int64_t stride, int64_t first, int count, int tid) {
     const __amdgpu_buffer_rsrc_t r = rows_buffer<D>(base, first, stride, count);
@@ -557,8 +563,8 @@ __device__ __forceinline__ void chunk(const LinearPlan& p, Shared<K, V, kOut>& s
   }
   // State. The decayed values x (fp32) go in as bf16 terms against the stored keys, which are bf16.
   // Three terms of 8 bits each, cut off rather than rounded, are x exactly: the state keeps fp32
-  // accuracy. Two rounded terms leave 3e-6 of x, which serves where the state is stored in 16 bits or
-  // not at all.
+  // accuracy. Two rounded terms leave 2^-17 of x (8e-6) at most, which serves where the state is stored in 16
+  // bits (fp16: 2^-12 of it) or, without one, goes into outputs alone.
   const float total = dec.total;
 #pragma unroll
   for (int vt = 0; vt < VT; ++vt)

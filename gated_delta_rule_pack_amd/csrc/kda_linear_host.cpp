@@ -111,12 +111,12 @@ int64_t axis_of(const kda_linear_args* a) {
 // output, one workgroup on a compute unit); every segment costs a step of the combine's chain (0.06 us)
 // and, for each head, a state that is written, chained and read back (0.059 us at K = V = 128). The sum
 // is least at a length that grows with the root of the tokens: measured best at H = 12 for 1024 tokens
-// 128, 4096 tokens 192 (41.0 us; 128: 47.2, 384: 47.8), 8192 tokens 384; at H = 32 for 1536 tokens 192,
-// 6144 tokens 384; at H = 1 for 168 K tokens (V = 64) 384 to 768 (91 us; 256: 108). Work for more
-// workgroups than the chip holds at once (two of 128 state rows on a compute unit, three of 64) takes
-// as many: 32768 tokens at H = 32, 2048 (399 us; 1024: 425). Little work takes one segment and one
-// kernel: 128 tokens 12.6 us, 16.4 in two segments; 192 tokens 16.1 and 16.8, 256 tokens 19.5 and 17.0;
-// two sequences of 10 tokens 15.0 and 15.2, three 20.8 and 15.0.
+// 128 (24.6 us; 64: 28.4, 192: 27.8), 4096 tokens 192 (40.9 us; 128: 48.8, 384: 50.5), 8192 tokens 384; at H = 32
+// for 1536 tokens 192, 6144 tokens 384; at H = 1 for 168 K tokens (V = 64) 384 to 768 (94 us; 256: 110). Work for
+// more workgroups than the chip holds at once (two of 128 state rows on a compute unit, three of 64) takes
+// as many: 32768 tokens at H = 32, 2048 (415 us; 1024: 436). Little work takes one segment and one
+// kernel: 128 tokens 12.6 us, 15.0 in two segments; 192 tokens 16.5 and 18.9, 256 tokens 20.4 and 20.1;
+// two sequences of 10 tokens 15.1 and 14.1, three 20.9 and 14.3. (Replays of a captured call.)
 int32_t seg_len_of(const kda_linear_args* a) {
   if (a->seg_len > 0) return a->seg_len;
   constexpr int64_t C = kda::kLinChunk;
@@ -329,8 +329,8 @@ kda_status kda_linear_fwd(kda_ctx* ctx, const kda_linear_args* a, void* ws, size
   p.seg_len = seg_len_of(a);
   p.head_cost = head_cost_of(a);
   p.n_seg = segments_of(a);
-  // Slices of 64 state rows where they still get a compute unit each: 37 tokens at H = 12 take 8.0
-  // instead of 10.0 us; 4096 tokens (252 units) would take 45.8 instead of 43.2.
+  // Slices of 64 state rows where they still get a compute unit each: 37 tokens at H = 12 take 8.7
+  // instead of 9.8 us; 4096 tokens (264 units) would take 46.8 instead of 43.0.
   p.slices = a->V == 128 && (int64_t)p.n_seg * a->H <= 128 ? 2 : 1;
   p.maps = reinterpret_cast<float*>(base + w.maps);
   p.initials = reinterpret_cast<float*>(base + w.initials);

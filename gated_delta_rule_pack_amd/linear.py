@@ -289,7 +289,8 @@ def linear_fwd(q, k, v, g, cu_seqlens, *, cu_seqlens_cpu=None, scale=None, initi
     for ``[K, V]`` planes.
 
     With ``positions`` (``[T]``) and ``inv_freq`` (fp64, see :func:`rotary_frequencies`) q and k are
-    rotated first, in bf16, by the kernel of :func:`rotary`. ``seg_len`` overrides the segment
+    rotated first, by the kernel of :func:`rotary` and, like its results, rounded to bf16
+    (:func:`linear_step` keeps fp32). ``seg_len`` overrides the segment
     length policy (a multiple of 64). Returns ``(out, final_state)``, final_state None unless dense
     and asked for."""
     with _Call(q, stream) as call:

@@ -355,8 +355,9 @@ kda_status kda_reset_stats(kda_ctx* ctx);
  * on and the final state, a value of v or of a state row the same of its own channel (where an Inf may
  * become NaN).
  *
- * With rotary positions (inv_freq not null) q and k are rotated first, as kda_rotary does,
- * into the workspace, in bf16.
+ * With rotary positions (inv_freq not null) kda_linear_fwd rotates q and k first, as kda_rotary
+ * does, into the workspace, in bf16: the results are those of the call on rotated rows, and a state
+ * holds keys rounded once more (1.6e-3 rel-L2). kda_linear_step rotates in fp32.
  *
  * The linear and rotary calls use of their context only its runtime and keep nothing in it, so
  * threads may share one; kda_stats does not count them, and profiling does not time them. */
