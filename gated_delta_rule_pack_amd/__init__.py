@@ -3,7 +3,9 @@
 ``chunk_fwd`` marshals torch tensors into the C ABI of ``libkda.so`` (``include/kda.h``)
 and enqueues the HIP kernels on the current torch stream. torch provides device memory
 and streams only; the computation is entirely in the library. ``linear_fwd``, ``linear_step`` and
-``rotary`` (``linear.py``) do the same for linear attention with a decay per head and rotary positions.
+``rotary`` (``linear.py``) do the same for linear attention with a decay per head and rotary positions,
+``gated_delta_fwd`` and ``gated_delta_step`` (``delta.py``) for the gated delta rule with a decay per head, ``qk_norm``
+and ``qk_norm_backward`` (``norm.py``) for norms of q and k with the rotation in the same pass.
 """
 from __future__ import annotations
 
@@ -15,18 +17,24 @@ from typing import Optional
 from . import _lib
 
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "Context", "get_context", "workspace_bytes", "KDAError",
-           "linear_fwd", "linear_step", "rotary", "rotary_frequencies"]
+           "linear_fwd", "linear_step", "rotary", "rotary_frequencies",
+           "gated_delta_fwd", "gated_delta_step", "qk_norm", "qk_norm_backward"]
 
-# Linear attention and rotary positions (linear.py), loaded on first use: importing the package
-# does not import torch.
-_LINEAR = ("linear_fwd", "linear_step", "rotary", "rotary_frequencies", "make_linear_args", "make_rotary_args")
+# The modules that import torch, loaded on first use: importing the package does not.
+_LATER = {
+    "linear": ("linear_fwd", "linear_step", "rotary", "rotary_frequencies", "make_linear_args", "make_rotary_args"),
+    "delta": ("gated_delta_fwd", "gated_delta_step", "make_gated_delta_args"),
+    "norm": ("qk_norm", "qk_norm_backward", "make_qk_norm_args"),
+}
 
 
 def __getattr__(name):
-    if name in _LINEAR:
-        from . import linear
-        globals().update({n: getattr(linear, n) for n in _LINEAR})
-        return globals()[name]
+    for module, names in _LATER.items():
+        if name in names:
+            from importlib import import_module
+            found = import_module("." + module, __name__)
+            globals().update({n: getattr(found, n) for n in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

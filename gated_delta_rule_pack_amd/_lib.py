@@ -35,6 +35,10 @@ KDA_F32 = 0
 KDA_F16 = 1
 KDA_BF16 = 2
 
+# kda_norm_kind
+KDA_NORM_RMS = 0
+KDA_NORM_L2 = 1
+
 
 class FwdArgs(Structure):
     _fields_ = [
@@ -79,6 +83,28 @@ class RotaryArgs(Structure):
         ("out_q_stride_t", c_int64), ("out_q_stride_h", c_int64), ("out_k_stride_t", c_int64), ("out_k_stride_h", c_int64),
         ("positions", c_void_p), ("positions_i64", c_int32), ("inv_freq", c_void_p), ("factor", c_float),
         ("interleaved", c_int32), ("inverse", c_int32),
+    ]
+
+
+class GatedDeltaArgs(Structure):
+    _fields_ = [
+        ("lin", LinearArgs),
+        ("beta", c_void_p), ("beta_dtype", c_int), ("dtype", c_int), ("normalize", c_int32),
+    ]
+
+
+class QkNormArgs(Structure):
+    _fields_ = [
+        ("T", c_int32), ("H_q", c_int32), ("H_k", c_int32), ("D", c_int32), ("rot_dim", c_int32),
+        ("dtype", c_int), ("weight_dtype", c_int), ("kind", c_int), ("eps", c_float), ("weight_offset", c_float),
+        ("q", c_void_p), ("k", c_void_p), ("out_q", c_void_p), ("out_k", c_void_p),
+        ("q_stride_t", c_int64), ("q_stride_h", c_int64), ("k_stride_t", c_int64), ("k_stride_h", c_int64),
+        ("out_q_stride_t", c_int64), ("out_q_stride_h", c_int64), ("out_k_stride_t", c_int64), ("out_k_stride_h", c_int64),
+        ("q_weight", c_void_p), ("k_weight", c_void_p),
+        ("positions", c_void_p), ("positions_i64", c_int32), ("inv_freq", c_void_p), ("interleaved", c_int32),
+        ("grad_q", c_void_p), ("grad_k", c_void_p),
+        ("grad_q_stride_t", c_int64), ("grad_q_stride_h", c_int64), ("grad_k_stride_t", c_int64), ("grad_k_stride_h", c_int64),
+        ("grad_q_weight", c_void_p), ("grad_k_weight", c_void_p),
     ]
 
 
@@ -208,6 +234,32 @@ def load() -> ctypes.CDLL:
         raise ImportError("kda_linear_args layout mismatch between include/kda.h and the binding")
     if lib.kda_rotary_args_size() != ctypes.sizeof(RotaryArgs):
         raise ImportError("kda_rotary_args layout mismatch between include/kda.h and the binding")
+    for name in ("kda_gated_delta_fwd_validate", "kda_gated_delta_step_validate"):
+        getattr(lib, name).restype = c_int
+        getattr(lib, name).argtypes = [POINTER(GatedDeltaArgs)]
+    lib.kda_gated_delta_fwd_workspace_bytes.restype = c_size_t
+    lib.kda_gated_delta_fwd_workspace_bytes.argtypes = [POINTER(GatedDeltaArgs)]
+    lib.kda_gated_delta_fwd.restype = c_int
+    lib.kda_gated_delta_fwd.argtypes = [P, POINTER(GatedDeltaArgs), P, c_size_t, P]
+    lib.kda_gated_delta_step.restype = c_int
+    lib.kda_gated_delta_step.argtypes = [P, POINTER(GatedDeltaArgs), P]
+    for name in ("kda_qk_norm_validate", "kda_qk_norm_backward_validate"):
+        getattr(lib, name).restype = c_int
+        getattr(lib, name).argtypes = [POINTER(QkNormArgs)]
+    lib.kda_qk_norm.restype = c_int
+    lib.kda_qk_norm.argtypes = [P, POINTER(QkNormArgs), P]
+    lib.kda_qk_norm_backward_workspace_bytes.restype = c_size_t
+    lib.kda_qk_norm_backward_workspace_bytes.argtypes = [POINTER(QkNormArgs)]
+    lib.kda_qk_norm_backward.restype = c_int
+    lib.kda_qk_norm_backward.argtypes = [P, POINTER(QkNormArgs), P, c_size_t, P]
+    lib.kda_gated_delta_args_size.restype = c_size_t
+    lib.kda_gated_delta_args_size.argtypes = []
+    lib.kda_qk_norm_args_size.restype = c_size_t
+    lib.kda_qk_norm_args_size.argtypes = []
+    if lib.kda_gated_delta_args_size() != ctypes.sizeof(GatedDeltaArgs):
+        raise ImportError("kda_gated_delta_args layout mismatch between include/kda.h and the binding")
+    if lib.kda_qk_norm_args_size() != ctypes.sizeof(QkNormArgs):
+        raise ImportError("kda_qk_norm_args layout mismatch between include/kda.h and the binding")
     _lib = lib
     return lib
 
@@ -228,4 +280,8 @@ EXPORTS = [
     "kda_linear_fwd", "kda_linear_fwd_validate", "kda_linear_fwd_workspace_bytes", "kda_linear_seg_len",
     "kda_linear_step", "kda_linear_step_validate", "kda_rotary", "kda_rotary_validate",
     "kda_linear_args_size", "kda_rotary_args_size",
+    "kda_gated_delta_fwd", "kda_gated_delta_fwd_validate", "kda_gated_delta_fwd_workspace_bytes",
+    "kda_gated_delta_step", "kda_gated_delta_step_validate", "kda_qk_norm", "kda_qk_norm_validate",
+    "kda_qk_norm_backward", "kda_qk_norm_backward_validate", "kda_qk_norm_backward_workspace_bytes",
+    "kda_gated_delta_args_size", "kda_qk_norm_args_size",
 ]

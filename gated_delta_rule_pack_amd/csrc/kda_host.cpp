@@ -24,6 +24,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_delta.h"
 #include "kda_linear.h"
 
 using kda::kChunk;
@@ -72,6 +73,10 @@ int rt_launch(void*, int kernel, const void* plan, void* s, void* start, void* s
     case 7: return kda::launch_linear_output(*reinterpret_cast<const kda::LinearPlan*>(plan), s);
     case 8: return kda::launch_linear_step(*reinterpret_cast<const kda::LinearPlan*>(plan), s);
     case 9: return kda::launch_rotary(*reinterpret_cast<const kda::RotaryPlan*>(plan), s);
+    case 10: return kda::launch_delta_walk(*reinterpret_cast<const kda::DeltaPlan*>(plan), s);
+    case 11: return kda::launch_delta_step(*reinterpret_cast<const kda::DeltaPlan*>(plan), s);
+    case 12: return kda::launch_qk_norm(*reinterpret_cast<const kda::NormPlan*>(plan), s);
+    case 13: return kda::launch_qk_norm_backward(*reinterpret_cast<const kda::NormPlan*>(plan), s);
   }
   const kda::Plan& p = *reinterpret_cast<const kda::Plan*>(plan);
   switch (kernel) {

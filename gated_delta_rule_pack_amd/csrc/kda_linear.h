@@ -70,6 +70,15 @@ int launch_linear_output(const LinearPlan& p, void* stream);
 int launch_linear_step(const LinearPlan& p, void* stream);
 int launch_rotary(const RotaryPlan& p, void* stream);
 
+// Argument checks and plan fields that the linear and gated delta entry points have in common, and the rotation's.
+kda_status check_linear(const kda_linear_args* a);
+LinearPlan plan_of(const kda_linear_args* a);
+kda_status check_rotation(int32_t rot_dim, int32_t D, const double* inv_freq, const void* positions, int32_t positions_i64,
+                          int32_t interleaved, float factor, int32_t T);
+int32_t heads_qk(const kda_linear_args* a);
+// Runs one kernel through the context's runtime table.
+int launch(kda_ctx* ctx, int kernel, const void* plan, void* stream);
+
 // The context's runtime table (kda_host.cpp owns the context's definition).
 const kda_runtime& context_runtime(kda_ctx* ctx);
 

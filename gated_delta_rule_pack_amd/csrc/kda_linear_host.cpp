@@ -8,167 +8,12 @@
 
 #include "kda.h"
 #include "kda_linear.h"
+#include "kda_rows.h"
 
-namespace {
+namespace kda {
 
-using kda::LinearPlan;
-using kda::RotaryPlan;
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-size_t state_bytes(kda_dtype d) { return d == KDA_F32 ? 4 : 2; }
-
-// Bytes [lo, hi) of rows t < T, heads h < H of D adjacent elements (strides are not negative).
-struct Range {
-  uintptr_t lo = 0, hi = 0;
-};
-Range range_of(const void* p, int64_t T, int64_t H, int64_t D, int64_t st, int64_t sh, size_t es) {
-  Range r;
-  if (T < 1 || H < 1) return r;
-  r.lo = (uintptr_t)p;
-  r.hi = r.lo + (uintptr_t)((T - 1) * st + (H - 1) * sh + D) * es;
-  return r;
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// Strides 0, 0 mean dense.
-struct Strides {
-  int64_t t, h;
-};
-Strides strides_of(int64_t t, int64_t h, int64_t H, int64_t D) {
-  return t == 0 && h == 0 ? Strides{H * D, D} : Strides{t, h};
-}
-// Largest stride: far above any real row, and far below what would overflow 64-bit offsets.
-constexpr int64_t kMaxStride = int64_t(1) << 31;
-constexpr int64_t kMaxTokenStride = int64_t(1) << 23;
-// Workgroups of 256 threads in one launch: its work-items are counted in 32 bits.
-constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
-bool stride_ok(Strides s) { return s.t >= 0 && s.h >= 0 && s.t <= kMaxStride && s.h <= kMaxStride; }
-// No two rows of an output overlap: heads inside tokens, or tokens inside heads.
-bool distinct_rows(Strides s, int64_t T, int64_t H, int64_t D) {
-  if (T < 1 || H < 1) return true;
-  const int64_t heads = (H - 1) * s.h + D, tokens = (T - 1) * s.t + D;
-  const bool h_ok = H == 1 || s.h >= D, t_ok = T == 1 || s.t >= D;
-  return h_ok && t_ok && (T == 1 || H == 1 || s.t >= heads || s.h >= tokens);
-}
-
-// T tokens of H rows of D elements of es bytes at `at`.
-struct Rows {
-  const void* at;
-  int64_t T, H, D;
-  Strides s;
-  size_t es;
-};
-bool overlap(const Rows& a, const Rows& b) {
-  return overlap(range_of(a.at, a.T, a.H, a.D, a.s.t, a.s.h, a.es), range_of(b.at, b.T, b.H, b.D, b.s.t, b.s.h, b.es));
-}
-bool same_rows(const Rows& a, const Rows& b) {
-  return a.at == b.at && a.H == b.H && (a.T == 1 || a.s.t == b.s.t) && (a.H == 1 || a.s.h == b.s.h);
-}
-// Whether no element belongs to both (of equal T, D and es), where their byte ranges may interleave: in the rows of
-// one projection, or of one buffer whose heads hold both in turn. Different token strides are not looked into.
-bool disjoint(const Rows& a, const Rows& b) {
-  if (!overlap(a, b)) return true;
-  if (a.T > 1 && (a.s.t != b.s.t || a.s.t < 1)) return false;
-  const auto mod = [](int64_t x, int64_t m) { return (x % m + m) % m; };
-  const int64_t D = a.D, gap = ((intptr_t)b.at - (intptr_t)a.at) / (intptr_t)a.es;
-  const int64_t wa = (a.H - 1) * a.s.h + D, wb = (b.H - 1) * b.s.h + D;
-  // All heads of one beside those of the other.
-  if (a.T > 1 && mod(gap, a.s.t) >= wa && mod(gap, a.s.t) + wb <= a.s.t) return true;
-  // A head of one beside a head of the other.
-  const int64_t h = a.H > 1 ? a.s.h : b.s.h;
-  if ((a.H == 1 || b.H == 1 || a.s.h == b.s.h) && h > 0 && (a.T == 1 || a.s.t % h == 0) && mod(gap, h) >= D && mod(gap, h) + D <= h)
-    return true;
-  // Each pair of heads: the tokens that come nearest.
-  if (a.H * b.H > 1024) return false;
-  for (int64_t i = 0; i < a.H; ++i)
-    for (int64_t j = 0; j < b.H; ++j) {
-      const int64_t off = gap + j * b.s.h - i * a.s.h;
-      int64_t far = off;
-      if (a.T > 1) {
-        const int64_t k = std::min(std::max(-off / a.s.t, 1 - a.T), a.T - 1);
-        for (int64_t t : {k - 1, k, k + 1})
-          if (std::abs(t) < a.T && std::abs(off + t * a.s.t) < std::abs(far)) far = off + t * a.s.t;
-      }
-      if (std::abs(far) < D) return false;
-    }
-  return true;
-}
 
 int32_t heads_qk(const kda_linear_args* a) { return a->H_qk > 0 ? a->H_qk : a->H; }
-
-// A sequence's state, read and written once, in tokens' worth of q, k, v and out bytes.
-int32_t head_cost_of(const kda_linear_args* a) {
-  const bool state = a->initial_state || a->final_state || a->state_cache;
-  if (!state) return 2;
-  return (int32_t)((size_t)a->K * a->V * state_bytes(a->state_dtype) * 2 / ((size_t)(a->K + a->V) * 2 * 2));
-}
-
-int64_t axis_of(const kda_linear_args* a) {
-  return std::max<int64_t>(a->T, 1) + (int64_t)head_cost_of(a) * (a->N - 1);
-}
-
-// Segment length. A long segment costs its own walk (5 us for each 64 tokens of K = V = 128, map and
-// output, one workgroup on a compute unit); every segment costs a step of the combine's chain (0.06 us)
-// and, for each head, a state that is written, chained and read back (0.059 us at K = V = 128). The sum
-// is least at a length that grows with the root of the tokens: measured best at H = 12 for 1024 tokens
-// 128 (24.6 us; 64: 28.4, 192: 27.8), 4096 tokens 192 (40.9 us; 128: 48.8, 384: 50.5), 8192 tokens 384; at H = 32
-// for 1536 tokens 192, 6144 tokens 384; at H = 1 for 168 K tokens (V = 64) 384 to 768 (94 us; 256: 110). Work for
-// more workgroups than the chip holds at once (two of 128 state rows on a compute unit, three of 64) takes
-// as many: 32768 tokens at H = 32, 2048 (415 us; 1024: 436). Little work takes one segment and one
-// kernel: 128 tokens 12.6 us, 15.0 in two segments; 192 tokens 16.5 and 18.9, 256 tokens 20.4 and 20.1;
-// two sequences of 10 tokens 15.1 and 14.1, three 20.9 and 14.3. (Replays of a captured call.)
-int32_t seg_len_of(const kda_linear_args* a) {
-  if (a->seg_len > 0) return a->seg_len;
-  constexpr int64_t C = kda::kLinChunk;
-  const int64_t axis = axis_of(a), units = a->V == 64 ? 768 : 512;
-  const int64_t fit = std::max<int64_t>(1, units / a->H), fill = (axis + fit - 1) / fit;
-  const double per_segment = 0.06 + 0.059 * a->H * a->K * a->V / (128 * 128), per_token = 5.0 / C;
-  const int64_t root = (int64_t)(std::sqrt(per_segment * (double)axis / per_token) / C + 0.5) * C;
-  const auto whole = [](int64_t n) { return (std::max<int64_t>(n, 1) + C - 1) / C * C; };
-  const auto count = [axis](int64_t l) { return (axis + l - 1) / l; };
-  int64_t len = whole(a->T + 128 * ((int64_t)a->N - 1) <= 224 ? axis : std::max(fill, root));
-  // Workgroups for more than one on each of 256 compute units, and for two at most: the units with two decide the
-  // time. As many whole segments as leave one to a unit are taken instead where that is an eighth less by these
-  // costs (3 us for each 64 tokens of a single segment, which has no map). 65536 tokens at H = 2: 342 workgroups 97
-  // us, 256: 85; 16384 at H = 192: 384 in two segments 1183 us, 192 in one 1015; at H = 256: 1397 and 1196. Where the
-  // two ways cost as much, two to a unit run faster, one working while the other waits: 16384 at H = 48: 480
-  // workgroups 349 us, 240: 371; at H = 160: 480 in three segments 966 us, 160 in one 1004.
-  const int64_t n = count(len), most = std::max<int64_t>(1, 256 / a->H), alone = whole((axis + most - 1) / most);
-  if (n * a->H > 264 && n * a->H <= 512 && count(alone) < n) {
-    const double two = 2 * (double)len * per_token + (double)n * per_segment;
-    const double one = (double)alone * (count(alone) == 1 ? 0.6 : 1.0) * per_token + (double)count(alone) * per_segment;
-    if (one < 0.875 * two) len = alone;
-  }
-  return (int32_t)std::min<int64_t>(len, 1 << 30);
-}
-int32_t segments_of(const kda_linear_args* a) {
-  const int64_t L = seg_len_of(a);
-  return (int32_t)((axis_of(a) + L - 1) / L);
-}
-
-struct LinearWs {
-  size_t maps = 0, initials = 0, decays = 0, spans = 0, rot_q = 0, rot_k = 0, total = 0;
-};
-LinearWs workspace_of(const kda_linear_args* a) {
-  LinearWs w;
-  const size_t borders = (size_t)segments_of(a) - 1;
-  const size_t plane = (size_t)a->H * a->K * a->V * sizeof(float);
-  auto take = [&](size_t bytes) {
-    const size_t at = w.total;
-    w.total += (bytes + 255) / 256 * 256;
-    return at;
-  };
-  w.maps = take(borders * plane);
-  w.initials = take(a->initial_state || a->state_cache ? borders * plane : 0);
-  w.decays = take(borders * a->H * sizeof(float));
-  w.spans = take(borders * sizeof(int32_t));
-  if (a->inv_freq) {
-    const size_t rows = (size_t)a->T * heads_qk(a) * a->K * 2;
-    w.rot_q = take(rows);
-    w.rot_k = take(rows);
-  }
-  return w;
-}
 
 kda_status check_rotation(int32_t rot_dim, int32_t D, const double* inv_freq, const void* positions,
                           int32_t positions_i64, int32_t interleaved, float factor, int32_t T) {
@@ -290,6 +135,86 @@ LinearPlan plan_of(const kda_linear_args* a) {
 int launch(kda_ctx* ctx, int kernel, const void* plan, void* stream) {
   const kda_runtime& rt = kda::context_runtime(ctx);
   return rt.launch(rt.user, kernel, plan, stream, nullptr, nullptr);
+}
+
+}  // namespace kda
+
+namespace {
+
+using namespace kda;
+
+// A sequence's state, read and written once, in tokens' worth of q, k, v and out bytes.
+int32_t head_cost_of(const kda_linear_args* a) {
+  const bool state = a->initial_state || a->final_state || a->state_cache;
+  if (!state) return 2;
+  return (int32_t)((size_t)a->K * a->V * state_bytes(a->state_dtype) * 2 / ((size_t)(a->K + a->V) * 2 * 2));
+}
+
+int64_t axis_of(const kda_linear_args* a) {
+  return std::max<int64_t>(a->T, 1) + (int64_t)head_cost_of(a) * (a->N - 1);
+}
+
+// Segment length. A long segment costs its own walk (5 us for each 64 tokens of K = V = 128, map and
+// output, one workgroup on a compute unit); every segment costs a step of the combine's chain (0.06 us)
+// and, for each head, a state that is written, chained and read back (0.059 us at K = V = 128). The sum
+// is least at a length that grows with the root of the tokens: measured best at H = 12 for 1024 tokens
+// 128 (24.6 us; 64: 28.4, 192: 27.8), 4096 tokens 192 (40.9 us; 128: 48.8, 384: 50.5), 8192 tokens 384; at H = 32
+// for 1536 tokens 192, 6144 tokens 384; at H = 1 for 168 K tokens (V = 64) 384 to 768 (94 us; 256: 110). Work for
+// more workgroups than the chip holds at once (two of 128 state rows on a compute unit, three of 64) takes
+// as many: 32768 tokens at H = 32, 2048 (415 us; 1024: 436). Little work takes one segment and one
+// kernel: 128 tokens 12.6 us, 15.0 in two segments; 192 tokens 16.5 and 18.9, 256 tokens 20.4 and 20.1;
+// two sequences of 10 tokens 15.1 and 14.1, three 20.9 and 14.3. (Replays of a captured call.)
+int32_t seg_len_of(const kda_linear_args* a) {
+  if (a->seg_len > 0) return a->seg_len;
+  constexpr int64_t C = kda::kLinChunk;
+  const int64_t axis = axis_of(a), units = a->V == 64 ? 768 : 512;
+  const int64_t fit = std::max<int64_t>(1, units / a->H), fill = (axis + fit - 1) / fit;
+  const double per_segment = 0.06 + 0.059 * a->H * a->K * a->V / (128 * 128), per_token = 5.0 / C;
+  const int64_t root = (int64_t)(std::sqrt(per_segment * (double)axis / per_token) / C + 0.5) * C;
+  const auto whole = [](int64_t n) { return (std::max<int64_t>(n, 1) + C - 1) / C * C; };
+  const auto count = [axis](int64_t l) { return (axis + l - 1) / l; };
+  int64_t len = whole(a->T + 128 * ((int64_t)a->N - 1) <= 224 ? axis : std::max(fill, root));
+  // Workgroups for more than one on each of 256 compute units, and for two at most: the units with two decide the
+  // time. As many whole segments as leave one to a unit are taken instead where that is an eighth less by these
+  // costs (3 us for each 64 tokens of a single segment, which has no map). 65536 tokens at H = 2: 342 workgroups 97
+  // us, 256: 85; 16384 at H = 192: 384 in two segments 1183 us, 192 in one 1015; at H = 256: 1397 and 1196. Where the
+  // two ways cost as much, two to a unit run faster, one working while the other waits: 16384 at H = 48: 480
+  // workgroups 349 us, 240: 371; at H = 160: 480 in three segments 966 us, 160 in one 1004.
+  const int64_t n = count(len), most = std::max<int64_t>(1, 256 / a->H), alone = whole((axis + most - 1) / most);
+  if (n * a->H > 264 && n * a->H <= 512 && count(alone) < n) {
+    const double two = 2 * (double)len * per_token + (double)n * per_segment;
+    const double one = (double)alone * (count(alone) == 1 ? 0.6 : 1.0) * per_token + (double)count(alone) * per_segment;
+    if (one < 0.875 * two) len = alone;
+  }
+  return (int32_t)std::min<int64_t>(len, 1 << 30);
+}
+int32_t segments_of(const kda_linear_args* a) {
+  const int64_t L = seg_len_of(a);
+  return (int32_t)((axis_of(a) + L - 1) / L);
+}
+
+struct LinearWs {
+  size_t maps = 0, initials = 0, decays = 0, spans = 0, rot_q = 0, rot_k = 0, total = 0;
+};
+LinearWs workspace_of(const kda_linear_args* a) {
+  LinearWs w;
+  const size_t borders = (size_t)segments_of(a) - 1;
+  const size_t plane = (size_t)a->H * a->K * a->V * sizeof(float);
+  auto take = [&](size_t bytes) {
+    const size_t at = w.total;
+    w.total += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  w.maps = take(borders * plane);
+  w.initials = take(a->initial_state || a->state_cache ? borders * plane : 0);
+  w.decays = take(borders * a->H * sizeof(float));
+  w.spans = take(borders * sizeof(int32_t));
+  if (a->inv_freq) {
+    const size_t rows = (size_t)a->T * heads_qk(a) * a->K * 2;
+    w.rot_q = take(rows);
+    w.rot_k = take(rows);
+  }
+  return w;
 }
 
 }  // namespace

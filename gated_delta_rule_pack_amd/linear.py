@@ -103,6 +103,20 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
                      seg_len=0) -> "_lib.LinearArgs":
     """Fill a ``kda_linear_args`` from tensors (no allocation), checking everything the C side
     cannot see: dtypes, shapes, strides and element counts."""
+    a = _lib.LinearArgs()
+    _fill_linear(a, q, k, v, g, _BF16, N, cu_seqlens, cu_seqlens_cpu, scale, initial_state, final_state, state_cache,
+                 state_indices, has_initial_state, out, state_k_first)
+    if positions is not None or inv_freq is not None:
+        _fill_rotation(a, a.T, a.K, positions, inv_freq, interleaved)
+        a.rot_factor = rotary_factor
+    if seg_len:
+        a.seg_len = seg_len
+    return a
+
+
+def _fill_linear(a, q, k, v, g, dtype, N, cu_seqlens, cu_seqlens_cpu, scale, initial_state, final_state, state_cache,
+                 state_indices, has_initial_state, out, state_k_first):
+    """The fields that the linear and gated delta calls have in common; dtype: of q, k, v and out."""
     if _grads_on() and (q.requires_grad or k.requires_grad or v.requires_grad or (g is not None and g.requires_grad) or
                         (state_cache is not None and state_cache.requires_grad) or (out is not None and out.requires_grad) or
                         (initial_state is not None and initial_state.requires_grad)):
@@ -116,9 +130,9 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
         raise ValueError("v must have q's token count")
     if H_qk < 1 or H % H_qk != 0 or H < 1:
         raise ValueError(f"q/k heads ({H_qk}) must divide v heads ({H})")
-    if q.dtype != _BF16 or k.dtype != _BF16 or v.dtype != _BF16:
-        raise TypeError(f"q, k and v must be bf16, got {q.dtype}, {k.dtype}, {v.dtype}")
-    a = _lib.LinearArgs()
+    if q.dtype != dtype or k.dtype != dtype or v.dtype != dtype:
+        name = "bf16" if dtype == _BF16 else "fp16"
+        raise TypeError(f"q, k and v must be {name}, got {q.dtype}, {k.dtype}, {v.dtype}")
     if N is None:
         N = T
     if cu_seqlens is not None:
@@ -141,8 +155,8 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
         a.v_stride_t, a.v_stride_h = _strides("v", v, T, H, V)
     if out is not None:
         out = _packed("out", out)
-        if out.dtype != _BF16:
-            raise TypeError(f"out must be bf16, got {out.dtype}")
+        if out.dtype != dtype:
+            raise TypeError(f"out must be {'bf16' if dtype == _BF16 else 'fp16'}, got {out.dtype}")
         if out.shape != v.shape:
             raise ValueError(f"out must have v's shape {tuple(v.shape)}, got {tuple(out.shape)}")
         a.out = out.data_ptr()
@@ -203,12 +217,6 @@ def make_linear_args(q, k, v, g, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None
                 raise TypeError("final_state must have initial_state's dtype")
     if state_k_first:
         a.state_k_first = 1
-    if positions is not None or inv_freq is not None:
-        _fill_rotation(a, T, K, positions, inv_freq, interleaved)
-        a.rot_factor = rotary_factor
-    if seg_len:
-        a.seg_len = seg_len
-    return a
 
 
 def _check(rc, where):

@@ -25,7 +25,9 @@
  * Changes).
  *
  * Beside it: linear attention with a decay for each head (kda_linear_fwd, kda_linear_step)
- * over the same pool, and rotary positions (kda_rotary), at the end of this file.
+ * over the same pool, rotary positions (kda_rotary), the gated delta rule with one decay for each
+ * head (kda_gated_delta_fwd, kda_gated_delta_step), and norms of q and k with the rotation in the same
+ * pass (kda_qk_norm, kda_qk_norm_backward), at the end of this file.
  *
  * Conventions for every function below:
  *  - Pointers are device memory owned by the caller unless marked "host".
@@ -478,6 +480,108 @@ kda_status kda_rotary_validate(const kda_rotary_args* args);
 /* sizeof the two structs, so a binding can check its mirrors. */
 size_t kda_linear_args_size(void);
 size_t kda_rotary_args_size(void);
+
+/* ---- The gated delta rule with one decay for each head. ------------------------------
+ * For every token t of sequence n and value head h, with the V-first state S in R^{V x K}, the log
+ * decay g and the step size beta of the token and head:
+ *
+ *     S = e^g S;   S = S + beta (v - S k) k^T;   o = scale * S q
+ *
+ * (kda_chunk_fwd decays every key channel by itself, through a bounded gate; kda_linear_fwd has no delta
+ * rule.) With normalize, q and k are taken as q / sqrt(sum q^2 + 1e-6) and k / sqrt(sum k^2 + 1e-6).
+ * Everything else is as in kda_linear_args: packed bounds, pool and slots, grouped value heads, strides,
+ * workspace and stream; no host metadata, so a captured call replays with other bounds. The token tensors
+ * are all bf16 or all fp16.
+ *
+ * Rules for the data. g <= 0 (-inf forgets everything before the token; anything below -120 counts as
+ * -inf). A step is stable for |beta| |k|^2 <= 2, which normalised keys and 0 <= beta <= 2 satisfy; keys that
+ * break it may overflow the products' fp16 terms within 64 tokens, which gives values that are not finite.
+ * What is not finite stays causal in its own sequence and head: a row of q takes its own output; a row of k, a
+ * beta, and a log decay that is NaN or above 0 every output from its token on and the final state; a value of v
+ * or of a state row the same of its own channel. A token with k = 0 or beta = 0 only decays. */
+typedef struct kda_gated_delta_args {
+  kda_linear_args lin;  /* inv_freq and seg_len must be 0; the tensors are of type dtype */
+  const void* beta;     /* [T, H], contiguous */
+  kda_dtype beta_dtype; /* KDA_F32 or KDA_BF16 */
+  kda_dtype dtype;      /* of q, k, v and out: KDA_BF16 or KDA_F16 */
+  int32_t normalize;    /* 0 or 1 */
+} kda_gated_delta_args;
+
+/* Prompts. Errors as kda_linear_fwd. */
+kda_status kda_gated_delta_fwd(kda_ctx* ctx, const kda_gated_delta_args* args, void* workspace, size_t workspace_bytes,
+                               void* stream);
+/* Host-only, pure: every argument check of kda_gated_delta_fwd. */
+kda_status kda_gated_delta_fwd_validate(const kda_gated_delta_args* args);
+/* Host-only, pure: bytes of caller workspace (256-byte aligned), from shapes and types alone; 0 for invalid
+ * arguments. */
+size_t kda_gated_delta_fwd_workspace_bytes(const kda_gated_delta_args* args);
+
+/* Single tokens, as kda_linear_step: one kernel, no workspace, capturable; padding rows are left as they were. */
+kda_status kda_gated_delta_step(kda_ctx* ctx, const kda_gated_delta_args* args, void* stream);
+kda_status kda_gated_delta_step_validate(const kda_gated_delta_args* args);
+
+/* ---- Norms of q and k for each head, with the position rotation in the same pass. --------
+ * For every row x of D channels (one head of one token), with m = 1 / D (kind KDA_NORM_RMS) or m = 1
+ * (KDA_NORM_L2) and r = 1 / sqrt(m sum x^2 + eps):
+ *
+ *     y = R (x r (weight_offset + weight))
+ *
+ * where R is the rotation that kda_rotary_args describes (none for rot_dim 0 and a null inv_freq; no factor) and weight is one vector of
+ * D for q and one for k (null: 1, and no offset). Squares are summed in 64 bits, so no finite row overflows; the rest is
+ * fp32, rounded once.
+ *
+ * The gradient, with z = R^T dy:  dweight = sum over rows of z x r;  with u = z (weight_offset + weight):
+ * dx = r (u - m x r^2 sum(u x)). Weight gradients are summed in fp32, in an order that depends on the shapes
+ * alone. */
+typedef enum kda_norm_kind { KDA_NORM_RMS = 0, KDA_NORM_L2 = 1 } kda_norm_kind;
+typedef struct kda_qk_norm_args {
+  int32_t T;              /* tokens, may be 0 */
+  int32_t H_q, H_k;       /* heads of q (>= 1) and of k (0: no k) */
+  int32_t D;              /* head size, 1..1024 */
+  int32_t rot_dim;        /* 0 (no rotation), or even, 2..D */
+  kda_dtype dtype;        /* of q, k, out and grad: KDA_BF16, KDA_F16 or KDA_F32 */
+  kda_dtype weight_dtype; /* KDA_F32, or dtype */
+  kda_norm_kind kind;
+  float eps;              /* finite, above 0 */
+  float weight_offset;    /* finite */
+  const void* q;          /* [T, H_q, D], element strides below; the D elements adjacent */
+  const void* k;          /* [T, H_k, D] or null */
+  void* out_q;            /* kda_qk_norm: y, which may be q's memory with the same strides (in place); */
+  void* out_k;            /* kda_qk_norm_backward: dx, which may be grad's. Otherwise no element in common with */
+                          /* any other tensor of the call; byte ranges may interleave as in kda_rotary_args */
+  int64_t q_stride_t, q_stride_h; /* each pair: 0, 0 means dense */
+  int64_t k_stride_t, k_stride_h;
+  int64_t out_q_stride_t, out_q_stride_h;
+  int64_t out_k_stride_t, out_k_stride_h;
+  const void* q_weight;   /* [D] or null */
+  const void* k_weight;
+  const void* positions;  /* device [T], int32 or int64 */
+  int32_t positions_i64;
+  const double* inv_freq; /* device [rot_dim / 2] */
+  int32_t interleaved;
+  /* kda_qk_norm_backward only. */
+  const void* grad_q;     /* dy, as q */
+  const void* grad_k;
+  int64_t grad_q_stride_t, grad_q_stride_h;
+  int64_t grad_k_stride_t, grad_k_stride_h;
+  void* grad_q_weight;    /* [D] of weight_dtype, written; required with q_weight, null without */
+  void* grad_k_weight;
+} kda_qk_norm_args;
+
+/* One kernel (one for each 2^22 tokens); a refused call enqueues nothing. */
+kda_status kda_qk_norm(kda_ctx* ctx, const kda_qk_norm_args* args, void* stream);
+kda_status kda_qk_norm_validate(const kda_qk_norm_args* args);
+/* One kernel, and with weights a second that joins the first one's sums, in the workspace. T = 0 writes zeros for
+ * weight gradients. */
+kda_status kda_qk_norm_backward(kda_ctx* ctx, const kda_qk_norm_args* args, void* workspace, size_t workspace_bytes,
+                                void* stream);
+kda_status kda_qk_norm_backward_validate(const kda_qk_norm_args* args);
+/* Host-only, pure: bytes of caller workspace (256-byte aligned); 0 without weights and for invalid arguments. */
+size_t kda_qk_norm_backward_workspace_bytes(const kda_qk_norm_args* args);
+
+/* sizeof the structs, so a binding can check its mirrors. */
+size_t kda_gated_delta_args_size(void);
+size_t kda_qk_norm_args_size(void);
 
 #ifdef __cplusplus
 }

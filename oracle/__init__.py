@@ -8,3 +8,4 @@ from .kda_oracle import (  # noqa: F401
     L2_EPS, chunk_indices, kda_forward, kda_sequence, l2_normalize, sigmoid,
 )
 from .linear_oracle import linear_forward, rotate  # noqa: F401
+from .delta_oracle import NORM_EPS, delta_forward, qk_norm, qk_norm_gradient  # noqa: F401
