@@ -39,6 +39,11 @@ KDA_BF16 = 2
 KDA_NORM_RMS = 0
 KDA_NORM_L2 = 1
 
+# kda_delta_path
+KDA_DELTA_POLICY = 0
+KDA_DELTA_WALK = 1
+KDA_DELTA_SCAN = 2
+
 
 class FwdArgs(Structure):
     _fields_ = [
@@ -89,7 +94,7 @@ class RotaryArgs(Structure):
 class GatedDeltaArgs(Structure):
     _fields_ = [
         ("lin", LinearArgs),
-        ("beta", c_void_p), ("beta_dtype", c_int), ("dtype", c_int), ("normalize", c_int32),
+        ("beta", c_void_p), ("beta_dtype", c_int), ("dtype", c_int), ("normalize", c_int32), ("path", c_int32),
     ]
 
 

@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["kda_host.cpp", "kda_prep.hip", "kda_scan.hip", "kda_seg.hip", "kda_decode.hip", "kda_noalloc.hip", "kda_meta.hip",
            "kda_linear_host.cpp", "kda_linear.hip", "kda_linear_step.hip", "kda_rotary.hip",
-           "kda_delta_host.cpp", "kda_delta.hip", "kda_delta_step.hip", "kda_norm.hip"]
+           "kda_delta_host.cpp", "kda_delta.hip", "kda_delta_scan.hip", "kda_delta_step.hip", "kda_norm.hip"]
 ARCH = "gfx950"
 # Packed fp32 instructions are disabled for every HIP translation unit.
 COMMON_FLAGS = [

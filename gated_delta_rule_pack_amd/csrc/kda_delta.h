@@ -14,9 +14,22 @@ struct DeltaPlan : LinearPlan {
   int beta_bf16;
   int f16;           // q, k, v and out are fp16, not bf16
   int normalize;
+  // The chunks' records, for the scan. A chunk has a place: sequence n's are floor(cu[n] / 64) + n on.
+  int places;
+  char* records;     // [places][H] of kDeltaRecord bytes
+  char* keys;        // [places][H_qk] of 64 K fp16 values, in operand order
+  char* queries;
 };
+constexpr int kDeltaRecord = 19712;
+
+// Whether one fp16 term of the state and what goes into it serves. A state in bf16 has 8 bits, and one that is not stored goes
+// into outputs alone; both leave outputs in bf16 as far off as their own rounding does. Outputs in fp16 have 11 bits of their
+// own: two terms (2.7e-4 rel-L2; one term: 3.6e-4).
+inline bool one_term(const DeltaPlan& p) { return !p.f16 && (p.out_mode == kStateNone || p.state_dtype == kBF16); }
 
 int launch_delta_walk(const DeltaPlan& p, void* stream);
+int launch_delta_prep(const DeltaPlan& p, void* stream);
+int launch_delta_scan(const DeltaPlan& p, void* stream);
 int launch_delta_step(const DeltaPlan& p, void* stream);
 
 // Norms of q and k: the rotation's fields (in: x, out: y or dx) and the norm's.

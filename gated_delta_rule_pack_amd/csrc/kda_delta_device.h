@@ -1,0 +1,295 @@
+// Device side that the gated delta rule's prompt kernels share: operands in fp16 terms, scaled rows, a chunk's
+// numbers, and the triangular inverse T. kda_delta.hip has the mathematics.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "kda_delta.h"
+#include "kda_device.h"
+#include "kda_unit.h"
+#include "kda_walk.h"
+
+namespace kda {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+// fp32 operands: A row l % 16, B column l % 16, both k = l / 16.
+__device__ __forceinline__ f32x4 mfma32(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ float ldexp2(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
+
+// Two tiles (rows 4g + i and 16 + 4g + i) as an operand, in one or two terms.
+__device__ __forceinline__ f16x8 to_f16(f32x4 a, f32x4 b) {
+  f16x8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (_Float16)a[i], r[4 + i] = (_Float16)b[i];
+  return r;
+}
+// A value that is split into terms is rounded to fp32 first, once: of a product or a sum the compiler would otherwise make the
+// first term in one instruction, which rounds the exact value, and the second from the rounded one. Where those fall on two sides
+// of a middle the terms miss the value by 2^-10 of it.
+__device__ __forceinline__ void settle(f32x4& x) { asm("" : "+v"(x)); }
+__device__ __forceinline__ f16x8 rest_f16(f32x4 a, f32x4 b, f16x8 hi) {
+  f16x8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (_Float16)(a[i] - (float)hi[i]), r[4 + i] = (_Float16)(b[i] - (float)hi[4 + i]);
+  return r;
+}
+
+// One tile (rows 4g + i) as half a fragment, in one or two terms.
+__device__ __forceinline__ void put_half(char* high, char* low, int at, f32x4 x) {
+  f16x4 hi, lo;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = (_Float16)x[i];
+    lo[i] = (_Float16)(x[i] - (float)hi[i]);
+  }
+  *reinterpret_cast<f16x4*>(high + at) = hi;
+  if (low) *reinterpret_cast<f16x4*>(low + at) = lo;
+}
+
+// A token's element of a 16-bit word, by type.
+template <bool kF16In>
+__device__ __forceinline__ float token_value(uint32_t half) {
+  if constexpr (kF16In) return (float)__builtin_bit_cast(_Float16, (uint16_t)half);
+  else return __uint_as_float(half << 16);
+}
+template <bool kF16In>
+__device__ __forceinline__ float low_value(uint32_t w) {
+  return kF16In ? token_value<true>(w & 0xffff) : __uint_as_float(w << 16);
+}
+template <bool kF16In>
+__device__ __forceinline__ float high_value(uint32_t w) {
+  return kF16In ? token_value<true>(w >> 16) : __uint_as_float(w & 0xffff0000u);
+}
+
+// Maximum and sum over the 8 or 16 lanes of a row: quads, halves, whole rows.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+}
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  x = max(x, dpp<0xb1>(x));   // quad_perm [1, 0, 3, 2]
+  x = max(x, dpp<0x4e>(x));   // quad_perm [2, 3, 0, 1]
+  x = max(x, dpp<0x141>(x));  // row_half_mirror
+  if constexpr (kLanes == 16) x = max(x, dpp<0x140>(x));  // row_mirror
+  return x;
+}
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float x) {
+  x += __uint_as_float(dpp<0xb1>(__float_as_uint(x)));
+  x += __uint_as_float(dpp<0x4e>(__float_as_uint(x)));
+  x += __uint_as_float(dpp<0x141>(__float_as_uint(x)));
+  if constexpr (kLanes == 16) x += __uint_as_float(dpp<0x140>(__float_as_uint(x)));
+  return x;
+}
+
+constexpr int kBadRow = 1 << 20;  // exponent of a row that is not finite
+// A scaled row's exponent and the sum of its scaled squares.
+struct RowInfo {
+  int e;
+  float squares;
+};
+
+// Rows of a tile of q or k in LDS as fp16, each scaled by 2^-e.
+template <int D, int kThreads, bool kF16In>
+__device__ __forceinline__ void put_scaled(const Rows<D, kThreads>& rows, char* tile, RowInfo* info, int tid, bool squares) {
+  typedef Rows<D, kThreads> R;
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  tid = local_copy(tid);
+  char* at = tile + row_at<D>(tid / R::kUnits) + (tid % R::kUnits) * 16;
+#pragma unroll
+  for (int i = 0; i < R::kPasses; ++i) {
+    const u32x4 w = rows.w[i];
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
+    const uint32_t most = row_max<R::kUnits>(max((uint32_t)top[0], (uint32_t)top[1]));
+    const bool bad = most >= (kF16In ? 0x7c00u : 0x7f80u);
+    const int e = most == 0 || bad ? 0 : __builtin_amdgcn_frexp_expf(token_value<kF16In>(most)) + 1;
+    u32x4 out = {0, 0, 0, 0};
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = ldexp2(low_value<kF16In>(w[j]), -e), b = ldexp2(high_value<kF16In>(w[j]), -e);
+      s += a * a;
+      s += b * b;
+      const f16x2 h = {(_Float16)a, (_Float16)b};
+      out[j] = bad ? 0u : __builtin_bit_cast(uint32_t, h);
+    }
+    *reinterpret_cast<u32x4*>(at + i * R::kRows * kRowBytes<D>) = out;
+    if (squares) s = row_sum<R::kUnits>(s);
+    if (tid % R::kUnits == 0) info[tid / R::kUnits + i * R::kRows] = RowInfo{bad ? kBadRow : e, s};
+  }
+}
+
+// What the walk needs of a chunk beside its tiles; t, s are tokens.
+//   K'_t, Q'_t: scaled rows; rk_t, rq_t: what takes them to the keys and queries of the rule, as it is scaled here:
+// keys by 2^-X, step sizes by 2^{2X}, states by 2^X, with X other than 0 only for keys far from unit length; states
+// are scaled by 2^Y more, with Y other than 0 only where all step sizes are small.
+struct Chunk {
+  double G[kC];                // inclusive cumsum of g
+  alignas(16) float bk[kC];    // beta rk
+  alignas(16) float rk[kC];
+  alignas(16) float h[kC];     // rk e^G 2^-Y: the share of K' S in what is to be learnt
+  alignas(16) float c[kC];     // rk e^{G_C - G}: what of D reaches the chunk's end
+  alignas(16) float col[kC];   // beta 2^Y: the columns of T
+  alignas(16) float e[kC];     // e^G
+  alignas(16) float f[kC];     // scale rq 2^-Y: outputs; NaN from the first bad token on
+  float total;                 // e^{G_C}; NaN with a bad token
+  int shift;                   // X + Y
+};
+
+// One lane for each token.
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x = max(x, __shfl_xor(x, d));
+  return x;
+}
+__device__ __forceinline__ void put_chunk(Chunk& ch, const DeltaPlan& p, RowInfo k, RowInfo q, float g, float beta, int lane) {
+  const bool bad = k.e == kBadRow || !(g <= 0.f) || !(fabsf(beta) < INFINITY);
+  const uint64_t all_bad = __ballot(bad);
+  const int first = all_bad ? __builtin_ctzll(all_bad) : kC;
+  if (bad) beta = 0.f, g = 0.f, k = RowInfo{0, 0.f};
+  // Exponents of the chunk. A row's largest element is 2^-1 of its power of two at most: unit length means -2 to 2.
+  int X = 0;
+  float rk = 1.f, rq = 1.f;
+  if (p.normalize) {
+    rk = rsqrtf(k.squares + ldexp2(kNormEps, -2 * k.e));
+    rq = rsqrtf(q.squares + ldexp2(kNormEps, -2 * q.e));
+  } else {
+    const int top = wave_max(k.squares > 0.f ? k.e : -1000);
+    X = top < -2 || top > 2 ? (top == -1000 ? 0 : top) : 0;
+    rk = ldexp2(1.f, k.e - X);
+    rq = ldexp2(1.f, q.e - X);
+  }
+  beta = ldexp2(beta, 2 * X);
+  const int big = wave_max(beta != 0.f ? __builtin_amdgcn_frexp_expf(beta) : -1000);  // |beta| < 2^big
+  const int Y = big == -1000 || (big >= -1 && big <= 2) ? 0 : -big;
+  const double G = prefix_sum((double)(g < kMinLogDecay ? kMinLogDecay : g));
+  const uint64_t u = __builtin_bit_cast(uint64_t, G);
+  const double end = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
+                                                    (uint32_t)__builtin_amdgcn_readlane((int)u, 63));
+  const float eG = __expf((float)G);
+  ch.G[lane] = G;
+  ch.bk[lane] = beta * rk;
+  ch.rk[lane] = rk;
+  ch.h[lane] = ldexp2(rk * eG, -Y);
+  ch.c[lane] = rk * __expf((float)(end - G));
+  ch.col[lane] = ldexp2(beta, Y);
+  ch.e[lane] = eG;
+  ch.f[lane] = lane >= first || q.e == kBadRow ? __builtin_nanf("") : p.scale * ldexp2(rq, -Y);
+  if (lane == 0) {
+    ch.total = all_bad ? __builtin_nanf("") : __expf((float)end);
+    ch.shift = X + Y;
+  }
+}
+
+// A's ten causal 16 x 16 blocks in fp32, each as [s][t] with rows of 20 floats; T's take their places.
+constexpr int kBlockRow = 20, kBlock = 16 * kBlockRow;
+__device__ __forceinline__ constexpr int block_at(int tt, int st) { return (tt * (tt + 1) / 2 + st) * kBlock; }
+
+// Fragment (token tile tt, sources 32 b ..) of P or one term of T.
+__device__ __forceinline__ f16x8 read_fragment(const char* p, int lane, int tt, int b) { return __builtin_bit_cast(f16x8, read_p(p, lane, tt, b)); }
+// Tile (tt, st) of it, of which a lane holds token l % 16 and sources 4g + i.
+__device__ __forceinline__ void put_fragment(char* p, int lane, int tt, int st, f16x4 x) {
+  const int b = st >> 1;
+  *reinterpret_cast<f16x4*>(p + fragment(tt, b) + (half_fragment(tt, b) ? lane * 8 : lane * 16 + (st & 1) * 8)) = x;
+}
+
+// Tile (tt, st) of K' K'^T or K' Q'^T, rows s = 4g + i, column t = l % 16.
+template <int K>
+__device__ __forceinline__ f32x4 tile_product(const char* k, const char* other, int lane, int tt, int st) {
+  f32x4 d = zero4();
+#pragma unroll
+  for (int m = 0; m < K / 32; ++m)
+    d = mfma(__builtin_bit_cast(f16x8, read_row<K>(k, lane, 16 * st, m)), __builtin_bit_cast(f16x8, read_row<K>(other, lane, 16 * tt, m)), d);
+  return d;
+}
+// e^{G_t - G_s} for a tile's elements.
+__device__ __forceinline__ f32x4 tile_decay(const Chunk& ch, int lane, int tt, int st) {
+  const double Gt = ch.G[16 * tt + (lane & 15)];
+  f32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __expf((float)(Gt - ch.G[16 * st + 4 * (lane >> 4) + i]));
+  return x;
+}
+
+// The diagonal blocks of T, one for each 16 lanes, a column to a lane.
+__device__ __forceinline__ void invert_diagonal(float* blocks, int lane) {
+  float* a = blocks + block_at(lane >> 4, lane >> 4);
+  const int j = lane & 15;
+  float x[16];
+#pragma unroll
+  for (int t = 0; t < 16; ++t) x[t] = t == j ? 1.f : 0.f;
+#pragma unroll
+  for (int s = 0; s < 15; ++s) {
+#pragma unroll
+    for (int c = (s + 1) / 4; c < 4; ++c) {
+      const f32x4 col = *reinterpret_cast<const f32x4*>(a + s * kBlockRow + 4 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * c + i > s) x[4 * c + i] -= col[i] * x[s];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) *reinterpret_cast<f32x4*>(a + j * kBlockRow + 4 * c) = f32x4{x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]};
+}
+// d + L^T R^T for blocks stored as [s][t]: L's (r, u) at [u][r] is the left operand, row u; R's (t, r) the right one.
+__device__ __forceinline__ f32x4 block_product(const float* left, const float* right, int lane, f32x4 d) {
+  const int g = lane >> 4, l16 = lane & 15;
+  const f32x4 a = *reinterpret_cast<const f32x4*>(left + l16 * kBlockRow + 4 * g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = mfma32(a[i], right[(4 * g + i) * kBlockRow + l16], d);
+  return d;
+}
+__device__ __forceinline__ f32x4 block_product(const float* left, f32x4 right, int lane, f32x4 d) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(left + (lane & 15) * kBlockRow + 4 * (lane >> 4));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = mfma32(a[i], right[i], d);
+  return d;
+}
+// Tile (tt, st) of T as its fragments' two terms, its columns times col.
+__device__ __forceinline__ void put_t(char* frags, const Chunk& ch, int lane, int tt, int st, f32x4 x) {
+  const f32x4 col = *reinterpret_cast<const f32x4*>(&ch.col[16 * st + 4 * (lane >> 4)]);
+  x *= col;
+  settle(x);
+  f16x4 hi, lo;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = (_Float16)x[i];
+    lo[i] = (_Float16)(x[i] - (float)hi[i]);
+  }
+  put_fragment(frags, lane, tt, st, hi);
+  put_fragment(frags + kTermP, lane, tt, st, lo);
+}
+
+// Powers of two that hold one value channel's state and V in fp16's range: S' = S 2^{ex + shift}, V' = V 2^ex. The larger of
+// both is kept in [1, 16): fp16's least step, 2^-24, is then nothing beside it, and what 64 tokens learn stays below fp16's largest
+// number, 2^16: |v' - S' k| is at most 2^7.6, and no stable rule makes more than 64 times that of it.
+struct Scale {
+  int ex, shift;
+  float v;         // 2^ex
+  f32x4 out;       // 2^-ex of the channels 4g + i, for tiles that hold channels as rows
+  __device__ __forceinline__ void set(int lane, int to) {
+    ex = to;
+    v = ldexp2(1.f, to);
+    const float back = ldexp2(1.f, -to);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = __shfl(back, 4 * (lane >> 4) + i);
+  }
+};
+
+// The exponent of x >= 0: x < 2^e.
+constexpr int kNoExponent = -4096;
+__device__ __forceinline__ int exponent(float x) { return x > 0.f && x < INFINITY ? __builtin_amdgcn_frexp_expf(x) : kNoExponent; }
+// Over the four lanes that hold one channel.
+__device__ __forceinline__ int channel_max(int x) {
+  x = max(x, __shfl_xor(x, 16));
+  return max(x, __shfl_xor(x, 32));
+}
+
+}  // namespace kda

@@ -21,6 +21,7 @@ kda_status check_delta(const kda_gated_delta_args* a) {
   if (a->dtype != KDA_BF16 && a->dtype != KDA_F16) return KDA_ERR_UNSUPPORTED;
   if (a->beta_dtype != KDA_F32 && a->beta_dtype != KDA_BF16) return KDA_ERR_UNSUPPORTED;
   if (a->normalize != 0 && a->normalize != 1) return KDA_ERR_INVALID_ARG;
+  if (a->path < KDA_DELTA_POLICY || a->path > KDA_DELTA_SCAN) return KDA_ERR_INVALID_ARG;
   if (a->lin.T > 0 && (!a->beta || !aligned(a->beta, state_bytes(a->beta_dtype)))) return KDA_ERR_INVALID_ARG;
   return KDA_OK;
 }
@@ -33,6 +34,37 @@ DeltaPlan delta_plan_of(const kda_gated_delta_args* a) {
   p.f16 = a->dtype == KDA_F16;
   p.normalize = a->normalize;
   return p;
+}
+
+int32_t places_of(const kda_gated_delta_args* a) { return a->lin.T / kLinChunk + a->lin.N; }
+// One launch counts its work-items in 32 bits.
+bool fits_scan(const kda_gated_delta_args* a) {
+  const kda_linear_args& l = a->lin;
+  return (int64_t)places_of(a) * l.H <= kMaxGroups && ((int64_t)l.N * l.H + 7) * (l.V / 16) <= kMaxGroups / 2;
+}
+// Whether a call makes its chunks' records in one kernel and scans them with workgroups of 16 value channels.
+bool scans(const kda_gated_delta_args* a) {
+  const kda_linear_args& l = a->lin;
+  if (a->path != KDA_DELTA_POLICY) return a->path == KDA_DELTA_SCAN;
+  return (int64_t)l.N * l.H <= 256 && fits_scan(a);
+}
+
+struct DeltaWs {
+  size_t records = 0, keys = 0, queries = 0, total = 0;
+};
+DeltaWs workspace_of(const kda_gated_delta_args* a) {
+  DeltaWs w;
+  if (!scans(a)) return w;
+  const size_t places = (size_t)places_of(a), rows = places * heads_qk(&a->lin) * kLinChunk * a->lin.K * 2;
+  const auto take = [&](size_t bytes) {
+    const size_t at = w.total;
+    w.total += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  w.records = take(places * a->lin.H * kDeltaRecord);
+  w.keys = take(rows);
+  w.queries = take(rows);
+  return w;
 }
 
 // The rows of one tensor of a norm's call: x, its result, or a gradient.
@@ -155,23 +187,36 @@ kda_status kda_gated_delta_fwd_validate(const kda_gated_delta_args* a) {
   const kda_linear_args& l = a->lin;
   if (!l.cu_seqlens || !aligned(l.cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
   if (l.state_cache && (!l.state_indices || !l.has_initial_state)) return KDA_ERR_INVALID_ARG;
-  if ((int64_t)l.N * l.H > kMaxGroups / 4) return KDA_ERR_UNSUPPORTED;  // two slices of up to 512 threads
   if (const int32_t* cu = l.cu_seqlens_host) {
     if (cu[0] != 0 || cu[l.N] > l.T) return KDA_ERR_INVALID_ARG;
     for (int i = 0; i < l.N; ++i)
       if (cu[i + 1] < cu[i]) return KDA_ERR_INVALID_ARG;
   }
+  // A launch counts its work-items in 32 bits: two slices of up to 512 threads.
+  if (scans(a) ? !fits_scan(a) : (int64_t)l.N * l.H > kMaxGroups / 4) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 
-size_t kda_gated_delta_fwd_workspace_bytes(const kda_gated_delta_args* a) { return 0; }
+size_t kda_gated_delta_fwd_workspace_bytes(const kda_gated_delta_args* a) {
+  return kda_gated_delta_fwd_validate(a) == KDA_OK ? workspace_of(a).total : 0;
+}
 
 kda_status kda_gated_delta_fwd(kda_ctx* ctx, const kda_gated_delta_args* a, void* ws, size_t ws_bytes, void* stream) {
   if (!ctx) return KDA_ERR_INVALID_ARG;
   if (kda_status st = kda_gated_delta_fwd_validate(a)) return st;
+  const DeltaWs w = workspace_of(a);
+  if (w.total > 0 && (!ws || ws_bytes < w.total || !aligned(ws, 256))) return KDA_ERR_WORKSPACE;
   DeltaPlan p = delta_plan_of(a);
-  p.slices = p.V == 128 && (int64_t)p.N * p.H <= 128 ? 2 : 1;
-  return launch(ctx, 10, &p, stream) ? KDA_ERR_HIP : KDA_OK;
+  if (!scans(a)) {
+    p.slices = p.V == 128 && (int64_t)p.N * p.H <= 128 ? 2 : 1;
+    return launch(ctx, 10, &p, stream) ? KDA_ERR_HIP : KDA_OK;
+  }
+  char* base = reinterpret_cast<char*>(ws);
+  p.places = places_of(a);
+  p.records = base + w.records;
+  p.keys = base + w.keys;
+  p.queries = base + w.queries;
+  return launch(ctx, 14, &p, stream) || launch(ctx, 15, &p, stream) ? KDA_ERR_HIP : KDA_OK;
 }
 
 kda_status kda_gated_delta_step_validate(const kda_gated_delta_args* a) {

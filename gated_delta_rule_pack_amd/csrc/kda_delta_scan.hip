@@ -1,0 +1,563 @@
+// The gated delta rule's prompts where there are few sequences and heads: the chunks' own work in one parallel kernel, and a
+// walk over the chunks that many workgroups share. kda_delta.hip has the mathematics, and the walk for many units.
+//
+// delta_prep takes one chunk of one value head to a workgroup and leaves its record: T and P as operand fragments,
+// and the chunk's factors; the first head of a group leaves the scaled rows K' and Q', in fragment order too.
+//
+// delta_scan walks a sequence's chunks for 16 value channels to a workgroup. A chunk's chain (K' S -> what is to be learnt -> D
+// -> S) is cut over four waves, one for each 16 tokens and, of the state, for each quarter of the key channels; they meet
+// three times a chunk in LDS, where every value passes as an operand fragment. Four more waves make the outputs behind them.
+// All read their fragments straight from memory, a few chunks ahead, each fragment in one wave alone.
+#include <hip/hip_runtime.h>
+
+#include "kda_delta_device.h"
+
+namespace kda {
+namespace {
+
+// A record: T in two terms and P, six fragments each, then the factors.
+constexpr int kFragments = 6 * 1024;
+__device__ __forceinline__ constexpr int padded_fragment(int tt, int b) { return (tt < 2 ? tt : 2 * tt - 2 + b) * 1024; }
+struct Factors {
+  float h[kC], c[kC], e[kC], f[kC];
+  float total;
+  int shift;
+};
+static_assert(3 * kFragments + sizeof(Factors) <= kDeltaRecord, "record size");
+constexpr int kRecP = 2 * kFragments, kRecFactors = 3 * kFragments;
+
+// Sequence n's chunks have the places floor(cu[n] / 64) + n on: at least as many as it has chunks.
+__device__ __forceinline__ int chunk_place(const DeltaPlan& p, int n) { return bound(p, n) / kC + n; }
+// The last sequence that starts at or before a place.
+__device__ __forceinline__ int find_chunk(const DeltaPlan& p, int place, int lane) {
+  int lo = 0, hi = p.N;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) >> 6;
+    const int at = lo + lane * step;
+    const uint64_t mask = __ballot(at < hi && chunk_place(p, at) <= place) | 1;
+    lo += __builtin_amdgcn_readfirstlane(63 - __builtin_clzll(mask)) * step;
+    hi = min(lo + step, hi);
+  }
+  return lo;
+}
+
+// Tile (tt, st) of P or one term of T in a record, with the zeros beside a tile on the diagonal.
+__device__ __forceinline__ void put_padded(char* frags, int lane, int tt, int st, f16x4 x) {
+  char* at = frags + padded_fragment(tt, st >> 1) + lane * 16;
+  *reinterpret_cast<f16x4*>(at + (st & 1) * 8) = x;
+  if (tt == st && !(st & 1)) *reinterpret_cast<f16x4*>(at + 8) = f16x4{0, 0, 0, 0};
+}
+__device__ __forceinline__ void put_padded_t(char* rec, const Chunk& ch, int lane, int tt, int st, f32x4 x) {
+  x *= *reinterpret_cast<const f32x4*>(&ch.col[16 * st + 4 * (lane >> 4)]);
+  settle(x);
+  f16x4 hi, lo;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = (_Float16)x[i];
+    lo[i] = (_Float16)(x[i] - (float)hi[i]);
+  }
+  put_padded(rec, lane, tt, st, hi);
+  put_padded(rec + kFragments, lane, tt, st, lo);
+}
+
+// A tile's rows in LDS to memory as operand fragments: 16 rows and 32 channels to 1 KB.
+template <int D, int kThreads>
+__device__ __forceinline__ void store_fragments(const char* tile, char* to, int tid) {
+#pragma unroll
+  for (int i = 0; i < kC * D * 2 / 16 / kThreads; ++i) {
+    const int unit = i * kThreads + tid, lane = unit & 63, m = (unit >> 6) % (D / 32), tt = (unit >> 6) / (D / 32);
+    *reinterpret_cast<u32x4*>(to + unit * 16) =
+        *reinterpret_cast<const u32x4*>(tile + row_at<D>(16 * tt + (lane & 15)) + m * 64 + (lane >> 4) * 16);
+  }
+}
+
+template <int K, bool kF16In>
+__global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
+  constexpr int kThreads = 256, kWaves = 4;
+  __shared__ struct {
+    alignas(16) char k[kC * kRowBytes<K>];
+    alignas(16) char q[kC * kRowBytes<K>];
+    alignas(16) float blocks[10 * kBlock];
+    Chunk chunk;
+    RowInfo info[2][kC];
+  } sh;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int place = blockIdx.x / p.H, h = blockIdx.x % p.H, g4 = lane >> 4, l16 = lane & 15;
+  const int n = find_chunk(p, place, lane);
+  const int begin = bound(p, n), len = bound(p, n + 1) - begin;
+  const int in = (place - chunk_place(p, n)) * kC;
+  if (len <= 1 || in < 0 || in >= len) return;  // no chunk stands here (or the bounds fall)
+  const int count = min(len - in, kC);
+  const int64_t first = begin + in;
+  const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + (h / p.group) * p.q_h;
+  const uint16_t* k = reinterpret_cast<const uint16_t*>(p.k) + (h / p.group) * p.k_h;
+  Rows<K, kThreads> rq, rk;
+  rk.load(reinterpret_cast<const __bf16*>(k), p.k_t, first, count, tid);
+  rq.load(reinterpret_cast<const __bf16*>(q), p.q_t, first, count, tid);
+  float g = 0.f, beta = 0.f;
+  if (wave == kWaves - 1 && lane < count) {
+    const int64_t at = (first + lane) * p.H + h;
+    if (p.g) {
+      const int64_t ag = p.g_per_token ? at : h;
+      g = p.g_bf16 ? (float)reinterpret_cast<const __bf16*>(p.g)[ag] : reinterpret_cast<const float*>(p.g)[ag];
+    }
+    beta = p.beta_bf16 ? (float)reinterpret_cast<const __bf16*>(p.beta)[at] : reinterpret_cast<const float*>(p.beta)[at];
+  }
+  put_scaled<K, kThreads, kF16In>(rk, sh.k, sh.info[0], tid, true);
+  put_scaled<K, kThreads, kF16In>(rq, sh.q, sh.info[1], tid, p.normalize);
+  barrier_lds();
+  char* rec = p.records + ((int64_t)place * p.H + h) * kDeltaRecord;
+  if (h % p.group == 0) {
+    const int64_t at = ((int64_t)place * (p.H / p.group) + h / p.group) * (kC * K * 2);
+    store_fragments<K, kThreads>(sh.k, p.keys + at, tid);
+    store_fragments<K, kThreads>(sh.q, p.queries + at, tid);
+  }
+  const Chunk& ch = sh.chunk;
+  if (wave == kWaves - 1) {
+    put_chunk(sh.chunk, p, sh.info[0][lane], sh.info[1][lane], g, beta, lane);
+    Factors* to = reinterpret_cast<Factors*>(rec + kRecFactors);
+    to->h[lane] = ch.h[lane], to->c[lane] = ch.c[lane], to->e[lane] = ch.e[lane], to->f[lane] = ch.f[lane];
+    if (lane == 0) to->total = ch.total, to->shift = ch.shift;
+  }
+  f32x4 product[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    const int job = j * kWaves + wave, tile = job < 10 ? job : job - 10;
+    product[j] = tile_product<K>(sh.k, job < 10 ? sh.k : sh.q, lane, tile_t(tile), tile_s(tile));
+  }
+  barrier_lds();
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    const int job = j * kWaves + wave, tile = job < 10 ? job : job - 10, tt = tile_t(tile), st = tile_s(tile), t = 16 * tt + l16;
+    const f32x4 d = product[j] * tile_decay(ch, lane, tt, st) * *reinterpret_cast<const f32x4*>(&ch.rk[16 * st + 4 * g4]);
+    if (job < 10) {
+      const float bk = ch.bk[t];
+      float* to = sh.blocks + block_at(tt, st) + 4 * g4 * kBlockRow + l16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[i * kBlockRow] = 16 * st + 4 * g4 + i < t ? d[i] * bk : 0.f;
+    } else {
+      f16x4 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = (_Float16)(16 * st + 4 * g4 + i <= t ? d[i] : 0.f);
+      put_padded(rec + kRecP, lane, tt, st, x);
+    }
+  }
+  barrier_lds();
+  if (wave == 0) invert_diagonal(sh.blocks, lane);
+  barrier_lds();
+  const auto block = [&](int tt, int st) { return sh.blocks + block_at(tt, st); };
+  if (wave < 2) {
+    const int t = 2 * wave + 1, s = 2 * wave;
+    const f32x4 y = -block_product(block(s, s), block_product(block(t, s), block(t, t), lane, zero4()), lane, zero4());
+    put_padded_t(rec, ch, lane, t, s, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) block(t, s)[(4 * g4 + i) * kBlockRow + l16] = y[i];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int tt = 2 * (wave - 2) + j;
+      f32x4 y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = block(tt, tt)[(4 * g4 + i) * kBlockRow + l16];
+      put_padded_t(rec, ch, lane, tt, tt, y);
+    }
+  }
+  barrier_lds();
+  if (wave < 2) {
+    const int t = 2 + wave;
+    f32x4 z0 = block_product(block(2, 0), block(t, 2), lane, zero4()), z1 = block_product(block(2, 1), block(t, 2), lane, zero4());
+    if (wave == 1) z0 = block_product(block(3, 0), block(3, 3), lane, z0), z1 = block_product(block(3, 1), block(3, 3), lane, z1);
+    put_padded_t(rec, ch, lane, t, 0, -block_product(block(1, 0), z1, lane, block_product(block(0, 0), z0, lane, zero4())));
+    put_padded_t(rec, ch, lane, t, 1, -block_product(block(1, 1), z1, lane, zero4()));
+  }
+}
+
+constexpr int kBadTop = 1 << 20;  // exponent that stands for a value that is not finite
+
+template <int K>
+struct ScanShared {
+  static constexpr int KB = K / 32;
+  alignas(16) char s[KB][2][1024];   // the state's fragments, two terms
+  alignas(16) char x[2][2][1024];    // what is to be learnt
+  alignas(16) char d[2][2][1024];    // D times its decay to the chunk's end
+  alignas(16) char dh[2][2][1024];   // D
+  alignas(16) char k[kC * kRowBytes<K>];
+  alignas(16) int top[16][4];        // largest exponent of a channel, by wave
+  alignas(16) int bad[16][4];        // its first token whose value is not finite
+  alignas(16) float sum[2][4][16];
+};
+
+// A wave's share of a chunk on its way from memory, in the same registers for both kinds of wave.
+template <int K>
+struct Fetch {
+  u32x4 rows[K / 32];  // 16 tokens of K' (chain) or Q' (outputs)
+  f16x8 frag[2][2];    // [term][b] of T's row of tiles; [0][b] of P's
+  uint32_t v[4];       // V, chain
+  f32x4 h, c;          // chain: factors of tokens 4g + i; outputs: e and f of token l % 16 in h
+  float total;
+  int shift;
+};
+
+template <int K, int kTerms, bool kF16In>
+__global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
+  constexpr int KB = K / 32, KTW = K / 64;  // tiles of a chain wave's state
+  __shared__ ScanShared<K> sh;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+  // The slices of a unit run on one XCD, whose L2 then reads a record once.
+  const int slices = p.V / 16, j = blockIdx.x >> 3, slice = j % slices, unit = (j / slices) * 8 + (blockIdx.x & 7);
+  if (unit >= p.N * p.H) return;
+  const int n = unit / p.H, h = unit % p.H, v0 = slice * 16;
+  const bool chain = wave < 4;
+  const int w = wave & 3;  // token tile; a chain wave's part of the state too
+  const int begin = bound(p, n), len = max(bound(p, n + 1) - begin, 0);
+  const Slots slots = slots_of(p, n);
+  const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + h * p.v_h + v0;
+  uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + h * p.o_h + v0;
+
+  // The state: S[j] holds channel v0 + l16 and keys k0 + 4 j + i.
+  const int k0 = KTW == 2 ? 32 * w + 8 * g4 : 32 * (w >> 1) + 8 * g4 + 4 * (w & 1);
+  f32x4 S[KTW];
+#pragma unroll
+  for (int kt = 0; kt < KTW; ++kt) S[kt] = zero4();
+  if (chain && slots.from >= 0) {
+    const int64_t plane = plane_at(p, slots.from, h);
+#pragma unroll
+    for (int kt = 0; kt < KTW; ++kt) {
+      if (!p.kfirst) {
+        const int64_t at = plane + (int64_t)(v0 + l16) * K + k0 + 4 * kt;
+        if (p.state_dtype == kF32) S[kt] = load_state4<kF32>(p.state_in, at);
+        else if (p.state_dtype == kF16) S[kt] = load_state4<kF16>(p.state_in, at);
+        else S[kt] = load_state4<kBF16>(p.state_in, at);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t at = plane + (int64_t)(k0 + 4 * kt + i) * p.V + v0 + l16;
+          if (p.state_dtype == kF32) S[kt][i] = load_state1<kF32>(p.state_in, at);
+          else if (p.state_dtype == kF16) S[kt][i] = load_state1<kF16>(p.state_in, at);
+          else S[kt][i] = load_state1<kBF16>(p.state_in, at);
+        }
+      }
+    }
+  }
+  const auto store_state = [&]() {
+    if (!chain || slots.to < 0) return;
+    const int64_t plane = plane_at(p, slots.to, h);
+#pragma unroll
+    for (int kt = 0; kt < KTW; ++kt) {
+      if (!p.kfirst) {
+        const int64_t at = plane + (int64_t)(v0 + l16) * K + k0 + 4 * kt;
+        if (p.state_dtype == kF32) store_state4<kF32>(p.state_out, at, S[kt]);
+        else if (p.state_dtype == kF16) store_state4<kF16>(p.state_out, at, S[kt]);
+        else store_state4<kBF16>(p.state_out, at, S[kt]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t at = plane + (int64_t)(k0 + 4 * kt + i) * p.V + v0 + l16;
+          if (p.state_dtype == kF32) store_state1<kF32>(p.state_out, at, S[kt][i]);
+          else if (p.state_dtype == kF16) store_state1<kF16>(p.state_out, at, S[kt][i]);
+          else store_state1<kBF16>(p.state_out, at, S[kt][i]);
+        }
+      }
+    }
+  };
+  if (len == 0) {
+    store_state();
+    return;
+  }
+  if (len == 1) {  // the recurrent step, in fp32
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + (int64_t)begin * p.q_t + (h / p.group) * p.q_h;
+    const uint16_t* k = reinterpret_cast<const uint16_t*>(p.k) + (int64_t)begin * p.k_t + (h / p.group) * p.k_h;
+    const int64_t at = (int64_t)begin * p.H + h;
+    float g = 0.f;
+    if (p.g) {
+      const int64_t ag = p.g_per_token ? at : h;
+      g = p.g_bf16 ? (float)reinterpret_cast<const __bf16*>(p.g)[ag] : reinterpret_cast<const float*>(p.g)[ag];
+    }
+    float beta = p.beta_bf16 ? (float)reinterpret_cast<const __bf16*>(p.beta)[at] : reinterpret_cast<const float*>(p.beta)[at];
+    if (!(g <= 0.f)) beta = __builtin_nanf("");
+    const float decay = __expf(g);
+    // Every wave takes the whole rows: two channels a lane at K = 128.
+    float kk[KTW], qq[KTW];
+#pragma unroll
+    for (int i = 0; i < KTW; ++i) kk[i] = token_value<kF16In>(k[lane + 64 * i]), qq[i] = token_value<kF16In>(q[lane + 64 * i]);
+    float rk = 1.f, rq = 1.f;
+    if (p.normalize) rk = unit_factor(kk), rq = unit_factor(qq);
+    float kq = 0.f;
+#pragma unroll
+    for (int i = 0; i < KTW; ++i) kq += (kk[i] * rk) * (qq[i] * rq);
+    kq = wave_sum(kq);
+    float u = 0.f, o = 0.f, key[4 * KTW];
+    if (chain) {
+#pragma unroll
+      for (int i = 0; i < 4 * KTW; ++i) {
+        key[i] = token_value<kF16In>(k[k0 + i]) * rk;
+        u += S[i / 4][i % 4] * key[i];
+        o += S[i / 4][i % 4] * (token_value<kF16In>(q[k0 + i]) * rq);
+      }
+      u += __shfl_xor(u, 16), o += __shfl_xor(o, 16);
+      u += __shfl_xor(u, 32), o += __shfl_xor(o, 32);
+      if (g4 == 0) sh.sum[0][w][l16] = u, sh.sum[1][w][l16] = o;
+    }
+    barrier_lds();
+    if (!chain) return;
+    u = o = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u += sh.sum[0][i][l16], o += sh.sum[1][i][l16];
+    const float delta = beta * (token_value<kF16In>(v[(int64_t)begin * p.v_t + l16]) - decay * u);
+#pragma unroll
+    for (int i = 0; i < 4 * KTW; ++i) S[i / 4][i % 4] = S[i / 4][i % 4] * decay + delta * key[i];
+    store_state();
+    if (w == 0 && g4 == 0) {
+      const float x = p.scale * (decay * o + delta * kq);
+      out[(int64_t)begin * p.o_t + l16] = kF16In ? __builtin_bit_cast(uint16_t, (_Float16)x) : __builtin_bit_cast(uint16_t, to_bf16(x));
+    }
+    return;
+  }
+
+  const int chunks = (len + kC - 1) / kC, place = chunk_place(p, n);
+  const int H_qk = p.H / p.group, hq = h / p.group;
+  const auto record = [&](int i) { return p.records + ((int64_t)(place + i) * p.H + h) * kDeltaRecord; };
+  const auto rows = [&](int i) { return ((int64_t)(place + i) * H_qk + hq) * (kC * K * 2); };
+  // Rows of V or the outputs, 16 channels: those behind the sequence's end are out of range.
+  const auto buffer = [&](const uint16_t* base, int64_t stride, int i) {
+    const int count = min(len - i * kC, kC);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (begin + (int64_t)i * kC) * stride), (short)0,
+                                             ((count - 1) * (int)stride + 16) * 2, kBufWord3);
+  };
+  constexpr int kAhead = 3;
+  Fetch<K> fetched[kAhead];
+  const auto fetch = [&](Fetch<K>& f, int i) {
+    if (i >= chunks) return;
+    const char* rec = record(i);
+    const Factors* factors = reinterpret_cast<const Factors*>(rec + kRecFactors);
+    const char* from = (chain ? p.keys : p.queries) + rows(i) + w * (KB * 1024) + lane * 16;
+#pragma unroll
+    for (int m = 0; m < KB; ++m) f.rows[m] = *reinterpret_cast<const u32x4*>(from + m * 1024);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (b > 0 && w < 2) break;
+      const char* at = rec + (chain ? 0 : kRecP) + padded_fragment(w, b) + lane * 16;
+      f.frag[0][b] = *reinterpret_cast<const f16x8*>(at);
+      if (kTerms == 2 && chain) f.frag[1][b] = *reinterpret_cast<const f16x8*>(at + kFragments);
+    }
+    if (chain) {
+      const __amdgpu_buffer_rsrc_t r = buffer(v, p.v_t, i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f.v[e] = __builtin_amdgcn_raw_buffer_load_b16(r, ((16 * w + 4 * g4 + e) * (int)p.v_t + l16) * 2, 0, 0);
+      f.h = *reinterpret_cast<const f32x4*>(&factors->h[16 * w + 4 * g4]);
+      f.c = *reinterpret_cast<const f32x4*>(&factors->c[16 * w + 4 * g4]);
+      f.total = factors->total;
+      f.shift = factors->shift;
+    } else {
+      f.h[0] = factors->e[16 * w + l16];
+      f.h[1] = factors->f[16 * w + l16];
+    }
+  };
+  Scale scale;
+  scale.shift = 0;
+  scale.set(lane, 0);
+  const auto put_state = [&]() {
+#pragma unroll
+    for (int kt = 0; kt < KTW; ++kt) settle(S[kt]);
+    if constexpr (KTW == 2) {
+      const f16x8 hi = to_f16(S[0], S[1]);
+      *reinterpret_cast<f16x8*>(sh.s[w][0] + lane * 16) = hi;
+      if constexpr (kTerms == 2) *reinterpret_cast<f16x8*>(sh.s[w][1] + lane * 16) = rest_f16(S[0], S[1], hi);
+    } else {
+      put_half(sh.s[w >> 1][0], kTerms == 2 ? sh.s[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, S[0]);
+    }
+  };
+  const auto state_top = [&]() {
+    float m = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[kt][i]));
+    return exponent(m);
+  };
+  constexpr uint32_t kInf = kF16In ? 0x7c00u : 0x7f80u;
+
+  const auto step = [&](Fetch<K>& f, int i) {
+    // The state's fragments and the channel's largest exponent.
+    if (chain) {
+      if (f.shift != scale.shift) {
+#pragma unroll
+        for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], f.shift - scale.shift);
+        scale.shift = f.shift;
+      }
+      put_state();
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) most = max(most, f.v[e] & 0x7fffu);
+      int top = most >= kInf ? kBadTop : max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex);
+      top = channel_max(top);
+      if (g4 == 0) sh.top[l16][w] = top;
+    }
+    barrier_lds();
+    int first_bad = kC;
+    {
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      const i32x4 t = *reinterpret_cast<const i32x4*>(sh.top[l16]);
+      const int e = max(max(t[0], t[1]), max(t[2], t[3]));
+      if (__ballot(e > 4 || (e < 1 && e > kNoExponent / 2))) {  // the same in all waves
+        barrier_lds();
+        if (chain) {
+          uint32_t most = 0;
+          int bad = kC;
+#pragma unroll
+          for (int x = 3; x >= 0; --x) {
+            if ((f.v[x] & 0x7fffu) >= kInf) bad = 16 * w + 4 * g4 + x, f.v[x] = 0;
+            most = max(most, f.v[x] & 0x7fffu);
+          }
+          const int top = channel_max(max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex));
+          bad = -channel_max(-bad);
+          if (g4 == 0) sh.top[l16][w] = top, sh.bad[l16][w] = bad;
+        }
+        barrier_lds();
+        const i32x4 u = *reinterpret_cast<const i32x4*>(sh.top[l16]), b = *reinterpret_cast<const i32x4*>(sh.bad[l16]);
+        const int e = max(max(u[0], u[1]), max(u[2], u[3]));
+        first_bad = min(min(b[0], b[1]), min(b[2], b[3]));
+        const bool off = e > 4 || (e < 1 && e > kNoExponent / 2);
+        const int by = off ? min(max(scale.ex + 4 - e, -120), 120) - scale.ex : 0;
+        scale.set(lane, scale.ex + by);
+        if (chain) {
+#pragma unroll
+          for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) S[kt][x] = ldexp2(S[kt][x], by);
+          put_state();
+        }
+        barrier_lds();
+      }
+    }
+    f32x4 o = zero4();
+    if (chain) {
+#pragma unroll
+      for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(sh.k + 16 * w * kRowBytes<K> + row_at<K>(l16) + m * 64 + g4 * 16) = f.rows[m];
+      // K' S0, tokens 4g + i, channel l % 16, and what is to be learnt.
+      f32x4 a = zero4(), b = zero4();
+#pragma unroll
+      for (int m = 0; m < KB; ++m) {
+        const f16x8 k = __builtin_bit_cast(f16x8, f.rows[m]);
+        a = mfma(k, *reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), a);
+        if constexpr (kTerms == 2) b = mfma(k, *reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), b);
+      }
+      f32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(f.v[e]) * scale.v - f.h[e] * (a[e] + b[e]);
+      settle(x);
+      put_half(sh.x[w >> 1][0], kTerms == 2 ? sh.x[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, x);
+    } else {
+      // S0 Q', channels 4g + i, token l % 16.
+#pragma unroll
+      for (int m = 0; m < KB; ++m) {
+        const f16x8 q = __builtin_bit_cast(f16x8, f.rows[m]);
+        if constexpr (kF16In) o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), q, o);
+        o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), q, o);
+      }
+      o *= f.h[0];
+    }
+    barrier_lds();
+    if (chain) {
+      f32x4 a = zero4(), b = zero4(), c = zero4();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s > 0 && w < 2) break;
+        const f16x8 hi = *reinterpret_cast<const f16x8*>(sh.x[s][0] + lane * 16);
+        a = mfma(f.frag[0][s], hi, a);
+        if constexpr (kTerms == 2) {
+          b = mfma(f.frag[1][s], hi, b);
+          c = mfma(f.frag[0][s], *reinterpret_cast<const f16x8*>(sh.x[s][1] + lane * 16), c);
+        }
+      }
+      f32x4 d = a + (b + c);
+      settle(d);
+      put_half(sh.dh[w >> 1][0], kF16In ? sh.dh[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, d);
+      d *= f.c;
+      settle(d);
+      put_half(sh.d[w >> 1][0], kTerms == 2 ? sh.d[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, d);
+#pragma unroll
+      for (int kt = 0; kt < KTW; ++kt) S[kt] *= f.total;
+    }
+    barrier_lds();
+    if (chain) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const f16x8 hi = *reinterpret_cast<const f16x8*>(sh.d[s][0] + lane * 16);
+        f16x8 lo;
+        if constexpr (kTerms == 2) lo = *reinterpret_cast<const f16x8*>(sh.d[s][1] + lane * 16);
+#pragma unroll
+        for (int kt = 0; kt < KTW; ++kt) {
+          const f16x8 k = __builtin_bit_cast(f16x8, read_col<K, true>(sh.k, lane, 32 * s, w * KTW + kt));
+          if constexpr (kTerms == 2) S[kt] = mfma(k, lo, S[kt]);
+          S[kt] = mfma(k, hi, S[kt]);
+        }
+      }
+      if (first_bad < kC)
+#pragma unroll
+        for (int kt = 0; kt < KTW; ++kt) S[kt] = zero4() + __builtin_nanf("");
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s > 0 && w < 2) break;
+        if constexpr (kF16In) o = mfma(*reinterpret_cast<const f16x8*>(sh.dh[s][1] + lane * 16), f.frag[0][s], o);
+        o = mfma(*reinterpret_cast<const f16x8*>(sh.dh[s][0] + lane * 16), f.frag[0][s], o);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= f.h[1] * scale.out[e];
+      if (__ballot(first_bad < kC)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (16 * w + l16 >= __shfl(first_bad, 4 * g4 + e)) o[e] = __builtin_nanf("");
+      }
+      u32x2 packed;
+      if constexpr (kF16In) packed = __builtin_bit_cast(u32x2, f16x4{(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]});
+      else packed = __builtin_bit_cast(u32x2, bf16x4{to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])});
+      __builtin_amdgcn_raw_buffer_store_b64(packed, buffer(out, p.o_t, i), ((16 * w + l16) * (int)p.o_t + 4 * g4) * 2, 0, 0);
+    }
+    fetch(f, i + kAhead);
+  };
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) fetch(fetched[a], a);
+  for (int i = 0; i < chunks; i += kAhead) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (i + a < chunks) step(fetched[a], i + a);
+  }
+#pragma unroll
+  for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], -(scale.ex + scale.shift));
+  store_state();
+}
+
+template <int K, bool kF16In>
+int launch_prep(const DeltaPlan& p, hipStream_t s) {
+  delta_prep<K, kF16In><<<(unsigned)((int64_t)p.places * p.H), 256, 0, s>>>(p);
+  return (int)hipGetLastError();
+}
+template <int K, int kTerms, bool kF16In>
+int launch_scan(const DeltaPlan& p, hipStream_t s) {
+  const int64_t units = (int64_t)p.N * p.H;
+  delta_scan<K, kTerms, kF16In><<<(unsigned)((units + 7) / 8 * 8 * (p.V / 16)), 512, 0, s>>>(p);
+  return (int)hipGetLastError();
+}
+
+}  // namespace
+
+int launch_delta_prep(const DeltaPlan& p, void* stream) {
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (p.K == 128) return p.f16 ? launch_prep<128, true>(p, s) : launch_prep<128, false>(p, s);
+  return p.f16 ? launch_prep<64, true>(p, s) : launch_prep<64, false>(p, s);
+}
+
+int launch_delta_scan(const DeltaPlan& p, void* stream) {
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (p.f16) return p.K == 128 ? launch_scan<128, 2, true>(p, s) : launch_scan<64, 2, true>(p, s);
+  if (one_term(p)) return p.K == 128 ? launch_scan<128, 1, false>(p, s) : launch_scan<64, 1, false>(p, s);
+  return p.K == 128 ? launch_scan<128, 2, false>(p, s) : launch_scan<64, 2, false>(p, s);
+}
+
+}  // namespace kda

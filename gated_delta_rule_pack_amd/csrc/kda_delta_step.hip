@@ -10,6 +10,7 @@
 
 #include "kda_delta.h"
 #include "kda_device.h"
+#include "kda_unit.h"
 
 namespace kda {
 namespace {
@@ -34,35 +35,7 @@ __device__ __forceinline__ void store_token(void* base, int64_t at, int f16, flo
   if (f16) reinterpret_cast<_Float16*>(base)[at] = (_Float16)x;
   else reinterpret_cast<__bf16*>(base)[at] = to_bf16(x);
 }
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-  return x;
-}
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d));
-  return x;
-}
 __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) { return (a[0] * b[0] + a[1] * b[1]) + (a[2] * b[2] + a[3] * b[3]); }
-
-// 1 / sqrt(sum x^2 + eps) over the wave's K values, scaled by their largest power of two so that no finite
-// row overflows.
-template <int N>
-__device__ __forceinline__ float unit_factor(const float (&x)[N]) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(x[i]));
-  m = wave_max(m);
-  const int e = m > 0.f && m < INFINITY ? __builtin_amdgcn_frexp_expf(m) : 0;
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float y = __builtin_amdgcn_ldexpf(x[i], -e);
-    s += y * y;
-  }
-  return __builtin_amdgcn_ldexpf(rsqrtf(wave_sum(s) + __builtin_amdgcn_ldexpf(kNormEps, -2 * e)), -e);
-}
 
 // The state as stored is a plane of kRows x kCols, columns adjacent: [V][K] or, K-first, [K][V].
 // V-first: the lanes of a row sum over it. K-first: a lane holds 8 columns and walks rows; lanes and

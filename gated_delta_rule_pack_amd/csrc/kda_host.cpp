@@ -77,6 +77,8 @@ int rt_launch(void*, int kernel, const void* plan, void* s, void* start, void* s
     case 11: return kda::launch_delta_step(*reinterpret_cast<const kda::DeltaPlan*>(plan), s);
     case 12: return kda::launch_qk_norm(*reinterpret_cast<const kda::NormPlan*>(plan), s);
     case 13: return kda::launch_qk_norm_backward(*reinterpret_cast<const kda::NormPlan*>(plan), s);
+    case 14: return kda::launch_delta_prep(*reinterpret_cast<const kda::DeltaPlan*>(plan), s);
+    case 15: return kda::launch_delta_scan(*reinterpret_cast<const kda::DeltaPlan*>(plan), s);
   }
   const kda::Plan& p = *reinterpret_cast<const kda::Plan*>(plan);
   switch (kernel) {

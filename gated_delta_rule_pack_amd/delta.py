@@ -17,11 +17,12 @@ from .linear import _BF16, _Call, _check, _context, _fill_linear, _grads_on, _li
 __all__ = ["gated_delta_fwd", "gated_delta_step"]
 
 _F16 = torch.float16
+_PATHS = {"walk": _lib.KDA_DELTA_WALK, "scan": _lib.KDA_DELTA_SCAN}
 
 
 def make_gated_delta_args(q, k, v, g, beta, *, N=None, cu_seqlens=None, cu_seqlens_cpu=None, scale=None, normalize=False,
                           initial_state=None, final_state=None, state_cache=None, state_indices=None,
-                          has_initial_state=None, out=None, state_k_first=False) -> "_lib.GatedDeltaArgs":
+                          has_initial_state=None, out=None, state_k_first=False, path=None) -> "_lib.GatedDeltaArgs":
     """Fill a ``kda_gated_delta_args`` from tensors (no allocation), checking what the C side cannot see."""
     if beta is None:
         raise ValueError("beta is required")
@@ -51,12 +52,16 @@ def make_gated_delta_args(q, k, v, g, beta, *, N=None, cu_seqlens=None, cu_seqle
     a.beta = beta.data_ptr()
     if normalize:
         a.normalize = 1
+    if path is not None:
+        if path not in _PATHS:
+            raise ValueError(f"unknown path {path!r}: None, 'walk' or 'scan'")
+        a.path = _PATHS[path]
     return a
 
 
 def gated_delta_fwd(q, k, v, g, beta, cu_seqlens, *, cu_seqlens_cpu=None, scale=None, normalize=False, initial_state=None,
                     output_final_state=False, state_cache=None, state_indices=None, has_initial_state=None, out=None,
-                    workspace=None, stream=None, context=None, state_k_first=False):
+                    workspace=None, stream=None, context=None, state_k_first=False, path=None):
     """The gated delta rule over packed prompts, for each token and head
     ``S <- e^g S``, ``S <- S + beta (v - S k) k^T``, ``o = scale S q``.
 
@@ -67,7 +72,8 @@ def gated_delta_fwd(q, k, v, g, beta, cu_seqlens, *, cu_seqlens_cpu=None, scale=
     themselves, or at least keep ``|beta| |k|^2 <= 2``, beyond which a step grows the state.
     scale defaults to ``K ** -0.5``.
 
-    cu_seqlens, states, ``out``, ``workspace``, ``stream`` and ``context`` as in :func:`linear_fwd`. Returns ``(out,
+    cu_seqlens, states, ``out``, ``workspace``, ``stream`` and ``context`` as in :func:`linear_fwd`. ``path`` overrides the
+    choice between one kernel that walks every sequence of a head ("walk") and two that split the work further ("scan"). Returns ``(out,
     final_state)``, final_state None unless dense and asked for."""
     with _Call(q, stream) as call:
         _on(call.index, "k v g beta cu_seqlens initial_state state_cache state_indices has_initial_state out workspace",
@@ -85,7 +91,7 @@ def gated_delta_fwd(q, k, v, g, beta, cu_seqlens, *, cu_seqlens_cpu=None, scale=
         a = make_gated_delta_args(q, k, v, g, beta, cu_seqlens=cu_seqlens, cu_seqlens_cpu=cu_seqlens_cpu, scale=scale,
                                   normalize=normalize, initial_state=initial_state, final_state=final_state,
                                   state_cache=state_cache, state_indices=state_indices, has_initial_state=has_initial_state,
-                                  out=out, state_k_first=state_k_first)
+                                  out=out, state_k_first=state_k_first, path=path)
         lib = _lib.load()
         ref = ctypes.byref(a)
         need = lib.kda_gated_delta_fwd_workspace_bytes(ref)  # 0 for a refused call too: the call says why

@@ -499,12 +499,18 @@ size_t kda_rotary_args_size(void);
  * What is not finite stays causal in its own sequence and head: a row of q takes its own output; a row of k, a
  * beta, and a log decay that is NaN or above 0 every output from its token on and the final state; a value of v
  * or of a state row the same of its own channel. A token with k = 0 or beta = 0 only decays. */
+typedef enum kda_delta_path {
+  KDA_DELTA_POLICY = 0,
+  KDA_DELTA_WALK = 1, /* one kernel: a workgroup walks a sequence of a head; no workspace */
+  KDA_DELTA_SCAN = 2  /* two kernels: all chunks in parallel, then workgroups of 16 value channels scan them */
+} kda_delta_path;
 typedef struct kda_gated_delta_args {
   kda_linear_args lin;  /* inv_freq and seg_len must be 0; the tensors are of type dtype */
   const void* beta;     /* [T, H], contiguous */
   kda_dtype beta_dtype; /* KDA_F32 or KDA_BF16 */
   kda_dtype dtype;      /* of q, k, v and out: KDA_BF16 or KDA_F16 */
   int32_t normalize;    /* 0 or 1 */
+  int32_t path;         /* kda_gated_delta_fwd only: a kda_delta_path, 0 = the policy */
 } kda_gated_delta_args;
 
 /* Prompts. Errors as kda_linear_fwd. */

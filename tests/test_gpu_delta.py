@@ -44,13 +44,14 @@ PROMPTS = {
 }
 
 
+@pytest.mark.parametrize("path", ["walk", "scan"])
 @pytest.mark.parametrize("name", sorted(PROMPTS))
-def test_prompts(name):
+def test_prompts(name, path):
     case = DeltaCase(**PROMPTS[name], seed=11)
     d = case.device()
     out = torch.full((case.T, case.H, case.V), 7.0, dtype=case.dtype, device="cuda")
     before = d["store"].clone() if "store" in d else None
-    _, final = case.forward(d, out=out)
+    _, final = case.forward(d, out=out, path=path)
     check(case, out, d, final)
     rows = int(case.cu[-1])
     assert torch.all(out[rows:] == 7.0)
