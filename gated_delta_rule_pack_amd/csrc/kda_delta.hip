@@ -191,7 +191,6 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, 2) void delta_walk(const DeltaPla
     for (int tt = 0; tt < 4; ++tt) x[tt] = o[tt] = zero4();
 #pragma unroll
     for (int m = 0; m < KB; ++m) {
-      settle(S[2 * m]), settle(S[2 * m + 1]);
       const f16x8 hi = to_f16(S[2 * m], S[2 * m + 1]);
       if constexpr (kTerms == 2) {
         const f16x8 lo = rest_f16(S[2 * m], S[2 * m + 1], hi);
@@ -218,7 +217,6 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, 2) void delta_walk(const DeltaPla
         x[tt][i] = y * scale.v - hh[i] * x[tt][i];
         o[tt][i] *= e;
       }
-      settle(x[tt]);
     }
     barrier_lds();
     // T below the diagonal: first beside it, then the square of four blocks.
@@ -319,10 +317,7 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, 2) void delta_walk(const DeltaPla
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) S[kt] *= total;
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      d[tt] *= *reinterpret_cast<const f32x4*>(&ch.c[16 * tt + 4 * g4]);
-      settle(d[tt]);
-    }
+    for (int tt = 0; tt < 4; ++tt) d[tt] *= *reinterpret_cast<const f32x4*>(&ch.c[16 * tt + 4 * g4]);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const f16x8 hi = to_f16(d[2 * b], d[2 * b + 1]);

@@ -20,34 +20,35 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) { return __buil
 __device__ __forceinline__ f32x4 mfma32(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ float ldexp2(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
 
+// Two fp32 values as fp16, low first, rounded to nearest.
+__device__ __forceinline__ uint32_t pair_f16(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  uint32_t r = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+  asm("" : "+v"(r));
+  return r;
+}
+// What two values leave of those, exactly, rounded to fp16: one instruction each. (Written as conversions and differences
+// the compiler takes three; and where a and b are a product or a sum it makes the first term of the exact value in one
+// instruction and this one of the rounded value: where those fall on two sides of a middle, both terms miss it by 2^-10.)
+__device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t first) {
+  const f16x2 h = __builtin_bit_cast(f16x2, first);
+  const f16x2 r = {(_Float16)__builtin_fmaf((float)h[0], -1.f, a), (_Float16)__builtin_fmaf((float)h[1], -1.f, b)};
+  return __builtin_bit_cast(uint32_t, r);
+}
 // Two tiles (rows 4g + i and 16 + 4g + i) as an operand, in one or two terms.
 __device__ __forceinline__ f16x8 to_f16(f32x4 a, f32x4 b) {
-  f16x8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = (_Float16)a[i], r[4 + i] = (_Float16)b[i];
-  return r;
+  return __builtin_bit_cast(f16x8, u32x4{pair_f16(a[0], a[1]), pair_f16(a[2], a[3]), pair_f16(b[0], b[1]), pair_f16(b[2], b[3])});
 }
-// A value that is split into terms is rounded to fp32 first, once: of a product or a sum the compiler would otherwise make the
-// first term in one instruction, which rounds the exact value, and the second from the rounded one. Where those fall on two sides
-// of a middle the terms miss the value by 2^-10 of it.
-__device__ __forceinline__ void settle(f32x4& x) { asm("" : "+v"(x)); }
 __device__ __forceinline__ f16x8 rest_f16(f32x4 a, f32x4 b, f16x8 hi) {
-  f16x8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = (_Float16)(a[i] - (float)hi[i]), r[4 + i] = (_Float16)(b[i] - (float)hi[4 + i]);
-  return r;
+  const u32x4 h = __builtin_bit_cast(u32x4, hi);
+  return __builtin_bit_cast(f16x8, u32x4{rest_pair(a[0], a[1], h[0]), rest_pair(a[2], a[3], h[1]), rest_pair(b[0], b[1], h[2]),
+                                         rest_pair(b[2], b[3], h[3])});
 }
-
 // One tile (rows 4g + i) as half a fragment, in one or two terms.
 __device__ __forceinline__ void put_half(char* high, char* low, int at, f32x4 x) {
-  f16x4 hi, lo;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = (_Float16)x[i];
-    lo[i] = (_Float16)(x[i] - (float)hi[i]);
-  }
-  *reinterpret_cast<f16x4*>(high + at) = hi;
-  if (low) *reinterpret_cast<f16x4*>(low + at) = lo;
+  const u32x2 h = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])};
+  *reinterpret_cast<u32x2*>(high + at) = h;
+  if (low) *reinterpret_cast<u32x2*>(low + at) = u32x2{rest_pair(x[0], x[1], h[0]), rest_pair(x[2], x[3], h[1])};
 }
 
 // A token's element of a 16-bit word, by type.
@@ -256,15 +257,9 @@ __device__ __forceinline__ f32x4 block_product(const float* left, f32x4 right, i
 __device__ __forceinline__ void put_t(char* frags, const Chunk& ch, int lane, int tt, int st, f32x4 x) {
   const f32x4 col = *reinterpret_cast<const f32x4*>(&ch.col[16 * st + 4 * (lane >> 4)]);
   x *= col;
-  settle(x);
-  f16x4 hi, lo;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = (_Float16)x[i];
-    lo[i] = (_Float16)(x[i] - (float)hi[i]);
-  }
-  put_fragment(frags, lane, tt, st, hi);
-  put_fragment(frags + kTermP, lane, tt, st, lo);
+  const u32x2 hi = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}, lo = {rest_pair(x[0], x[1], hi[0]), rest_pair(x[2], x[3], hi[1])};
+  put_fragment(frags, lane, tt, st, __builtin_bit_cast(f16x4, hi));
+  put_fragment(frags + kTermP, lane, tt, st, __builtin_bit_cast(f16x4, lo));
 }
 
 // Powers of two that hold one value channel's state and V in fp16's range: S' = S 2^{ex + shift}, V' = V 2^ex. The larger of
@@ -286,10 +281,12 @@ struct Scale {
 // The exponent of x >= 0: x < 2^e.
 constexpr int kNoExponent = -4096;
 __device__ __forceinline__ int exponent(float x) { return x > 0.f && x < INFINITY ? __builtin_amdgcn_frexp_expf(x) : kNoExponent; }
-// Over the four lanes that hold one channel.
+// Over the four lanes that hold one channel: exchanges of half waves and of rows, without LDS.
 __device__ __forceinline__ int channel_max(int x) {
-  x = max(x, __shfl_xor(x, 16));
-  return max(x, __shfl_xor(x, 32));
+  const auto a = __builtin_amdgcn_permlane32_swap((unsigned)x, (unsigned)x, false, false);
+  x = max((int)a[0], (int)a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap((unsigned)x, (unsigned)x, false, false);
+  return max((int)b[0], (int)b[1]);
 }
 
 }  // namespace kda

@@ -10,6 +10,9 @@
 // All read their fragments straight from memory, a few chunks ahead, each fragment in one wave alone.
 #include <hip/hip_runtime.h>
 
+#include <cstddef>
+#include <type_traits>
+
 #include "kda_delta_device.h"
 
 namespace kda {
@@ -49,15 +52,9 @@ __device__ __forceinline__ void put_padded(char* frags, int lane, int tt, int st
 }
 __device__ __forceinline__ void put_padded_t(char* rec, const Chunk& ch, int lane, int tt, int st, f32x4 x) {
   x *= *reinterpret_cast<const f32x4*>(&ch.col[16 * st + 4 * (lane >> 4)]);
-  settle(x);
-  f16x4 hi, lo;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = (_Float16)x[i];
-    lo[i] = (_Float16)(x[i] - (float)hi[i]);
-  }
-  put_padded(rec, lane, tt, st, hi);
-  put_padded(rec + kFragments, lane, tt, st, lo);
+  const u32x2 hi = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}, lo = {rest_pair(x[0], x[1], hi[0]), rest_pair(x[2], x[3], hi[1])};
+  put_padded(rec, lane, tt, st, __builtin_bit_cast(f16x4, hi));
+  put_padded(rec + kFragments, lane, tt, st, __builtin_bit_cast(f16x4, lo));
 }
 
 // A tile's rows in LDS to memory as operand fragments: 16 rows and 32 channels to 1 KB.
@@ -209,7 +206,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   const int n = unit / p.H, h = unit % p.H, v0 = slice * 16;
   const bool chain = wave < 4;
   const int w = wave & 3;  // token tile; a chain wave's part of the state too
-  const int begin = bound(p, n), len = max(bound(p, n + 1) - begin, 0);
+  const int begin = __builtin_amdgcn_readfirstlane(bound(p, n));
+  const int len = __builtin_amdgcn_readfirstlane(max(bound(p, n + 1) - begin, 0));
   const Slots slots = slots_of(p, n);
   const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + h * p.v_h + v0;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + h * p.o_h + v0;
@@ -316,141 +314,261 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 
   const int chunks = (len + kC - 1) / kC, place = chunk_place(p, n);
   const int H_qk = p.H / p.group, hq = h / p.group;
-  const auto record = [&](int i) { return p.records + ((int64_t)(place + i) * p.H + h) * kDeltaRecord; };
-  const auto rows = [&](int i) { return ((int64_t)(place + i) * H_qk + hq) * (kC * K * 2); };
+  const auto whole = [](const char* at, int bytes) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), (short)0, bytes, kBufWord3); };
   // Rows of V or the outputs, 16 channels: those behind the sequence's end are out of range.
-  const auto buffer = [&](const uint16_t* base, int64_t stride, int i) {
-    const int count = min(len - i * kC, kC);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (begin + (int64_t)i * kC) * stride), (short)0,
-                                             ((count - 1) * (int)stride + 16) * 2, kBufWord3);
+  const auto buffer = [&](const uint16_t* at, int64_t stride, int left) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(at), (short)0, ((min(left, kC) - 1) * (int)stride + 16) * 2, kBufWord3);
   };
   constexpr int kAhead = 3;
   Fetch<K> fetched[kAhead];
-  const auto fetch = [&](Fetch<K>& f, int i) {
-    if (i >= chunks) return;
-    const char* rec = record(i);
-    const Factors* factors = reinterpret_cast<const Factors*>(rec + kRecFactors);
-    const char* from = (chain ? p.keys : p.queries) + rows(i) + w * (KB * 1024) + lane * 16;
+  const auto load = [](__amdgpu_buffer_rsrc_t r, int at, int uniform) { return __builtin_amdgcn_raw_buffer_load_b128(r, at, uniform, 0); };
+  // Where the next chunk to be fetched lies. Behind the last chunk it is fetched again, without a branch, so that a wait can count
+  // the loads behind its own.
+  const char* next_record = p.records + ((int64_t)place * p.H + h) * kDeltaRecord;
+  const char* next_rows = (chain ? p.keys : p.queries) + ((int64_t)place * H_qk + hq) * (kC * K * 2);
+  const uint16_t* next_v = v + (int64_t)begin * p.v_t;
+  int next_left = len;
+  const int at16 = lane * 16, at_row = l16 * 4, at_group = g4 * 16, v_row = (int)p.v_t * 2, at_v = 4 * g4 * v_row + l16 * 2;
+  const auto advance = [&]() {
+    const bool more = next_left > kC;
+    next_record += more ? (int64_t)p.H * kDeltaRecord : 0;
+    next_rows += more ? (int64_t)H_qk * (kC * K * 2) : 0;
+    next_v += more ? p.v_t * kC : 0;
+    next_left -= more ? kC : 0;
+  };
+  const auto fetch_rows = [&](Fetch<K>& f) {
+    const __amdgpu_buffer_rsrc_t row = whole(next_rows, kC * K * 2);
 #pragma unroll
-    for (int m = 0; m < KB; ++m) f.rows[m] = *reinterpret_cast<const u32x4*>(from + m * 1024);
+    for (int m = 0; m < KB; ++m) f.rows[m] = load(row, at16 + m * 1024, w * (KB * 1024));
+  };
+  const auto fetch_record = [&](Fetch<K>& f, auto for_chain) {
+    const __amdgpu_buffer_rsrc_t rec = whole(next_record, kDeltaRecord);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if (b > 0 && w < 2) break;
-      const char* at = rec + (chain ? 0 : kRecP) + padded_fragment(w, b) + lane * 16;
-      f.frag[0][b] = *reinterpret_cast<const f16x8*>(at);
-      if (kTerms == 2 && chain) f.frag[1][b] = *reinterpret_cast<const f16x8*>(at + kFragments);
+    for (int b = 0; b < 2; ++b) {  // the first two rows of tiles have one fragment
+      const int from = (for_chain ? 0 : kRecP) + padded_fragment(w, w < 2 ? 0 : b);
+      f.frag[0][b] = __builtin_bit_cast(f16x8, load(rec, at16, from));
+      if constexpr (kTerms == 2 && for_chain) f.frag[1][b] = __builtin_bit_cast(f16x8, load(rec, at16, from + kFragments));
     }
-    if (chain) {
-      const __amdgpu_buffer_rsrc_t r = buffer(v, p.v_t, i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f.v[e] = __builtin_amdgcn_raw_buffer_load_b16(r, ((16 * w + 4 * g4 + e) * (int)p.v_t + l16) * 2, 0, 0);
-      f.h = *reinterpret_cast<const f32x4*>(&factors->h[16 * w + 4 * g4]);
-      f.c = *reinterpret_cast<const f32x4*>(&factors->c[16 * w + 4 * g4]);
-      f.total = factors->total;
-      f.shift = factors->shift;
+    if constexpr (for_chain) {
+      f.c = __builtin_bit_cast(f32x4, load(rec, at_group, kRecFactors + (int)offsetof(Factors, c) + 64 * w));
+      const u32x2 last = __builtin_amdgcn_raw_buffer_load_b64(rec, 0, kRecFactors + (int)offsetof(Factors, total), 0);
+      f.total = __uint_as_float(last[0]);
+      f.shift = (int)last[1];
     } else {
-      f.h[0] = factors->e[16 * w + l16];
-      f.h[1] = factors->f[16 * w + l16];
+      f.h[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, at_row, kRecFactors + (int)offsetof(Factors, e) + 64 * w, 0));
+      f.h[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, at_row, kRecFactors + (int)offsetof(Factors, f) + 64 * w, 0));
     }
+  };
+  const auto fetch_v = [&](Fetch<K>& f) {
+    const __amdgpu_buffer_rsrc_t r = buffer(next_v, p.v_t, next_left);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.v[e] = __builtin_amdgcn_raw_buffer_load_b16(r, at_v + e * v_row, 16 * w * v_row, 0);
+    f.h = __builtin_bit_cast(f32x4, load(whole(next_record, kDeltaRecord), at_group, kRecFactors + (int)offsetof(Factors, h) + 64 * w));
   };
   Scale scale;
   scale.shift = 0;
   scale.set(lane, 0);
-  const auto put_state = [&]() {
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  const auto largest = [&](const int (&of)[16][4]) {
+    const i32x4 t = *reinterpret_cast<const i32x4*>(of[l16]);
+    return max(max(t[0], t[1]), max(t[2], t[3]));
+  };
+  const auto least = [&](const int (&of)[16][4]) {
+    const i32x4 t = *reinterpret_cast<const i32x4*>(of[l16]);
+    return min(min(t[0], t[1]), min(t[2], t[3]));
+  };
+  const auto outside = [](int e) { return e > 4 || (e < 1 && e > kNoExponent / 2); };
+  const auto rescaled = [&](int e) { return outside(e) ? min(max(scale.ex + 4 - e, -120), 120) - scale.ex : 0; };
+  const auto walk_chunks = [&](auto step) {
+    int i = 0;
+    for (; i + kAhead <= chunks; i += kAhead) {
 #pragma unroll
-    for (int kt = 0; kt < KTW; ++kt) settle(S[kt]);
-    if constexpr (KTW == 2) {
-      const f16x8 hi = to_f16(S[0], S[1]);
-      *reinterpret_cast<f16x8*>(sh.s[w][0] + lane * 16) = hi;
-      if constexpr (kTerms == 2) *reinterpret_cast<f16x8*>(sh.s[w][1] + lane * 16) = rest_f16(S[0], S[1], hi);
-    } else {
-      put_half(sh.s[w >> 1][0], kTerms == 2 ? sh.s[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, S[0]);
+      for (int a = 0; a < kAhead; ++a) step(fetched[a], i + a);
     }
-  };
-  const auto state_top = [&]() {
-    float m = 0.f;
 #pragma unroll
-    for (int kt = 0; kt < KTW; ++kt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[kt][i]));
-    return exponent(m);
+    for (int a = 0; a + 1 < kAhead; ++a)
+      if (i + a < chunks) step(fetched[a], i + a);
   };
-  constexpr uint32_t kInf = kF16In ? 0x7c00u : 0x7f80u;
-
-  const auto step = [&](Fetch<K>& f, int i) {
-    // The state's fragments and the channel's largest exponent.
-    if (chain) {
-      if (f.shift != scale.shift) {
+  // Both kinds of wave take the same barriers: three a chunk, and three more where a channel's scale has to move or a value
+  // is not finite, which all of them see in sh.top.
+  if (chain) {
+    constexpr uint32_t kInf = kF16In ? 0x7c00u : 0x7f80u;
+    const auto put_state = [&]() {
+      if constexpr (KTW == 2) {
+        const f16x8 hi = to_f16(S[0], S[1]);
+        *reinterpret_cast<f16x8*>(sh.s[w][0] + lane * 16) = hi;
+        if constexpr (kTerms == 2) *reinterpret_cast<f16x8*>(sh.s[w][1] + lane * 16) = rest_f16(S[0], S[1], hi);
+      } else {
+        put_half(sh.s[w >> 1][0], kTerms == 2 ? sh.s[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, S[0]);
+      }
+    };
+    const auto state_top = [&]() {
+      float m = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[kt][i]));
+      return exponent(m);
+    };
+    char* const k_rows = sh.k + 16 * w * kRowBytes<K> + row_at<K>(l16) + g4 * 16;
+    __builtin_amdgcn_s_setprio(3);  // the outputs' waves fill its gaps
+    const auto step = [&](Fetch<K>& f, int i) {
+      const int shift = __builtin_amdgcn_readfirstlane(f.shift);
+      const float total = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(f.total)));
+      if (shift != scale.shift) {
 #pragma unroll
         for (int kt = 0; kt < KTW; ++kt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], f.shift - scale.shift);
-        scale.shift = f.shift;
+          for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], shift - scale.shift);
+        scale.shift = shift;
       }
+      // The state's fragments and the channel's largest exponent.
       put_state();
-      uint32_t most = 0;
+      uint32_t value[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) most = max(most, f.v[e] & 0x7fffu);
-      int top = most >= kInf ? kBadTop : max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex);
-      top = channel_max(top);
-      if (g4 == 0) sh.top[l16][w] = top;
-    }
-    barrier_lds();
-    int first_bad = kC;
-    {
-      typedef int i32x4 __attribute__((ext_vector_type(4)));
-      const i32x4 t = *reinterpret_cast<const i32x4*>(sh.top[l16]);
-      const int e = max(max(t[0], t[1]), max(t[2], t[3]));
-      if (__ballot(e > 4 || (e < 1 && e > kNoExponent / 2))) {  // the same in all waves
-        barrier_lds();
-        if (chain) {
-          uint32_t most = 0;
-          int bad = kC;
+      for (int e = 0; e < 4; ++e) value[e] = f.v[e];
+      uint32_t most = max(max(value[0] & 0x7fffu, value[1] & 0x7fffu), max(value[2] & 0x7fffu, value[3] & 0x7fffu));
+      int top = max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex);
+      sh.top[l16][w] = channel_max(most >= kInf ? kBadTop : top);
+      barrier_lds();
+      f16x8 hi[KB], lo[KB];
+      const int tops = largest(sh.top);
+      const auto read_state = [&]() {
 #pragma unroll
-          for (int x = 3; x >= 0; --x) {
-            if ((f.v[x] & 0x7fffu) >= kInf) bad = 16 * w + 4 * g4 + x, f.v[x] = 0;
-            most = max(most, f.v[x] & 0x7fffu);
-          }
-          const int top = channel_max(max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex));
-          bad = -channel_max(-bad);
-          if (g4 == 0) sh.top[l16][w] = top, sh.bad[l16][w] = bad;
+        for (int m = 0; m < KB; ++m) {
+          hi[m] = *reinterpret_cast<const f16x8*>(sh.s[m][0] + at16);
+          if constexpr (kTerms == 2) lo[m] = *reinterpret_cast<const f16x8*>(sh.s[m][1] + at16);
         }
+      };
+      read_state();
+      __builtin_amdgcn_sched_barrier(0);  // all reads before the first wait
+      int first_bad = kC;
+      if (__ballot(outside(tops))) {
         barrier_lds();
-        const i32x4 u = *reinterpret_cast<const i32x4*>(sh.top[l16]), b = *reinterpret_cast<const i32x4*>(sh.bad[l16]);
-        const int e = max(max(u[0], u[1]), max(u[2], u[3]));
-        first_bad = min(min(b[0], b[1]), min(b[2], b[3]));
-        const bool off = e > 4 || (e < 1 && e > kNoExponent / 2);
-        const int by = off ? min(max(scale.ex + 4 - e, -120), 120) - scale.ex : 0;
+        int bad = kC;
+        most = 0;
+#pragma unroll
+        for (int x = 3; x >= 0; --x) {
+          if ((value[x] & 0x7fffu) >= kInf) bad = 16 * w + 4 * g4 + x, value[x] = 0;
+          most = max(most, value[x] & 0x7fffu);
+        }
+        sh.top[l16][w] = channel_max(max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex));
+        sh.bad[l16][w] = -channel_max(-bad);
+        barrier_lds();
+        first_bad = least(sh.bad);
+        const int by = rescaled(largest(sh.top));
         scale.set(lane, scale.ex + by);
-        if (chain) {
 #pragma unroll
-          for (int kt = 0; kt < KTW; ++kt)
+        for (int kt = 0; kt < KTW; ++kt)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) S[kt][x] = ldexp2(S[kt][x], by);
-          put_state();
-        }
+          for (int x = 0; x < 4; ++x) S[kt][x] = ldexp2(S[kt][x], by);
+        put_state();
         barrier_lds();
-      }
-    }
-    f32x4 o = zero4();
-    if (chain) {
-#pragma unroll
-      for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(sh.k + 16 * w * kRowBytes<K> + row_at<K>(l16) + m * 64 + g4 * 16) = f.rows[m];
-      // K' S0, tokens 4g + i, channel l % 16, and what is to be learnt.
-      f32x4 a = zero4(), b = zero4();
-#pragma unroll
-      for (int m = 0; m < KB; ++m) {
-        const f16x8 k = __builtin_bit_cast(f16x8, f.rows[m]);
-        a = mfma(k, *reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), a);
-        if constexpr (kTerms == 2) b = mfma(k, *reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), b);
+        read_state();
       }
       f32x4 x;
+      {
+        // K' S0, tokens 4g + i, channel l % 16, and what is to be learnt.
+        f32x4 a = zero4(), b = zero4();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(f.v[e]) * scale.v - f.h[e] * (a[e] + b[e]);
-      settle(x);
-      put_half(sh.x[w >> 1][0], kTerms == 2 ? sh.x[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, x);
-    } else {
+        for (int m = 0; m < KB; ++m) {
+          const f16x8 k = __builtin_bit_cast(f16x8, f.rows[m]);
+          a = mfma(k, hi[m], a);
+          if constexpr (kTerms == 2) b = mfma(k, lo[m], b);
+        }
+#pragma unroll
+        for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(k_rows + m * 64) = f.rows[m];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(value[e]) * scale.v - f.h[e] * (a[e] + b[e]);
+        put_half(sh.x[w >> 1][0], kTerms == 2 ? sh.x[w >> 1][1] : nullptr, at16 + (w & 1) * 8, x);
+      }
+      barrier_lds();
+      f16x8 kk[2][KTW];
+      {
+        f16x8 xh[2], xl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          xh[s] = *reinterpret_cast<const f16x8*>(sh.x[s][0] + at16);
+          if constexpr (kTerms == 2) xl[s] = *reinterpret_cast<const f16x8*>(sh.x[s][1] + at16);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int kt = 0; kt < KTW; ++kt) kk[s][kt] = __builtin_bit_cast(f16x8, read_col<K, true>(sh.k, lane, 32 * s, w * KTW + kt));
+        fetch_rows(f);
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 a = mfma(f.frag[0][0], xh[0], zero4()), b = zero4(), c = zero4();
+        if constexpr (kTerms == 2) {
+          b = mfma(f.frag[1][0], xh[0], b);
+          c = mfma(f.frag[0][0], xl[0], c);
+        }
+        if (w >= 2) {
+          a = mfma(f.frag[0][1], xh[1], a);
+          if constexpr (kTerms == 2) {
+            b = mfma(f.frag[1][1], xh[1], b);
+            c = mfma(f.frag[0][1], xl[1], c);
+          }
+        }
+        f32x4 d = a + (b + c), decayed = d * f.c;
+        put_half(sh.d[w >> 1][0], kTerms == 2 ? sh.d[w >> 1][1] : nullptr, at16 + (w & 1) * 8, decayed);
+        put_half(sh.dh[w >> 1][0], kF16In ? sh.dh[w >> 1][1] : nullptr, at16 + (w & 1) * 8, d);
+#pragma unroll
+        for (int kt = 0; kt < KTW; ++kt) S[kt] *= total;
+      }
+      barrier_lds();
+      {
+        f16x8 dh[2], dl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          dh[s] = *reinterpret_cast<const f16x8*>(sh.d[s][0] + at16);
+          if constexpr (kTerms == 2) dl[s] = *reinterpret_cast<const f16x8*>(sh.d[s][1] + at16);
+        }
+        fetch_v(f);
+        fetch_record(f, std::true_type());
+        advance();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+          for (int kt = 0; kt < KTW; ++kt) {
+            if constexpr (kTerms == 2) S[kt] = mfma(kk[s][kt], dl[s], S[kt]);
+          }
+#pragma unroll
+          for (int kt = 0; kt < KTW; ++kt) S[kt] = mfma(kk[s][kt], dh[s], S[kt]);
+        }
+      }
+      if (first_bad < kC)
+#pragma unroll
+        for (int kt = 0; kt < KTW; ++kt) S[kt] = zero4() + __builtin_nanf("");
+    };
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      fetch_rows(fetched[a]);
+      fetch_v(fetched[a]);
+      fetch_record(fetched[a], std::true_type());
+      advance();
+      __builtin_amdgcn_sched_barrier(0);  // in this order, for the first chunks' waits
+    }
+    walk_chunks(step);
+#pragma unroll
+    for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], -(scale.ex + scale.shift));
+    store_state();
+  } else {
+    const int at_out = ((16 * w + l16) * (int)p.o_t + 4 * g4) * 2;
+    const auto step = [&](Fetch<K>& f, int i) {
+      barrier_lds();
+      int first_bad = kC;
+      if (__ballot(outside(largest(sh.top)))) {
+        barrier_lds();
+        barrier_lds();
+        first_bad = least(sh.bad);
+        scale.set(lane, scale.ex + rescaled(largest(sh.top)));
+        barrier_lds();
+      }
       // S0 Q', channels 4g + i, token l % 16.
+      f32x4 o = zero4();
 #pragma unroll
       for (int m = 0; m < KB; ++m) {
         const f16x8 q = __builtin_bit_cast(f16x8, f.rows[m]);
@@ -458,47 +576,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), q, o);
       }
       o *= f.h[0];
-    }
-    barrier_lds();
-    if (chain) {
-      f32x4 a = zero4(), b = zero4(), c = zero4();
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s > 0 && w < 2) break;
-        const f16x8 hi = *reinterpret_cast<const f16x8*>(sh.x[s][0] + lane * 16);
-        a = mfma(f.frag[0][s], hi, a);
-        if constexpr (kTerms == 2) {
-          b = mfma(f.frag[1][s], hi, b);
-          c = mfma(f.frag[0][s], *reinterpret_cast<const f16x8*>(sh.x[s][1] + lane * 16), c);
-        }
-      }
-      f32x4 d = a + (b + c);
-      settle(d);
-      put_half(sh.dh[w >> 1][0], kF16In ? sh.dh[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, d);
-      d *= f.c;
-      settle(d);
-      put_half(sh.d[w >> 1][0], kTerms == 2 ? sh.d[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, d);
-#pragma unroll
-      for (int kt = 0; kt < KTW; ++kt) S[kt] *= f.total;
-    }
-    barrier_lds();
-    if (chain) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const f16x8 hi = *reinterpret_cast<const f16x8*>(sh.d[s][0] + lane * 16);
-        f16x8 lo;
-        if constexpr (kTerms == 2) lo = *reinterpret_cast<const f16x8*>(sh.d[s][1] + lane * 16);
-#pragma unroll
-        for (int kt = 0; kt < KTW; ++kt) {
-          const f16x8 k = __builtin_bit_cast(f16x8, read_col<K, true>(sh.k, lane, 32 * s, w * KTW + kt));
-          if constexpr (kTerms == 2) S[kt] = mfma(k, lo, S[kt]);
-          S[kt] = mfma(k, hi, S[kt]);
-        }
-      }
-      if (first_bad < kC)
-#pragma unroll
-        for (int kt = 0; kt < KTW; ++kt) S[kt] = zero4() + __builtin_nanf("");
-    } else {
+      barrier_lds();
+      barrier_lds();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (s > 0 && w < 2) break;
@@ -512,25 +591,23 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         for (int e = 0; e < 4; ++e)
           if (16 * w + l16 >= __shfl(first_bad, 4 * g4 + e)) o[e] = __builtin_nanf("");
       }
+      fetch_rows(f);
+      fetch_record(f, std::false_type());
+      advance();
       u32x2 packed;
       if constexpr (kF16In) packed = __builtin_bit_cast(u32x2, f16x4{(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]});
       else packed = __builtin_bit_cast(u32x2, bf16x4{to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])});
-      __builtin_amdgcn_raw_buffer_store_b64(packed, buffer(out, p.o_t, i), ((16 * w + l16) * (int)p.o_t + 4 * g4) * 2, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(packed, buffer(out + (begin + (int64_t)i * kC) * p.o_t, p.o_t, len - i * kC), at_out, 0, 0);
+    };
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      fetch_rows(fetched[a]);
+      fetch_record(fetched[a], std::false_type());
+      advance();
+      __builtin_amdgcn_sched_barrier(0);
     }
-    fetch(f, i + kAhead);
-  };
-#pragma unroll
-  for (int a = 0; a < kAhead; ++a) fetch(fetched[a], a);
-  for (int i = 0; i < chunks; i += kAhead) {
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (i + a < chunks) step(fetched[a], i + a);
+    walk_chunks(step);
   }
-#pragma unroll
-  for (int kt = 0; kt < KTW; ++kt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], -(scale.ex + scale.shift));
-  store_state();
 }
 
 template <int K, bool kF16In>
