@@ -17,10 +17,12 @@
 // range by exact powers of two: the state and V of one value channel by a power of two of that channel's own (Scale), step
 // sizes by one of the chunk (Chunk::shift). One term serves for outputs in bf16.
 //
-// A workgroup walks one sequence of one value head, or a slice of 64 of its state rows; each wave holds 16 of them as
-// S^T[k][v] in fp32 MFMA accumulators. Lanes (l, g = l / 16): an accumulator tile holds column l % 16, rows 4g + i. The
-// chain K S0^T -> D -> state keeps the columns v, so that every accumulator is the next product's operand as it stands
-// (rows t in the order 4g + i, 16 + 4g + i of two tiles), and no wave waits for another's values.
+// A workgroup walks one sequence of one value head, or a slice of 64 of its state rows, with four chain waves and four
+// making waves. The chain waves hold the state as S^T[k][v] in fp32 MFMA accumulators, 32 or 16 value channels each. Lanes
+// (l, g = l / 16): an accumulator tile holds column l % 16, rows 4g + i. The chain K S0^T -> D -> state keeps the columns
+// v, so that every accumulator is the next product's operand as it stands (rows t in the order 4g + i, 16 + 4g + i of two tiles),
+// and no chain wave waits for another's values. Meanwhile the making waves turn the next chunk's rows into operands, T and P in
+// the other half of LDS.
 #include <hip/hip_runtime.h>
 
 #include "kda_delta.h"
@@ -29,42 +31,304 @@
 namespace kda {
 namespace {
 
+// A chunk's operands in LDS.
 template <int K, int V>
-struct DeltaShared {
-  static constexpr int kTileV = kC * kRowBytes<V>, kBlocks = 10 * kBlock * 4;
+struct Slot {
   alignas(16) char k[kC * kRowBytes<K>];
   alignas(16) char q[kC * kRowBytes<K>];
-  // V's rows, then A's and T's blocks, then the outputs' rows.
-  alignas(16) char v[kTileV > kBlocks ? kTileV : kBlocks];
-  // T in two terms; between a sequence's chunks and the next one's, 1 KB of each wave's for its state.
-  alignas(16) char t[2 * kTermP > 1024 * kWavesOf<V> ? 2 * kTermP : 1024 * kWavesOf<V>];
+  alignas(16) char v[kC * kRowBytes<V>];  // then, once its chain wave has its columns, the outputs
+  alignas(16) char t[2 * kTermP];
   alignas(16) char p[kTermP];
-  Chunk chunk;
+  alignas(16) Factors factors;
+};
+template <int K, int V>
+struct DeltaShared {
+  Slot<K, V> slot[2];
+  alignas(16) float blocks[10 * kBlock];
+  Making making;
   RowInfo info[2][kC];
+};
+constexpr int kChainWaves = 4, kMakingWaves = 4, kWalkThreads = 64 * (kChainWaves + kMakingWaves);
+// Barriers of a chunk: the making waves' parts meet at them, and the chain waves pass them on their way.
+constexpr int kBarriers = 6;
+
+template <int K, int V, int kTerms, bool kF16In>
+struct Chain {
+  typedef Walk<K, V, kChainWaves> State;
+  static constexpr int VT = State::VT, KT = K / 16, KB = K / 32;
+  State state;
+  Scale scale[VT];
+  int shift;
+
+  __device__ __forceinline__ void ldexp_state(int vt, int by) {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) state.S[vt][kt][i] = ldexp2(state.S[vt][kt][i], by);
+  }
+
+  // One chunk; passes kBarriers - 1 barriers.
+  __device__ __forceinline__ void step(Slot<K, V>& slot, int wave, int lane_) {
+    const int lane = local_copy(lane_), g4 = lane >> 4, l16 = lane & 15;
+    constexpr uint32_t kInf = kF16In ? 0x7c00u : 0x7f80u;
+    const Factors& fa = slot.factors;
+    // V's columns, tokens 4g + i of each tile; finite values alone.
+    u32x2 raw[VT][4];
+    int first_bad[VT];
+    bool any_bad = false;
+    if (fa.shift != shift) {
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) ldexp_state(vt, fa.shift - shift);
+      shift = fa.shift;
+    }
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const u32x4 w = __builtin_bit_cast(u32x4, read_col<V, false>(slot.v, lane, 32 * b, wave * VT + vt));
+        raw[vt][2 * b] = u32x2{w[0], w[1]}, raw[vt][2 * b + 1] = u32x2{w[2], w[3]};
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) most = max(most, max(raw[vt][tt][j] & 0x7fffu, (raw[vt][tt][j] >> 16) & 0x7fffu));
+      first_bad[vt] = kC;
+      if (__ballot(most >= kInf)) {
+        any_bad = true;
+        most = 0;
+        int bad = kC;
+#pragma unroll
+        for (int tt = 3; tt >= 0; --tt)
+#pragma unroll
+          for (int j = 3; j >= 0; --j) {
+            const uint32_t x = (raw[vt][tt][j / 2] >> (16 * (j & 1))) & 0x7fffu;
+            if (x >= kInf) {
+              bad = 16 * tt + 4 * g4 + j;
+              raw[vt][tt][j / 2] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+            } else {
+              most = max(most, x);
+            }
+          }
+        first_bad[vt] = -channel_max(-bad);
+      }
+      // The channel's scale.
+      float top = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(state.S[vt][kt][i]));
+      const int e = channel_max(max(exponent(top), exponent(token_value<kF16In>(most)) + scale[vt].ex));
+      if (__ballot(e > 4 || (e < 1 && e > kNoExponent / 2))) {
+        const int by = e > kNoExponent / 2 ? min(max(scale[vt].ex + 4 - e, -120), 120) - scale[vt].ex : 0;
+        ldexp_state(vt, by);
+        scale[vt].set(lane, scale[vt].ex + by);
+      }
+    }
+    barrier_lds();
+    // K' S0^T, rows t = 4g + i, column v; S0 Q'^T, rows v, column t.
+    f32x4 x[VT][4], o[VT][4];
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) x[vt][tt] = o[vt][tt] = zero4();
+#pragma unroll
+    for (int m = 0; m < KB; ++m) {
+      f16x8 hi[VT], lo[VT];
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        hi[vt] = to_f16(state.S[vt][2 * m], state.S[vt][2 * m + 1]);
+        if constexpr (kTerms == 2) lo[vt] = rest_f16(state.S[vt][2 * m], state.S[vt][2 * m + 1], hi[vt]);
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const f16x8 kk = __builtin_bit_cast(f16x8, read_row<K>(slot.k, lane, 16 * tt, m));
+        const f16x8 qq = __builtin_bit_cast(f16x8, read_row<K>(slot.q, lane, 16 * tt, m));
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          if constexpr (kTerms == 2) x[vt][tt] = mfma(kk, lo[vt], x[vt][tt]);
+          if constexpr (kF16In) o[vt][tt] = mfma(lo[vt], qq, o[vt][tt]);
+        }
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          x[vt][tt] = mfma(kk, hi[vt], x[vt][tt]);
+          o[vt][tt] = mfma(hi[vt], qq, o[vt][tt]);
+        }
+      }
+      if (m == KB / 2 - 1) barrier_lds();
+    }
+    barrier_lds();
+    // What is to be learnt, V' - h K' S.
+    f16x8 xh[VT][2], xl[VT][2];
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      const f32x4 hh = *reinterpret_cast<const f32x4*>(&fa.h[16 * tt + 4 * g4]);
+      const float e = fa.e[16 * tt + l16];
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = i & 1 ? high_value<kF16In>(raw[vt][tt][i / 2]) : low_value<kF16In>(raw[vt][tt][i / 2]);
+          x[vt][tt][i] = y * scale[vt].v - hh[i] * x[vt][tt][i];
+          o[vt][tt][i] *= e;
+        }
+    }
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        xh[vt][b] = to_f16(x[vt][2 * b], x[vt][2 * b + 1]);
+        if constexpr (kTerms == 2) xl[vt][b] = rest_f16(x[vt][2 * b], x[vt][2 * b + 1], xh[vt][b]);
+      }
+    // D = T x, rows t, column v.
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) x[vt][tt] = zero4();
+#pragma unroll
+      for (int b = 0; b <= tt / 2; ++b) {
+        const f16x8 th = read_fragment(slot.t, lane, tt, b);
+        f16x8 tl;
+        if constexpr (kTerms == 2) tl = read_fragment(slot.t + kTermP, lane, tt, b);
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          if constexpr (kTerms == 2) {
+            x[vt][tt] = mfma(tl, xh[vt][b], x[vt][tt]);
+            x[vt][tt] = mfma(th, xl[vt][b], x[vt][tt]);
+          }
+          x[vt][tt] = mfma(th, xh[vt][b], x[vt][tt]);
+        }
+      }
+    }
+    barrier_lds();
+    // O^T += D^T P^T, and the outputs, rows v = 4g + i, column t, to V's tile.
+    {
+      f16x8 dh[VT][2], dl[VT][2];
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          dh[vt][b] = to_f16(x[vt][2 * b], x[vt][2 * b + 1]);
+          if constexpr (kF16In) dl[vt][b] = rest_f16(x[vt][2 * b], x[vt][2 * b + 1], dh[vt][b]);
+        }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const float f = fa.f[16 * tt + l16];
+#pragma unroll
+        for (int b = 0; b <= tt / 2; ++b) {
+          const f16x8 pp = read_fragment(slot.p, lane, tt, b);
+#pragma unroll
+          for (int vt = 0; vt < VT; ++vt) {
+            if constexpr (kF16In) o[vt][tt] = mfma(dl[vt][b], pp, o[vt][tt]);
+            o[vt][tt] = mfma(dh[vt][b], pp, o[vt][tt]);
+          }
+        }
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[vt][tt][i] *= f * scale[vt].out[i];
+      }
+    }
+    if (any_bad) {
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int from = __shfl(first_bad[vt], 4 * g4 + i);
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+            if (16 * tt + l16 >= from) o[vt][tt][i] = __builtin_nanf("");
+        }
+        if (first_bad[vt] < kC)
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) state.S[vt][kt] = zero4() + __builtin_nanf("");
+      }
+    }
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        char* at = slot.v + row_at<V>(16 * tt + l16) + ((wave * VT + vt) * 16 + 4 * g4) * 2;
+        const f32x4 y = o[vt][tt];
+        if constexpr (kF16In) *reinterpret_cast<f16x4*>(at) = f16x4{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+        else *reinterpret_cast<bf16x4*>(at) = bf16x4{to_bf16(y[0]), to_bf16(y[1]), to_bf16(y[2]), to_bf16(y[3])};
+      }
+    barrier_lds();
+    // The state.
+    const float total = fa.total;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f16x8 dh[VT], dl[VT];
+      const f32x4 c0 = *reinterpret_cast<const f32x4*>(&fa.c[32 * b + 4 * g4]), c1 = *reinterpret_cast<const f32x4*>(&fa.c[32 * b + 16 + 4 * g4]);
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        const f32x4 y0 = x[vt][2 * b] * c0, y1 = x[vt][2 * b + 1] * c1;
+        dh[vt] = to_f16(y0, y1);
+        if constexpr (kTerms == 2) dl[vt] = rest_f16(y0, y1, dh[vt]);
+      }
+#pragma unroll
+      for (int kt = 0; kt < KT; kt += 2) {
+        const f16x8 k0 = __builtin_bit_cast(f16x8, read_col<K, true>(slot.k, lane, 32 * b, kt));
+        const f16x8 k1 = __builtin_bit_cast(f16x8, read_col<K, true>(slot.k, lane, 32 * b, kt + 1));
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          f32x4 &s0 = state.S[vt][kt], &s1 = state.S[vt][kt + 1];
+          if (b == 0) s0 *= total, s1 *= total;
+          if constexpr (kTerms == 2) s0 = mfma(k0, dl[vt], s0), s1 = mfma(k1, dl[vt], s1);
+          s0 = mfma(k0, dh[vt], s0), s1 = mfma(k1, dh[vt], s1);
+        }
+      }
+    }
+  }
 };
 
 template <int K, int V, int kTerms, bool kF16In>
-__global__ __launch_bounds__(64 * kWavesOf<V>, 2) void delta_walk(const DeltaPlan p) {
-  constexpr int kWaves = kWavesOf<V>, kThreads = 64 * kWaves, KT = K / 16, KB = K / 32;
+__global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p) {
+  constexpr int kThreads = 64 * kMakingWaves;
   __shared__ DeltaShared<K, V> sh;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int g4 = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int slice = blockIdx.x % p.slices, unit = blockIdx.x / p.slices;
   const int n = unit / p.H, h = unit % p.H, v0 = slice * V;
+  const int begin = __builtin_amdgcn_readfirstlane(bound(p, n));
+  const int len = __builtin_amdgcn_readfirstlane(max(bound(p, n + 1) - begin, 0)), chunks = (len + kC - 1) / kC;
+  const Slots slots = slots_of(p, n);
+  if (wave < kChainWaves) {
+    Chain<K, V, kTerms, kF16In> chain;
+    char* const stage = sh.slot[1].k + wave * 1024;  // no row stands there yet
+    chain.state.zero();
+    if (slots.from >= 0) chain.state.load_plane(p, stage, plane_at(p, slots.from, h), v0, wave, lane);
+    chain.shift = 0;
+#pragma unroll
+    for (int vt = 0; vt < chain.VT; ++vt) chain.scale[vt].set(lane, 0);
+    if (chunks > 0) {
+      for (int i = 0; i < kBarriers; ++i) barrier_lds();
+      for (int i = 0; i < chunks; ++i) {
+        chain.step(sh.slot[i & 1], wave, lane);
+        barrier_lds();
+      }
+    }
+    if (slots.to >= 0) {
+#pragma unroll
+      for (int vt = 0; vt < chain.VT; ++vt) chain.ldexp_state(vt, -(chain.scale[vt].ex + chain.shift));
+      chain.state.store_plane(p, sh.slot[chunks & 1].k + wave * 1024, plane_at(p, slots.to, h), v0, wave, lane);
+    }
+    return;
+  }
+  if (chunks == 0) return;
+  const int tid = threadIdx.x - 64 * kChainWaves, w = wave - kChainWaves;
   const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + (h / p.group) * p.q_h;
   const uint16_t* k = reinterpret_cast<const uint16_t*>(p.k) + (h / p.group) * p.k_h;
   const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + h * p.v_h + v0;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + h * p.o_h + v0;
-  const int begin = bound(p, n), len = max(bound(p, n + 1) - begin, 0);
-  const Slots slots = slots_of(p, n);
-  char* stage = sh.t + wave * 1024;
-  Walk<K, V> walk;
-  f32x4* S = walk.S[0];
   Rows<K, kThreads> rq, rk;
   Rows<V, kThreads> rv;
-  float g_next = 0.f, beta_next = 0.f;  // this lane's token of the next chunk, in the last wave
-  const auto fetch = [&](int64_t first, int count) {
-    if (wave == kWaves - 1) {
+  float g_next = 0.f, beta_next = 0.f;  // this lane's token of the next chunk, in the first making wave
+  const auto count_of = [&](int i) { return min(len - i * kC, kC); };
+  const auto first_of = [&](int i) { return begin + (int64_t)i * kC; };
+  const auto fetch = [&](int i) {
+    const int64_t first = first_of(i);
+    const int count = count_of(i);
+    if (w == 0) {
       g_next = beta_next = 0.f;
       if (lane < count) {
         const int64_t at = (first + lane) * p.H + h;
@@ -76,279 +340,58 @@ __global__ __launch_bounds__(64 * kWavesOf<V>, 2) void delta_walk(const DeltaPla
       }
     }
     rk.load(reinterpret_cast<const __bf16*>(k), p.k_t, first, count, tid);
-    rv.load(reinterpret_cast<const __bf16*>(v), p.v_t, first, count, tid);
     rq.load(reinterpret_cast<const __bf16*>(q), p.q_t, first, count, tid);
+    rv.load(reinterpret_cast<const __bf16*>(v), p.v_t, first, count, tid);
   };
-  int64_t first = begin;
-  int left = len;
-  if (left > 0) fetch(first, min(left, kC));
-  walk.zero();
-  if (slots.from >= 0) walk.load_plane(p, stage, plane_at(p, slots.from, h), v0, wave, lane);
-  Scale scale;
-  scale.shift = 0;
-  scale.set(lane, 0);
-  while (left > 0) {
-    const int count = min(left, kC);
-    put_scaled<K, kThreads, kF16In>(rk, sh.k, sh.info[0], tid, true);
-    put_scaled<K, kThreads, kF16In>(rq, sh.q, sh.info[1], tid, p.normalize);
-    rv.put(sh.v, tid);
+  const auto store = [&](int i) {
+    Rows<V, kThreads>::store(sh.slot[i & 1].v, reinterpret_cast<__bf16*>(out), p.o_t, first_of(i), count_of(i), tid);
+  };
+  fetch(0);
+  // In turn i the chain waves walk chunk i - 1 and these make chunk i, in the place of chunk i - 2, whose outputs leave first.
+  for (int i = 0; i <= chunks; ++i) {
+    if (i >= 2) store(i - 2);
+    if (i == chunks) {
+      for (int j = 0; j < kBarriers; ++j) barrier_lds();
+      break;
+    }
+    Slot<K, V>& slot = sh.slot[i & 1];
+    put_scaled<K, kThreads, kF16In>(rk, slot.k, sh.info[0], tid, true);
+    put_scaled<K, kThreads, kF16In>(rq, slot.q, sh.info[1], tid, p.normalize);
+    rv.put(slot.v, tid);
+    const float g = g_next, beta = beta_next;
+    if (i + 1 < chunks) fetch(i + 1);
     barrier_lds();
-    if (wave == kWaves - 1) put_chunk(sh.chunk, p, sh.info[0][lane], sh.info[1][lane], g_next, beta_next, lane);
-    const int64_t here = first;
-    first += count;
-    left -= count;
-    if (left > 0) fetch(first, min(left, kC));
-
-    // V's column of this lane, tokens 4g + i of each tile, finite values alone.
-    u32x2 raw[4];
-    uint32_t most = 0;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const u32x4 w = __builtin_bit_cast(u32x4, read_col<V, false>(sh.v, lane, 32 * b, wave));
-      raw[2 * b] = u32x2{w[0], w[1]}, raw[2 * b + 1] = u32x2{w[2], w[3]};
-    }
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) most = max(most, max(raw[tt][j] & 0x7fffu, (raw[tt][j] >> 16) & 0x7fffu));
-    constexpr uint32_t kInf = kF16In ? 0x7c00u : 0x7f80u;
-    int first_bad = kC;  // of this lane's channel
-    if (__ballot(most >= kInf)) {
-      most = 0;
-#pragma unroll
-      for (int tt = 3; tt >= 0; --tt)
-#pragma unroll
-        for (int j = 3; j >= 0; --j) {
-          const uint32_t x = (raw[tt][j / 2] >> (16 * (j & 1))) & 0x7fffu;
-          if (x >= kInf) {
-            first_bad = 16 * tt + 4 * g4 + j;
-            raw[tt][j / 2] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
-          } else {
-            most = max(most, x);
-          }
-        }
-      first_bad = min(first_bad, __shfl_xor(first_bad, 16));
-      first_bad = min(first_bad, __shfl_xor(first_bad, 32));
-    }
-    barrier_lds();  // the chunk's numbers; V's tile has been read
-
-    // The channel's scale.
-    const Chunk& ch = sh.chunk;
-    if (ch.shift != scale.shift) {
-      const int by = ch.shift - scale.shift;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[kt][i] = ldexp2(S[kt][i], by);
-      scale.shift = ch.shift;
-    }
-    float top = 0.f;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(S[kt][i]));
-    const int e = channel_max(max(exponent(top), exponent(token_value<kF16In>(most)) + scale.ex));
-    if (__ballot(e > 4 || (e < 1 && e > kNoExponent / 2))) {
-      const int by = e > kNoExponent / 2 ? min(max(scale.ex + 4 - e, -120), 120) - scale.ex : 0;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[kt][i] = ldexp2(S[kt][i], by);
-      scale.set(lane, scale.ex + by);
-    }
-
-    // A's and P's tiles, dealt over the waves.
-#pragma unroll
-    for (int j = 0; j < (20 + kWaves - 1) / kWaves; ++j) {
-      const int job = j * kWaves + wave;
-      if (job >= 20) break;
-      const int tile = job < 10 ? job : job - 10, tt = tile_t(tile), st = tile_s(tile);
-      const int t = 16 * tt + l16;
-      const f32x4 decay = tile_decay(ch, lane, tt, st);
-      if (job < 10) {
-        const f32x4 d = tile_product<K>(sh.k, sh.k, lane, tt, st) * decay;
-        const f32x4 r = *reinterpret_cast<const f32x4*>(&ch.rk[16 * st + 4 * g4]);
-        const float bk = ch.bk[t];
-        float* to = reinterpret_cast<float*>(sh.v) + block_at(tt, st) + 4 * g4 * kBlockRow + l16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[i * kBlockRow] = 16 * st + 4 * g4 + i < t ? d[i] * (bk * r[i]) : 0.f;
-      } else {
-        const f32x4 d = tile_product<K>(sh.k, sh.q, lane, tt, st) * decay;
-        const f32x4 r = *reinterpret_cast<const f32x4*>(&ch.rk[16 * st + 4 * g4]);
-        f16x4 x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (_Float16)(16 * st + 4 * g4 + i <= t ? d[i] * r[i] : 0.f);
-        put_fragment(sh.p, lane, tt, st, x);
-      }
-    }
+    if (w == 0) put_chunk(sh.making, slot.factors, p, sh.info[0][lane], sh.info[1][lane], g, beta, lane);
+    f32x4 kk[4], kq[4];
+    tile_products<K>(slot.k, slot.q, local_copy(lane), w, kk, kq);
     barrier_lds();
-    float* blocks = reinterpret_cast<float*>(sh.v);
-    if (wave == 0) invert_diagonal(blocks, lane);
-
-    // K' S0^T, rows t = 4g + i, column v; S0 Q'^T, rows v, column t.
-    f32x4 x[4], o[4];
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) x[tt] = o[tt] = zero4();
-#pragma unroll
-    for (int m = 0; m < KB; ++m) {
-      const f16x8 hi = to_f16(S[2 * m], S[2 * m + 1]);
-      if constexpr (kTerms == 2) {
-        const f16x8 lo = rest_f16(S[2 * m], S[2 * m + 1], hi);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          x[tt] = mfma(__builtin_bit_cast(f16x8, read_row<K>(sh.k, lane, 16 * tt, m)), lo, x[tt]);
-          if constexpr (kF16In) o[tt] = mfma(lo, __builtin_bit_cast(f16x8, read_row<K>(sh.q, lane, 16 * tt, m)), o[tt]);
-        }
-      }
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        x[tt] = mfma(__builtin_bit_cast(f16x8, read_row<K>(sh.k, lane, 16 * tt, m)), hi, x[tt]);
-        o[tt] = mfma(hi, __builtin_bit_cast(f16x8, read_row<K>(sh.q, lane, 16 * tt, m)), o[tt]);
-      }
-    }
-    // What is to be learnt, V' - h K' S.
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      const f32x4 hh = *reinterpret_cast<const f32x4*>(&ch.h[16 * tt + 4 * g4]);
-      const float e = ch.e[16 * tt + l16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float y = i & 1 ? high_value<kF16In>(raw[tt][i / 2]) : low_value<kF16In>(raw[tt][i / 2]);
-        x[tt][i] = y * scale.v - hh[i] * x[tt][i];
-        o[tt][i] *= e;
-      }
-    }
+    const int l = local_copy(lane);
+    put_tiles(sh.blocks, sh.making, l, w, kk, kq, [&](int st, f16x4 x) { put_fragment(slot.p, l, w, st, x); });
     barrier_lds();
-    // T below the diagonal: first beside it, then the square of four blocks.
-    const auto block = [&](int tt, int st) { return blocks + block_at(tt, st); };
-    const auto read_block = [&](int tt, int st) {
-      f32x4 y;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = block(tt, st)[(4 * g4 + i) * kBlockRow + l16];
-      return y;
+    if (w == 0) invert_diagonal(sh.blocks, l);
+    barrier_lds();
+    const auto put_t = [&](int tt, int st, f32x4 x) {
+      const Terms y = t_terms(sh.making, l, st, x);
+      put_fragment(slot.t, l, tt, st, y.hi);
+      put_fragment(slot.t + kTermP, l, tt, st, y.lo);
     };
-    if (wave < 2) {
-      const int t = 2 * wave + 1, s = 2 * wave;
-      const f32x4 y = -block_product(block(s, s), block_product(block(t, s), block(t, t), lane, zero4()), lane, zero4());
-      put_t(sh.t, ch, lane, t, s, y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) block(t, s)[(4 * g4 + i) * kBlockRow + l16] = y[i];
-    } else if (wave == 2) {
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) put_t(sh.t, ch, lane, tt, tt, read_block(tt, tt));
-    }
+    near_blocks(sh.blocks, l, w, put_t);
     barrier_lds();
-    if (wave < 2) {
-      const int t = 2 + wave;
-      f32x4 z0 = block_product(block(2, 0), block(t, 2), lane, zero4()), z1 = block_product(block(2, 1), block(t, 2), lane, zero4());
-      if (wave == 1) z0 = block_product(block(3, 0), block(3, 3), lane, z0), z1 = block_product(block(3, 1), block(3, 3), lane, z1);
-      put_t(sh.t, ch, lane, t, 0, -block_product(block(1, 0), z1, lane, block_product(block(0, 0), z0, lane, zero4())));
-      put_t(sh.t, ch, lane, t, 1, -block_product(block(1, 1), z1, lane, zero4()));
-    }
+    far_blocks(sh.blocks, l, w, put_t);
     barrier_lds();
-
-    // D = T x, rows t, column v.
-    f32x4 d[4];
-    {
-      f16x8 hi[2], lo[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        hi[b] = to_f16(x[2 * b], x[2 * b + 1]);
-        if constexpr (kTerms == 2) lo[b] = rest_f16(x[2 * b], x[2 * b + 1], hi[b]);
-      }
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        d[tt] = zero4();
-#pragma unroll
-        for (int b = 0; b <= tt / 2; ++b) {
-          const f16x8 th = read_fragment(sh.t, lane, tt, b);
-          if constexpr (kTerms == 2) {
-            d[tt] = mfma(read_fragment(sh.t + kTermP, lane, tt, b), hi[b], d[tt]);
-            d[tt] = mfma(th, lo[b], d[tt]);
-          }
-          d[tt] = mfma(th, hi[b], d[tt]);
-        }
-      }
-    }
-    // O^T += D^T P^T, and the outputs, rows v = 4g + i, column t, to V's tile.
-    {
-      f16x8 dh[2], dl[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        dh[b] = to_f16(d[2 * b], d[2 * b + 1]);
-        if constexpr (kF16In) dl[b] = rest_f16(d[2 * b], d[2 * b + 1], dh[b]);
-      }
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-        for (int b = 0; b <= tt / 2; ++b) {
-          const f16x8 pp = read_fragment(sh.p, lane, tt, b);
-          if constexpr (kF16In) o[tt] = mfma(dl[b], pp, o[tt]);
-          o[tt] = mfma(dh[b], pp, o[tt]);
-        }
-        const float f = ch.f[16 * tt + l16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[tt][i] *= f * scale.out[i];
-      }
-    }
-    if (__ballot(first_bad < kC)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int from = __shfl(first_bad, 4 * g4 + i);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-          if (16 * tt + l16 >= from) o[tt][i] = __builtin_nanf("");
-      }
-      if (first_bad < kC)
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) S[kt] = zero4() + __builtin_nanf("");
-    }
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      char* at = sh.v + row_at<V>(16 * tt + l16) + (wave * 16 + 4 * g4) * 2;
-      if constexpr (kF16In) {
-        *reinterpret_cast<f16x4*>(at) = f16x4{(_Float16)o[tt][0], (_Float16)o[tt][1], (_Float16)o[tt][2], (_Float16)o[tt][3]};
-      } else {
-        *reinterpret_cast<bf16x4*>(at) = bf16x4{to_bf16(o[tt][0]), to_bf16(o[tt][1]), to_bf16(o[tt][2]), to_bf16(o[tt][3])};
-      }
-    }
-    // The state.
-    const float total = ch.total;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) S[kt] *= total;
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) d[tt] *= *reinterpret_cast<const f32x4*>(&ch.c[16 * tt + 4 * g4]);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const f16x8 hi = to_f16(d[2 * b], d[2 * b + 1]);
-      f16x8 lo;
-      if constexpr (kTerms == 2) lo = rest_f16(d[2 * b], d[2 * b + 1], hi);
-#pragma unroll
-      for (int kt = 0; kt < KT; kt += 2) {
-        const f16x8 k0 = __builtin_bit_cast(f16x8, read_col<K, true>(sh.k, lane, 32 * b, kt));
-        const f16x8 k1 = __builtin_bit_cast(f16x8, read_col<K, true>(sh.k, lane, 32 * b, kt + 1));
-        if constexpr (kTerms == 2) S[kt] = mfma(k0, lo, S[kt]), S[kt + 1] = mfma(k1, lo, S[kt + 1]);
-        S[kt] = mfma(k0, hi, S[kt]), S[kt + 1] = mfma(k1, hi, S[kt + 1]);
-      }
-    }
-    barrier_lds();
-    Rows<V, kThreads>::store(sh.v, reinterpret_cast<__bf16*>(out), p.o_t, here, count, tid);
   }
-  if (slots.to >= 0) {
-    const int by = -(scale.ex + scale.shift);
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) S[kt][i] = ldexp2(S[kt][i], by);
-    walk.store_plane(p, stage, plane_at(p, slots.to, h), v0, wave, lane);
-  }
+  store(chunks - 1);
 }
 
 template <int K, int V, int kTerms>
 int launch_kv(const DeltaPlan& p, hipStream_t s) {
   const unsigned grid = (unsigned)((int64_t)p.N * p.H * p.slices);
-  if (p.f16) delta_walk<K, V, kTerms, true><<<grid, 64 * kWavesOf<V>, 0, s>>>(p);
-  else delta_walk<K, V, kTerms, false><<<grid, 64 * kWavesOf<V>, 0, s>>>(p);
+  if constexpr (kTerms == 2)
+    if (p.f16) {
+      delta_walk<K, V, 2, true><<<grid, kWalkThreads, 0, s>>>(p);
+      return (int)hipGetLastError();
+    }
+  delta_walk<K, V, kTerms, false><<<grid, kWalkThreads, 0, s>>>(p);
   return (int)hipGetLastError();
 }
 template <int kTerms>

@@ -32,7 +32,9 @@ __device__ __forceinline__ uint32_t pair_f16(float a, float b) {
 // instruction and this one of the rounded value: where those fall on two sides of a middle, both terms miss it by 2^-10.)
 __device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t first) {
   const f16x2 h = __builtin_bit_cast(f16x2, first);
-  const f16x2 r = {(_Float16)__builtin_fmaf((float)h[0], -1.f, a), (_Float16)__builtin_fmaf((float)h[1], -1.f, b)};
+  float minus = -1.f;
+  asm("" : "+s"(minus));  // a known factor would become a difference, which has no such instruction
+  const f16x2 r = {(_Float16)__builtin_fmaf((float)h[0], minus, a), (_Float16)__builtin_fmaf((float)h[1], minus, b)};
   return __builtin_bit_cast(uint32_t, r);
 }
 // Two tiles (rows 4g + i and 16 + 4g + i) as an operand, in one or two terms.
@@ -88,6 +90,17 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// The exponent of x >= 0: x < 2^e.
+constexpr int kNoExponent = -4096;
+__device__ __forceinline__ int exponent(float x) { return x > 0.f && x < INFINITY ? __builtin_amdgcn_frexp_expf(x) : kNoExponent; }
+// Over the four lanes that hold one channel: exchanges of half waves and of rows, without LDS.
+__device__ __forceinline__ int channel_max(int x) {
+  const auto a = __builtin_amdgcn_permlane32_swap((unsigned)x, (unsigned)x, false, false);
+  x = max((int)a[0], (int)a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap((unsigned)x, (unsigned)x, false, false);
+  return max((int)b[0], (int)b[1]);
+}
+
 constexpr int kBadRow = 1 << 20;  // exponent of a row that is not finite
 // A scaled row's exponent and the sum of its scaled squares.
 struct RowInfo {
@@ -131,26 +144,31 @@ __device__ __forceinline__ void put_scaled(const Rows<D, kThreads>& rows, char* 
 //   K'_t, Q'_t: scaled rows; rk_t, rq_t: what takes them to the keys and queries of the rule, as it is scaled here:
 // keys by 2^-X, step sizes by 2^{2X}, states by 2^X, with X other than 0 only for keys far from unit length; states
 // are scaled by 2^Y more, with Y other than 0 only where all step sizes are small.
-struct Chunk {
-  double G[kC];                // inclusive cumsum of g
-  alignas(16) float bk[kC];    // beta rk
+struct Factors {
+  float h[kC];  // rk e^G 2^-Y: the share of K' S in what is to be learnt
+  float c[kC];  // rk e^{G_C - G}: what of D reaches the chunk's end
+  float e[kC];  // e^G
+  float f[kC];  // scale rq 2^-Y: outputs; NaN from the first bad token on
+  float total;  // e^{G_C}; NaN with a bad token
+  int shift;    // X + Y
+};
+// For the making of T and P alone.
+struct Making {
+  double G[kC];               // inclusive cumsum of g
+  alignas(16) float bk[kC];   // beta rk
   alignas(16) float rk[kC];
-  alignas(16) float h[kC];     // rk e^G 2^-Y: the share of K' S in what is to be learnt
-  alignas(16) float c[kC];     // rk e^{G_C - G}: what of D reaches the chunk's end
-  alignas(16) float col[kC];   // beta 2^Y: the columns of T
-  alignas(16) float e[kC];     // e^G
-  alignas(16) float f[kC];     // scale rq 2^-Y: outputs; NaN from the first bad token on
-  float total;                 // e^{G_C}; NaN with a bad token
-  int shift;                   // X + Y
+  alignas(16) float col[kC];  // beta 2^Y: the columns of T
 };
 
-// One lane for each token.
 __device__ __forceinline__ int wave_max(int x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x = max(x, __shfl_xor(x, d));
-  return x;
+  x = max(x, (int)dpp<0xb1>((uint32_t)x));
+  x = max(x, (int)dpp<0x4e>((uint32_t)x));
+  x = max(x, (int)dpp<0x141>((uint32_t)x));
+  x = max(x, (int)dpp<0x140>((uint32_t)x));
+  return channel_max(x);
 }
-__device__ __forceinline__ void put_chunk(Chunk& ch, const DeltaPlan& p, RowInfo k, RowInfo q, float g, float beta, int lane) {
+// One lane for each token.
+__device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPlan& p, RowInfo k, RowInfo q, float g, float beta, int lane) {
   const bool bad = k.e == kBadRow || !(g <= 0.f) || !(fabsf(beta) < INFINITY);
   const uint64_t all_bad = __ballot(bad);
   const int first = all_bad ? __builtin_ctzll(all_bad) : kC;
@@ -175,17 +193,17 @@ __device__ __forceinline__ void put_chunk(Chunk& ch, const DeltaPlan& p, RowInfo
   const double end = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
                                                     (uint32_t)__builtin_amdgcn_readlane((int)u, 63));
   const float eG = __expf((float)G);
-  ch.G[lane] = G;
-  ch.bk[lane] = beta * rk;
-  ch.rk[lane] = rk;
-  ch.h[lane] = ldexp2(rk * eG, -Y);
-  ch.c[lane] = rk * __expf((float)(end - G));
-  ch.col[lane] = ldexp2(beta, Y);
-  ch.e[lane] = eG;
-  ch.f[lane] = lane >= first || q.e == kBadRow ? __builtin_nanf("") : p.scale * ldexp2(rq, -Y);
+  mk.G[lane] = G;
+  mk.bk[lane] = beta * rk;
+  mk.rk[lane] = rk;
+  mk.col[lane] = ldexp2(beta, Y);
+  to.h[lane] = ldexp2(rk * eG, -Y);
+  to.c[lane] = rk * __expf((float)(end - G));
+  to.e[lane] = eG;
+  to.f[lane] = lane >= first || q.e == kBadRow ? __builtin_nanf("") : p.scale * ldexp2(rq, -Y);
   if (lane == 0) {
-    ch.total = all_bad ? __builtin_nanf("") : __expf((float)end);
-    ch.shift = X + Y;
+    to.total = all_bad ? __builtin_nanf("") : __expf((float)end);
+    to.shift = X + Y;
   }
 }
 
@@ -201,22 +219,50 @@ __device__ __forceinline__ void put_fragment(char* p, int lane, int tt, int st, 
   *reinterpret_cast<f16x4*>(p + fragment(tt, b) + (half_fragment(tt, b) ? lane * 8 : lane * 16 + (st & 1) * 8)) = x;
 }
 
-// Tile (tt, st) of K' K'^T or K' Q'^T, rows s = 4g + i, column t = l % 16.
+// Making T and P, by four waves of which wave w takes the token tile w: the tiles (w, st <= w) of K' K'^T and K' Q'^T, rows
+// s = 4g + i, column t = l % 16. A tile of sources is read once for both.
 template <int K>
-__device__ __forceinline__ f32x4 tile_product(const char* k, const char* other, int lane, int tt, int st) {
-  f32x4 d = zero4();
+__device__ __forceinline__ void tile_products(const char* k, const char* q, int lane, int w, f32x4 (&kk)[4], f32x4 (&kq)[4]) {
+  constexpr int KB = K / 32;
+  f16x8 own_k[KB], own_q[KB];
 #pragma unroll
-  for (int m = 0; m < K / 32; ++m)
-    d = mfma(__builtin_bit_cast(f16x8, read_row<K>(k, lane, 16 * st, m)), __builtin_bit_cast(f16x8, read_row<K>(other, lane, 16 * tt, m)), d);
-  return d;
+  for (int m = 0; m < KB; ++m) {
+    own_k[m] = __builtin_bit_cast(f16x8, read_row<K>(k, lane, 16 * w, m));
+    own_q[m] = __builtin_bit_cast(f16x8, read_row<K>(q, lane, 16 * w, m));
+  }
+#pragma unroll
+  for (int st = 0; st < 4; ++st) {
+    if (st > w) break;
+    kk[st] = kq[st] = zero4();
+#pragma unroll
+    for (int m = 0; m < KB; ++m) {
+      const f16x8 s = __builtin_bit_cast(f16x8, read_row<K>(k, lane, 16 * st, m));
+      kk[st] = mfma(s, own_k[m], kk[st]);
+      kq[st] = mfma(s, own_q[m], kq[st]);
+    }
+  }
 }
-// e^{G_t - G_s} for a tile's elements.
-__device__ __forceinline__ f32x4 tile_decay(const Chunk& ch, int lane, int tt, int st) {
-  const double Gt = ch.G[16 * tt + (lane & 15)];
-  f32x4 x;
+// A's blocks and P's tiles from them; put_p(st, x) takes a tile of P.
+template <typename PutP>
+__device__ __forceinline__ void put_tiles(float* blocks, const Making& mk, int lane, int w, f32x4 (&kk)[4], f32x4 (&kq)[4], PutP put_p) {
+  const int g4 = lane >> 4, t = 16 * w + (lane & 15);
+  const double Gt = mk.G[t];
+  const float bk = mk.bk[t];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = __expf((float)(Gt - ch.G[16 * st + 4 * (lane >> 4) + i]));
-  return x;
+  for (int st = 0; st < 4; ++st) {
+    if (st > w) break;
+    const int s0 = 16 * st + 4 * g4;
+    const f32x4 r = *reinterpret_cast<const f32x4*>(&mk.rk[s0]);
+    float* to = blocks + block_at(w, st) + 4 * g4 * kBlockRow + (lane & 15);
+    f16x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float factor = r[i] * __expf((float)(Gt - mk.G[s0 + i]));
+      to[i * kBlockRow] = s0 + i < t ? kk[st][i] * (factor * bk) : 0.f;
+      x[i] = (_Float16)(s0 + i <= t ? kq[st][i] * factor : 0.f);
+    }
+    put_p(st, x);
+  }
 }
 
 // The diagonal blocks of T, one for each 16 lanes, a column to a lane.
@@ -253,13 +299,48 @@ __device__ __forceinline__ f32x4 block_product(const float* left, f32x4 right, i
   for (int i = 0; i < 4; ++i) d = mfma32(a[i], right[i], d);
   return d;
 }
-// Tile (tt, st) of T as its fragments' two terms, its columns times col.
-__device__ __forceinline__ void put_t(char* frags, const Chunk& ch, int lane, int tt, int st, f32x4 x) {
-  const f32x4 col = *reinterpret_cast<const f32x4*>(&ch.col[16 * st + 4 * (lane >> 4)]);
-  x *= col;
+// T's blocks below the diagonal, in two parts with a barrier of the four waves between them (and one before each): those
+// beside the diagonal, then the square of four. put_t(tt, st, x) takes a block, rows s = 4g + i, column t = l % 16.
+template <typename PutT>
+__device__ __forceinline__ void near_blocks(float* blocks, int lane, int w, PutT put_t) {
+  const int g4 = lane >> 4, l16 = lane & 15;
+  if (w < 2) {
+    const int t = 2 * w + 1, s = 2 * w;
+    float* at = blocks + block_at(t, s);
+    const f32x4 y = -block_product(blocks + block_at(s, s), block_product(at, blocks + block_at(t, t), lane, zero4()), lane, zero4());
+    put_t(t, s, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[(4 * g4 + i) * kBlockRow + l16] = y[i];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int tt = 2 * (w - 2) + j;
+      const float* at = blocks + block_at(tt, tt);
+      f32x4 y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = at[(4 * g4 + i) * kBlockRow + l16];
+      put_t(tt, tt, y);
+    }
+  }
+}
+template <typename PutT>
+__device__ __forceinline__ void far_blocks(const float* blocks, int lane, int w, PutT put_t) {
+  if (w >= 2) return;
+  const int t = 2 + w;
+  const auto block = [&](int tt, int st) { return blocks + block_at(tt, st); };
+  f32x4 z0 = block_product(block(2, 0), block(t, 2), lane, zero4()), z1 = block_product(block(2, 1), block(t, 2), lane, zero4());
+  if (w == 1) z0 = block_product(block(3, 0), block(3, 3), lane, z0), z1 = block_product(block(3, 1), block(3, 3), lane, z1);
+  put_t(t, 0, -block_product(block(1, 0), z1, lane, block_product(block(0, 0), z0, lane, zero4())));
+  put_t(t, 1, -block_product(block(1, 1), z1, lane, zero4()));
+}
+// A block of T with its columns' factors, in two terms.
+struct Terms {
+  f16x4 hi, lo;
+};
+__device__ __forceinline__ Terms t_terms(const Making& mk, int lane, int st, f32x4 x) {
+  x *= *reinterpret_cast<const f32x4*>(&mk.col[16 * st + 4 * (lane >> 4)]);
   const u32x2 hi = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}, lo = {rest_pair(x[0], x[1], hi[0]), rest_pair(x[2], x[3], hi[1])};
-  put_fragment(frags, lane, tt, st, __builtin_bit_cast(f16x4, hi));
-  put_fragment(frags + kTermP, lane, tt, st, __builtin_bit_cast(f16x4, lo));
+  return Terms{__builtin_bit_cast(f16x4, hi), __builtin_bit_cast(f16x4, lo)};
 }
 
 // Powers of two that hold one value channel's state and V in fp16's range: S' = S 2^{ex + shift}, V' = V 2^ex. The larger of
@@ -277,16 +358,5 @@ struct Scale {
     for (int i = 0; i < 4; ++i) out[i] = __shfl(back, 4 * (lane >> 4) + i);
   }
 };
-
-// The exponent of x >= 0: x < 2^e.
-constexpr int kNoExponent = -4096;
-__device__ __forceinline__ int exponent(float x) { return x > 0.f && x < INFINITY ? __builtin_amdgcn_frexp_expf(x) : kNoExponent; }
-// Over the four lanes that hold one channel: exchanges of half waves and of rows, without LDS.
-__device__ __forceinline__ int channel_max(int x) {
-  const auto a = __builtin_amdgcn_permlane32_swap((unsigned)x, (unsigned)x, false, false);
-  x = max((int)a[0], (int)a[1]);
-  const auto b = __builtin_amdgcn_permlane16_swap((unsigned)x, (unsigned)x, false, false);
-  return max((int)b[0], (int)b[1]);
-}
 
 }  // namespace kda

@@ -21,11 +21,6 @@ namespace {
 // A record: T in two terms and P, six fragments each, then the factors.
 constexpr int kFragments = 6 * 1024;
 __device__ __forceinline__ constexpr int padded_fragment(int tt, int b) { return (tt < 2 ? tt : 2 * tt - 2 + b) * 1024; }
-struct Factors {
-  float h[kC], c[kC], e[kC], f[kC];
-  float total;
-  int shift;
-};
 static_assert(3 * kFragments + sizeof(Factors) <= kDeltaRecord, "record size");
 constexpr int kRecP = 2 * kFragments, kRecFactors = 3 * kFragments;
 
@@ -50,12 +45,6 @@ __device__ __forceinline__ void put_padded(char* frags, int lane, int tt, int st
   *reinterpret_cast<f16x4*>(at + (st & 1) * 8) = x;
   if (tt == st && !(st & 1)) *reinterpret_cast<f16x4*>(at + 8) = f16x4{0, 0, 0, 0};
 }
-__device__ __forceinline__ void put_padded_t(char* rec, const Chunk& ch, int lane, int tt, int st, f32x4 x) {
-  x *= *reinterpret_cast<const f32x4*>(&ch.col[16 * st + 4 * (lane >> 4)]);
-  const u32x2 hi = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}, lo = {rest_pair(x[0], x[1], hi[0]), rest_pair(x[2], x[3], hi[1])};
-  put_padded(rec, lane, tt, st, __builtin_bit_cast(f16x4, hi));
-  put_padded(rec + kFragments, lane, tt, st, __builtin_bit_cast(f16x4, lo));
-}
 
 // A tile's rows in LDS to memory as operand fragments: 16 rows and 32 channels to 1 KB.
 template <int D, int kThreads>
@@ -70,16 +59,16 @@ __device__ __forceinline__ void store_fragments(const char* tile, char* to, int 
 
 template <int K, bool kF16In>
 __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
-  constexpr int kThreads = 256, kWaves = 4;
+  constexpr int kThreads = 256;
   __shared__ struct {
     alignas(16) char k[kC * kRowBytes<K>];
     alignas(16) char q[kC * kRowBytes<K>];
     alignas(16) float blocks[10 * kBlock];
-    Chunk chunk;
+    Making making;
     RowInfo info[2][kC];
   } sh;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int place = blockIdx.x / p.H, h = blockIdx.x % p.H, g4 = lane >> 4, l16 = lane & 15;
+  const int place = blockIdx.x / p.H, h = blockIdx.x % p.H;
   const int n = find_chunk(p, place, lane);
   const int begin = bound(p, n), len = bound(p, n + 1) - begin;
   const int in = (place - chunk_place(p, n)) * kC;
@@ -92,7 +81,7 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
   rk.load(reinterpret_cast<const __bf16*>(k), p.k_t, first, count, tid);
   rq.load(reinterpret_cast<const __bf16*>(q), p.q_t, first, count, tid);
   float g = 0.f, beta = 0.f;
-  if (wave == kWaves - 1 && lane < count) {
+  if (wave == 0 && lane < count) {
     const int64_t at = (first + lane) * p.H + h;
     if (p.g) {
       const int64_t ag = p.g_per_token ? at : h;
@@ -109,64 +98,22 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
     store_fragments<K, kThreads>(sh.k, p.keys + at, tid);
     store_fragments<K, kThreads>(sh.q, p.queries + at, tid);
   }
-  const Chunk& ch = sh.chunk;
-  if (wave == kWaves - 1) {
-    put_chunk(sh.chunk, p, sh.info[0][lane], sh.info[1][lane], g, beta, lane);
-    Factors* to = reinterpret_cast<Factors*>(rec + kRecFactors);
-    to->h[lane] = ch.h[lane], to->c[lane] = ch.c[lane], to->e[lane] = ch.e[lane], to->f[lane] = ch.f[lane];
-    if (lane == 0) to->total = ch.total, to->shift = ch.shift;
-  }
-  f32x4 product[5];
-#pragma unroll
-  for (int j = 0; j < 5; ++j) {
-    const int job = j * kWaves + wave, tile = job < 10 ? job : job - 10;
-    product[j] = tile_product<K>(sh.k, job < 10 ? sh.k : sh.q, lane, tile_t(tile), tile_s(tile));
-  }
+  if (wave == 0) put_chunk(sh.making, *reinterpret_cast<Factors*>(rec + kRecFactors), p, sh.info[0][lane], sh.info[1][lane], g, beta, lane);
+  f32x4 kk[4], kq[4];
+  tile_products<K>(sh.k, sh.q, lane, wave, kk, kq);
   barrier_lds();
-#pragma unroll
-  for (int j = 0; j < 5; ++j) {
-    const int job = j * kWaves + wave, tile = job < 10 ? job : job - 10, tt = tile_t(tile), st = tile_s(tile), t = 16 * tt + l16;
-    const f32x4 d = product[j] * tile_decay(ch, lane, tt, st) * *reinterpret_cast<const f32x4*>(&ch.rk[16 * st + 4 * g4]);
-    if (job < 10) {
-      const float bk = ch.bk[t];
-      float* to = sh.blocks + block_at(tt, st) + 4 * g4 * kBlockRow + l16;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) to[i * kBlockRow] = 16 * st + 4 * g4 + i < t ? d[i] * bk : 0.f;
-    } else {
-      f16x4 x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = (_Float16)(16 * st + 4 * g4 + i <= t ? d[i] : 0.f);
-      put_padded(rec + kRecP, lane, tt, st, x);
-    }
-  }
+  put_tiles(sh.blocks, sh.making, lane, wave, kk, kq, [&](int st, f16x4 x) { put_padded(rec + kRecP, lane, wave, st, x); });
   barrier_lds();
   if (wave == 0) invert_diagonal(sh.blocks, lane);
   barrier_lds();
-  const auto block = [&](int tt, int st) { return sh.blocks + block_at(tt, st); };
-  if (wave < 2) {
-    const int t = 2 * wave + 1, s = 2 * wave;
-    const f32x4 y = -block_product(block(s, s), block_product(block(t, s), block(t, t), lane, zero4()), lane, zero4());
-    put_padded_t(rec, ch, lane, t, s, y);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) block(t, s)[(4 * g4 + i) * kBlockRow + l16] = y[i];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int tt = 2 * (wave - 2) + j;
-      f32x4 y;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = block(tt, tt)[(4 * g4 + i) * kBlockRow + l16];
-      put_padded_t(rec, ch, lane, tt, tt, y);
-    }
-  }
+  const auto put_t = [&](int tt, int st, f32x4 x) {
+    const Terms y = t_terms(sh.making, lane, st, x);
+    put_padded(rec, lane, tt, st, y.hi);
+    put_padded(rec + kFragments, lane, tt, st, y.lo);
+  };
+  near_blocks(sh.blocks, lane, wave, put_t);
   barrier_lds();
-  if (wave < 2) {
-    const int t = 2 + wave;
-    f32x4 z0 = block_product(block(2, 0), block(t, 2), lane, zero4()), z1 = block_product(block(2, 1), block(t, 2), lane, zero4());
-    if (wave == 1) z0 = block_product(block(3, 0), block(3, 3), lane, z0), z1 = block_product(block(3, 1), block(3, 3), lane, z1);
-    put_padded_t(rec, ch, lane, t, 0, -block_product(block(1, 0), z1, lane, block_product(block(0, 0), z0, lane, zero4())));
-    put_padded_t(rec, ch, lane, t, 1, -block_product(block(1, 1), z1, lane, zero4()));
-  }
+  far_blocks(sh.blocks, lane, wave, put_t);
 }
 
 constexpr int kBadTop = 1 << 20;  // exponent that stands for a value that is not finite

@@ -106,9 +106,9 @@ __device__ __forceinline__ void store8(void* base, size_t at, f32x4 a, f32x4 b) 
 
 // The walk's state registers: S[vt][2 m + h] holds v = 16 vt + l % 16 of the wave's rows and
 // k = 32 m + 8 g + 4 h + i.
-template <int K, int V>
+template <int K, int V, int kWaves = kWavesOf<V>>
 struct Walk {
-  static constexpr int VT = V / (16 * kWavesOf<V>);  // 16-row tiles of V per wave
+  static constexpr int VT = V / (16 * kWaves);  // 16-row tiles of V per wave
   static constexpr int KT = K / 16;
   f32x4 S[VT][KT];
 
