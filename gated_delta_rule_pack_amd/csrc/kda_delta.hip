@@ -51,6 +51,7 @@ struct DeltaShared {
 constexpr int kChainWaves = 4, kMakingWaves = 4, kWalkThreads = 64 * (kChainWaves + kMakingWaves);
 // Barriers of a chunk: the making waves' parts meet at them, and the chain waves pass them on their way.
 constexpr int kBarriers = 6;
+constexpr int kNumbersWave = 3;  // of the making waves, one with few tiles
 
 template <int K, int V, int kTerms, bool kF16In>
 struct Chain {
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
 #pragma unroll
     for (int vt = 0; vt < chain.VT; ++vt) chain.scale[vt].set(lane, 0);
     if (chunks > 0) {
-      for (int i = 0; i < kBarriers; ++i) barrier_lds();
+      for (int i = 0; i <= kBarriers; ++i) barrier_lds();
       for (int i = 0; i < chunks; ++i) {
         chain.step(sh.slot[i & 1], wave, lane);
         barrier_lds();
@@ -320,34 +321,47 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
   const uint16_t* k = reinterpret_cast<const uint16_t*>(p.k) + (h / p.group) * p.k_h;
   const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + h * p.v_h + v0;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + h * p.o_h + v0;
-  Rows<K, kThreads> rq, rk;
+  ScaledRows<K, kThreads, kF16In> rq, rk;
   Rows<V, kThreads> rv;
-  float g_next = 0.f, beta_next = 0.f;  // this lane's token of the next chunk, in the first making wave
+  uint32_t g_next = 0, beta_next = 0;  // this lane's token of the next chunk as it is stored, in one wave
+  Decays decays = {};
+  TileDecays between;
   const auto count_of = [&](int i) { return min(len - i * kC, kC); };
-  const auto first_of = [&](int i) { return begin + (int64_t)i * kC; };
-  const auto fetch = [&](int i) {
+  // (Not a running pointer: the compiler would keep that in vector registers, and take every lane's buffer by itself.)
+  const auto first_of = [&](int i) { return (int64_t)__builtin_amdgcn_readfirstlane(begin + i * kC); };
+  const auto fetch = [&](int i) __attribute__((always_inline)) {
     const int64_t first = first_of(i);
     const int count = count_of(i);
-    if (w == 0) {
-      g_next = beta_next = 0.f;
+    if (w == kNumbersWave) {
+      g_next = beta_next = 0;
       if (lane < count) {
         const int64_t at = (first + lane) * p.H + h;
-        if (p.g) {
-          const int64_t ag = p.g_per_token ? at : h;
-          g_next = p.g_bf16 ? (float)reinterpret_cast<const __bf16*>(p.g)[ag] : reinterpret_cast<const float*>(p.g)[ag];
-        }
-        beta_next = p.beta_bf16 ? (float)reinterpret_cast<const __bf16*>(p.beta)[at] : reinterpret_cast<const float*>(p.beta)[at];
+        if (p.g) g_next = load_bits(p.g, p.g_per_token ? at : h, p.g_bf16);
+        beta_next = load_bits(p.beta, at, p.beta_bf16);
       }
     }
-    rk.load(reinterpret_cast<const __bf16*>(k), p.k_t, first, count, tid);
-    rq.load(reinterpret_cast<const __bf16*>(q), p.q_t, first, count, tid);
+    rk.rows.load(reinterpret_cast<const __bf16*>(k), p.k_t, first, count, tid);
+    rq.rows.load(reinterpret_cast<const __bf16*>(q), p.q_t, first, count, tid);
     rv.load(reinterpret_cast<const __bf16*>(v), p.v_t, first, count, tid);
   };
+  const auto scale_rows = [&]() __attribute__((always_inline)) {
+    rk.scale();
+    rq.scale();
+  };
+  const auto make_decays = [&]() __attribute__((always_inline)) { decays = put_decays(sh.making, bits_value(g_next, p.g_bf16), lane); };
   const auto store = [&](int i) {
     Rows<V, kThreads>::store(sh.slot[i & 1].v, reinterpret_cast<__bf16*>(out), p.o_t, first_of(i), count_of(i), tid);
   };
   fetch(0);
-  // In turn i the chain waves walk chunk i - 1 and these make chunk i, in the place of chunk i - 2, whose outputs leave first.
+  if (w == kNumbersWave) make_decays();
+  scale_rows();
+  barrier_lds();
+  const auto make_between = [&](int l) __attribute__((always_inline)) {
+    by_wave(w, [&](auto W) { tile_decays<decltype(W)::value>(sh.making, l, between); });
+  };
+  make_between(local_copy(lane));
+  // In turn i the chain waves walk chunk i - 1 and these make chunk i, in the place of chunk i - 2, whose outputs leave first. What
+  // of chunk i + 1 waits for no tile, its rows' scales and its decays, is made where a turn leaves waves without work.
   for (int i = 0; i <= chunks; ++i) {
     if (i >= 2) store(i - 2);
     if (i == chunks) {
@@ -355,20 +369,24 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
       break;
     }
     Slot<K, V>& slot = sh.slot[i & 1];
-    put_scaled<K, kThreads, kF16In>(rk, slot.k, sh.info[0], tid, true);
-    put_scaled<K, kThreads, kF16In>(rq, slot.q, sh.info[1], tid, p.normalize);
+    rk.put(slot.k, sh.info[0], tid);
+    rq.put(slot.q, sh.info[1], tid);
     rv.put(slot.v, tid);
-    const float g = g_next, beta = beta_next;
-    if (i + 1 < chunks) fetch(i + 1);
-    barrier_lds();
-    if (w == 0) put_chunk(sh.making, slot.factors, p, sh.info[0][lane], sh.info[1][lane], g, beta, lane);
-    f32x4 kk[4], kq[4];
-    tile_products<K>(slot.k, slot.q, local_copy(lane), w, kk, kq);
+    const float beta = bits_value(beta_next, p.beta_bf16);
+    fetch(min(i + 1, chunks - 1));
     barrier_lds();
     const int l = local_copy(lane);
-    put_tiles(sh.blocks, sh.making, l, w, kk, kq, [&](int st, f16x4 x) { put_fragment(slot.p, l, w, st, x); });
+    if (w == kNumbersWave) put_chunk(sh.making, slot.factors, p, decays, sh.info[0][l], sh.info[1][l], beta, l);
+    TileProducts products;
+    by_wave(w, [&](auto W) { tile_products<K, decltype(W)::value>(slot.k, slot.q, l, products); });
+    barrier_lds();
+    by_wave(w, [&](auto W) {
+      put_tiles<decltype(W)::value>(sh.blocks, sh.making, l, products, between, [&](int tt, int st, f16x4 x) { put_fragment(slot.p, l, tt, st, x); });
+    });
     barrier_lds();
     if (w == 0) invert_diagonal(sh.blocks, l);
+    if (w == kNumbersWave) make_decays();
+    if (w != 0) scale_rows();  // the first wave's in the next two parts, in which it has none
     barrier_lds();
     const auto put_t = [&](int tt, int st, f32x4 x) {
       const Terms y = t_terms(sh.making, l, st, x);
@@ -376,8 +394,11 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
       put_fragment(slot.t + kTermP, l, tt, st, y.lo);
     };
     near_blocks(sh.blocks, l, w, put_t);
+    if (w == 0) rk.scale();
     barrier_lds();
     far_blocks(sh.blocks, l, w, put_t);
+    if (w == 0) rq.scale();
+    make_between(l);
     barrier_lds();
   }
   store(chunks - 1);

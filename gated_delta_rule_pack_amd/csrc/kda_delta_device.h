@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "kda_delta.h"
 #include "kda_device.h"
 #include "kda_unit.h"
@@ -68,6 +70,12 @@ __device__ __forceinline__ float high_value(uint32_t w) {
   return kF16In ? token_value<true>(w >> 16) : __uint_as_float(w & 0xffff0000u);
 }
 
+// A decay's or step size's bits on their way, fp32 or bf16: widened where they are used, not where they land.
+__device__ __forceinline__ uint32_t load_bits(const void* base, int64_t at, int bf16) {
+  return bf16 ? (uint32_t)reinterpret_cast<const uint16_t*>(base)[at] : reinterpret_cast<const uint32_t*>(base)[at];
+}
+__device__ __forceinline__ float bits_value(uint32_t x, int bf16) { return __uint_as_float(bf16 ? x << 16 : x); }
+
 // Maximum and sum over the 8 or 16 lanes of a row: quads, halves, whole rows.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t x) {
@@ -108,37 +116,93 @@ struct RowInfo {
   float squares;
 };
 
-// Rows of a tile of q or k in LDS as fp16, each scaled by 2^-e.
+// Rows of q or k on their way to LDS as fp16, each scaled by 2^-e: e = 0 for rows whose length is between 2^-4 and 2^5, where all
+// that counts of them fits as it stands, else what brings their largest element into [1/4, 1/2).
 template <int D, int kThreads, bool kF16In>
-__device__ __forceinline__ void put_scaled(const Rows<D, kThreads>& rows, char* tile, RowInfo* info, int tid, bool squares) {
+struct ScaledRows {
   typedef Rows<D, kThreads> R;
-  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-  tid = local_copy(tid);
-  char* at = tile + row_at<D>(tid / R::kUnits) + (tid % R::kUnits) * 16;
+  static constexpr float kLeast = 0x1p-8f, kMost = 0x1p10f;
+  R rows;
+  RowInfo info[R::kPasses];
+
+  // All rows side by side, so that their chains of sums run beside each other; one look for rows out of the ordinary.
+  __device__ __forceinline__ void squares(const u32x4 (&x)[R::kPasses], float (&s)[R::kPasses]) {
 #pragma unroll
-  for (int i = 0; i < R::kPasses; ++i) {
-    const u32x4 w = rows.w[i];
-    u16x2 top = {0, 0};
+    for (int i = 0; i < R::kPasses; ++i) s[i] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
-    const uint32_t most = row_max<R::kUnits>(max((uint32_t)top[0], (uint32_t)top[1]));
-    const bool bad = most >= (kF16In ? 0x7c00u : 0x7f80u);
-    const int e = most == 0 || bad ? 0 : __builtin_amdgcn_frexp_expf(token_value<kF16In>(most)) + 1;
-    u32x4 out = {0, 0, 0, 0};
-    float s = 0.f;
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = ldexp2(low_value<kF16In>(w[j]), -e), b = ldexp2(high_value<kF16In>(w[j]), -e);
-      s += a * a;
-      s += b * b;
-      const f16x2 h = {(_Float16)a, (_Float16)b};
-      out[j] = bad ? 0u : __builtin_bit_cast(uint32_t, h);
+      for (int i = 0; i < R::kPasses; ++i) {
+        const uint32_t word = x[i][j];
+        const f16x2 h = __builtin_bit_cast(f16x2, word);
+        s[i] = __builtin_amdgcn_fdot2(h, h, s[i], false);
+      }
+#pragma unroll
+    for (int i = 0; i < R::kPasses; ++i) s[i] += __uint_as_float(dpp<0xb1>(__float_as_uint(s[i])));
+#pragma unroll
+    for (int i = 0; i < R::kPasses; ++i) s[i] += __uint_as_float(dpp<0x4e>(__float_as_uint(s[i])));
+#pragma unroll
+    for (int i = 0; i < R::kPasses; ++i) s[i] += __uint_as_float(dpp<0x141>(__float_as_uint(s[i])));
+    if constexpr (R::kUnits == 16) {
+#pragma unroll
+      for (int i = 0; i < R::kPasses; ++i) s[i] += __uint_as_float(dpp<0x140>(__float_as_uint(s[i])));
     }
-    *reinterpret_cast<u32x4*>(at + i * R::kRows * kRowBytes<D>) = out;
-    if (squares) s = row_sum<R::kUnits>(s);
-    if (tid % R::kUnits == 0) info[tid / R::kUnits + i * R::kRows] = RowInfo{bad ? kBadRow : e, s};
   }
-}
+  __device__ __forceinline__ void scale() {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u32x4 out[R::kPasses];
+    float s[R::kPasses];
+#pragma unroll
+    for (int i = 0; i < R::kPasses; ++i) {
+      out[i] = rows.w[i];
+      if constexpr (!kF16In) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[i][j] = pair_f16(low_value<false>(rows.w[i][j]), high_value<false>(rows.w[i][j]));
+      }
+    }
+    squares(out, s);
+    // (Elements that fp16 does not hold make the sum large or not finite.)
+    float least = s[0], most = s[0];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < R::kPasses; ++i) {
+      least = fminf(least, s[i]), most = fmaxf(most, s[i]);
+      nan = nan || s[i] != s[i];
+      info[i] = RowInfo{0, s[i]};
+    }
+    if (__ballot(nan || !(least >= kLeast && most <= kMost))) {
+#pragma unroll
+      for (int i = 0; i < R::kPasses; ++i) {
+        const bool plain = s[i] >= kLeast && s[i] <= kMost;
+        u16x2 top = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, rows.w[i][j] & 0x7fff7fffu));
+        const uint32_t largest = row_max<R::kUnits>(max((uint32_t)top[0], (uint32_t)top[1]));
+        const bool bad = largest >= (kF16In ? 0x7c00u : 0x7f80u);
+        const int e = largest == 0 || bad || plain ? 0 : __builtin_amdgcn_frexp_expf(token_value<kF16In>(largest)) + 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t word = bad ? 0u : rows.w[i][j];
+          out[i][j] = pair_f16(ldexp2(low_value<kF16In>(word), -e), ldexp2(high_value<kF16In>(word), -e));
+        }
+        info[i].e = bad ? kBadRow : e;
+      }
+      squares(out, s);
+#pragma unroll
+      for (int i = 0; i < R::kPasses; ++i) info[i].squares = s[i];
+    }
+#pragma unroll
+    for (int i = 0; i < R::kPasses; ++i) rows.w[i] = out[i];
+  }
+  __device__ __forceinline__ void put(char* tile, RowInfo* to, int tid) const {
+    rows.put(tile, tid);
+    const unsigned u = (unsigned)local_copy(tid);
+    if (u % R::kUnits == 0) {
+#pragma unroll
+      for (int i = 0; i < R::kPasses; ++i) to[u / R::kUnits + i * R::kRows] = info[i];
+    }
+  }
+};
 
 // What the walk needs of a chunk beside its tiles; t, s are tokens.
 //   K'_t, Q'_t: scaled rows; rk_t, rq_t: what takes them to the keys and queries of the rule, as it is scaled here:
@@ -154,7 +218,8 @@ struct Factors {
 };
 // For the making of T and P alone.
 struct Making {
-  double G[kC];               // inclusive cumsum of g
+  alignas(16) float G[kC];    // inclusive cumsum of g, and what its rounding left
+  alignas(16) float rest[kC];
   alignas(16) float bk[kC];   // beta rk
   alignas(16) float rk[kC];
   alignas(16) float col[kC];  // beta 2^Y: the columns of T
@@ -167,13 +232,34 @@ __device__ __forceinline__ int wave_max(int x) {
   x = max(x, (int)dpp<0x140>((uint32_t)x));
   return channel_max(x);
 }
-// One lane for each token.
-__device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPlan& p, RowInfo k, RowInfo q, float g, float beta, int lane) {
-  const bool bad = k.e == kBadRow || !(g <= 0.f) || !(fabsf(beta) < INFINITY);
-  const uint64_t all_bad = __ballot(bad);
+// A token's decays, one lane for each token: what does not wait for the chunk's rows.
+struct Decays {
+  float e, c;     // e^G, e^{G_C - G}
+  float total;    // e^{G_C}
+  uint64_t bad;   // tokens whose log decay is not allowed
+};
+__device__ __forceinline__ Decays put_decays(Making& mk, float g, int lane) {
+  Decays d;
+  const bool bad = !(g <= 0.f);
+  d.bad = __ballot(bad);
+  if (bad) g = 0.f;
+  const double G = prefix_sum((double)(g < kMinLogDecay ? kMinLogDecay : g));
+  const uint64_t u = __builtin_bit_cast(uint64_t, G);
+  const double end = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
+                                                    (uint32_t)__builtin_amdgcn_readlane((int)u, 63));
+  d.e = __expf((float)G);
+  d.c = __expf((float)(end - G));
+  d.total = __expf((float)end);
+  mk.G[lane] = (float)G;
+  mk.rest[lane] = (float)(G - (double)(float)G);
+  return d;
+}
+__device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPlan& p, const Decays& d, RowInfo k, RowInfo q, float beta, int lane) {
+  const bool bad = k.e == kBadRow || !(fabsf(beta) < INFINITY);
+  const uint64_t all_bad = __ballot(bad) | d.bad;
   const int first = all_bad ? __builtin_ctzll(all_bad) : kC;
-  if (bad) beta = 0.f, g = 0.f, k = RowInfo{0, 0.f};
-  // Exponents of the chunk. A row's largest element is 2^-1 of its power of two at most: unit length means -2 to 2.
+  if (all_bad >> lane & 1) beta = 0.f, k = RowInfo{0, 0.f};
+  // Exponents of the chunk. Rows that were not scaled are near enough to unit length.
   int X = 0;
   float rk = 1.f, rq = 1.f;
   if (p.normalize) {
@@ -181,28 +267,22 @@ __device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPl
     rq = rsqrtf(q.squares + ldexp2(kNormEps, -2 * q.e));
   } else {
     const int top = wave_max(k.squares > 0.f ? k.e : -1000);
-    X = top < -2 || top > 2 ? (top == -1000 ? 0 : top) : 0;
+    X = top == -1000 ? 0 : top;
     rk = ldexp2(1.f, k.e - X);
     rq = ldexp2(1.f, q.e - X);
   }
   beta = ldexp2(beta, 2 * X);
   const int big = wave_max(beta != 0.f ? __builtin_amdgcn_frexp_expf(beta) : -1000);  // |beta| < 2^big
   const int Y = big == -1000 || (big >= -1 && big <= 2) ? 0 : -big;
-  const double G = prefix_sum((double)(g < kMinLogDecay ? kMinLogDecay : g));
-  const uint64_t u = __builtin_bit_cast(uint64_t, G);
-  const double end = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
-                                                    (uint32_t)__builtin_amdgcn_readlane((int)u, 63));
-  const float eG = __expf((float)G);
-  mk.G[lane] = G;
   mk.bk[lane] = beta * rk;
   mk.rk[lane] = rk;
   mk.col[lane] = ldexp2(beta, Y);
-  to.h[lane] = ldexp2(rk * eG, -Y);
-  to.c[lane] = rk * __expf((float)(end - G));
-  to.e[lane] = eG;
+  to.h[lane] = ldexp2(rk * d.e, -Y);
+  to.c[lane] = rk * d.c;
+  to.e[lane] = d.e;
   to.f[lane] = lane >= first || q.e == kBadRow ? __builtin_nanf("") : p.scale * ldexp2(rq, -Y);
   if (lane == 0) {
-    to.total = all_bad ? __builtin_nanf("") : __expf((float)end);
+    to.total = all_bad ? __builtin_nanf("") : d.total;
     to.shift = X + Y;
   }
 }
@@ -219,49 +299,94 @@ __device__ __forceinline__ void put_fragment(char* p, int lane, int tt, int st, 
   *reinterpret_cast<f16x4*>(p + fragment(tt, b) + (half_fragment(tt, b) ? lane * 8 : lane * 16 + (st & 1) * 8)) = x;
 }
 
-// Making T and P, by four waves of which wave w takes the token tile w: the tiles (w, st <= w) of K' K'^T and K' Q'^T, rows
-// s = 4g + i, column t = l % 16. A tile of sources is read once for both.
-template <int K>
-__device__ __forceinline__ void tile_products(const char* k, const char* q, int lane, int w, f32x4 (&kk)[4], f32x4 (&kq)[4]) {
+// Making T and P, by four waves. The ten tiles (tt, st <= tt) of K' K'^T and K' Q'^T, rows s = 4g + i, column t = l % 16, are dealt
+// out as rows of tiles: 0 and 1, 2, and two halves of 3. Each wave has code of its own, in which all places are constants.
+constexpr int kTileJobs = 3;
+template <int W>
+struct TileJobs {
+  static constexpr int kCount = W < 2 ? 3 : 2;
+  static constexpr int tt(int j) { return W == 0 ? (j > 0) : W == 1 ? 2 : 3; }
+  static constexpr int st(int j) { return W == 0 ? (j == 2) : W == 1 ? j : 2 * (W - 2) + j; }
+};
+template <typename F>
+__device__ __forceinline__ void by_wave(int w, F f) {
+  if (w == 0) f(std::integral_constant<int, 0>());
+  else if (w == 1) f(std::integral_constant<int, 1>());
+  else if (w == 2) f(std::integral_constant<int, 2>());
+  else f(std::integral_constant<int, 3>());
+}
+struct TileProducts {
+  f32x4 kk[kTileJobs], kq[kTileJobs];
+};
+template <int K, int W>
+__device__ __forceinline__ void tile_products(const char* k, const char* q, int lane, TileProducts& t) {
+  typedef TileJobs<W> Jobs;
   constexpr int KB = K / 32;
-  f16x8 own_k[KB], own_q[KB];
+#pragma unroll
+  for (int j = 0; j < Jobs::kCount; ++j) t.kk[j] = t.kq[j] = zero4();
 #pragma unroll
   for (int m = 0; m < KB; ++m) {
-    own_k[m] = __builtin_bit_cast(f16x8, read_row<K>(k, lane, 16 * w, m));
-    own_q[m] = __builtin_bit_cast(f16x8, read_row<K>(q, lane, 16 * w, m));
-  }
+    f16x8 own_k, own_q;
 #pragma unroll
-  for (int st = 0; st < 4; ++st) {
-    if (st > w) break;
-    kk[st] = kq[st] = zero4();
-#pragma unroll
-    for (int m = 0; m < KB; ++m) {
-      const f16x8 s = __builtin_bit_cast(f16x8, read_row<K>(k, lane, 16 * st, m));
-      kk[st] = mfma(s, own_k[m], kk[st]);
-      kq[st] = mfma(s, own_q[m], kq[st]);
+    for (int j = 0; j < Jobs::kCount; ++j) {
+      if (j == 0 || Jobs::tt(j) != Jobs::tt(j - 1)) {
+        own_k = __builtin_bit_cast(f16x8, read_row<K>(k, lane, 16 * Jobs::tt(j), m));
+        own_q = __builtin_bit_cast(f16x8, read_row<K>(q, lane, 16 * Jobs::tt(j), m));
+      }
+      const f16x8 s = Jobs::st(j) == Jobs::tt(j) ? own_k : __builtin_bit_cast(f16x8, read_row<K>(k, lane, 16 * Jobs::st(j), m));
+      t.kk[j] = mfma(s, own_k, t.kk[j]);
+      t.kq[j] = mfma(s, own_q, t.kq[j]);
     }
   }
 }
-// A's blocks and P's tiles from them; put_p(st, x) takes a tile of P.
-template <typename PutP>
-__device__ __forceinline__ void put_tiles(float* blocks, const Making& mk, int lane, int w, f32x4 (&kk)[4], f32x4 (&kq)[4], PutP put_p) {
-  const int g4 = lane >> 4, t = 16 * w + (lane & 15);
-  const double Gt = mk.G[t];
-  const float bk = mk.bk[t];
+// The decays between a tile's tokens, e^{G_t - G_s}. A difference of prefix sums is taken of their two parts each: exact but for 2^-24 of
+// itself.
+struct TileDecays {
+  f32x4 of[kTileJobs];
+};
+template <int W>
+__device__ __forceinline__ void tile_decays(const Making& mk, int lane, TileDecays& d) {
+  typedef TileJobs<W> Jobs;
+  f32x4 Gs[kTileJobs], rest_s[kTileJobs];
+  float Gt[kTileJobs], rest[kTileJobs];
 #pragma unroll
-  for (int st = 0; st < 4; ++st) {
-    if (st > w) break;
-    const int s0 = 16 * st + 4 * g4;
-    const f32x4 r = *reinterpret_cast<const f32x4*>(&mk.rk[s0]);
-    float* to = blocks + block_at(w, st) + 4 * g4 * kBlockRow + (lane & 15);
-    f16x4 x;
+  for (int j = 0; j < Jobs::kCount; ++j) {
+    const int t = 16 * Jobs::tt(j) + (lane & 15), s0 = 16 * Jobs::st(j) + 4 * (lane >> 4);
+    Gt[j] = mk.G[t], rest[j] = mk.rest[t];
+    Gs[j] = *reinterpret_cast<const f32x4*>(&mk.G[s0]), rest_s[j] = *reinterpret_cast<const f32x4*>(&mk.rest[s0]);
+  }
+#pragma unroll
+  for (int j = 0; j < Jobs::kCount; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d.of[j][i] = __expf((Gt[j] - Gs[j][i]) + (rest[j] - rest_s[j][i]));
+}
+// A's blocks and P's tiles; put_p(tt, st, x) takes a tile of P.
+template <int W, typename PutP>
+__device__ __forceinline__ void put_tiles(float* blocks, const Making& mk, int lane, const TileProducts& p, const TileDecays& d, PutP put_p) {
+  typedef TileJobs<W> Jobs;
+  const int g4 = lane >> 4, l16 = lane & 15;
+  f32x4 rk[kTileJobs];
+  float bk[kTileJobs];
+#pragma unroll
+  for (int j = 0; j < Jobs::kCount; ++j) {
+    rk[j] = *reinterpret_cast<const f32x4*>(&mk.rk[16 * Jobs::st(j) + 4 * g4]);
+    bk[j] = mk.bk[16 * Jobs::tt(j) + l16];
+  }
+  float* const at = blocks + 4 * g4 * kBlockRow + l16;
+#pragma unroll
+  for (int j = 0; j < Jobs::kCount; ++j) {
+    const f32x4 factor = rk[j] * d.of[j];
+    float* to = at + block_at(Jobs::tt(j), Jobs::st(j));
+    const bool diagonal = Jobs::tt(j) == Jobs::st(j);
+    f32x4 x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float factor = r[i] * __expf((float)(Gt - mk.G[s0 + i]));
-      to[i * kBlockRow] = s0 + i < t ? kk[st][i] * (factor * bk) : 0.f;
-      x[i] = (_Float16)(s0 + i <= t ? kq[st][i] * factor : 0.f);
+      const float a = p.kk[j][i] * (factor[i] * bk[j]);
+      x[i] = p.kq[j][i] * factor[i];
+      to[i * kBlockRow] = diagonal && 4 * g4 + i >= l16 ? 0.f : a;
+      if (diagonal && 4 * g4 + i > l16) x[i] = 0.f;
     }
-    put_p(st, x);
+    put_p(Jobs::tt(j), Jobs::st(j), __builtin_bit_cast(f16x4, u32x2{pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}));
   }
 }
 
@@ -273,65 +398,96 @@ __device__ __forceinline__ void invert_diagonal(float* blocks, int lane) {
 #pragma unroll
   for (int t = 0; t < 16; ++t) x[t] = t == j ? 1.f : 0.f;
 #pragma unroll
-  for (int s = 0; s < 15; ++s) {
+  for (int part = 0; part < 3; ++part) {  // a part's reads first: one wait for LDS each
+    constexpr int kFrom[4] = {0, 3, 8, 15};
+    f32x4 col[15][4];
 #pragma unroll
-    for (int c = (s + 1) / 4; c < 4; ++c) {
-      const f32x4 col = *reinterpret_cast<const f32x4*>(a + s * kBlockRow + 4 * c);
+    for (int s = kFrom[part]; s < kFrom[part + 1]; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (4 * c + i > s) x[4 * c + i] -= col[i] * x[s];
-    }
+      for (int c = (s + 1) / 4; c < 4; ++c) col[s][c] = *reinterpret_cast<const f32x4*>(a + s * kBlockRow + 4 * c);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = kFrom[part]; s < kFrom[part + 1]; ++s)
+#pragma unroll
+      for (int t = s + 1; t < 16; ++t) x[t] -= col[s][t / 4][t % 4] * x[s];
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) *reinterpret_cast<f32x4*>(a + j * kBlockRow + 4 * c) = f32x4{x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]};
 }
-// d + L^T R^T for blocks stored as [s][t]: L's (r, u) at [u][r] is the left operand, row u; R's (t, r) the right one.
-__device__ __forceinline__ f32x4 block_product(const float* left, const float* right, int lane, f32x4 d) {
-  const int g = lane >> 4, l16 = lane & 15;
-  const f32x4 a = *reinterpret_cast<const f32x4*>(left + l16 * kBlockRow + 4 * g);
+// d + L^T R^T for blocks stored as [s][t]: of L (r, u) at [u][r] is the left operand, row u; of R (t, r) the right one.
+__device__ __forceinline__ f32x4 left_block(const float* at, int lane) { return *reinterpret_cast<const f32x4*>(at + (lane & 15) * kBlockRow + 4 * (lane >> 4)); }
+__device__ __forceinline__ f32x4 right_block(const float* at, int lane) {
+  f32x4 y;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) d = mfma32(a[i], right[(4 * g + i) * kBlockRow + l16], d);
-  return d;
+  for (int i = 0; i < 4; ++i) y[i] = at[(4 * (lane >> 4) + i) * kBlockRow + (lane & 15)];
+  return y;
 }
-__device__ __forceinline__ f32x4 block_product(const float* left, f32x4 right, int lane, f32x4 d) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(left + (lane & 15) * kBlockRow + 4 * (lane >> 4));
+__device__ __forceinline__ f32x4 product(f32x4 left, f32x4 right, f32x4 d) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) d = mfma32(a[i], right[i], d);
+  for (int i = 0; i < 4; ++i) d = mfma32(left[i], right[i], d);
   return d;
 }
 // T's blocks below the diagonal, in two parts with a barrier of the four waves between them (and one before each): those
-// beside the diagonal, then the square of four. put_t(tt, st, x) takes a block, rows s = 4g + i, column t = l % 16.
+// beside the diagonal (and the diagonal's own as fragments), then the square of four. put_t(tt, st, x) takes a block, rows s = 4g + i,
+// column t = l % 16. The first wave, which inverts the diagonal, has no part in them.
 template <typename PutT>
 __device__ __forceinline__ void near_blocks(float* blocks, int lane, int w, PutT put_t) {
-  const int g4 = lane >> 4, l16 = lane & 15;
-  if (w < 2) {
-    const int t = 2 * w + 1, s = 2 * w;
-    float* at = blocks + block_at(t, s);
-    const f32x4 y = -block_product(blocks + block_at(s, s), block_product(at, blocks + block_at(t, t), lane, zero4()), lane, zero4());
+  if (w == 0) return;
+  const auto block = [&](int tt, int st) { return blocks + block_at(tt, st); };
+  if (w == 3) {
+    f32x4 y[4];
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) y[tt] = right_block(block(tt, tt), lane);
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) put_t(tt, tt, y[tt]);
+    return;
+  }
+  const auto make = [&](int t, int s) __attribute__((always_inline)) {
+    float* at = block(t, s);
+    const f32x4 low = left_block(at, lane), right = right_block(block(t, t), lane), top = left_block(block(s, s), lane);
+    const f32x4 y = -product(top, product(low, right, zero4()), zero4());
     put_t(t, s, y);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) at[(4 * g4 + i) * kBlockRow + l16] = y[i];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int tt = 2 * (w - 2) + j;
-      const float* at = blocks + block_at(tt, tt);
-      f32x4 y;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = at[(4 * g4 + i) * kBlockRow + l16];
-      put_t(tt, tt, y);
-    }
-  }
+    for (int i = 0; i < 4; ++i) at[(4 * (lane >> 4) + i) * kBlockRow + (lane & 15)] = y[i];
+  };
+  if (w == 1) make(1, 0);
+  else make(3, 2);
 }
 template <typename PutT>
 __device__ __forceinline__ void far_blocks(const float* blocks, int lane, int w, PutT put_t) {
-  if (w >= 2) return;
-  const int t = 2 + w;
+  if (w == 0) return;
   const auto block = [&](int tt, int st) { return blocks + block_at(tt, st); };
-  f32x4 z0 = block_product(block(2, 0), block(t, 2), lane, zero4()), z1 = block_product(block(2, 1), block(t, 2), lane, zero4());
-  if (w == 1) z0 = block_product(block(3, 0), block(3, 3), lane, z0), z1 = block_product(block(3, 1), block(3, 3), lane, z1);
-  put_t(t, 0, -block_product(block(1, 0), z1, lane, block_product(block(0, 0), z0, lane, zero4())));
-  put_t(t, 1, -block_product(block(1, 1), z1, lane, zero4()));
+  const f32x4 t22 = right_block(block(2, 2), lane), t32 = right_block(block(3, 2), lane), t33 = right_block(block(3, 3), lane);
+  const f32x4 a21 = left_block(block(2, 1), lane), a31 = left_block(block(3, 1), lane);
+  if (w == 3) {  // (2, 1) and (3, 1)
+    const f32x4 t11 = left_block(block(1, 1), lane);
+    f32x4 z2 = zero4(), z3 = zero4(), y2 = zero4(), y3 = zero4();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z3 = mfma32(a21[i], t32[i], z3), z2 = mfma32(a21[i], t22[i], z2);
+    z3 = product(a31, t33, z3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y2 = mfma32(t11[i], z2[i], y2), y3 = mfma32(t11[i], z3[i], y3);
+    put_t(2, 1, -y2);
+    put_t(3, 1, -y3);
+    return;
+  }
+  const f32x4 a20 = left_block(block(2, 0), lane), a30 = left_block(block(3, 0), lane);
+  const f32x4 t00 = left_block(block(0, 0), lane), t10 = left_block(block(1, 0), lane);
+  f32x4 z0 = zero4(), z1 = zero4(), y0 = zero4(), y1 = zero4();
+  if (w == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z0 = mfma32(a20[i], t32[i], z0), z1 = mfma32(a21[i], t32[i], z1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z0 = mfma32(a30[i], t33[i], z0), z1 = mfma32(a31[i], t33[i], z1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z0 = mfma32(a20[i], t22[i], z0), z1 = mfma32(a21[i], t22[i], z1);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y0 = mfma32(t00[i], z0[i], y0), y1 = mfma32(t10[i], z1[i], y1);
+  const f32x4 y = -(y0 + y1);
+  if (w == 1) put_t(3, 0, y);
+  else put_t(2, 0, y);
 }
 // A block of T with its columns' factors, in two terms.
 struct Terms {

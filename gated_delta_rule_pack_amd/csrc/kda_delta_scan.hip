@@ -77,9 +77,9 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
   const int64_t first = begin + in;
   const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + (h / p.group) * p.q_h;
   const uint16_t* k = reinterpret_cast<const uint16_t*>(p.k) + (h / p.group) * p.k_h;
-  Rows<K, kThreads> rq, rk;
-  rk.load(reinterpret_cast<const __bf16*>(k), p.k_t, first, count, tid);
-  rq.load(reinterpret_cast<const __bf16*>(q), p.q_t, first, count, tid);
+  ScaledRows<K, kThreads, kF16In> rq, rk;
+  rk.rows.load(reinterpret_cast<const __bf16*>(k), p.k_t, first, count, tid);
+  rq.rows.load(reinterpret_cast<const __bf16*>(q), p.q_t, first, count, tid);
   float g = 0.f, beta = 0.f;
   if (wave == 0 && lane < count) {
     const int64_t at = (first + lane) * p.H + h;
@@ -89,8 +89,12 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
     }
     beta = p.beta_bf16 ? (float)reinterpret_cast<const __bf16*>(p.beta)[at] : reinterpret_cast<const float*>(p.beta)[at];
   }
-  put_scaled<K, kThreads, kF16In>(rk, sh.k, sh.info[0], tid, true);
-  put_scaled<K, kThreads, kF16In>(rq, sh.q, sh.info[1], tid, p.normalize);
+  Decays decays = {};
+  if (wave == 0) decays = put_decays(sh.making, g, lane);
+  rk.scale();
+  rq.scale();
+  rk.put(sh.k, sh.info[0], tid);
+  rq.put(sh.q, sh.info[1], tid);
   barrier_lds();
   char* rec = p.records + ((int64_t)place * p.H + h) * kDeltaRecord;
   if (h % p.group == 0) {
@@ -98,11 +102,17 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
     store_fragments<K, kThreads>(sh.k, p.keys + at, tid);
     store_fragments<K, kThreads>(sh.q, p.queries + at, tid);
   }
-  if (wave == 0) put_chunk(sh.making, *reinterpret_cast<Factors*>(rec + kRecFactors), p, sh.info[0][lane], sh.info[1][lane], g, beta, lane);
-  f32x4 kk[4], kq[4];
-  tile_products<K>(sh.k, sh.q, lane, wave, kk, kq);
+  if (wave == 0) put_chunk(sh.making, *reinterpret_cast<Factors*>(rec + kRecFactors), p, decays, sh.info[0][lane], sh.info[1][lane], beta, lane);
+  TileDecays between;
+  TileProducts products;
+  by_wave(wave, [&](auto W) {
+    tile_decays<decltype(W)::value>(sh.making, lane, between);
+    tile_products<K, decltype(W)::value>(sh.k, sh.q, lane, products);
+  });
   barrier_lds();
-  put_tiles(sh.blocks, sh.making, lane, wave, kk, kq, [&](int st, f16x4 x) { put_padded(rec + kRecP, lane, wave, st, x); });
+  by_wave(wave, [&](auto W) {
+    put_tiles<decltype(W)::value>(sh.blocks, sh.making, lane, products, between, [&](int tt, int st, f16x4 x) { put_padded(rec + kRecP, lane, tt, st, x); });
+  });
   barrier_lds();
   if (wave == 0) invert_diagonal(sh.blocks, lane);
   barrier_lds();

@@ -232,8 +232,8 @@ struct Rows {
   u32x4 w[kPasses];
   __device__ __forceinline__ void load(const __bf16* base, int64_t stride, int64_t first, int count, int tid) {
     const __amdgpu_buffer_rsrc_t r = rows_buffer<D>(base, first, stride, count);
-    tid = local_copy(tid);
-    const int at = (tid / kUnits) * (int)stride * 2 + (tid % kUnits) * 16;
+    const unsigned u = (unsigned)local_copy(tid);
+    const int at = (int)(u / kUnits) * (int)stride * 2 + (int)(u % kUnits) * 16;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
       w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRows * (int)stride * 2, 0, 0));
@@ -244,18 +244,18 @@ struct Rows {
   // next, so no barrier stands between.
   static __device__ __forceinline__ void store(const char* tile, __bf16* base, int64_t stride, int64_t first, int count, int tid) {
     const __amdgpu_buffer_rsrc_t r = rows_buffer<D>(base, first, stride, count);
-    tid = local_copy(tid);
-    const int at = (tid / kUnits) * (int)stride * 2 + (tid % kUnits) * 16;
+    const unsigned u = (unsigned)local_copy(tid);
+    const int at = (int)(u / kUnits) * (int)stride * 2 + (int)(u % kUnits) * 16;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(tile + row_at<D>(tid / kUnits) + i * kRows * kRowBytes<D> + (tid % kUnits) * 16);
+      const u32x4 x = *reinterpret_cast<const u32x4*>(tile + row_at<D>((int)(u / kUnits)) + i * kRows * kRowBytes<D> + (u % kUnits) * 16);
       __builtin_amdgcn_raw_buffer_store_b128(x, r, at + i * kRows * (int)stride * 2, 0, kStreamLoad);
     }
   }
   __device__ __forceinline__ void put(char* tile, int tid) const {
-    tid = local_copy(tid);
+    const unsigned u = (unsigned)local_copy(tid);
     static_assert(kRows % 16 == 0, "whole groups of rows");
-    char* at = tile + row_at<D>(tid / kUnits) + (tid % kUnits) * 16;
+    char* at = tile + row_at<D>((int)(u / kUnits)) + (u % kUnits) * 16;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) *reinterpret_cast<u32x4*>(at + i * kRows * kRowBytes<D>) = w[i];
   }
