@@ -342,17 +342,20 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     }
     rk.rows.load(reinterpret_cast<const __bf16*>(k), p.k_t, first, count, tid);
     rq.rows.load(reinterpret_cast<const __bf16*>(q), p.q_t, first, count, tid);
-    rv.load(reinterpret_cast<const __bf16*>(v), p.v_t, first, count, tid);
+  };
+  const auto fetch_v = [&](int i) __attribute__((always_inline)) {
+    rv.load(reinterpret_cast<const __bf16*>(v), p.v_t, first_of(i), count_of(i), tid);
   };
   const auto scale_rows = [&]() __attribute__((always_inline)) {
     rk.scale();
     rq.scale();
   };
   const auto make_decays = [&]() __attribute__((always_inline)) { decays = put_decays(sh.making, bits_value(g_next, p.g_bf16), lane); };
-  const auto store = [&](int i) {
+  const auto store = [&](int i) __attribute__((always_inline)) {
     Rows<V, kThreads>::store(sh.slot[i & 1].v, reinterpret_cast<__bf16*>(out), p.o_t, first_of(i), count_of(i), tid);
   };
   fetch(0);
+  fetch_v(0);
   if (w == kNumbersWave) make_decays();
   scale_rows();
   barrier_lds();
@@ -362,27 +365,28 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
   make_between(local_copy(lane));
   // In turn i the chain waves walk chunk i - 1 and these make chunk i, in the place of chunk i - 2, whose outputs leave first. What
   // of chunk i + 1 waits for no tile, its rows' scales and its decays, is made where a turn leaves waves without work.
-  for (int i = 0; i <= chunks; ++i) {
-    if (i >= 2) store(i - 2);
-    if (i == chunks) {
-      for (int j = 0; j < kBarriers; ++j) barrier_lds();
-      break;
-    }
+  // (Loads and stores are spread over a turn, and none stands in a branch, so that a wait counts what is behind its own.)
+  for (int i = 0; i < chunks; ++i) {
     Slot<K, V>& slot = sh.slot[i & 1];
     rk.put(slot.k, sh.info[0], tid);
     rq.put(slot.q, sh.info[1], tid);
-    rv.put(slot.v, tid);
-    const float beta = bits_value(beta_next, p.beta_bf16);
-    fetch(min(i + 1, chunks - 1));
     barrier_lds();
-    const int l = local_copy(lane);
-    if (w == kNumbersWave) put_chunk(sh.making, slot.factors, p, decays, sh.info[0][l], sh.info[1][l], beta, l);
+    const int l = local_copy(lane), next = min(i + 1, chunks - 1);
+    if (w == kNumbersWave)
+      put_chunk(sh.making, slot.factors, p, decays, sh.info[0][l], sh.info[1][l], bits_value(beta_next, p.beta_bf16), l);
     TileProducts products;
     by_wave(w, [&](auto W) { tile_products<K, decltype(W)::value>(slot.k, slot.q, l, products); });
+    fetch(next);
     barrier_lds();
     by_wave(w, [&](auto W) {
       put_tiles<decltype(W)::value>(sh.blocks, sh.making, l, products, between, [&](int tt, int st, f16x4 x) { put_fragment(slot.p, l, tt, st, x); });
     });
+    {
+      // The outputs of chunk i - 2; for the first two a buffer of no rows.
+      const __amdgpu_buffer_rsrc_t to = i < 2 ? __builtin_amdgcn_make_buffer_rsrc(out, (short)0, 0, kBufWord3)
+                                              : rows_buffer<V>(reinterpret_cast<__bf16*>(out), first_of(i - 2), p.o_t, kC);
+      Rows<V, kThreads>::store(slot.v, to, p.o_t, tid);
+    }
     barrier_lds();
     if (w == 0) invert_diagonal(sh.blocks, l);
     if (w == kNumbersWave) make_decays();
@@ -394,6 +398,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
       put_fragment(slot.t + kTermP, l, tt, st, y.lo);
     };
     near_blocks(sh.blocks, l, w, put_t);
+    rv.put(slot.v, tid);
+    fetch_v(next);
     if (w == 0) rk.scale();
     barrier_lds();
     far_blocks(sh.blocks, l, w, put_t);
@@ -401,6 +407,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     make_between(l);
     barrier_lds();
   }
+  if (chunks >= 2) store(chunks - 2);
+  for (int j = 0; j < kBarriers; ++j) barrier_lds();
   store(chunks - 1);
 }
 

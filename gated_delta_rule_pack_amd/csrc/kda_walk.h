@@ -243,7 +243,9 @@ struct Rows {
   // which have no use for them (385 us without the hint then). A thread reads the bytes that its own put writes
   // next, so no barrier stands between.
   static __device__ __forceinline__ void store(const char* tile, __bf16* base, int64_t stride, int64_t first, int count, int tid) {
-    const __amdgpu_buffer_rsrc_t r = rows_buffer<D>(base, first, stride, count);
+    store(tile, rows_buffer<D>(base, first, stride, count), stride, tid);
+  }
+  static __device__ __forceinline__ void store(const char* tile, __amdgpu_buffer_rsrc_t r, int64_t stride, int tid) {
     const unsigned u = (unsigned)local_copy(tid);
     const int at = (int)(u / kUnits) * (int)stride * 2 + (int)(u % kUnits) * 16;
 #pragma unroll
