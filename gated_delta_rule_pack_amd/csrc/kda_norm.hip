@@ -3,10 +3,14 @@
 // For a row x of D channels, r = 1 / sqrt(m sum x^2 + eps) (m = 1 / D or 1), w the offset weight and R the rotation:
 //   forward   y = R (x r w)
 //   backward  z = R^T dy;  dw = sum over rows of z x r;  u = z w;  dx = r (u - m x r sum(u x r)).
-// Every element is read and written once, so in 16-byte vectors both are bound by memory. A row's sums are taken over
-// the lanes that hold it before anything of it is written, so a result may take its input's place. Squares are
-// summed in 64 bits: their sum overflows in 32 from |x| = 1.8e19 on, and these kernels wait for memory anyway.
+// Every element is read and written once, so in vectors both are bound by memory: bf16 tokens of 32 + 8 heads of 128,
+// 16384 forward in 67 us and 8192 backward in 54, both at 5.0 TB/s with their weight gradients' sums counted; a few
+// tokens by the angles' latency, 6 us. A row's sums are taken over the lanes that hold it before anything of it is
+// written, so a result may take its input's place. Squares are summed in 64 bits: their sum overflows in 32 from
+// |x| = 1.8e19 on, and these kernels wait for memory anyway.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "kda_delta.h"
 #include "kda_device.h"
@@ -17,6 +21,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+// As many workgroups as the registers of their 16-byte form let stay on the chip, each walking its share of the tokens
+// (16384 tokens of 32 + 8 heads of 128, backward 8192, bf16: 1024 and 512 took 67 and 54 us; 2048 and 1024 67 and 59, 512
+// and 256 groups of a backward pass 54 and 77, 768 with their uneven share 61).
+constexpr int kForwardGroups = 1024, kBackwardGroups = 512;
 
 template <int DT>
 struct Elem;
@@ -39,6 +47,8 @@ __device__ __forceinline__ double xor_lanes(double x, int d) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+__device__ __forceinline__ float xor_lanes(float x, int d) { return __shfl_xor(x, d); }
+
 // 1 / sqrt(s) for s = m sum x^2 + eps, which may lie outside fp32 where its root does not.
 __device__ __forceinline__ float inverse_root(double s) {
   if (!(s < 1e300)) return __builtin_nanf("");  // a row that is not finite
@@ -57,100 +67,192 @@ __device__ __forceinline__ E* row_at(const void* base, int64_t t, int h, int64_t
   return reinterpret_cast<E*>(const_cast<void*>(base)) + t * stride_t + h * stride_h;
 }
 
-// 16-byte vectors. A row is held by `lanes` lanes (a power of two), two vectors each: a pair that is rotated, or two
-// that pass through. A workgroup takes `tokens` tokens at a time, whose angles meet in LDS, and its groups of lanes
-// walk their q rows and then their k rows. The backward pass keeps the sums of its lanes' weight gradients in
-// registers over all its tokens, and leaves them in the workspace.
-template <int DT, int VEC, bool kInterleaved, bool kBack>
+// The sum over the `lanes` neighbours (a power of two) that hold a row, in each of them.
+template <int kCtrl>
+__device__ __forceinline__ float moved(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xf, 0xf, true));
+}
+template <int kCtrl>
+__device__ __forceinline__ double moved(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)u, kCtrl, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), kCtrl, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <typename X>
+__device__ __forceinline__ X lane_sum(X x, int lanes) {
+  if (lanes > 1) x += moved<0xb1>(x);   // quad_perm 1 0 3 2
+  if (lanes > 2) x += moved<0x4e>(x);   // quad_perm 2 3 0 1
+  if (lanes > 4) x += moved<0x141>(x);  // the half row mirrored: its quads are uniform by now
+  if (lanes > 8) x += moved<0x140>(x);  // the row of 16 mirrored
+  if (lanes > 16) x += xor_lanes(x, 16);
+  if (lanes > 32) x += xor_lanes(x, 32);
+  return x;
+}
+
+// Vectors of VEC elements. A row is held by `lanes` lanes (a power of two), two vectors each: a pair that is rotated, or
+// two that pass through. A workgroup takes `tokens` tokens at a time, whose angles meet in LDS beside the weights, and
+// its groups of lanes walk their q rows and then their k rows, each row's loads issued while the one before is worked on.
+// The backward pass keeps the sums of its lanes' weight gradients in registers over all its tokens, and leaves
+// them in the workspace.
+template <int DT, int VEC, bool kBack>
 __global__ __launch_bounds__(kThreads) void norm_wide(const NormPlan p, int tokens, int pairs, int items, int lanes) {
   typedef typename Elem<DT>::type E;
   typedef E V __attribute__((ext_vector_type(VEC)));
-  extern __shared__ __align__(16) char shared[];
-  float2* turn = reinterpret_cast<float2*>(shared);  // [tokens][half]
+  typedef float FV __attribute__((ext_vector_type(VEC)));
+  typedef float TV __attribute__((ext_vector_type(2 * VEC)));
+  extern __shared__ __align__(64) char shared[];
   const int half = p.rot_dim / 2, u = threadIdx.x % lanes, group = threadIdx.x / lanes, groups = kThreads / lanes;
-  const auto place = [&](int u, int& d0, int& d1) {
+  float2* turn = reinterpret_cast<float2*>(shared);                    // [tokens][half]
+  float* weights = reinterpret_cast<float*>(turn + tokens * half);     // [2][D]
+  const auto place = [&](int u, int& d0, int& d1) __attribute__((always_inline)) {
     if (u >= pairs) d0 = p.rot_dim + (u - pairs) * 2 * VEC, d1 = d0 + VEC;
-    else if (kInterleaved) d0 = 2 * u * VEC, d1 = d0 + VEC;
+    else if (p.interleaved) d0 = 2 * u * VEC, d1 = d0 + VEC;
     else d0 = u * VEC, d1 = d0 + half;
   };
   int d0, d1;
   place(u, d0, d1);
   const bool rotate = u < pairs, here = u < items, second = here && d1 < p.D;
+  // Lanes without a vector load the row's first, which counts in no sum and is not written.
+  d0 = here ? d0 : 0, d1 = second ? d1 : 0;
   const float share = p.l2 ? 1.f : 1.f / (float)p.D;
   const double m = p.l2 ? 1. : 1. / p.D;
-  float w[2][2 * VEC], sum[kBack ? 2 : 1][2 * VEC];
+  float sum[kBack ? 2 : 1][2 * VEC];
+  if constexpr (kBack)
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+    for (int j = 0; j < 2 * VEC; ++j) sum[0][j] = sum[1][j] = 0.f;
+
+  // A turn of the walk: each group's i-th row of the tokens from `first` on, all of q or all of k.
+  struct Turn {
+    int64_t first;
+    int i;
+  };
+  struct Row {
+    V x0, x1, z0, z1;
+  };
+  const int64_t step = (int64_t)gridDim.x * tokens;
+  const auto count_of = [&](const Turn& w) __attribute__((always_inline)) { return (int)min((int64_t)tokens, p.T - w.first); };
+  const auto turns_of = [&](int count, int c) __attribute__((always_inline)) { return (count * p.H[c] + groups - 1) / groups; };
+  const auto next_of = [&](Turn w) __attribute__((always_inline)) {
+    const int count = count_of(w);
+    if (++w.i == turns_of(count, 0) + turns_of(count, 1)) w.i = 0, w.first += step;
+    return w;
+  };
+  // Its tensor, token and head, and whether there is such a row (the last one else). At most 8 tokens of at most 2^16
+  // heads: the quotient is off by less than its distance from a whole number.
+  const auto row_of = [&](const Turn& w, int& c, int& t, int& h) __attribute__((always_inline)) {
+    const int count = count_of(w), of_q = turns_of(count, 0);
+    c = w.i >= of_q;
+    const int heads = p.H[c], row = (c ? w.i - of_q : w.i) * groups + group, at = min(row, count * heads - 1);
+    t = (int)(((float)at + 0.5f) * __builtin_amdgcn_rcpf((float)heads));
+    h = at - t * heads;
+    return row == at;
+  };
+  const auto fetch = [&](Row& r, const Turn& w) __attribute__((always_inline)) {
+    int c, t, h;
+    row_of(w, c, t, h);
+    const E* in = row_at<E>(p.in[c], w.first + t, h, p.in_t[c], p.in_h[c]);
+    r.x0 = *reinterpret_cast<const V*>(in + d0);
+    r.x1 = *reinterpret_cast<const V*>(in + d1);
+    if constexpr (kBack) {
+      const E* grad = row_at<E>(p.grad[c], w.first + t, h, p.grad_t[c], p.grad_h[c]);
+      r.z0 = *reinterpret_cast<const V*>(grad + d0);
+      r.z1 = *reinterpret_cast<const V*>(grad + d1);
+    }
+  };
+  const auto angles = [&](const Turn& w) __attribute__((always_inline)) {
+    if (w.i > 0) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < count_of(w) * half; i += kThreads) turn[i] = rotation(p, (int)w.first + i / half, i % half, kBack);
+    __syncthreads();
+  };
+  const auto work = [&](const Row& row, const Turn& w) __attribute__((always_inline)) {
+    int c, t, h;
+    const bool real = row_of(w, c, t, h);
+    float x[2 * VEC], z[2 * VEC], wt[2 * VEC];
+    double s0 = 0., s1 = 0.;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      w[c][j] = here ? weight_at<E>(p, c, d0 + j) : 1.f;
-      w[c][VEC + j] = second ? weight_at<E>(p, c, d1 + j) : 1.f;
-      if constexpr (kBack) sum[c][j] = sum[c][VEC + j] = 0.f;
+      x[j] = (float)row.x0[j], x[VEC + j] = (float)row.x1[j];
+      s0 += (double)x[j] * x[j];
+      s1 += (double)x[VEC + j] * x[VEC + j];
     }
-  const int64_t step = (int64_t)gridDim.x * tokens;
-  for (int64_t first = (int64_t)blockIdx.x * tokens; first < p.T; first += step) {
-    const int count = (int)min((int64_t)tokens, p.T - first);
-    if (half > 0) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < count * half; i += kThreads) turn[i] = rotation(p, (int)first + i / half, i % half, kBack);
-      __syncthreads();
+    const double s = lane_sum((here ? s0 : 0.) + (second ? s1 : 0.), lanes);
+    const float r = inverse_root(m * s + p.eps);
+    const FV w0 = *reinterpret_cast<const FV*>(weights + c * p.D + d0), w1 = *reinterpret_cast<const FV*>(weights + c * p.D + d1);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) wt[j] = w0[j], wt[VEC + j] = w1[j];
+#pragma unroll
+    for (int j = 0; j < 2 * VEC; ++j) {
+      x[j] *= r;
+      z[j] = kBack ? (float)(j < VEC ? row.z0[j % VEC] : row.z1[j % VEC]) : x[j] * wt[j];
     }
+    if (rotate) {
+      const TV cs = *reinterpret_cast<const TV*>(turn + t * half + u * VEC);
+      const auto rotated = [&](float& a, float& b, int j) __attribute__((always_inline)) {
+        const float ao = a * cs[2 * j] - b * cs[2 * j + 1], bo = a * cs[2 * j + 1] + b * cs[2 * j];
+        a = ao, b = bo;
+      };
+      if (p.interleaved) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      for (int row = group; row < count * p.H[c]; row += groups) {
-        const int t = row / p.H[c], h = row - t * p.H[c];
-        const E* in = row_at<E>(p.in[c], first + t, h, p.in_t[c], p.in_h[c]);
-        V x0 = {}, x1 = {}, z0 = {}, z1 = {};
-        if (here) x0 = *reinterpret_cast<const V*>(in + d0);
-        if (second) x1 = *reinterpret_cast<const V*>(in + d1);
-        if constexpr (kBack) {
-          const E* grad = row_at<E>(p.grad[c], first + t, h, p.grad_t[c], p.grad_h[c]);
-          if (here) z0 = *reinterpret_cast<const V*>(grad + d0);
-          if (second) z1 = *reinterpret_cast<const V*>(grad + d1);
-        }
-        float x[2 * VEC], z[2 * VEC];
-        double s = 0.;
+        for (int j = 0; j < VEC; ++j) rotated(z[2 * j], z[2 * j + 1], j);
+      } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          x[j] = (float)x0[j], x[VEC + j] = (float)x1[j];
-          s += (double)x[j] * x[j];
-          s += (double)x[VEC + j] * x[VEC + j];
-        }
-        for (int d = 1; d < lanes; d <<= 1) s += xor_lanes(s, d);
-        const float r = inverse_root(m * s + p.eps);
-#pragma unroll
-        for (int j = 0; j < 2 * VEC; ++j) {
-          x[j] *= r;
-          z[j] = kBack ? (float)(j < VEC ? z0[j % VEC] : z1[j % VEC]) : x[j] * w[c][j];
-        }
-        if (rotate) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float2 cs = turn[t * half + u * VEC + j];
-            float &a = z[kInterleaved ? 2 * j : j], &b = z[kInterleaved ? 2 * j + 1 : VEC + j];
-            const float ao = a * cs.x - b * cs.y, bo = a * cs.y + b * cs.x;
-            a = ao, b = bo;
-          }
-        }
-        if constexpr (kBack) {
-          float dot = 0.f;
-#pragma unroll
-          for (int j = 0; j < 2 * VEC; ++j) {
-            sum[c][j] += z[j] * x[j];
-            z[j] *= w[c][j];
-            dot += z[j] * x[j];
-          }
-          for (int d = 1; d < lanes; d <<= 1) dot += __shfl_xor(dot, d);
-          dot *= share;
-#pragma unroll
-          for (int j = 0; j < 2 * VEC; ++j) z[j] = r * (z[j] - x[j] * dot);
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x0[j] = (E)z[j], x1[j] = (E)z[VEC + j];
-        E* out = row_at<E>(p.out[c], first + t, h, p.out_t[c], p.out_h[c]);
-        if (here) *reinterpret_cast<V*>(out + d0) = x0;
-        if (second) *reinterpret_cast<V*>(out + d1) = x1;
+        for (int j = 0; j < VEC; ++j) rotated(z[j], z[VEC + j], j);
       }
+    }
+    if constexpr (kBack) {
+      if (real) {
+        if (c == 0) {
+#pragma unroll
+          for (int j = 0; j < 2 * VEC; ++j) sum[0][j] += z[j] * x[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2 * VEC; ++j) sum[1][j] += z[j] * x[j];
+        }
+      }
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        z[j] *= wt[j], z[VEC + j] *= wt[VEC + j];
+        a += z[j] * x[j], b += z[VEC + j] * x[VEC + j];
+      }
+      const float dot = share * lane_sum((here ? a : 0.f) + (second ? b : 0.f), lanes);
+#pragma unroll
+      for (int j = 0; j < 2 * VEC; ++j) z[j] = r * (z[j] - x[j] * dot);
+    }
+    V y0, y1;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) y0[j] = (E)z[j], y1[j] = (E)z[VEC + j];
+    E* out = row_at<E>(p.out[c], w.first + t, h, p.out_t[c], p.out_h[c]);
+    if (real && here) *reinterpret_cast<V*>(out + d0) = y0;
+    if (real && second) *reinterpret_cast<V*>(out + d1) = y1;
+  };
+
+  Turn w = {(int64_t)blockIdx.x * tokens, 0};
+  if (w.first < p.T) {
+    Row a, b;
+    fetch(a, w);
+    for (int i = threadIdx.x; i < 2 * p.D; i += kThreads) weights[i] = weight_at<E>(p, i >= p.D, i >= p.D ? i - p.D : i);
+    for (;;) {
+      angles(w);
+      Turn n = next_of(w);
+      if (n.first >= p.T) {
+        work(a, w);
+        break;
+      }
+      fetch(b, n);
+      work(a, w);
+      w = n;
+      angles(w);
+      n = next_of(w);
+      if (n.first >= p.T) {
+        work(b, w);
+        break;
+      }
+      fetch(a, n);
+      work(b, w);
+      w = n;
     }
   }
   if constexpr (kBack) {
@@ -181,7 +283,8 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Single elements, for rows that 16-byte accesses do not fit: a workgroup for each token at a time, a wave for each of its
+// Single elements, for rows of more than 64 pairs of the vectors that fit them (more than 128 channels with an odd half
+// or at an odd address, more than 512 in fp32): a workgroup for each token at a time, a wave for each of its
 // rows. The row passes through the wave's LDS, where its lanes find the other halves of their pairs.
 template <int DT, bool kBack>
 __global__ __launch_bounds__(kThreads) void norm_narrow(const NormPlan p) {
@@ -257,61 +360,75 @@ __global__ __launch_bounds__(kThreads) void norm_narrow(const NormPlan p) {
   }
 }
 
-// The workgroups' sums of weight gradients, joined: 16 channels to a workgroup, 16 threads to a channel.
+// The workgroups' sums of weight gradients, joined: 16 channels to a workgroup, 64 threads to a channel, four loads in
+// flight at a time (512 workgroups' sums of 128 channels: 4.6 us; 16 threads to a channel and one load at a time took 20 for 1024).
 template <int DT>
-__global__ __launch_bounds__(kThreads) void norm_sums(const NormPlan p) {
+__global__ __launch_bounds__(1024) void norm_sums(const NormPlan p) {
   typedef typename Elem<DT>::type E;
-  __shared__ float part[16][17];
+  constexpr int kWays = 64;
+  __shared__ float part[kWays][17];
   const int c = blockIdx.y, lane = threadIdx.x & 15, way = threadIdx.x >> 4, d = blockIdx.x * 16 + lane;
+  const float* from = p.sums + c * p.D + min(d, p.D - 1);
   float x = 0.f;
-  if (d < p.D)
-    for (int i = way; i < p.groups; i += 16) x += p.sums[((int64_t)i * 2 + c) * p.D + d];
+  for (int i = way; i < p.groups; i += 4 * kWays) {
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = from[(int64_t)min(i + j * kWays, p.groups - 1) * 2 * p.D];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x += i + j * kWays < p.groups ? y[j] : 0.f;
+  }
   part[way][lane] = x;
   __syncthreads();
   void* to = p.grad_weight[c];
   if (way != 0 || d >= p.D || !to) return;
   x = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x += part[i][lane];
+  for (int i = 0; i < kWays; ++i) x += part[i][lane];
   if (p.weight_f32) reinterpret_cast<float*>(to)[d] = x;
   else reinterpret_cast<E*>(to)[d] = (E)x;
 }
 
+// The widest vectors that the rows allow, 16 bytes at most; rows of more than 64 pairs of vectors take single elements.
 template <int DT, int VEC, bool kBack>
-int launch_wide(const NormPlan& p, unsigned grid, int tokens, int pairs, int items, int lanes, hipStream_t s) {
-  size_t shared = (size_t)tokens * (p.rot_dim / 2) * sizeof(float2);
-  if (kBack && shared < (size_t)kThreads * 2 * VEC * sizeof(float)) shared = (size_t)kThreads * 2 * VEC * sizeof(float);
-  if (p.interleaved) norm_wide<DT, VEC, true, kBack><<<grid, kThreads, shared, s>>>(p, tokens, pairs, items, lanes);
-  else norm_wide<DT, VEC, false, kBack><<<grid, kThreads, shared, s>>>(p, tokens, pairs, items, lanes);
-  return (int)hipGetLastError();
-}
-
-// 16-byte accesses where the rows allow them, single elements otherwise.
-template <int DT, bool kBack>
-int launch_dt(const NormPlan& p, hipStream_t s) {
-  constexpr int VEC = DT == kF32 ? 4 : 8;
+int launch_vec(const NormPlan& p, hipStream_t s) {
   const int half = p.rot_dim / 2;
-  const auto fits = [](const void* at, int64_t st, int64_t sh) { return (uintptr_t)at % 16 == 0 && st % VEC == 0 && sh % VEC == 0; };
+  constexpr int kBytes = VEC * (DT == kF32 ? 4 : 2);
+  const auto fits = [](const void* at, int64_t st, int64_t sh) { return (uintptr_t)at % kBytes == 0 && st % VEC == 0 && sh % VEC == 0; };
   bool wide = half % VEC == 0 && p.D % VEC == 0;
   for (int c = 0; c < 2; ++c) {
     if (p.H[c] == 0) continue;
     wide = wide && fits(p.in[c], p.in_t[c], p.in_h[c]) && fits(p.out[c], p.out_t[c], p.out_h[c]);
     if (kBack) wide = wide && fits(p.grad[c], p.grad_t[c], p.grad_h[c]);
   }
+  if constexpr (VEC > 1) {
+    if (!wide) return launch_vec<DT, VEC / 2, kBack>(p, s);
+  }
   const int pairs = half / VEC, items = pairs + ((p.D - p.rot_dim) / VEC + 1) / 2;
   int lanes = 1;
   while (lanes < items) lanes *= 2;
-  if (!wide || lanes > 64) {
+  if (lanes > 64) {
     const unsigned grid = kBack ? (unsigned)p.groups : (unsigned)(p.T < (1 << 20) ? p.T : 1 << 20);
     const size_t shared = (size_t)half * sizeof(float2) + (size_t)kWaves * p.D * sizeof(float) * (kBack ? 3 : 1);
     norm_narrow<DT, kBack><<<grid, kThreads, shared, s>>>(p);
     return (int)hipGetLastError();
   }
-  // Four tokens share a workgroup's start where there are enough to fill the chip.
-  const int tokens = p.T >= 2048 ? 4 : 1;
+  // Angles are made, between two barriers, for four tokens at a time, and for up to eight where that lets each group of
+  // lanes walk five rows behind them; for fewer where the workgroups would run out of tokens (16384 tokens of 32 + 8
+  // heads, 64 of 128 channels rotated: 1, 2, 4, 8 tokens 86, 71, 67, 71 us; of 8 + 2 heads of 256: 4 and 8 tokens
+  // 40 and 37 us, backward 68 and 60).
+  const int most = kBack ? p.groups : kForwardGroups, even = (int)(((int64_t)p.T + most - 1) / most);
+  const int heads = p.H[0] + p.H[1], long_enough = (5 * (kThreads / lanes) + heads - 1) / heads;
+  const int tokens = std::min(even, std::max(4, std::min(8, long_enough)));
   const int batches = (p.T + tokens - 1) / tokens;
-  const unsigned grid = kBack ? (unsigned)p.groups : (unsigned)(batches < (1 << 20) ? batches : 1 << 20);
-  return launch_wide<DT, VEC, kBack>(p, grid, tokens, pairs, items, lanes, s);
+  const unsigned grid = kBack ? (unsigned)p.groups : (unsigned)(batches < most ? batches : most);
+  size_t shared = (size_t)tokens * half * sizeof(float2) + 2 * p.D * sizeof(float);
+  if (kBack && shared < (size_t)kThreads * 2 * VEC * sizeof(float)) shared = (size_t)kThreads * 2 * VEC * sizeof(float);
+  norm_wide<DT, VEC, kBack><<<grid, kThreads, shared, s>>>(p, tokens, pairs, items, lanes);
+  return (int)hipGetLastError();
+}
+template <int DT, bool kBack>
+int launch_dt(const NormPlan& p, hipStream_t s) {
+  return launch_vec<DT, DT == kF32 ? 4 : 8, kBack>(p, s);
 }
 
 template <int DT>
@@ -321,13 +438,13 @@ int launch_back(const NormPlan& p, hipStream_t s) {
     if (error) return error;
   }
   if (!p.grad_weight[0] && !p.grad_weight[1]) return 0;
-  norm_sums<DT><<<dim3((unsigned)(p.D + 15) / 16, 2), kThreads, 0, s>>>(p);
+  norm_sums<DT><<<dim3((unsigned)(p.D + 15) / 16, 2), 1024, 0, s>>>(p);
   return (int)hipGetLastError();
 }
 
 }  // namespace
 
-int norm_groups(int T) { return T < 1024 ? T : 1024; }
+int norm_groups(int T) { return std::min(T, kBackwardGroups); }
 
 int launch_qk_norm(const NormPlan& p, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
