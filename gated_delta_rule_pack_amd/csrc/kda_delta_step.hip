@@ -18,15 +18,54 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// 8 neighbouring elements of the state, as they lie in memory.
 template <int SDT>
-__device__ __forceinline__ void load8(const void* base, int64_t at, f32x4& a, f32x4& b) {
-  a = load_state4<SDT>(base, at);
-  b = load_state4<SDT>(base, at + 4);
+struct Raw8 {
+  u32x4 x[SDT == kF32 ? 2 : 1];
+};
+template <int SDT>
+__device__ __forceinline__ Raw8<SDT> load8(const void* base, int64_t at) {
+  return *reinterpret_cast<const Raw8<SDT>*>(reinterpret_cast<const char*>(base) + at * (SDT == kF32 ? 4 : 2));
+}
+// In fp32, or zeros where `keep` is 0 (all bits set else): a slot that starts anew may hold anything.
+template <int SDT>
+__device__ __forceinline__ void unpack8(const Raw8<SDT>& r, uint32_t keep, f32x4& a, f32x4& b) {
+  if constexpr (SDT == kF32) {
+    a = __builtin_bit_cast(f32x4, r.x[0] & keep);
+    b = __builtin_bit_cast(f32x4, r.x[1] & keep);
+  } else if constexpr (SDT == kF16) {
+    const f16x8 h = __builtin_bit_cast(f16x8, r.x[0] & keep);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = (float)h[j], b[j] = (float)h[4 + j];
+  } else {
+    const u32x4 u = r.x[0] & keep;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t x = u[j], y = u[2 + j];
+      a[2 * j] = __builtin_bit_cast(float, x << 16), a[2 * j + 1] = __builtin_bit_cast(float, x & 0xffff0000u);
+      b[2 * j] = __builtin_bit_cast(float, y << 16), b[2 * j + 1] = __builtin_bit_cast(float, y & 0xffff0000u);
+    }
+  }
 }
 template <int SDT>
 __device__ __forceinline__ void store8(void* base, int64_t at, f32x4 a, f32x4 b) {
-  store_state4<SDT>(base, at, a);
-  store_state4<SDT>(base, at + 4, b);
+  Raw8<SDT> r;
+  if constexpr (SDT == kF32) {
+    r.x[0] = __builtin_bit_cast(u32x4, a), r.x[1] = __builtin_bit_cast(u32x4, b);
+  } else if constexpr (SDT == kF16) {
+    f16x8 h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = (_Float16)a[j], h[4 + j] = (_Float16)b[j];
+    r.x[0] = __builtin_bit_cast(u32x4, h);
+  } else {
+    bf16x8 h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = to_bf16(a[j]), h[4 + j] = to_bf16(b[j]);
+    r.x[0] = __builtin_bit_cast(u32x4, h);
+  }
+  *reinterpret_cast<Raw8<SDT>*>(reinterpret_cast<char*>(base) + at * (SDT == kF32 ? 4 : 2)) = r;
 }
 __device__ __forceinline__ float load_token(const void* base, int64_t at, int f16) {
   return f16 ? (float)reinterpret_cast<const _Float16*>(base)[at] : (float)reinterpret_cast<const __bf16*>(base)[at];
@@ -47,9 +86,22 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaPlan p)
   __shared__ float skq;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int n = blockIdx.x / p.H, h = blockIdx.x % p.H;
+  // The row's own loads go out before its slot is known. Wave 0: q and k. Wave 1: v.
+  constexpr int kOf = K / 64;
+  float q[kOf], k[kOf], v[V / 64];
+  if (wave == 0) {
+#pragma unroll
+    for (int j = 0; j < kOf; ++j) {
+      q[j] = load_token(p.q, n * p.q_t + (h / p.group) * p.q_h + lane + 64 * j, p.f16);
+      k[j] = load_token(p.k, n * p.k_t + (h / p.group) * p.k_h + lane + 64 * j, p.f16);
+    }
+  } else if (wave == 1) {
+#pragma unroll
+    for (int j = 0; j < V / 64; ++j) v[j] = load_token(p.v, n * p.v_t + h * p.v_h + lane + 64 * j, p.f16);
+  }
   const int64_t slot = p.indices ? p.indices[n] : n;
   if (slot < 0 || slot >= p.num_slots) return;  // padding
-  const bool old = !p.flags || p.flags[n];
+  const uint32_t keep = !p.flags || p.flags[n] ? ~0u : 0u;
   const int64_t plane = slot * p.stride0 + (int64_t)h * K * V;
 
   constexpr int kCols = kKfirst ? V : K, kRows = kKfirst ? K : V;
@@ -60,13 +112,9 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaPlan p)
   const int col = (tid % kLanes) * 8;
   const int64_t at = plane + tid / kLanes * kCols + col;
   constexpr int kStep = kPer * kCols;
-  f32x4 a[kIters], b[kIters];
+  Raw8<SDT> raw[kIters];
 #pragma unroll
-  for (int i = 0; i < kIters; ++i) a[i] = b[i] = zero4();
-  if (old) {
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) load8<SDT>(p.state_in, at + i * kStep, a[i], b[i]);
-  }
+  for (int i = 0; i < kIters; ++i) raw[i] = load8<SDT>(p.state_in, at + i * kStep);
   float g = 0.f;
   if (p.g) {
     const int64_t i = p.g_per_token ? (int64_t)n * p.H + h : h;
@@ -77,15 +125,7 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaPlan p)
   if (!(g <= 0.f)) beta = __builtin_nanf("");
   const float decay = __expf(g);
 
-  // Wave 0: q and k. Wave 1: v.
   if (wave == 0) {
-    constexpr int kOf = K / 64;
-    float q[kOf], k[kOf];
-#pragma unroll
-    for (int j = 0; j < kOf; ++j) {
-      q[j] = load_token(p.q, n * p.q_t + (h / p.group) * p.q_h + lane + 64 * j, p.f16);
-      k[j] = load_token(p.k, n * p.k_t + (h / p.group) * p.k_h + lane + 64 * j, p.f16);
-    }
     if (p.normalize) {
       const float rq = unit_factor(q), rk = unit_factor(k);
 #pragma unroll
@@ -102,7 +142,7 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaPlan p)
     if (lane == 0) skq = kq;
   } else if (wave == 1) {
 #pragma unroll
-    for (int j = 0; j < V / 64; ++j) sv[lane + 64 * j] = load_token(p.v, n * p.v_t + h * p.v_h + lane + 64 * j, p.f16);
+    for (int j = 0; j < V / 64; ++j) sv[lane + 64 * j] = v[j];
   }
   __syncthreads();
 
@@ -114,13 +154,11 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaPlan p)
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
       const int row = tid / kLanes + i * kPer;
-      float u = dot4(a[i], k0) + dot4(b[i], k1), w = dot4(a[i], q0) + dot4(b[i], q1);
-#pragma unroll
-      for (int d = 1; d < kLanes; d <<= 1) u += __shfl_xor(u, d), w += __shfl_xor(w, d);
+      f32x4 a, b;
+      unpack8<SDT>(raw[i], keep, a, b);
+      const float u = lane_sum(dot4(a, k0) + dot4(b, k1), kLanes), w = lane_sum(dot4(a, q0) + dot4(b, q1), kLanes);
       const float delta = beta * (sv[row] - decay * u);
-      a[i] = a[i] * decay + k0 * delta;
-      b[i] = b[i] * decay + k1 * delta;
-      store8<SDT>(p.state_out, at + i * kStep, a[i], b[i]);
+      store8<SDT>(p.state_out, at + i * kStep, a * decay + k0 * delta, b * decay + k1 * delta);
       if (tid % kLanes == 0) store_token(p.out, out + row, p.f16, p.scale * (decay * w + delta * kq));
     }
   } else {
@@ -129,16 +167,20 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaPlan p)
     for (int i = 0; i < kIters; ++i) {
       const int row = tid / kLanes + i * kPer;
       const float k = sk[row], q = sq[row];
-      u0 += a[i] * k, u1 += b[i] * k;
-      w0 += a[i] * q, w1 += b[i] * q;
+      f32x4 a, b;
+      unpack8<SDT>(raw[i], keep, a, b);
+      u0 += a * k, u1 += b * k;
+      w0 += a * q, w1 += b * q;
     }
+    // Over the lanes of one column: half rows, rows and half waves.
+    const auto column_sum = [](float x) __attribute__((always_inline)) {
+      if (kLanes == 8) x += moved<0x128>(x);  // row_ror 8
+      return add_far(add_far(x, 16), 32);
+    };
 #pragma unroll
-    for (int d = kLanes; d < 64; d <<= 1) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u0[j] += __shfl_xor(u0[j], d), u1[j] += __shfl_xor(u1[j], d);
-        w0[j] += __shfl_xor(w0[j], d), w1[j] += __shfl_xor(w1[j], d);
-      }
+    for (int j = 0; j < 4; ++j) {
+      u0[j] = column_sum(u0[j]), u1[j] = column_sum(u1[j]);
+      w0[j] = column_sum(w0[j]), w1[j] = column_sum(w1[j]);
     }
     if (lane < kLanes) {
       *reinterpret_cast<f32x4*>(&part[wave][col]) = u0, *reinterpret_cast<f32x4*>(&part[wave][col + 4]) = u1;
@@ -157,7 +199,9 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaPlan p)
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
       const float k = sk[tid / kLanes + i * kPer];
-      store8<SDT>(p.state_out, at + i * kStep, a[i] * decay + d0 * k, b[i] * decay + d1 * k);
+      f32x4 a, b;
+      unpack8<SDT>(raw[i], keep, a, b);
+      store8<SDT>(p.state_out, at + i * kStep, a * decay + d0 * k, b * decay + d1 * k);
     }
     if (tid < V) {
       float u = 0.f, w = 0.f;

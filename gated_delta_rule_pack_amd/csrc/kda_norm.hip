@@ -15,6 +15,7 @@
 #include "kda_delta.h"
 #include "kda_device.h"
 #include "kda_rotary.h"
+#include "kda_unit.h"
 
 namespace kda {
 namespace {
@@ -41,14 +42,6 @@ struct Elem<kBF16> {
   typedef __bf16 type;
 };
 
-__device__ __forceinline__ double xor_lanes(double x, int d) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __shfl_xor((int)u, d), hi = __shfl_xor((int)(u >> 32), d);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-__device__ __forceinline__ float xor_lanes(float x, int d) { return __shfl_xor(x, d); }
-
 // 1 / sqrt(s) for s = m sum x^2 + eps, which may lie outside fp32 where its root does not.
 __device__ __forceinline__ float inverse_root(double s) {
   if (!(s < 1e300)) return __builtin_nanf("");  // a row that is not finite
@@ -65,29 +58,6 @@ __device__ __forceinline__ float weight_at(const NormPlan& p, int c, int d) {
 template <typename E>
 __device__ __forceinline__ E* row_at(const void* base, int64_t t, int h, int64_t stride_t, int64_t stride_h) {
   return reinterpret_cast<E*>(const_cast<void*>(base)) + t * stride_t + h * stride_h;
-}
-
-// The sum over the `lanes` neighbours (a power of two) that hold a row, in each of them.
-template <int kCtrl>
-__device__ __forceinline__ float moved(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xf, 0xf, true));
-}
-template <int kCtrl>
-__device__ __forceinline__ double moved(double x) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)u, kCtrl, 0xf, 0xf, true);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), kCtrl, 0xf, 0xf, true);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-template <typename X>
-__device__ __forceinline__ X lane_sum(X x, int lanes) {
-  if (lanes > 1) x += moved<0xb1>(x);   // quad_perm 1 0 3 2
-  if (lanes > 2) x += moved<0x4e>(x);   // quad_perm 2 3 0 1
-  if (lanes > 4) x += moved<0x141>(x);  // the half row mirrored: its quads are uniform by now
-  if (lanes > 8) x += moved<0x140>(x);  // the row of 16 mirrored
-  if (lanes > 16) x += xor_lanes(x, 16);
-  if (lanes > 32) x += xor_lanes(x, 32);
-  return x;
 }
 
 // Vectors of VEC elements. A row is held by `lanes` lanes (a power of two), two vectors each: a pair that is rotated, or
@@ -315,8 +285,7 @@ __global__ __launch_bounds__(kThreads) void norm_narrow(const NormPlan p) {
         s += (double)x * x;
         if constexpr (kBack) buf[d] = (float)grad[d];
       }
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) s += xor_lanes(s, d);
+      s = lane_sum(s, 64);
       const float r = inverse_root(m * s + p.eps);
       if constexpr (!kBack)
         for (int d = lane; d < D; d += 64) buf[d] = (float)in[d] * r * weight_at<E>(p, c, d);
@@ -341,9 +310,7 @@ __global__ __launch_bounds__(kThreads) void norm_narrow(const NormPlan p) {
           sums[c * D + d] += z * x;
           dot += z * weight_at<E>(p, c, d) * x;
         }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) dot += __shfl_xor(dot, d);
-        dot *= share;
+        dot = share * lane_sum(dot, 64);
         for (int d = lane; d < D; d += 64) out[d] = (E)(r * (turned(d) * weight_at<E>(p, c, d) - (float)in[d] * r * dot));
       }
       wave_sync();
