@@ -25,8 +25,11 @@
 // the other half of LDS.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "kda_delta.h"
 #include "kda_delta_device.h"
+#include "kda_delta_token.h"
 
 namespace kda {
 namespace {
@@ -283,6 +286,31 @@ struct Chain {
   }
 };
 
+// A sequence of one token, in fp32 as a step of its own. (As a chunk it would take as long
+// as 64 tokens: 16 prompts of 256 among 240 single tokens at H = 12 197 instead of 76 us.)
+template <int K, int V>
+__device__ __forceinline__ void one_token(DeltaShared<K, V>& shared, int begin, int h, int v0, Slots slots, int tid) {
+  // The plan read again from the kernel's arguments: with the walk's own copy of it the walk spills scalars (2 %).
+  typedef const __attribute__((address_space(4))) DeltaPlan* Arguments;
+  Arguments arguments = (Arguments)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(arguments));
+  const DeltaPlan& p = *(const DeltaPlan*)arguments;
+  auto& sh = *reinterpret_cast<TokenShared<K, V, kWalkThreads>*>(&shared);
+  static_assert(sizeof(TokenShared<K, V, kWalkThreads>) <= sizeof(shared), "fits");
+  uint16_t x[kTokenRow<K, V>], k[K / 64];
+  token_rows<K, V>(p, begin, h, v0, __builtin_amdgcn_readfirstlane(tid >> 6), tid & 63, x, k);
+  const int64_t from = slots.from >= 0 ? plane_at(p, slots.from, h) : 0, to = slots.to >= 0 ? plane_at(p, slots.to, h) : -1;
+  const uint32_t keep = slots.from >= 0 ? ~0u : 0u;
+  const auto of = [&](auto sdt) __attribute__((always_inline)) {
+    constexpr int SDT = decltype(sdt)::value;
+    if (p.kfirst) delta_token<K, V, SDT, true, kWalkThreads, true>(p, sh, x, k, begin, h, v0, from, to, keep, tid);
+    else delta_token<K, V, SDT, false, kWalkThreads, true>(p, sh, x, k, begin, h, v0, from, to, keep, tid);
+  };
+  if (p.state_dtype == kF32) of(std::integral_constant<int, kF32>());
+  else if (p.state_dtype == kF16) of(std::integral_constant<int, kF16>());
+  else of(std::integral_constant<int, kBF16>());
+}
+
 template <int K, int V, int kTerms, bool kF16In>
 __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p) {
   constexpr int kThreads = 64 * kMakingWaves;
@@ -293,6 +321,10 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
   const int begin = __builtin_amdgcn_readfirstlane(bound(p, n));
   const int len = __builtin_amdgcn_readfirstlane(max(bound(p, n + 1) - begin, 0)), chunks = (len + kC - 1) / kC;
   const Slots slots = slots_of(p, n);
+  if (len == 1) {
+    one_token<K, V>(sh, begin, h, v0, slots, threadIdx.x);
+    return;
+  }
   if (wave < kChainWaves) {
     Chain<K, V, kTerms, kF16In> chain;
     char* const stage = sh.slot[1].k + wave * 1024;  // no row stands there yet

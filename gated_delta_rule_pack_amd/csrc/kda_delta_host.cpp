@@ -42,11 +42,34 @@ bool fits_scan(const kda_gated_delta_args* a) {
   const kda_linear_args& l = a->lin;
   return (int64_t)places_of(a) * l.H <= kMaxGroups && ((int64_t)l.N * l.H + 7) * (l.V / 16) <= kMaxGroups / 2;
 }
-// Whether a call makes its chunks' records in one kernel and scans them with workgroups of 16 value channels.
+// Whether a call makes its chunks' records in one kernel and scans them with workgroups of 16 value channels, or
+// walks every sequence of a head in one workgroup. Times in turns of the scan (1.2 us); a chunk of the walk takes four.
+// Both wait for the longest sequence, or for all of them where there are more workgroups than 256: the walk has one for
+// each sequence and head, whose start takes about a chunk; the scan V / 16, whose start takes about two turns,
+// and its records are made 75 to a turn. Tokens that are their sequence's only one are a step in both. Without bounds on
+// the host all sequences count as equally long.
+//
+// Measured at K = V = 128 with 32-bit states, walk and scan: prompts of 1024 tokens at 12, 48, 64, 96, 128, 192 sequences and
+// heads 83 and 32, 84 and 59, 85 and 63, 86 and 91, 86 and 118, 106 and 197 us; one prompt of 64, 128, 192 at H = 12 13.4
+// and 17.7, 16.0 and 17.7, 20.8 and 17.7; one of 4096 among 31 single tokens 390 and 106, one of 512 among 127 at
+// H = 24 82 and 304; eight from 64 to 8192 625 and 216. K = V = 64, 1024 tokens at 96, 128, 144: 74 and 56, 74 and 62, 74 and 79.
 bool scans(const kda_gated_delta_args* a) {
   const kda_linear_args& l = a->lin;
   if (a->path != KDA_DELTA_POLICY) return a->path == KDA_DELTA_SCAN;
-  return (int64_t)l.N * l.H <= 256 && fits_scan(a);
+  if (!fits_scan(a)) return false;
+  const auto chunks_of = [](int64_t len) { return len > 1 ? (len + kLinChunk - 1) / kLinChunk : 0; };
+  int64_t longest = 0, chunks = 0;
+  if (const int32_t* cu = l.cu_seqlens_host) {
+    for (int i = 0; i < l.N; ++i) {
+      const int64_t c = chunks_of(cu[i + 1] - cu[i]);
+      longest = std::max(longest, c), chunks += c;
+    }
+  } else if (l.N > 0) {
+    longest = chunks_of((l.T + l.N - 1) / l.N), chunks = longest * l.N;
+  }
+  const double heads = l.H, walk = 4 * std::max(longest + 1., (double)(chunks + l.N) * heads / 256);
+  const double scan = std::max(longest + 2., (double)(chunks + 2 * (int64_t)l.N) * heads * l.V / 4096) + chunks * heads / 75 + 8;
+  return scan < walk;
 }
 
 struct DeltaWs {

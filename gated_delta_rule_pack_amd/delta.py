@@ -73,8 +73,10 @@ def gated_delta_fwd(q, k, v, g, beta, cu_seqlens, *, cu_seqlens_cpu=None, scale=
     scale defaults to ``K ** -0.5``.
 
     cu_seqlens, states, ``out``, ``workspace``, ``stream`` and ``context`` as in :func:`linear_fwd`. ``path`` overrides the
-    choice between one kernel that walks every sequence of a head ("walk") and two that split the work further ("scan"). Returns ``(out,
-    final_state)``, final_state None unless dense and asked for."""
+    choice between one kernel that walks every sequence of a head ("walk") and two that split the work further
+    ("scan"), which agree within rounding. The choice looks at the shapes and, where ``cu_seqlens_cpu`` is given, at the
+    lengths: give it where a batch mixes long prompts with single tokens. Returns ``(out, final_state)``, final_state
+    None unless dense and asked for."""
     with _Call(q, stream) as call:
         _on(call.index, "k v g beta cu_seqlens initial_state state_cache state_indices has_initial_state out workspace",
             k, v, g, beta, cu_seqlens, initial_state, state_cache, state_indices, has_initial_state, out, workspace)

@@ -493,6 +493,10 @@ size_t kda_rotary_args_size(void);
  * workspace and stream; no host metadata, so a captured call replays with other bounds. The token tensors
  * are all bf16 or all fp16.
  *
+ * A call of kda_gated_delta_fwd takes one of two paths, which agree within rounding. The policy chooses by the shapes
+ * and, where cu_seqlens_host is given, by its lengths (else all count as equally long): a long prompt
+ * among single tokens is told apart only with them. A captured call keeps the path, and the workspace, that it was captured with.
+ *
  * Rules for the data. g <= 0 (-inf forgets everything before the token; anything below -120 counts as
  * -inf). A step is stable for |beta| |k|^2 <= 2, which normalised keys and 0 <= beta <= 2 satisfy; keys that
  * break it may overflow the products' fp16 terms within 64 tokens, which gives values that are not finite.
@@ -518,8 +522,8 @@ kda_status kda_gated_delta_fwd(kda_ctx* ctx, const kda_gated_delta_args* args, v
                                void* stream);
 /* Host-only, pure: every argument check of kda_gated_delta_fwd. */
 kda_status kda_gated_delta_fwd_validate(const kda_gated_delta_args* args);
-/* Host-only, pure: bytes of caller workspace (256-byte aligned), from shapes and types alone; 0 for invalid
- * arguments. */
+/* Host-only, pure: bytes of caller workspace (256-byte aligned) of the path that the call takes (0 for the walk, and
+ * for invalid arguments); path = KDA_DELTA_SCAN gives what a call of these shapes needs at most. */
 size_t kda_gated_delta_fwd_workspace_bytes(const kda_gated_delta_args* args);
 
 /* Single tokens, as kda_linear_step: one kernel, no workspace, capturable; padding rows are left as they were. */
@@ -574,7 +578,7 @@ typedef struct kda_qk_norm_args {
   void* grad_k_weight;
 } kda_qk_norm_args;
 
-/* One kernel (one for each 2^22 tokens); a refused call enqueues nothing. */
+/* One kernel; a refused call enqueues nothing. */
 kda_status kda_qk_norm(kda_ctx* ctx, const kda_qk_norm_args* args, void* stream);
 kda_status kda_qk_norm_validate(const kda_qk_norm_args* args);
 /* One kernel, and with weights a second that joins the first one's sums, in the workspace. T = 0 writes zeros for
