@@ -14,6 +14,7 @@ struct DeltaPlan : LinearPlan {
   int beta_bf16;
   int f16;           // q, k, v and out are fp16, not bf16
   int normalize;
+  int ranked;        // workgroups take their sequences longest first
   // The chunks' records, for the scan. A chunk has a place: sequence n's are floor(cu[n] / 64) + n on.
   int places;
   char* records;     // [places][H] of kDeltaRecord bytes
@@ -21,6 +22,7 @@ struct DeltaPlan : LinearPlan {
   char* queries;
 };
 constexpr int kDeltaRecord = 19712;
+constexpr int kMostRanked = 512;  // sequences that a workgroup of the walk or the scan can rank, one to a thread
 
 // Whether one fp16 term of the state and what goes into it serves. A state in bf16 has 8 bits, and one that is not stored goes
 // into outputs alone; both leave outputs in bf16 as far off as their own rounding does. Outputs in fp16 have 11 bits of their

@@ -317,7 +317,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
   __shared__ DeltaShared<K, V> sh;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int slice = blockIdx.x % p.slices, unit = blockIdx.x / p.slices;
-  const int n = unit / p.H, h = unit % p.H, v0 = slice * V;
+  __shared__ Ranking ranking;
+  const int h = unit % p.H, v0 = slice * V, n = p.ranked ? ranked_sequence(p, ranking, unit / p.H, threadIdx.x) : unit / p.H;
   const int begin = __builtin_amdgcn_readfirstlane(bound(p, n));
   const int len = __builtin_amdgcn_readfirstlane(max(bound(p, n + 1) - begin, 0)), chunks = (len + kC - 1) / kC;
   const Slots slots = slots_of(p, n);

@@ -51,8 +51,8 @@ bool fits_scan(const kda_gated_delta_args* a) {
 //
 // Measured at K = V = 128 with 32-bit states, walk and scan: prompts of 1024 tokens at 12, 48, 64, 96, 128, 192 sequences and
 // heads 83 and 32, 84 and 59, 85 and 63, 86 and 91, 86 and 118, 106 and 197 us; one prompt of 64, 128, 192 at H = 12 13.4
-// and 17.7, 16.0 and 17.7, 20.8 and 17.7; one of 4096 among 31 single tokens 390 and 106, one of 512 among 127 at
-// H = 24 82 and 304; eight from 64 to 8192 625 and 216. K = V = 64, 1024 tokens at 96, 128, 144: 74 and 56, 74 and 62, 74 and 79.
+// and 17.7, 16.0 and 17.7, 20.8 and 17.7; one of 4096 among 31 single tokens 385 and 100, one of 512 among 127 at
+// H = 24 69 and 383; eight from 64 to 8192 627 and 215. K = V = 64, 1024 tokens at 96, 128, 144: 74 and 56, 74 and 62, 74 and 79.
 bool scans(const kda_gated_delta_args* a) {
   const kda_linear_args& l = a->lin;
   if (a->path != KDA_DELTA_POLICY) return a->path == KDA_DELTA_SCAN;
@@ -230,12 +230,17 @@ kda_status kda_gated_delta_fwd(kda_ctx* ctx, const kda_gated_delta_args* a, void
   const DeltaWs w = workspace_of(a);
   if (w.total > 0 && (!ws || ws_bytes < w.total || !aligned(ws, 256))) return KDA_ERR_WORKSPACE;
   DeltaPlan p = delta_plan_of(a);
+  const int64_t units = (int64_t)p.N * p.H;
+  // Ranking is for calls of more workgroups than run at once, and of as many sequences as a workgroup can rank.
+  const auto rank = [&](int64_t groups) { p.ranked = p.N > 1 && p.N <= kMostRanked && groups > 256; };
   if (!scans(a)) {
-    p.slices = p.V == 128 && (int64_t)p.N * p.H <= 128 ? 2 : 1;
+    p.slices = p.V == 128 && units <= 128 ? 2 : 1;
+    rank(units * p.slices);
     return launch(ctx, 10, &p, stream) ? KDA_ERR_HIP : KDA_OK;
   }
   char* base = reinterpret_cast<char*>(ws);
   p.places = places_of(a);
+  rank(units * (p.V / 16));
   p.records = base + w.records;
   p.keys = base + w.keys;
   p.queries = base + w.queries;

@@ -160,7 +160,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   // The slices of a unit run on one XCD, whose L2 then reads a record once.
   const int slices = p.V / 16, j = blockIdx.x >> 3, slice = j % slices, unit = (j / slices) * 8 + (blockIdx.x & 7);
   if (unit >= p.N * p.H) return;
-  const int n = unit / p.H, h = unit % p.H, v0 = slice * 16;
+  __shared__ Ranking ranking;
+  const int h = unit % p.H, v0 = slice * 16, n = p.ranked ? ranked_sequence(p, ranking, unit / p.H, tid) : unit / p.H;
   const bool chain = wave < 4;
   const int w = wave & 3;  // token tile; a chain wave's part of the state too
   const int begin = __builtin_amdgcn_readfirstlane(bound(p, n));
