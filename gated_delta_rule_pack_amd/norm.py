@@ -20,39 +20,32 @@ _KINDS = {"rms": _lib.KDA_NORM_RMS, "l2": _lib.KDA_NORM_L2}
 _ADVICE = " (the gradient is qk_norm_backward)"
 
 
-def _put(a, name, t, T, H, D):
-    """One strided tensor of rows and its strides."""
-    setattr(a, name, t.data_ptr())
-    if not t.is_contiguous():
-        st, sh = _strides(name, t, T, H, D)
-        setattr(a, name + "_stride_t", st)
-        setattr(a, name + "_stride_h", sh)
-
-
-def _put_weight(a, name, w, D, dtype, grad):
+def _weight(name, w, D, dtype):
     if w.dtype != dtype and w.dtype != torch.float32:
         raise TypeError(f"{name} must be fp32 or of q's dtype {dtype}, got {w.dtype}")
     if w.dim() != 1 or w.shape[0] != D or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {D} elements, got {tuple(w.shape)}")
-    setattr(a, name, w.data_ptr())
-    a.weight_dtype = _STATE_DT[w.dtype]
-    if grad is not None:
-        if grad.dtype != w.dtype or grad.shape != w.shape or not grad.is_contiguous():
-            raise ValueError(f"grad_{name} must be a contiguous vector like {name}")
-        setattr(a, "grad_" + name, grad.data_ptr())
+    return w.data_ptr()
+
+
+def _weight_gradient(name, grad, w):
+    if grad.dtype != w.dtype or grad.shape != w.shape or not grad.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector like the weight")
+    return grad.data_ptr()
 
 
 def make_qk_norm_args(q, k, q_weight, k_weight, positions, inv_freq, out_q, out_k, *, grad_q=None, grad_k=None,
                       grad_q_weight=None, grad_k_weight=None, kind="rms", eps=1e-6, weight_offset=0.0,
                       interleaved=False) -> "_lib.QkNormArgs":
     """Fill a ``kda_qk_norm_args`` from tensors (no allocation), checking what the C side cannot see."""
-    if _grads_on():
-        for t in (q, k, q_weight, k_weight, grad_q, grad_k, out_q, out_k):
-            if t is not None and t.requires_grad:
-                _refuse_gradient(_ADVICE)
+    if _grads_on() and (q.requires_grad or out_q.requires_grad or (k is not None and k.requires_grad) or
+                        (out_k is not None and out_k.requires_grad) or (q_weight is not None and q_weight.requires_grad) or
+                        (k_weight is not None and k_weight.requires_grad) or (grad_q is not None and grad_q.requires_grad) or
+                        (grad_k is not None and grad_k.requires_grad)):
+        _refuse_gradient(_ADVICE)
     q, out_q = _packed("q", q), _packed("out_q", out_q)
-    T, H, D = q.shape
-    dtype = q.dtype
+    shape, dtype = q.shape, q.dtype
+    T, H, D = shape
     a = _lib.QkNormArgs()
     if dtype not in _STATE_DT:
         raise TypeError(f"q must be fp32, fp16 or bf16, got {dtype}")
@@ -60,41 +53,55 @@ def make_qk_norm_args(q, k, q_weight, k_weight, positions, inv_freq, out_q, out_
         raise ValueError("q must have heads and channels")
     if (k is None) != (out_k is None):
         raise ValueError("out_k goes with k")
-    if out_q.dtype != dtype or out_q.shape != q.shape:
+    if out_q.dtype != dtype or out_q.shape != shape:
         raise ValueError("out_q must have q's shape and dtype")
-    a.T, a.H_q, a.D, a.dtype, a.weight_dtype = T, H, D, _STATE_DT[dtype], _lib.KDA_F32
-    _put(a, "q", q, T, H, D)
-    _put(a, "out_q", out_q, T, H, D)
+    a.T, a.H_q, a.D, a.dtype = T, H, D, _STATE_DT[dtype]
+    a.q, a.out_q = q.data_ptr(), out_q.data_ptr()
+    if not q.is_contiguous():
+        a.q_stride_t, a.q_stride_h = _strides("q", q, T, H, D)
+    if not out_q.is_contiguous():
+        a.out_q_stride_t, a.out_q_stride_h = _strides("out_q", out_q, T, H, D)
     if grad_q is not None:
         grad_q = _packed("grad_q", grad_q)
-        if grad_q.dtype != dtype or grad_q.shape != q.shape:
+        if grad_q.dtype != dtype or grad_q.shape != shape:
             raise ValueError("grad_q must have q's shape and dtype")
-        _put(a, "grad_q", grad_q, T, H, D)
+        a.grad_q = grad_q.data_ptr()
+        if not grad_q.is_contiguous():
+            a.grad_q_stride_t, a.grad_q_stride_h = _strides("grad_q", grad_q, T, H, D)
     if k is not None:
         k, out_k = _packed("k", k), _packed("out_k", out_k)
-        Tk, Hk, Dk = k.shape
+        shape = k.shape
+        Tk, Hk, Dk = shape
         if k.dtype != dtype:
             raise TypeError("q and k must have the same dtype")
         if Tk != T or Dk != D:
             raise ValueError("k must have q's token count and head size")
-        if out_k.dtype != dtype or out_k.shape != k.shape:
+        if out_k.dtype != dtype or out_k.shape != shape:
             raise ValueError("out_k must have k's shape and dtype")
-        a.H_k = Hk
-        _put(a, "k", k, T, Hk, D)
-        _put(a, "out_k", out_k, T, Hk, D)
+        a.H_k, a.k, a.out_k = Hk, k.data_ptr(), out_k.data_ptr()
+        if not k.is_contiguous():
+            a.k_stride_t, a.k_stride_h = _strides("k", k, T, Hk, D)
+        if not out_k.is_contiguous():
+            a.out_k_stride_t, a.out_k_stride_h = _strides("out_k", out_k, T, Hk, D)
         if grad_k is not None:
             grad_k = _packed("grad_k", grad_k)
-            if grad_k.dtype != dtype or grad_k.shape != k.shape:
+            if grad_k.dtype != dtype or grad_k.shape != shape:
                 raise ValueError("grad_k must have k's shape and dtype")
-            _put(a, "grad_k", grad_k, T, Hk, D)
+            a.grad_k = grad_k.data_ptr()
+            if not grad_k.is_contiguous():
+                a.grad_k_stride_t, a.grad_k_stride_h = _strides("grad_k", grad_k, T, Hk, D)
     elif k_weight is not None:
         raise ValueError("k_weight goes with k")
     if q_weight is not None:
-        _put_weight(a, "q_weight", q_weight, D, dtype, grad_q_weight)
-    if k_weight is not None:
-        _put_weight(a, "k_weight", k_weight, D, dtype, grad_k_weight)
-        if q_weight is not None and q_weight.dtype != k_weight.dtype:
+        a.q_weight, a.weight_dtype = _weight("q_weight", q_weight, D, dtype), _STATE_DT[q_weight.dtype]
+        if grad_q_weight is not None:
+            a.grad_q_weight = _weight_gradient("grad_q_weight", grad_q_weight, q_weight)
+        if k_weight is not None and q_weight.dtype != k_weight.dtype:
             raise TypeError("q_weight and k_weight must have the same dtype")
+    if k_weight is not None:
+        a.k_weight, a.weight_dtype = _weight("k_weight", k_weight, D, dtype), _STATE_DT[k_weight.dtype]
+        if grad_k_weight is not None:
+            a.grad_k_weight = _weight_gradient("grad_k_weight", grad_k_weight, k_weight)
     if positions is not None or inv_freq is not None:
         _fill_rotation(a, T, D, positions, inv_freq, interleaved)
     elif interleaved:
