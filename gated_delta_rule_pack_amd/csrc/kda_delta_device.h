@@ -89,15 +89,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x) {
   if constexpr (kLanes == 16) x = max(x, dpp<0x140>(x));  // row_mirror
   return x;
 }
-template <int kLanes>
-__device__ __forceinline__ float row_sum(float x) {
-  x += __uint_as_float(dpp<0xb1>(__float_as_uint(x)));
-  x += __uint_as_float(dpp<0x4e>(__float_as_uint(x)));
-  x += __uint_as_float(dpp<0x141>(__float_as_uint(x)));
-  if constexpr (kLanes == 16) x += __uint_as_float(dpp<0x140>(__float_as_uint(x)));
-  return x;
-}
-
 // The exponent of x >= 0: x < 2^e.
 constexpr int kNoExponent = -4096;
 __device__ __forceinline__ int exponent(float x) { return x > 0.f && x < INFINITY ? __builtin_amdgcn_frexp_expf(x) : kNoExponent; }
@@ -117,7 +108,7 @@ struct RowInfo {
 };
 
 // The sequence of a rank, the longest first: where workgroups wait for a place on the chip, those of long sequences start
-// early, so that none of them runs alone at the end (128 prompts of 64 to 2016 tokens at H = 12: 790 us in the call's order,
+// early, so that none of them runs alone at the end (128 prompts of 0 to 2016 tokens at H = 12: 790 us in the call's order,
 // 671 ranked). Lengths count by their half octave of chunks, and the call's order inside one: with 8 waves' ballots
 // that takes 0.7 us of a workgroup, where ranks by comparison with every length took 7 for 256 sequences.
 constexpr int kRankWaves = kMostRanked / 64, kRankClasses = 32;
