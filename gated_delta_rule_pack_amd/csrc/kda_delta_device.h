@@ -312,6 +312,9 @@ __device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPl
     rq = ldexp2(1.f, q.e - X);
   }
   beta = ldexp2(beta, 2 * X);
+  // One range holds a chunk's step sizes and, 2^{-Y / 2} below V, its states. Wider than this little would be left of
+  // the states: the chunk's outputs and its final state are then not finite, rather than wrong.
+  const bool wide = __ballot(!(fabsf(beta) < 0x1p28f)) != 0;
   const int big = wave_max(beta != 0.f ? __builtin_amdgcn_frexp_expf(beta) : -1000);  // |beta| < 2^big
   const int Y = big == -1000 || (big >= -1 && big <= 2) ? 0 : -big;
   mk.bk[lane] = beta * rk;
@@ -320,9 +323,9 @@ __device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPl
   to.h[lane] = ldexp2(rk * d.e, -Y);
   to.c[lane] = rk * d.c;
   to.e[lane] = d.e;
-  to.f[lane] = lane >= first || q.e == kBadRow ? __builtin_nanf("") : p.scale * ldexp2(rq, -Y);
+  to.f[lane] = wide || lane >= first || q.e == kBadRow ? __builtin_nanf("") : p.scale * ldexp2(rq, -Y);
   if (lane == 0) {
-    to.total = all_bad ? __builtin_nanf("") : d.total;
+    to.total = wide || all_bad ? __builtin_nanf("") : d.total;
     to.shift = X + Y;
   }
 }

@@ -102,6 +102,46 @@ def test_raw_keys_far_from_unit_length(exponent, K, path):
     check(case, (out.double() * s).cpu(), d, final.double() * s)
 
 
+# Keys of different lengths in one chunk, step sizes b / |k|^2: a column of T holds its token's step size beside the chunk's
+# largest, at least 2^-25 of that apart, so that what a key 2^a times as long as the shortest teaches is off by 2^(a - 24) of the
+# largest state, or is lost, 2^-a: 2^-12 at worst, where two terms leave 2^-20.
+@PATHS
+@pytest.mark.parametrize("shortest,longest,worst", [(-2, 3, 8 * 2.0 ** -20), (0, 12, 2.0 ** -12)])
+def test_raw_keys_of_different_lengths(shortest, longest, worst, path):
+    """(-2, 3): |beta k| is up to 4 where the harness takes 1, and 2^(5 - 24) twice 2^-20: 8 times its bound."""
+    lens = [140, 64, 3]
+    case = DeltaCase(lens, 2, seed=29, unit=True, state="dense")
+    gen = torch.Generator().manual_seed(3)
+    size = 2.0 ** torch.randint(shortest, longest + 1, (case.T, case.H, 1), generator=gen).float()
+    case.k = (case.k.float() * size).bfloat16()
+    case.beta = case.beta / size[..., 0] ** 2
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    o, S, M = case.oracle()
+    n = np.array(lens, np.float64)[:, None]
+    state_off = 4 * worst * (1 + np.sqrt(n)) * M
+    token_off = np.repeat(state_off + 4 * E1 * M, lens, axis=0)[:, :, None]
+    close("out", f64(out), o, 2.0 ** -8 * np.abs(o) + 1.01 * case.scale * case.query_size() * token_off)
+    close("state", f64(final), S, 2.0 ** -24 * np.abs(S) + 1.01 * state_off[:, :, None, None])
+
+
+@PATHS
+def test_raw_keys_too_far_apart_are_not_finite(path):
+    """Lengths 2^20 apart with step sizes to match: their chunk and what follows of the head's sequence is not finite, all else as it was."""
+    case = DeltaCase([200, 70], 2, seed=30, unit=True, state="dense")
+    d = case.device()
+    clean, final = case.forward(d, path=path)
+    d["k"], d["beta"] = d["k"].clone(), d["beta"].clone()
+    d["k"][80, 1] *= 2.0 ** 20
+    d["beta"][80, 1] /= 2.0 ** 40
+    out, bad = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    assert same_bits(out[:64], clean[:64]) and same_bits(out[:, 0], clean[:, 0]) and same_bits(out[200:], clean[200:])
+    assert not torch.isfinite(out[64:200, 1]).any() and not torch.isfinite(bad[0, 1]).any()
+    assert same_bits(bad[0, 0], final[0, 0]) and same_bits(bad[1], final[1])
+
+
 @PATHS
 def test_tiny_steps_keep_their_digits(path):
     """Step sizes of 2^-60: what is learnt is far below the values, and keeps its own relative accuracy."""
