@@ -96,15 +96,16 @@ def gated_delta_fwd(q, k, v, g, beta, cu_seqlens, *, cu_seqlens_cpu=None, scale=
                                   normalize=normalize, initial_state=initial_state, final_state=final_state,
                                   state_cache=state_cache, state_indices=state_indices, has_initial_state=has_initial_state,
                                   out=out, state_k_first=state_k_first, path=path)
-        lib = _lib.load()
-        ref = ctypes.byref(a)
-        need = lib.kda_gated_delta_fwd_workspace_bytes(ref)  # 0 for a refused call too: the call says why
         if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
             raise TypeError("workspace must be a contiguous uint8 tensor")
-        if need and (workspace is None or workspace.numel() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=call.device)
-        _check(lib.kda_gated_delta_fwd(_context(context, call.index), ref, workspace.data_ptr() if need else None, need, call.handle),
-               "kda_gated_delta_fwd")
+        lib, ref, context = _lib.load(), ctypes.byref(a), _context(context, call.index)
+        given = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
+        # Short calls need no workspace: it is asked for where the call says so, which has enqueued nothing then.
+        rc = lib.kda_gated_delta_fwd(context, ref, *given, call.handle)
+        if rc == _lib.KDA_ERR_WORKSPACE:
+            workspace = torch.empty(lib.kda_gated_delta_fwd_workspace_bytes(ref), dtype=torch.uint8, device=call.device)
+            rc = lib.kda_gated_delta_fwd(context, ref, workspace.data_ptr(), workspace.numel(), call.handle)
+        _check(rc, "kda_gated_delta_fwd")
     return out, final_state
 
 
