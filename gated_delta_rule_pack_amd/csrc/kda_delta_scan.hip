@@ -140,6 +140,7 @@ struct ScanShared {
   alignas(16) char d[2][2][1024];    // D times its decay to the chunk's end
   alignas(16) char dh[2][2][1024];   // D
   alignas(16) char k[kC * kRowBytes<K>];
+  alignas(16) char v[2][kC * 32];    // V of this chunk and of the next, 16 channels
   alignas(16) int top[16][4];        // largest exponent of a channel, by wave
   alignas(16) int bad[16][4];        // its first token whose value is not finite
   alignas(16) float sum[2][4][16];
@@ -150,7 +151,7 @@ template <int K>
 struct Fetch {
   u32x4 rows[K / 32];  // 16 tokens of K' (chain) or Q' (outputs)
   f16x8 frag[2][2];    // [term][b] of T's row of tiles; [0][b] of P's
-  uint32_t v[4];       // V, chain
+  u32x4 v;             // outputs: V of the next chunk, a token's 8 channels in half the lanes
   f32x4 h, c;          // chain: factors of tokens 4g + i; outputs: e and f of token l % 16 in h
   float total;
   int shift;
@@ -289,13 +290,12 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   const char* next_record = p.records + ((int64_t)place * p.H + h) * kDeltaRecord;
   const char* next_rows = (chain ? p.keys : p.queries) + ((int64_t)place * H_qk + hq) * (kC * K * 2);
   const uint16_t* next_v = v + (int64_t)begin * p.v_t;
-  int next_left = len;
-  const int at16 = lane * 16, at_row = l16 * 4, at_group = g4 * 16, v_row = (int)p.v_t * 2, at_v = 4 * g4 * v_row + l16 * 2;
+  int next_left = len, left_v = len;
+  const int at16 = lane * 16, at_row = l16 * 4, at_group = g4 * 16;
   const auto advance = [&]() {
     const bool more = next_left > kC;
     next_record += more ? (int64_t)p.H * kDeltaRecord : 0;
     next_rows += more ? (int64_t)H_qk * (kC * K * 2) : 0;
-    next_v += more ? p.v_t * kC : 0;
     next_left -= more ? kC : 0;
   };
   const auto fetch_rows = [&](Fetch<K>& f) {
@@ -313,6 +313,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     }
     if constexpr (for_chain) {
       f.c = __builtin_bit_cast(f32x4, load(rec, at_group, kRecFactors + (int)offsetof(Factors, c) + 64 * w));
+      f.h = __builtin_bit_cast(f32x4, load(rec, at_group, kRecFactors + (int)offsetof(Factors, h) + 64 * w));
       const u32x2 last = __builtin_amdgcn_raw_buffer_load_b64(rec, 0, kRecFactors + (int)offsetof(Factors, total), 0);
       f.total = __uint_as_float(last[0]);
       f.shift = (int)last[1];
@@ -321,11 +322,20 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       f.h[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, at_row, kRecFactors + (int)offsetof(Factors, f) + 64 * w, 0));
     }
   };
-  const auto fetch_v = [&](Fetch<K>& f) {
-    const __amdgpu_buffer_rsrc_t r = buffer(next_v, p.v_t, next_left);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f.v[e] = __builtin_amdgcn_raw_buffer_load_b16(r, at_v + e * v_row, 16 * w * v_row, 0);
-    f.h = __builtin_bit_cast(f32x4, load(whole(next_record, kDeltaRecord), at_group, kRecFactors + (int)offsetof(Factors, h) + 64 * w));
+  // V of one chunk, by the outputs' waves: token 16 w + l / 2, channels 8 (l % 2) on, twice.
+  const auto fetch_v = [&]() {
+    const int v_row = (int)p.v_t * 2;
+    return load(buffer(next_v, p.v_t, left_v), ((lane & 31) >> 1) * v_row + (lane & 1) * 16, 16 * w * v_row);
+  };
+  const auto advance_v = [&]() {
+    const bool more = left_v > kC;
+    next_v += more ? p.v_t * kC : 0;
+    left_v -= more ? kC : 0;
+  };
+  const auto put_v = [&](u32x4 x, int i) { *reinterpret_cast<u32x4*>(sh.v[i & 1] + 16 * w * 32 + (lane & 31) * 16) = x; };
+  // Tokens 16 w + 4g + i of channel l % 16.
+  const auto read_v = [&](int i) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sh.v[i & 1] + (16 * w + 4 * g4 + (l16 >> 2)) * 32 + (lane & 3) * 8));
   };
   Scale scale;
   scale.shift = 0;
@@ -374,6 +384,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     };
     char* const k_rows = sh.k + 16 * w * kRowBytes<K> + row_at<K>(l16) + g4 * 16;
     __builtin_amdgcn_s_setprio(3);  // the outputs' waves fill its gaps
+    barrier_lds();  // the first chunk's V
+    s16x4 values = read_v(0);
     const auto step = [&](Fetch<K>& f, int i) {
       const int shift = __builtin_amdgcn_readfirstlane(f.shift);
       const float total = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(f.total)));
@@ -388,7 +400,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       put_state();
       uint32_t value[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) value[e] = f.v[e];
+      for (int e = 0; e < 4; ++e) value[e] = (uint16_t)values[e];
       uint32_t most = max(max(value[0] & 0x7fffu, value[1] & 0x7fffu), max(value[2] & 0x7fffu, value[3] & 0x7fffu));
       int top = max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex);
       sh.top[l16][w] = channel_max(most >= kInf ? kBadTop : top);
@@ -485,7 +497,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           dh[s] = *reinterpret_cast<const f16x8*>(sh.d[s][0] + at16);
           if constexpr (kTerms == 2) dl[s] = *reinterpret_cast<const f16x8*>(sh.d[s][1] + at16);
         }
-        fetch_v(f);
+        values = read_v(i + 1);
         fetch_record(f, std::true_type());
         advance();
         __builtin_amdgcn_sched_barrier(0);
@@ -506,7 +518,6 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       fetch_rows(fetched[a]);
-      fetch_v(fetched[a]);
       fetch_record(fetched[a], std::true_type());
       advance();
       __builtin_amdgcn_sched_barrier(0);  // in this order, for the first chunks' waits
@@ -519,6 +530,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     store_state();
   } else {
     const int at_out = ((16 * w + l16) * (int)p.o_t + 4 * g4) * 2;
+    put_v(fetch_v(), 0);
+    advance_v();
     const auto step = [&](Fetch<K>& f, int i) {
       barrier_lds();
       int first_bad = kC;
@@ -529,6 +542,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         scale.set(lane, scale.ex + rescaled(largest(sh.top)));
         barrier_lds();
       }
+      put_v(f.v, i + 1);
       // S0 Q', channels 4g + i, token l % 16.
       f32x4 o = zero4();
 #pragma unroll
@@ -556,6 +570,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       fetch_rows(f);
       fetch_record(f, std::false_type());
       advance();
+      f.v = fetch_v();
+      advance_v();
       u32x2 packed;
       if constexpr (kF16In) packed = __builtin_bit_cast(u32x2, f16x4{(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]});
       else packed = __builtin_bit_cast(u32x2, bf16x4{to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])});
@@ -566,8 +582,11 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       fetch_rows(fetched[a]);
       fetch_record(fetched[a], std::false_type());
       advance();
+      fetched[a].v = fetch_v();
+      advance_v();
       __builtin_amdgcn_sched_barrier(0);
     }
+    barrier_lds();
     walk_chunks(step);
   }
 }
