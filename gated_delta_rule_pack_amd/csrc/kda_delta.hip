@@ -26,7 +26,7 @@
 //
 // Measured: a turn takes 14900 cycles, 6.2 us. The making waves' longest parts come to 13600 of them with six meetings, and the
 // chain waves work for 10000, each beside one of the others on its SIMD. 128 ragged prompts (135060 tokens) at H = 12 with bf16
-// states take 671 us: vector instructions 36 % of the time, the matrix unit 18 %, LDS 28 %, memory 1.15 GB at 1.7 TB/s; what is
+// states take 664 us: vector instructions 36 % of the time, the matrix unit 18 %, LDS 28 %, memory 1.15 GB at 1.7 TB/s; what is
 // left is one part waiting for the next. With all eight waves making and walking in turn they took 1507.
 #include <hip/hip_runtime.h>
 
@@ -292,7 +292,7 @@ struct Chain {
 };
 
 // A sequence of one token, in fp32 as a step of its own. (As a chunk it would take as long
-// as 64 tokens: 16 prompts of 256 among 240 single tokens at H = 12 197 instead of 76 us.)
+// as 64 tokens: 16 prompts of 256 among 240 single tokens at H = 12 197 instead of 84 us.)
 template <int K, int V>
 __device__ __forceinline__ void one_token(DeltaShared<K, V>& shared, int begin, int h, int v0, Slots slots, int tid) {
   // The plan read again from the kernel's arguments: with the walk's own copy of it the walk spills scalars (2 %).

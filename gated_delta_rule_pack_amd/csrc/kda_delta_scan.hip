@@ -10,8 +10,9 @@
 // All read their fragments straight from memory, a few chunks ahead, each fragment in one wave alone.
 //
 // Measured: delta_prep is bound by memory, 0.87 GB in 190 us for 32768 tokens at H = 32 (4.6 TB/s) and 50 us for 16384 at
-// H = 12; a chunk of delta_scan takes 1.2 us, 2900 cycles, of which 500 are its loads' issue and the rest its three dependent
-// products with what lies between them: 308 us for 16384 tokens at H = 12, where the walk took 1232 for all.
+// H = 12; a chunk of delta_scan takes 1.07 us, 2600 cycles, most of it its three dependent products with what lies between
+// them: 274 us for 16384 tokens at H = 12, where the walk took 1232 for all. V comes by the outputs' waves, through LDS and a
+// transposing read; by the chain's own, two bytes a lane, it took 308. K' by the outputs' waves too: 300.
 #include <hip/hip_runtime.h>
 
 #include <cstddef>
