@@ -323,10 +323,11 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       f.h[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, at_row, kRecFactors + (int)offsetof(Factors, f) + 64 * w, 0));
     }
   };
-  // V of one chunk, by the outputs' waves: token 16 w + l / 2, channels 8 (l % 2) on, twice.
+  // V of one chunk, by the outputs' waves: token 16 w + l / 2, channels 8 (l % 2) on, twice. (All of a row's offset is the
+  // lane's: the uniform one is not compared with the buffer's end.)
   const auto fetch_v = [&]() {
     const int v_row = (int)p.v_t * 2;
-    return load(buffer(next_v, p.v_t, left_v), ((lane & 31) >> 1) * v_row + (lane & 1) * 16, 16 * w * v_row);
+    return load(buffer(next_v, p.v_t, left_v), (16 * w + ((lane & 31) >> 1)) * v_row + (lane & 1) * 16, 0);
   };
   const auto advance_v = [&]() {
     const bool more = left_v > kC;

@@ -71,6 +71,27 @@ def test_what_is_not_finite_reaches_no_earlier_token(name, state, path):
 
 
 @PATHS
+@pytest.mark.parametrize("length", [1, 2, 15, 17, 33, 50, 63, 65, 70, 100, 127])
+def test_rows_behind_a_sequence_are_not_read(length, path):
+    """Every row behind the sequence's end is not finite: the next sequence's, and rows of the tensors behind the last bound."""
+    case = DeltaCase([length, 80], 2, seed=37, state="dense", extra_rows=70)
+    d = case.device()
+    clean, final = case.forward(d, path=path)
+    for x in ("q", "k", "v", "g", "beta"):
+        d[x] = d[x].clone()
+        d[x][length:] = NAN
+    out, bad = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    assert same_bits(out[:length], clean[:length]) and same_bits(bad[0], final[0])
+    d = case.device()
+    for x in ("q", "k", "v", "g", "beta"):
+        d[x][length + 80:] = INF
+    out, bad = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    assert same_bits(out[:length + 80], clean[:length + 80]) and same_bits(bad, final)
+
+
+@PATHS
 def test_state_rows_that_are_not_finite_lose_their_channel(path):
     case = DeltaCase([130, 5], 2, seed=22, state="dense")
     d = case.device()
