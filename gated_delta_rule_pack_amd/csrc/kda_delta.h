@@ -24,11 +24,6 @@ struct DeltaPlan : LinearPlan {
 constexpr int kDeltaRecord = 19712;
 constexpr int kMostRanked = 512;  // sequences that a workgroup of the walk or the scan can rank, one to a thread
 
-// Whether one fp16 term of the state and what goes into it serves. A state in bf16 has 8 bits, and one that is not stored goes
-// into outputs alone; both leave outputs in bf16 as far off as their own rounding does. Outputs in fp16 have 11 bits of their
-// own: two terms (2.7e-4 rel-L2; one term: 3.6e-4).
-inline bool one_term(const DeltaPlan& p) { return !p.f16 && (p.out_mode == kStateNone || p.state_dtype == kBF16); }
-
 int launch_delta_walk(const DeltaPlan& p, void* stream);
 int launch_delta_prep(const DeltaPlan& p, void* stream);
 int launch_delta_scan(const DeltaPlan& p, void* stream);

@@ -15,7 +15,7 @@
 // products where bf16 would take three. Keys and queries are exact in one term: each row is scaled by the power of two
 // that brings its largest element into [1/4, 1/2), near unit length, and 8 bits of bf16 (11 of fp16) fit. What else becomes an operand is held in a
 // range by exact powers of two: the state and V of one value channel by a power of two of that channel's own (Scale), step
-// sizes by one of the chunk (Chunk::shift). One term serves for outputs in bf16.
+// sizes by one of the chunk (Factors::shift). P's second term has 8 bits (p_rest).
 //
 // A workgroup walks one sequence of one value head, or a slice of 64 of its state rows, with four chain waves and four
 // making waves. The chain waves hold the state as S^T[k][v] in fp32 MFMA accumulators, 32 or 16 value channels each. Lanes
@@ -46,7 +46,7 @@ struct Slot {
   alignas(16) char q[kC * kRowBytes<K>];
   alignas(16) char v[kC * kRowBytes<V>];  // then, once its chain wave has its columns, the outputs
   alignas(16) char t[2 * kTermP];
-  alignas(16) char p[kTermP];
+  alignas(16) char p[kTermP + kRestP];
   alignas(16) Factors factors;
 };
 template <int K, int V>
@@ -61,7 +61,7 @@ constexpr int kChainWaves = 4, kMakingWaves = 4, kWalkThreads = 64 * (kChainWave
 constexpr int kBarriers = 6;
 constexpr int kNumbersWave = 3;  // of the making waves, one with few tiles
 
-template <int K, int V, int kTerms, bool kF16In>
+template <int K, int V, bool kF16In>
 struct Chain {
   typedef Walk<K, V, kChainWaves> State;
   static constexpr int VT = State::VT, KT = K / 16, KB = K / 32;
@@ -147,7 +147,7 @@ struct Chain {
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) {
         hi[vt] = to_f16(state.S[vt][2 * m], state.S[vt][2 * m + 1]);
-        if constexpr (kTerms == 2) lo[vt] = rest_f16(state.S[vt][2 * m], state.S[vt][2 * m + 1], hi[vt]);
+        lo[vt] = rest_f16(state.S[vt][2 * m], state.S[vt][2 * m + 1], hi[vt]);
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
@@ -155,8 +155,8 @@ struct Chain {
         const f16x8 qq = __builtin_bit_cast(f16x8, read_row<K>(slot.q, lane, 16 * tt, m));
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
-          if constexpr (kTerms == 2) x[vt][tt] = mfma(kk, lo[vt], x[vt][tt]);
-          if constexpr (kF16In) o[vt][tt] = mfma(lo[vt], qq, o[vt][tt]);
+          x[vt][tt] = mfma(kk, lo[vt], x[vt][tt]);
+          o[vt][tt] = mfma(lo[vt], qq, o[vt][tt]);
         }
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
@@ -187,7 +187,7 @@ struct Chain {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         xh[vt][b] = to_f16(x[vt][2 * b], x[vt][2 * b + 1]);
-        if constexpr (kTerms == 2) xl[vt][b] = rest_f16(x[vt][2 * b], x[vt][2 * b + 1], xh[vt][b]);
+        xl[vt][b] = rest_f16(x[vt][2 * b], x[vt][2 * b + 1], xh[vt][b]);
       }
     // D = T x, rows t, column v.
 #pragma unroll
@@ -197,14 +197,11 @@ struct Chain {
 #pragma unroll
       for (int b = 0; b <= tt / 2; ++b) {
         const f16x8 th = read_fragment(slot.t, lane, tt, b);
-        f16x8 tl;
-        if constexpr (kTerms == 2) tl = read_fragment(slot.t + kTermP, lane, tt, b);
+        const f16x8 tl = read_fragment(slot.t + kTermP, lane, tt, b);
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
-          if constexpr (kTerms == 2) {
-            x[vt][tt] = mfma(tl, xh[vt][b], x[vt][tt]);
-            x[vt][tt] = mfma(th, xl[vt][b], x[vt][tt]);
-          }
+          x[vt][tt] = mfma(tl, xh[vt][b], x[vt][tt]);
+          x[vt][tt] = mfma(th, xl[vt][b], x[vt][tt]);
           x[vt][tt] = mfma(th, xh[vt][b], x[vt][tt]);
         }
       }
@@ -218,20 +215,32 @@ struct Chain {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           dh[vt][b] = to_f16(x[vt][2 * b], x[vt][2 * b + 1]);
-          if constexpr (kF16In) dl[vt][b] = rest_f16(x[vt][2 * b], x[vt][2 * b + 1], dh[vt][b]);
+          dl[vt][b] = rest_up(x[vt][2 * b], x[vt][2 * b + 1], dh[vt][b]);
         }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         const float f = fa.f[16 * tt + l16];
+        f16x8 pp[2];
+        f32x4 rest[VT];
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) rest[vt] = zero4();
 #pragma unroll
         for (int b = 0; b <= tt / 2; ++b) {
-          const f16x8 pp = read_fragment(slot.p, lane, tt, b);
+          pp[b] = read_fragment(slot.p, lane, tt, b);
+          const f16x8 pl = read_rest(slot.p + kTermP, lane, tt, b);
 #pragma unroll
           for (int vt = 0; vt < VT; ++vt) {
-            if constexpr (kF16In) o[vt][tt] = mfma(dl[vt][b], pp, o[vt][tt]);
-            o[vt][tt] = mfma(dh[vt][b], pp, o[vt][tt]);
+            rest[vt] = mfma(dl[vt][b], pp[b], rest[vt]);
+            rest[vt] = mfma(dh[vt][b], pl, rest[vt]);
           }
         }
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt) {
+          o[vt][tt] += rest[vt] * kDown;
+#pragma unroll
+          for (int b = 0; b <= tt / 2; ++b) o[vt][tt] = mfma(dh[vt][b], pp[b], o[vt][tt]);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one row of tiles at a time: with all reads first the walk spills
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
@@ -273,7 +282,7 @@ struct Chain {
       for (int vt = 0; vt < VT; ++vt) {
         const f32x4 y0 = x[vt][2 * b] * c0, y1 = x[vt][2 * b + 1] * c1;
         dh[vt] = to_f16(y0, y1);
-        if constexpr (kTerms == 2) dl[vt] = rest_f16(y0, y1, dh[vt]);
+        dl[vt] = rest_f16(y0, y1, dh[vt]);
       }
 #pragma unroll
       for (int kt = 0; kt < KT; kt += 2) {
@@ -283,7 +292,7 @@ struct Chain {
         for (int vt = 0; vt < VT; ++vt) {
           f32x4 &s0 = state.S[vt][kt], &s1 = state.S[vt][kt + 1];
           if (b == 0) s0 *= total, s1 *= total;
-          if constexpr (kTerms == 2) s0 = mfma(k0, dl[vt], s0), s1 = mfma(k1, dl[vt], s1);
+          s0 = mfma(k0, dl[vt], s0), s1 = mfma(k1, dl[vt], s1);
           s0 = mfma(k0, dh[vt], s0), s1 = mfma(k1, dh[vt], s1);
         }
       }
@@ -316,7 +325,7 @@ __device__ __forceinline__ void one_token(DeltaShared<K, V>& shared, int begin, 
   else of(std::integral_constant<int, kBF16>());
 }
 
-template <int K, int V, int kTerms, bool kF16In>
+template <int K, int V, bool kF16In>
 __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p) {
   constexpr int kThreads = 64 * kMakingWaves;
   __shared__ DeltaShared<K, V> sh;
@@ -332,7 +341,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     return;
   }
   if (wave < kChainWaves) {
-    Chain<K, V, kTerms, kF16In> chain;
+    Chain<K, V, kF16In> chain;
     char* const stage = sh.slot[1].k + wave * 1024;  // no row stands there yet
     chain.state.zero();
     if (slots.from >= 0) chain.state.load_plane(p, stage, plane_at(p, slots.from, h), v0, wave, lane);
@@ -420,7 +429,10 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     if constexpr (kNext) fetch(i + 1);
     barrier_lds();
     by_wave(w, [&](auto W) {
-      put_tiles<decltype(W)::value>(sh.blocks, sh.making, l, products, between, [&](int tt, int st, f16x4 x) { put_fragment(slot.p, l, tt, st, x); });
+      put_tiles<decltype(W)::value>(sh.blocks, sh.making, l, products, between, [&](int tt, int st, f16x4 x, uint32_t rest) {
+        put_fragment(slot.p, l, tt, st, x);
+        put_rest(slot.p + kTermP, l, tt, st, rest);
+      });
     });
     {
       // The outputs of chunk i - 2; for the first two a buffer of no rows.
@@ -455,29 +467,21 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
   store(chunks - 1);
 }
 
-template <int K, int V, int kTerms>
+template <int K, int V>
 int launch_kv(const DeltaPlan& p, hipStream_t s) {
   const unsigned grid = (unsigned)((int64_t)p.N * p.H * p.slices);
-  if constexpr (kTerms == 2)
-    if (p.f16) {
-      delta_walk<K, V, 2, true><<<grid, kWalkThreads, 0, s>>>(p);
-      return (int)hipGetLastError();
-    }
-  delta_walk<K, V, kTerms, false><<<grid, kWalkThreads, 0, s>>>(p);
+  if (p.f16) delta_walk<K, V, true><<<grid, kWalkThreads, 0, s>>>(p);
+  else delta_walk<K, V, false><<<grid, kWalkThreads, 0, s>>>(p);
   return (int)hipGetLastError();
-}
-template <int kTerms>
-int launch_terms(const DeltaPlan& p, hipStream_t s) {
-  const int V = p.V / p.slices;
-  if (p.K == 128) return V == 128 ? launch_kv<128, 128, kTerms>(p, s) : launch_kv<128, 64, kTerms>(p, s);
-  return V == 128 ? launch_kv<64, 128, kTerms>(p, s) : launch_kv<64, 64, kTerms>(p, s);
 }
 
 }  // namespace
 
 int launch_delta_walk(const DeltaPlan& p, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return one_term(p) ? launch_terms<1>(p, s) : launch_terms<2>(p, s);
+  const int V = p.V / p.slices;
+  if (p.K == 128) return V == 128 ? launch_kv<128, 128>(p, s) : launch_kv<128, 64>(p, s);
+  return V == 128 ? launch_kv<64, 128>(p, s) : launch_kv<64, 64>(p, s);
 }
 
 }  // namespace kda

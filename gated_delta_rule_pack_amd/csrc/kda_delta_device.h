@@ -32,14 +32,13 @@ __device__ __forceinline__ uint32_t pair_f16(float a, float b) {
 // What two values leave of those, exactly, rounded to fp16: one instruction each. (Written as conversions and differences
 // the compiler takes three; and where a and b are a product or a sum it makes the first term of the exact value in one
 // instruction and this one of the rounded value: where those fall on two sides of a middle, both terms miss it by 2^-10.)
-__device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t first) {
+__device__ __forceinline__ uint32_t rest_pair(float a, float b, uint32_t first, float minus = -1.f) {
   const f16x2 h = __builtin_bit_cast(f16x2, first);
-  float minus = -1.f;
   asm("" : "+s"(minus));  // a known factor would become a difference, which has no such instruction
   const f16x2 r = {(_Float16)__builtin_fmaf((float)h[0], minus, a), (_Float16)__builtin_fmaf((float)h[1], minus, b)};
   return __builtin_bit_cast(uint32_t, r);
 }
-// Two tiles (rows 4g + i and 16 + 4g + i) as an operand, in one or two terms.
+// Two tiles (rows 4g + i and 16 + 4g + i) as an operand, in two terms.
 __device__ __forceinline__ f16x8 to_f16(f32x4 a, f32x4 b) {
   return __builtin_bit_cast(f16x8, u32x4{pair_f16(a[0], a[1]), pair_f16(a[2], a[3]), pair_f16(b[0], b[1]), pair_f16(b[2], b[3])});
 }
@@ -48,11 +47,46 @@ __device__ __forceinline__ f16x8 rest_f16(f32x4 a, f32x4 b, f16x8 hi) {
   return __builtin_bit_cast(f16x8, u32x4{rest_pair(a[0], a[1], h[0]), rest_pair(a[2], a[3], h[1]), rest_pair(b[0], b[1], h[2]),
                                          rest_pair(b[2], b[3], h[3])});
 }
-// One tile (rows 4g + i) as half a fragment, in one or two terms.
+// One tile (rows 4g + i) as half a fragment, in two terms.
 __device__ __forceinline__ void put_half(char* high, char* low, int at, f32x4 x) {
   const u32x2 h = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])};
   *reinterpret_cast<u32x2*>(high + at) = h;
-  if (low) *reinterpret_cast<u32x2*>(low + at) = u32x2{rest_pair(x[0], x[1], h[0]), rest_pair(x[2], x[3], h[1])};
+  *reinterpret_cast<u32x2*>(low + at) = u32x2{rest_pair(x[0], x[1], h[0]), rest_pair(x[2], x[3], h[1])};
+}
+
+// Second terms of outputs' operands, D and P, times 2^12: as large as the first ones, so that fp16's least step is far below
+// them. Their products are summed by themselves and taken back by 2^-12.
+constexpr float kUp = 0x1p12f, kDown = 0x1p-12f;
+__device__ __forceinline__ uint32_t rest_up(float a, float b, uint32_t first) {
+  return rest_pair(a * kUp, b * kUp, first, -kUp);
+}
+__device__ __forceinline__ f16x8 rest_up(f32x4 a, f32x4 b, f16x8 hi) {
+  const u32x4 h = __builtin_bit_cast(u32x4, hi);
+  return __builtin_bit_cast(f16x8, u32x4{rest_up(a[0], a[1], h[0]), rest_up(a[2], a[3], h[1]), rest_up(b[0], b[1], h[2]), rest_up(b[2], b[3], h[3])});
+}
+__device__ __forceinline__ void put_half_up(char* high, char* low, int at, f32x4 x) {
+  const u32x2 h = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])};
+  *reinterpret_cast<u32x2*>(high + at) = h;
+  *reinterpret_cast<u32x2*>(low + at) = u32x2{rest_up(x[0], x[1], h[0]), rest_up(x[2], x[3], h[1])};
+}
+// P's second term has 8 bits, five of exponent and two of fraction, fp16's upper byte: with them P is within 2^-14 of itself,
+// an eighth of the half step of outputs in fp16, and its records keep their size. It is stored times 2^15 (so that its least
+// step, 2^-16, stands for 2^-31), and read times 2^12.
+__device__ __forceinline__ uint32_t p_rest(f32x4 x, u32x2 first) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  const float up = 8 * kUp;
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const u16x2 r = __builtin_bit_cast(u16x2, rest_pair(x[2 * j] * up, x[2 * j + 1] * up, first[j], -up));
+    w[j] = __builtin_bit_cast(uint32_t, (u16x2)(r + (u16x2){0x80, 0x80}));  // to nearest
+  }
+  return __builtin_amdgcn_perm(w[1], w[0], 0x07050301);
+}
+__device__ __forceinline__ f16x8 p_rest_operand(u32x2 x) {
+  const u32x4 w = {__builtin_amdgcn_perm(0, x[0], 0x010c000c), __builtin_amdgcn_perm(0, x[0], 0x030c020c),
+                   __builtin_amdgcn_perm(0, x[1], 0x010c000c), __builtin_amdgcn_perm(0, x[1], 0x030c020c)};
+  return __builtin_bit_cast(f16x8, w) * (_Float16)0.125f;
 }
 
 // A token's element of a 16-bit word, by type.
@@ -342,6 +376,17 @@ __device__ __forceinline__ void put_fragment(char* p, int lane, int tt, int st, 
   *reinterpret_cast<f16x4*>(p + fragment(tt, b) + (half_fragment(tt, b) ? lane * 8 : lane * 16 + (st & 1) * 8)) = x;
 }
 
+// The same of P's second term, a byte for each value.
+constexpr int kRestP = kTermP / 2;
+__device__ __forceinline__ f16x8 read_rest(const char* p, int lane, int tt, int b) {
+  if (!half_fragment(tt, b)) return p_rest_operand(*reinterpret_cast<const u32x2*>(p + fragment(tt, b) / 2 + lane * 8));
+  return p_rest_operand(u32x2{*reinterpret_cast<const uint32_t*>(p + fragment(tt, b) / 2 + lane * 4), 0u});
+}
+__device__ __forceinline__ void put_rest(char* p, int lane, int tt, int st, uint32_t x) {
+  const int b = st >> 1;
+  *reinterpret_cast<uint32_t*>(p + fragment(tt, b) / 2 + (half_fragment(tt, b) ? lane * 4 : lane * 8 + (st & 1) * 4)) = x;
+}
+
 // Making T and P, by four waves. The ten tiles (tt, st <= tt) of K' K'^T and K' Q'^T, rows s = 4g + i, column t = l % 16, are dealt
 // out as rows of tiles: 0 and 1, 2, and two halves of 3. Each wave has code of its own, in which all places are constants.
 constexpr int kTileJobs = 3;
@@ -403,7 +448,7 @@ __device__ __forceinline__ void tile_decays(const Making& mk, int lane, TileDeca
 #pragma unroll
     for (int i = 0; i < 4; ++i) d.of[j][i] = __expf((Gt[j] - Gs[j][i]) + (rest[j] - rest_s[j][i]));
 }
-// A's blocks and P's tiles; put_p(tt, st, x) takes a tile of P.
+// A's blocks and P's tiles; put_p(tt, st, x, rest) takes a tile of P.
 template <int W, typename PutP>
 __device__ __forceinline__ void put_tiles(float* blocks, const Making& mk, int lane, const TileProducts& p, const TileDecays& d, PutP put_p) {
   typedef TileJobs<W> Jobs;
@@ -429,7 +474,8 @@ __device__ __forceinline__ void put_tiles(float* blocks, const Making& mk, int l
       to[i * kBlockRow] = diagonal && 4 * g4 + i >= l16 ? 0.f : a;
       if (diagonal && 4 * g4 + i > l16) x[i] = 0.f;
     }
-    put_p(Jobs::tt(j), Jobs::st(j), __builtin_bit_cast(f16x4, u32x2{pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}));
+    const u32x2 first = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])};
+    put_p(Jobs::tt(j), Jobs::st(j), __builtin_bit_cast(f16x4, first), p_rest(x, first));
   }
 }
 

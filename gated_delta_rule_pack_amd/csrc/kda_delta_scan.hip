@@ -23,11 +23,9 @@
 namespace kda {
 namespace {
 
-// A record: T in two terms and P, six fragments each, then the factors.
-constexpr int kFragments = 6 * 1024;
-__device__ __forceinline__ constexpr int padded_fragment(int tt, int b) { return (tt < 2 ? tt : 2 * tt - 2 + b) * 1024; }
-static_assert(3 * kFragments + sizeof(Factors) <= kDeltaRecord, "record size");
-constexpr int kRecP = 2 * kFragments, kRecFactors = 3 * kFragments;
+// A record: T in two terms, P's first, fragments as the walk has them in LDS, P's second, then the factors.
+constexpr int kRecP = 2 * kTermP, kRecRest = 3 * kTermP, kRecFactors = 3 * kTermP + kRestP;
+static_assert(kRecFactors + sizeof(Factors) <= kDeltaRecord, "record size");
 
 // Sequence n's chunks have the places floor(cu[n] / 64) + n on: at least as many as it has chunks.
 __device__ __forceinline__ int chunk_place(const DeltaPlan& p, int n) { return bound(p, n) / kC + n; }
@@ -42,13 +40,6 @@ __device__ __forceinline__ int find_chunk(const DeltaPlan& p, int place, int lan
     hi = min(lo + step, hi);
   }
   return lo;
-}
-
-// Tile (tt, st) of P or one term of T in a record, with the zeros beside a tile on the diagonal.
-__device__ __forceinline__ void put_padded(char* frags, int lane, int tt, int st, f16x4 x) {
-  char* at = frags + padded_fragment(tt, st >> 1) + lane * 16;
-  *reinterpret_cast<f16x4*>(at + (st & 1) * 8) = x;
-  if (tt == st && !(st & 1)) *reinterpret_cast<f16x4*>(at + 8) = f16x4{0, 0, 0, 0};
 }
 
 // A tile's rows in LDS to memory as operand fragments: 16 rows and 32 channels to 1 KB.
@@ -116,15 +107,18 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
   });
   barrier_lds();
   by_wave(wave, [&](auto W) {
-    put_tiles<decltype(W)::value>(sh.blocks, sh.making, lane, products, between, [&](int tt, int st, f16x4 x) { put_padded(rec + kRecP, lane, tt, st, x); });
+    put_tiles<decltype(W)::value>(sh.blocks, sh.making, lane, products, between, [&](int tt, int st, f16x4 x, uint32_t rest) {
+      put_fragment(rec + kRecP, lane, tt, st, x);
+      put_rest(rec + kRecRest, lane, tt, st, rest);
+    });
   });
   barrier_lds();
   if (wave == 0) invert_diagonal(sh.blocks, lane);
   barrier_lds();
   const auto put_t = [&](int tt, int st, f32x4 x) {
     const Terms y = t_terms(sh.making, lane, st, x);
-    put_padded(rec, lane, tt, st, y.hi);
-    put_padded(rec + kFragments, lane, tt, st, y.lo);
+    put_fragment(rec, lane, tt, st, y.hi);
+    put_fragment(rec + kTermP, lane, tt, st, y.lo);
   };
   near_blocks(sh.blocks, lane, wave, put_t);
   barrier_lds();
@@ -151,14 +145,14 @@ struct ScanShared {
 template <int K>
 struct Fetch {
   u32x4 rows[K / 32];  // 16 tokens of K' (chain) or Q' (outputs)
-  f16x8 frag[2][2];    // [term][b] of T's row of tiles; [0][b] of P's
+  u32x4 frag[2][2];    // [term][b] of T's or P's row of tiles
   u32x4 v;             // outputs: V of the next chunk, a token's 8 channels in half the lanes
   f32x4 h, c;          // chain: factors of tokens 4g + i; outputs: e and f of token l % 16 in h
   float total;
   int shift;
 };
 
-template <int K, int kTerms, bool kF16In>
+template <int K, bool kF16In>
 __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   constexpr int KB = K / 32, KTW = K / 64;  // tiles of a chain wave's state
   __shared__ ScanShared<K> sh;
@@ -293,6 +287,14 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   const uint16_t* next_v = v + (int64_t)begin * p.v_t;
   int next_left = len, left_v = len;
   const int at16 = lane * 16, at_row = l16 * 4, at_group = g4 * 16;
+  // The last fragment of a row of tiles: with one tile (half_fragment) a lane has 8 bytes of it, and reads 16; what is its neighbour's goes.
+  const int last_unit = w & 1 ? 16 : 8;
+  const uint32_t keep = w & 1 ? ~0u : 0u;
+  const auto operand = [&](u32x4 x, int b) {
+    if (b == w >> 1) x[2] &= keep, x[3] &= keep;
+    return __builtin_bit_cast(f16x8, x);
+  };
+  const auto rest_operand = [&](u32x4 x, int b) { return p_rest_operand(u32x2{x[0], b == w >> 1 ? x[1] & keep : x[1]}); };
   const auto advance = [&]() {
     const bool more = next_left > kC;
     next_record += more ? (int64_t)p.H * kDeltaRecord : 0;
@@ -308,9 +310,14 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     const __amdgpu_buffer_rsrc_t rec = whole(next_record, kDeltaRecord);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {  // the first two rows of tiles have one fragment
-      const int from = (for_chain ? 0 : kRecP) + padded_fragment(w, w < 2 ? 0 : b);
-      f.frag[0][b] = __builtin_bit_cast(f16x8, load(rec, at16, from));
-      if constexpr (kTerms == 2 && for_chain) f.frag[1][b] = __builtin_bit_cast(f16x8, load(rec, at16, from + kFragments));
+      const int from = fragment(w, w < 2 ? 0 : b), at = lane * (b == w >> 1 || w < 2 ? last_unit : 16);
+      f.frag[0][b] = load(rec, at, (for_chain ? 0 : kRecP) + from);
+      if constexpr (for_chain) {
+        f.frag[1][b] = load(rec, at, kTermP + from);
+      } else {
+        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rec, at / 2, kRecRest + from / 2, 0);
+        f.frag[1][b][0] = x[0], f.frag[1][b][1] = x[1];
+      }
     }
     if constexpr (for_chain) {
       f.c = __builtin_bit_cast(f32x4, load(rec, at_group, kRecFactors + (int)offsetof(Factors, c) + 64 * w));
@@ -371,9 +378,9 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       if constexpr (KTW == 2) {
         const f16x8 hi = to_f16(S[0], S[1]);
         *reinterpret_cast<f16x8*>(sh.s[w][0] + lane * 16) = hi;
-        if constexpr (kTerms == 2) *reinterpret_cast<f16x8*>(sh.s[w][1] + lane * 16) = rest_f16(S[0], S[1], hi);
+        *reinterpret_cast<f16x8*>(sh.s[w][1] + lane * 16) = rest_f16(S[0], S[1], hi);
       } else {
-        put_half(sh.s[w >> 1][0], kTerms == 2 ? sh.s[w >> 1][1] : nullptr, lane * 16 + (w & 1) * 8, S[0]);
+        put_half(sh.s[w >> 1][0], sh.s[w >> 1][1], lane * 16 + (w & 1) * 8, S[0]);
       }
     };
     const auto state_top = [&]() {
@@ -413,7 +420,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
         for (int m = 0; m < KB; ++m) {
           hi[m] = *reinterpret_cast<const f16x8*>(sh.s[m][0] + at16);
-          if constexpr (kTerms == 2) lo[m] = *reinterpret_cast<const f16x8*>(sh.s[m][1] + at16);
+          lo[m] = *reinterpret_cast<const f16x8*>(sh.s[m][1] + at16);
         }
       };
       read_state();
@@ -450,13 +457,13 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         for (int m = 0; m < KB; ++m) {
           const f16x8 k = __builtin_bit_cast(f16x8, f.rows[m]);
           a = mfma(k, hi[m], a);
-          if constexpr (kTerms == 2) b = mfma(k, lo[m], b);
+          b = mfma(k, lo[m], b);
         }
 #pragma unroll
         for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(k_rows + m * 64) = f.rows[m];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(value[e]) * scale.v - f.h[e] * (a[e] + b[e]);
-        put_half(sh.x[w >> 1][0], kTerms == 2 ? sh.x[w >> 1][1] : nullptr, at16 + (w & 1) * 8, x);
+        put_half(sh.x[w >> 1][0], sh.x[w >> 1][1], at16 + (w & 1) * 8, x);
       }
       barrier_lds();
       f16x8 kk[2][KTW];
@@ -465,7 +472,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           xh[s] = *reinterpret_cast<const f16x8*>(sh.x[s][0] + at16);
-          if constexpr (kTerms == 2) xl[s] = *reinterpret_cast<const f16x8*>(sh.x[s][1] + at16);
+          xl[s] = *reinterpret_cast<const f16x8*>(sh.x[s][1] + at16);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -473,21 +480,17 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           for (int kt = 0; kt < KTW; ++kt) kk[s][kt] = __builtin_bit_cast(f16x8, read_col<K, true>(sh.k, lane, 32 * s, w * KTW + kt));
         fetch_rows(f);
         __builtin_amdgcn_sched_barrier(0);
-        f32x4 a = mfma(f.frag[0][0], xh[0], zero4()), b = zero4(), c = zero4();
-        if constexpr (kTerms == 2) {
-          b = mfma(f.frag[1][0], xh[0], b);
-          c = mfma(f.frag[0][0], xl[0], c);
-        }
+        const f16x8 t0 = operand(f.frag[0][0], 0), t1 = operand(f.frag[1][0], 0);
+        f32x4 a = mfma(t0, xh[0], zero4()), b = mfma(t1, xh[0], zero4()), c = mfma(t0, xl[0], zero4());
         if (w >= 2) {
-          a = mfma(f.frag[0][1], xh[1], a);
-          if constexpr (kTerms == 2) {
-            b = mfma(f.frag[1][1], xh[1], b);
-            c = mfma(f.frag[0][1], xl[1], c);
-          }
+          const f16x8 u0 = operand(f.frag[0][1], 1), u1 = operand(f.frag[1][1], 1);
+          a = mfma(u0, xh[1], a);
+          b = mfma(u1, xh[1], b);
+          c = mfma(u0, xl[1], c);
         }
         f32x4 d = a + (b + c), decayed = d * f.c;
-        put_half(sh.d[w >> 1][0], kTerms == 2 ? sh.d[w >> 1][1] : nullptr, at16 + (w & 1) * 8, decayed);
-        put_half(sh.dh[w >> 1][0], kF16In ? sh.dh[w >> 1][1] : nullptr, at16 + (w & 1) * 8, d);
+        put_half(sh.d[w >> 1][0], sh.d[w >> 1][1], at16 + (w & 1) * 8, decayed);
+        put_half_up(sh.dh[w >> 1][0], sh.dh[w >> 1][1], at16 + (w & 1) * 8, d);
 #pragma unroll
         for (int kt = 0; kt < KTW; ++kt) S[kt] *= total;
       }
@@ -497,7 +500,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           dh[s] = *reinterpret_cast<const f16x8*>(sh.d[s][0] + at16);
-          if constexpr (kTerms == 2) dl[s] = *reinterpret_cast<const f16x8*>(sh.d[s][1] + at16);
+          dl[s] = *reinterpret_cast<const f16x8*>(sh.d[s][1] + at16);
         }
         values = read_v(i + 1);
         fetch_record(f, std::true_type());
@@ -507,7 +510,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
           for (int kt = 0; kt < KTW; ++kt) {
-            if constexpr (kTerms == 2) S[kt] = mfma(kk[s][kt], dl[s], S[kt]);
+            S[kt] = mfma(kk[s][kt], dl[s], S[kt]);
           }
 #pragma unroll
           for (int kt = 0; kt < KTW; ++kt) S[kt] = mfma(kk[s][kt], dh[s], S[kt]);
@@ -550,18 +553,22 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
       for (int m = 0; m < KB; ++m) {
         const f16x8 q = __builtin_bit_cast(f16x8, f.rows[m]);
-        if constexpr (kF16In) o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), q, o);
+        o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), q, o);
         o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), q, o);
       }
       o *= f.h[0];
       barrier_lds();
       barrier_lds();
+      f32x4 rest = zero4();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (s > 0 && w < 2) break;
-        if constexpr (kF16In) o = mfma(*reinterpret_cast<const f16x8*>(sh.dh[s][1] + lane * 16), f.frag[0][s], o);
-        o = mfma(*reinterpret_cast<const f16x8*>(sh.dh[s][0] + lane * 16), f.frag[0][s], o);
+        const f16x8 high = *reinterpret_cast<const f16x8*>(sh.dh[s][0] + lane * 16), pp = operand(f.frag[0][s], s);
+        rest = mfma(*reinterpret_cast<const f16x8*>(sh.dh[s][1] + lane * 16), pp, rest);
+        rest = mfma(high, rest_operand(f.frag[1][s], s), rest);
+        o = mfma(high, pp, o);
       }
+      o += rest * kDown;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] *= f.h[1] * scale.out[e];
       if (__ballot(first_bad < kC)) {
@@ -598,10 +605,10 @@ int launch_prep(const DeltaPlan& p, hipStream_t s) {
   delta_prep<K, kF16In><<<(unsigned)((int64_t)p.places * p.H), 256, 0, s>>>(p);
   return (int)hipGetLastError();
 }
-template <int K, int kTerms, bool kF16In>
+template <int K, bool kF16In>
 int launch_scan(const DeltaPlan& p, hipStream_t s) {
   const int64_t units = (int64_t)p.N * p.H;
-  delta_scan<K, kTerms, kF16In><<<(unsigned)((units + 7) / 8 * 8 * (p.V / 16)), 512, 0, s>>>(p);
+  delta_scan<K, kF16In><<<(unsigned)((units + 7) / 8 * 8 * (p.V / 16)), 512, 0, s>>>(p);
   return (int)hipGetLastError();
 }
 
@@ -615,9 +622,8 @@ int launch_delta_prep(const DeltaPlan& p, void* stream) {
 
 int launch_delta_scan(const DeltaPlan& p, void* stream) {
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (p.f16) return p.K == 128 ? launch_scan<128, 2, true>(p, s) : launch_scan<64, 2, true>(p, s);
-  if (one_term(p)) return p.K == 128 ? launch_scan<128, 1, false>(p, s) : launch_scan<64, 1, false>(p, s);
-  return p.K == 128 ? launch_scan<128, 2, false>(p, s) : launch_scan<64, 2, false>(p, s);
+  if (p.K == 128) return p.f16 ? launch_scan<128, true>(p, s) : launch_scan<128, false>(p, s);
+  return p.f16 ? launch_scan<64, true>(p, s) : launch_scan<64, false>(p, s);
 }
 
 }  // namespace kda
