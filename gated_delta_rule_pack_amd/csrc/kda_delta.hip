@@ -13,9 +13,9 @@
 //
 // Number formats. MFMA operands are fp16, whose 11 bits make two terms 22: the state keeps nearly fp32's accuracy in two
 // products where bf16 would take three. Keys and queries are exact in one term: each row is scaled by the power of two
-// that brings its largest element into [1/4, 1/2), near unit length, and 8 bits of bf16 (11 of fp16) fit. What else becomes an operand is held in a
-// range by exact powers of two: the state and V of one value channel by a power of two of that channel's own (Scale), step
-// sizes by one of the chunk (Factors::shift). P's second term has 8 bits (p_rest).
+// that brings its largest element into [1/4, 1/2), near unit length, and 8 bits of bf16 (11 of fp16) fit. The state and what is
+// to be learnt of one value channel are held in a range by a power of two of that channel's own (Scale); step sizes and
+// what the keys' scaling left of their lengths stay in fp32 (Factors), so that T's diagonal is 1. P's second term has 8 bits (p_rest).
 //
 // A workgroup walks one sequence of one value head, or a slice of 64 of its state rows, with four chain waves and four
 // making waves. The chain waves hold the state as S^T[k][v] in fp32 MFMA accumulators, 32 or 16 value channels each. Lanes
@@ -67,7 +67,6 @@ struct Chain {
   static constexpr int VT = State::VT, KT = K / 16, KB = K / 32;
   State state;
   Scale scale[VT];
-  int shift;
 
   __device__ __forceinline__ void ldexp_state(int vt, int by) {
 #pragma unroll
@@ -85,11 +84,7 @@ struct Chain {
     u32x2 raw[VT][4];
     int first_bad[VT];
     bool any_bad = false;
-    if (fa.shift != shift) {
-#pragma unroll
-      for (int vt = 0; vt < VT; ++vt) ldexp_state(vt, fa.shift - shift);
-      shift = fa.shift;
-    }
+    const int steps = fa.steps, reach = max(fa.reach, 0);
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt) {
       uint32_t most = 0;
@@ -127,9 +122,10 @@ struct Chain {
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(state.S[vt][kt][i]));
-      const int e = channel_max(max(exponent(top), exponent(token_value<kF16In>(most)) + scale[vt].ex));
-      if (__ballot(e > 4 || (e < 1 && e > kNoExponent / 2))) {
-        const int by = e > kNoExponent / 2 ? min(max(scale[vt].ex + 4 - e, -120), 120) - scale[vt].ex : 0;
+      const int e = channel_max(max(exponent(top) + reach, exponent(token_value<kF16In>(most)) + steps + scale[vt].ex));
+      const bool outside = e > 4 || (e < 1 && e > kNoExponent / 2);
+      if (__ballot(outside)) {  // each channel by itself: none depends on the others of its wave
+        const int by = outside ? min(max(scale[vt].ex + 4 - e, -120), 120) - scale[vt].ex : 0;
         ldexp_state(vt, by);
         scale[vt].set(lane, scale[vt].ex + by);
       }
@@ -167,18 +163,18 @@ struct Chain {
       if (m == KB / 2 - 1) barrier_lds();
     }
     barrier_lds();
-    // What is to be learnt, V' - h K' S.
+    // What is to be learnt, b V - h K' S.
     f16x8 xh[VT][2], xl[VT][2];
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
-      const f32x4 hh = *reinterpret_cast<const f32x4*>(&fa.h[16 * tt + 4 * g4]);
+      const f32x4 hh = *reinterpret_cast<const f32x4*>(&fa.h[16 * tt + 4 * g4]), bb = *reinterpret_cast<const f32x4*>(&fa.b[16 * tt + 4 * g4]);
       const float e = fa.e[16 * tt + l16];
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float y = i & 1 ? high_value<kF16In>(raw[vt][tt][i / 2]) : low_value<kF16In>(raw[vt][tt][i / 2]);
-          x[vt][tt][i] = y * scale[vt].v - hh[i] * x[vt][tt][i];
+          x[vt][tt][i] = y * (bb[i] * scale[vt].v) - hh[i] * x[vt][tt][i];
           o[vt][tt][i] *= e;
         }
     }
@@ -345,7 +341,6 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     char* const stage = sh.slot[1].k + wave * 1024;  // no row stands there yet
     chain.state.zero();
     if (slots.from >= 0) chain.state.load_plane(p, stage, plane_at(p, slots.from, h), v0, wave, lane);
-    chain.shift = 0;
 #pragma unroll
     for (int vt = 0; vt < chain.VT; ++vt) chain.scale[vt].set(lane, 0);
     if (chunks > 0) {
@@ -357,7 +352,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     }
     if (slots.to >= 0) {
 #pragma unroll
-      for (int vt = 0; vt < chain.VT; ++vt) chain.ldexp_state(vt, -(chain.scale[vt].ex + chain.shift));
+      for (int vt = 0; vt < chain.VT; ++vt) chain.ldexp_state(vt, -chain.scale[vt].ex);
       chain.state.store_plane(p, sh.slot[chunks & 1].k + wave * 1024, plane_at(p, slots.to, h), v0, wave, lane);
     }
     return;
@@ -446,7 +441,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     if (kNext && w != 0) scale_rows();  // the first wave's in the next two parts, in which it has none
     barrier_lds();
     const auto put_t = [&](int tt, int st, f32x4 x) {
-      const Terms y = t_terms(sh.making, l, st, x);
+      const Terms y = t_terms(x);
       put_fragment(slot.t, l, tt, st, y.hi);
       put_fragment(slot.t + kTermP, l, tt, st, y.lo);
     };

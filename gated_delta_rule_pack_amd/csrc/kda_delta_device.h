@@ -253,7 +253,7 @@ struct ScaledRows {
         for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, rows.w[i][j] & 0x7fff7fffu));
         const uint32_t largest = row_max<R::kUnits>(max((uint32_t)top[0], (uint32_t)top[1]));
         const bool bad = largest >= (kF16In ? 0x7c00u : 0x7f80u);
-        const int e = largest == 0 || bad || plain ? 0 : __builtin_amdgcn_frexp_expf(token_value<kF16In>(largest)) + 1;
+        const int e = largest == 0 || bad || plain ? 0 : min(__builtin_amdgcn_frexp_expf(token_value<kF16In>(largest)) + 1, 126);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t word = bad ? 0u : rows.w[i][j];
@@ -279,24 +279,23 @@ struct ScaledRows {
 };
 
 // What the walk needs of a chunk beside its tiles; t, s are tokens.
-//   K'_t, Q'_t: scaled rows; rk_t, rq_t: what takes them to the keys and queries of the rule, as it is scaled here:
-// keys by 2^-X, step sizes by 2^{2X}, states by 2^X, with X other than 0 only for keys far from unit length; states
-// are scaled by 2^Y more, with Y other than 0 only where all step sizes are small.
+//   K'_t, Q'_t: scaled rows; rk_t, rq_t: what takes them to the keys and queries of the rule. The rule of K' has the step
+// sizes beta rk^2 and the values V / rk, and the same states: what rk holds of a key's length stays in fp32.
 struct Factors {
-  float h[kC];  // rk e^G 2^-Y: the share of K' S in what is to be learnt
-  float c[kC];  // rk e^{G_C - G}: what of D reaches the chunk's end
+  float b[kC];  // beta rk: the share of V in what is to be learnt
+  float h[kC];  // beta rk^2 e^G: that of K' S0
+  float c[kC];  // e^{G_C - G}: what of D reaches the chunk's end
   float e[kC];  // e^G
-  float f[kC];  // scale rq 2^-Y: outputs; NaN from the first bad token on
+  float f[kC];  // scale rq: outputs; NaN from the first bad token on
   float total;  // e^{G_C}; NaN with a bad token
-  int shift;    // X + Y
+  int steps;    // |b| < 2^steps
+  int reach;    // |h K'| < 2^reach
 };
 // For the making of T and P alone.
 struct Making {
   alignas(16) float G[kC];    // inclusive cumsum of g, and what its rounding left
   alignas(16) float rest[kC];
-  alignas(16) float bk[kC];   // beta rk
-  alignas(16) float rk[kC];
-  alignas(16) float col[kC];  // beta 2^Y: the columns of T
+  alignas(16) float step[kC]; // beta rk^2
 };
 
 __device__ __forceinline__ int wave_max(int x) {
@@ -333,34 +332,35 @@ __device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPl
   const uint64_t all_bad = __ballot(bad) | d.bad;
   const int first = all_bad ? __builtin_ctzll(all_bad) : kC;
   if (all_bad >> lane & 1) beta = 0.f, k = RowInfo{0, 0.f};
-  // Exponents of the chunk. Rows that were not scaled are near enough to unit length.
-  int X = 0;
-  float rk = 1.f, rq = 1.f;
+  if (k.squares == 0.f) beta = 0.f;  // nothing is learnt of a zero key, whatever its step size
+  float share, step, rq;
+  int longest = 0;
   if (p.normalize) {
-    rk = rsqrtf(k.squares + ldexp2(kNormEps, -2 * k.e));
-    rq = rsqrtf(q.squares + ldexp2(kNormEps, -2 * q.e));
+    const float rk = rsqrtf(k.squares + ldexp2(kNormEps, -2 * k.e));
+    rq = p.scale * rsqrtf(q.squares + ldexp2(kNormEps, -2 * q.e));
+    share = beta * rk;
+    step = share * rk;
   } else {
+    share = ldexp2(beta, k.e);
+    step = ldexp2(beta, 2 * k.e);
+    rq = ldexp2(p.scale, q.e);
     const int top = wave_max(k.squares > 0.f ? k.e : -1000);
-    X = top == -1000 ? 0 : top;
-    rk = ldexp2(1.f, k.e - X);
-    rq = ldexp2(1.f, q.e - X);
+    longest = top == -1000 ? 0 : top;
   }
-  beta = ldexp2(beta, 2 * X);
-  // One range holds a chunk's step sizes and, 2^{-Y / 2} below V, its states. Wider than this little would be left of
-  // the states: the chunk's outputs and its final state are then not finite, rather than wrong.
-  const bool wide = __ballot(!(fabsf(beta) < 0x1p28f)) != 0;
-  const int big = wave_max(beta != 0.f ? __builtin_amdgcn_frexp_expf(beta) : -1000);  // |beta| < 2^big
-  const int Y = big == -1000 || (big >= -1 && big <= 2) ? 0 : -big;
-  mk.bk[lane] = beta * rk;
-  mk.rk[lane] = rk;
-  mk.col[lane] = ldexp2(beta, Y);
-  to.h[lane] = ldexp2(rk * d.e, -Y);
-  to.c[lane] = rk * d.c;
+  // Step sizes that break |beta| |k|^2 <= 2 so far that the products' fp16 would: outputs and the final state are not finite.
+  const bool wide = __ballot(!(fabsf(ldexp2(beta, 2 * longest)) < 0x1p28f)) != 0;
+  const float h = step * d.e;
+  mk.step[lane] = step;
+  to.b[lane] = share;
+  to.h[lane] = h;
+  to.c[lane] = d.c;
   to.e[lane] = d.e;
-  to.f[lane] = wide || lane >= first || q.e == kBadRow ? __builtin_nanf("") : p.scale * ldexp2(rq, -Y);
+  to.f[lane] = wide || lane >= first || q.e == kBadRow ? __builtin_nanf("") : rq;
+  const int steps = wave_max(exponent(fabsf(share))), reach = wave_max(exponent(fabsf(h) * __builtin_amdgcn_sqrtf(k.squares)));
   if (lane == 0) {
     to.total = wide || all_bad ? __builtin_nanf("") : d.total;
-    to.shift = X + Y;
+    to.steps = steps;
+    to.reach = reach;
   }
 }
 
@@ -453,24 +453,19 @@ template <int W, typename PutP>
 __device__ __forceinline__ void put_tiles(float* blocks, const Making& mk, int lane, const TileProducts& p, const TileDecays& d, PutP put_p) {
   typedef TileJobs<W> Jobs;
   const int g4 = lane >> 4, l16 = lane & 15;
-  f32x4 rk[kTileJobs];
-  float bk[kTileJobs];
+  float step[kTileJobs];
 #pragma unroll
-  for (int j = 0; j < Jobs::kCount; ++j) {
-    rk[j] = *reinterpret_cast<const f32x4*>(&mk.rk[16 * Jobs::st(j) + 4 * g4]);
-    bk[j] = mk.bk[16 * Jobs::tt(j) + l16];
-  }
+  for (int j = 0; j < Jobs::kCount; ++j) step[j] = mk.step[16 * Jobs::tt(j) + l16];
   float* const at = blocks + 4 * g4 * kBlockRow + l16;
 #pragma unroll
   for (int j = 0; j < Jobs::kCount; ++j) {
-    const f32x4 factor = rk[j] * d.of[j];
     float* to = at + block_at(Jobs::tt(j), Jobs::st(j));
     const bool diagonal = Jobs::tt(j) == Jobs::st(j);
     f32x4 x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = p.kk[j][i] * (factor[i] * bk[j]);
-      x[i] = p.kq[j][i] * factor[i];
+      const float a = p.kk[j][i] * (d.of[j][i] * step[j]);
+      x[i] = p.kq[j][i] * d.of[j][i];
       to[i * kBlockRow] = diagonal && 4 * g4 + i >= l16 ? 0.f : a;
       if (diagonal && 4 * g4 + i > l16) x[i] = 0.f;
     }
@@ -578,21 +573,20 @@ __device__ __forceinline__ void far_blocks(const float* blocks, int lane, int w,
   if (w == 1) put_t(3, 0, y);
   else put_t(2, 0, y);
 }
-// A block of T with its columns' factors, in two terms.
+// A block of T in two terms.
 struct Terms {
   f16x4 hi, lo;
 };
-__device__ __forceinline__ Terms t_terms(const Making& mk, int lane, int st, f32x4 x) {
-  x *= *reinterpret_cast<const f32x4*>(&mk.col[16 * st + 4 * (lane >> 4)]);
+__device__ __forceinline__ Terms t_terms(f32x4 x) {
   const u32x2 hi = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}, lo = {rest_pair(x[0], x[1], hi[0]), rest_pair(x[2], x[3], hi[1])};
   return Terms{__builtin_bit_cast(f16x4, hi), __builtin_bit_cast(f16x4, lo)};
 }
 
-// Powers of two that hold one value channel's state and V in fp16's range: S' = S 2^{ex + shift}, V' = V 2^ex. The larger of
-// both is kept in [1, 16): fp16's least step, 2^-24, is then nothing beside it, and what 64 tokens learn stays below fp16's largest
-// number, 2^16: |v' - S' k| is at most 2^7.6, and no stable rule makes more than 64 times that of it.
+// The power of two that holds one value channel's state and what is to be learnt in fp16's range: S' = S 2^ex. The larger of
+// both is kept in [1, 16) before products: fp16's least step, 2^-24, is then nothing beside it, and what 64 tokens learn stays
+// below fp16's largest number, 2^16: |b v' - h K' S'| is at most 2^7.6, and no stable rule makes more than 64 times that of it.
 struct Scale {
-  int ex, shift;
+  int ex;
   float v;         // 2^ex
   f32x4 out;       // 2^-ex of the channels 4g + i, for tiles that hold channels as rows
   __device__ __forceinline__ void set(int lane, int to) {

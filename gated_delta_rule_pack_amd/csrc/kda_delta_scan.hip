@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
   if (wave == 0) invert_diagonal(sh.blocks, lane);
   barrier_lds();
   const auto put_t = [&](int tt, int st, f32x4 x) {
-    const Terms y = t_terms(sh.making, lane, st, x);
+    const Terms y = t_terms(x);
     put_fragment(rec, lane, tt, st, y.hi);
     put_fragment(rec + kTermP, lane, tt, st, y.lo);
   };
@@ -136,6 +136,8 @@ struct ScanShared {
   alignas(16) char dh[2][2][1024];   // D
   alignas(16) char k[kC * kRowBytes<K>];
   alignas(16) char v[2][kC * 32];    // V of this chunk and of the next, 16 channels
+  alignas(16) float factors[2][3][kC];  // b, h and c of both
+  alignas(16) uint32_t numbers[2][4];   // total, steps, reach
   alignas(16) int top[16][4];        // largest exponent of a channel, by wave
   alignas(16) int bad[16][4];        // its first token whose value is not finite
   alignas(16) float sum[2][4][16];
@@ -147,9 +149,9 @@ struct Fetch {
   u32x4 rows[K / 32];  // 16 tokens of K' (chain) or Q' (outputs)
   u32x4 frag[2][2];    // [term][b] of T's or P's row of tiles
   u32x4 v;             // outputs: V of the next chunk, a token's 8 channels in half the lanes
-  f32x4 h, c;          // chain: factors of tokens 4g + i; outputs: e and f of token l % 16 in h
-  float total;
-  int shift;
+  // The outputs' alone.
+  float e, f;          // factors of token l % 16
+  uint32_t factor;     // of the next chunk, as V: b, h or c of token l % 16, or one of the chunk's numbers
 };
 
 template <int K, bool kF16In>
@@ -284,9 +286,10 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   // the loads behind its own.
   const char* next_record = p.records + ((int64_t)place * p.H + h) * kDeltaRecord;
   const char* next_rows = (chain ? p.keys : p.queries) + ((int64_t)place * H_qk + hq) * (kC * K * 2);
+  const char* next_factors = next_record;
   const uint16_t* next_v = v + (int64_t)begin * p.v_t;
   int next_left = len, left_v = len;
-  const int at16 = lane * 16, at_row = l16 * 4, at_group = g4 * 16;
+  const int at16 = lane * 16, at_row = l16 * 4;
   // The last fragment of a row of tiles: with one tile (half_fragment) a lane has 8 bytes of it, and reads 16; what is its neighbour's goes.
   const int last_unit = w & 1 ? 16 : 8;
   const uint32_t keep = w & 1 ? ~0u : 0u;
@@ -319,15 +322,9 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         f.frag[1][b][0] = x[0], f.frag[1][b][1] = x[1];
       }
     }
-    if constexpr (for_chain) {
-      f.c = __builtin_bit_cast(f32x4, load(rec, at_group, kRecFactors + (int)offsetof(Factors, c) + 64 * w));
-      f.h = __builtin_bit_cast(f32x4, load(rec, at_group, kRecFactors + (int)offsetof(Factors, h) + 64 * w));
-      const u32x2 last = __builtin_amdgcn_raw_buffer_load_b64(rec, 0, kRecFactors + (int)offsetof(Factors, total), 0);
-      f.total = __uint_as_float(last[0]);
-      f.shift = (int)last[1];
-    } else {
-      f.h[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, at_row, kRecFactors + (int)offsetof(Factors, e) + 64 * w, 0));
-      f.h[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, at_row, kRecFactors + (int)offsetof(Factors, f) + 64 * w, 0));
+    if constexpr (!for_chain) {
+      f.e = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, at_row, kRecFactors + (int)offsetof(Factors, e) + 64 * w, 0));
+      f.f = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rec, at_row, kRecFactors + (int)offsetof(Factors, f) + 64 * w, 0));
     }
   };
   // V of one chunk, by the outputs' waves: token 16 w + l / 2, channels 8 (l % 2) on, twice. (All of a row's offset is the
@@ -339,15 +336,33 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   const auto advance_v = [&]() {
     const bool more = left_v > kC;
     next_v += more ? p.v_t * kC : 0;
+    next_factors += more ? (int64_t)p.H * kDeltaRecord : 0;
     left_v -= more ? kC : 0;
   };
   const auto put_v = [&](u32x4 x, int i) { *reinterpret_cast<u32x4*>(sh.v[i & 1] + 16 * w * 32 + (lane & 31) * 16) = x; };
+  // The factors that the chain takes: b, h and c of tokens 16 w + l % 16 in 48 lanes, the chunk's numbers behind them.
+  static_assert(offsetof(Factors, b) == 0 && offsetof(Factors, h) == 4 * kC && offsetof(Factors, c) == 8 * kC &&
+                offsetof(Factors, steps) == offsetof(Factors, total) + 4 && offsetof(Factors, reach) == offsetof(Factors, total) + 8, "as they are fetched");
+  const int number = min(lane - 48, 2), at_factor = lane < 48 ? 4 * kC * g4 + 64 * w + 4 * l16 : (int)offsetof(Factors, total) + 4 * number;
+  const auto fetch_factor = [&]() { return __builtin_amdgcn_raw_buffer_load_b32(whole(next_factors, kDeltaRecord), at_factor, kRecFactors, 0); };
+  const auto put_factor = [&](uint32_t x, int i) {
+    if (lane < 48) sh.factors[i & 1][g4][16 * w + l16] = __uint_as_float(x);
+    else if (w == 0) sh.numbers[i & 1][number] = x;
+  };
+  struct OwnFactors {
+    f32x4 b, h, c;  // of tokens 16 w + 4g + i
+    uint32_t total, steps, reach;
+  };
+  const auto read_factors = [&](int i) {
+    const auto of = [&](int j) { return *reinterpret_cast<const f32x4*>(&sh.factors[i & 1][j][16 * w + 4 * g4]); };
+    const u32x4 n = *reinterpret_cast<const u32x4*>(sh.numbers[i & 1]);
+    return OwnFactors{of(0), of(1), of(2), n[0], n[1], n[2]};
+  };
   // Tokens 16 w + 4g + i of channel l % 16.
   const auto read_v = [&](int i) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sh.v[i & 1] + (16 * w + 4 * g4 + (l16 >> 2)) * 32 + (lane & 3) * 8));
   };
   Scale scale;
-  scale.shift = 0;
   scale.set(lane, 0);
   typedef int i32x4 __attribute__((ext_vector_type(4)));
   const auto largest = [&](const int (&of)[16][4]) {
@@ -393,25 +408,19 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     };
     char* const k_rows = sh.k + 16 * w * kRowBytes<K> + row_at<K>(l16) + g4 * 16;
     __builtin_amdgcn_s_setprio(3);  // the outputs' waves fill its gaps
-    barrier_lds();  // the first chunk's V
+    barrier_lds();  // the first chunk's V and factors
     s16x4 values = read_v(0);
+    OwnFactors own = read_factors(0);
     const auto step = [&](Fetch<K>& f, int i) {
-      const int shift = __builtin_amdgcn_readfirstlane(f.shift);
-      const float total = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(f.total)));
-      if (shift != scale.shift) {
-#pragma unroll
-        for (int kt = 0; kt < KTW; ++kt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], shift - scale.shift);
-        scale.shift = shift;
-      }
+      const int steps = (int)__builtin_amdgcn_readfirstlane(own.steps), reach = max((int)__builtin_amdgcn_readfirstlane(own.reach), 0);
+      const float total = __uint_as_float(__builtin_amdgcn_readfirstlane(own.total));
       // The state's fragments and the channel's largest exponent.
       put_state();
       uint32_t value[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) value[e] = (uint16_t)values[e];
       uint32_t most = max(max(value[0] & 0x7fffu, value[1] & 0x7fffu), max(value[2] & 0x7fffu, value[3] & 0x7fffu));
-      int top = max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex);
+      int top = max(state_top() + reach, exponent(token_value<kF16In>(most)) + steps + scale.ex);
       sh.top[l16][w] = channel_max(most >= kInf ? kBadTop : top);
       barrier_lds();
       f16x8 hi[KB], lo[KB];
@@ -435,7 +444,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           if ((value[x] & 0x7fffu) >= kInf) bad = 16 * w + 4 * g4 + x, value[x] = 0;
           most = max(most, value[x] & 0x7fffu);
         }
-        sh.top[l16][w] = channel_max(max(state_top(), exponent(token_value<kF16In>(most)) + scale.ex));
+        sh.top[l16][w] = channel_max(max(state_top() + reach, exponent(token_value<kF16In>(most)) + steps + scale.ex));
         sh.bad[l16][w] = -channel_max(-bad);
         barrier_lds();
         first_bad = least(sh.bad);
@@ -462,7 +471,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
         for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(k_rows + m * 64) = f.rows[m];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(value[e]) * scale.v - f.h[e] * (a[e] + b[e]);
+        for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(value[e]) * (own.b[e] * scale.v) - own.h[e] * (a[e] + b[e]);
         put_half(sh.x[w >> 1][0], sh.x[w >> 1][1], at16 + (w & 1) * 8, x);
       }
       barrier_lds();
@@ -488,7 +497,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           b = mfma(u1, xh[1], b);
           c = mfma(u0, xl[1], c);
         }
-        f32x4 d = a + (b + c), decayed = d * f.c;
+        f32x4 d = a + (b + c), decayed = d * own.c;
         put_half(sh.d[w >> 1][0], sh.d[w >> 1][1], at16 + (w & 1) * 8, decayed);
         put_half_up(sh.dh[w >> 1][0], sh.dh[w >> 1][1], at16 + (w & 1) * 8, d);
 #pragma unroll
@@ -503,6 +512,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           dl[s] = *reinterpret_cast<const f16x8*>(sh.d[s][1] + at16);
         }
         values = read_v(i + 1);
+        own = read_factors(i + 1);
         fetch_record(f, std::true_type());
         advance();
         __builtin_amdgcn_sched_barrier(0);
@@ -531,11 +541,12 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
     for (int kt = 0; kt < KTW; ++kt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], -(scale.ex + scale.shift));
+      for (int e = 0; e < 4; ++e) S[kt][e] = ldexp2(S[kt][e], -scale.ex);
     store_state();
   } else {
     const int at_out = ((16 * w + l16) * (int)p.o_t + 4 * g4) * 2;
     put_v(fetch_v(), 0);
+    put_factor(fetch_factor(), 0);
     advance_v();
     const auto step = [&](Fetch<K>& f, int i) {
       barrier_lds();
@@ -548,6 +559,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         barrier_lds();
       }
       put_v(f.v, i + 1);
+      put_factor(f.factor, i + 1);
       // S0 Q', channels 4g + i, token l % 16.
       f32x4 o = zero4();
 #pragma unroll
@@ -556,7 +568,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), q, o);
         o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), q, o);
       }
-      o *= f.h[0];
+      o *= f.e;
       barrier_lds();
       barrier_lds();
       f32x4 rest = zero4();
@@ -570,7 +582,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       }
       o += rest * kDown;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] *= f.h[1] * scale.out[e];
+      for (int e = 0; e < 4; ++e) o[e] *= f.f * scale.out[e];
       if (__ballot(first_bad < kC)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -580,6 +592,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       fetch_record(f, std::false_type());
       advance();
       f.v = fetch_v();
+      f.factor = fetch_factor();
       advance_v();
       u32x2 packed;
       if constexpr (kF16In) packed = __builtin_bit_cast(u32x2, f16x4{(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]});
@@ -592,6 +605,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       fetch_record(fetched[a], std::false_type());
       advance();
       fetched[a].v = fetch_v();
+      fetched[a].factor = fetch_factor();
       advance_v();
       __builtin_amdgcn_sched_barrier(0);
     }

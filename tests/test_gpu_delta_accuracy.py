@@ -60,3 +60,54 @@ def test_outputs_and_states_are_off_by_their_own_rounding(name, path):
             ratio = rel / own(S, sdt)
             print(f"  state: {ratio:.4f} of its own rounding", flush=True)
             assert ratio < 1.005
+
+
+@PATHS
+@pytest.mark.parametrize("exponent", [6, 9, 12, 13, 14, 30])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_zero_keys_among_long_ones(normalize, exponent, path):
+    """A token with k = 0 only decays, whatever its step size; the other keys are s times a unit key's length, with step sizes over
+    s^2: the same rule, of states over s, exactly. Normalised keys have no length, and their zero rows the largest steps."""
+    case = DeltaCase([140, 3, 64], 2, seed=42, unit=not normalize, state="dense")
+    gen = torch.Generator().manual_seed(5)
+    zero = torch.rand(case.T, generator=gen) < 0.1
+    zero[:2] = True  # the first tokens too
+    case.k[zero] = 0
+    case.beta[zero] = 0.5 if not normalize else 2.0
+    d = case.device()
+    s = 1.0 if normalize else 2.0 ** exponent
+    steps = d["beta"] / s ** 2
+    steps[zero.cuda()] = d["beta"][zero.cuda()]
+    scaled = dict(d, k=(d["k"].float() * s).bfloat16(), beta=steps, initial=d["initial"] / s)
+    out, final = case.forward(scaled, path=path)
+    torch.cuda.synchronize()
+    o, S, M = case.oracle()
+    n = np.array(case.lengths, np.float64)[:, None]
+    state_off = 4 * E2 * (1 + np.sqrt(n)) * M
+    token_off = np.repeat(state_off + 4 * (E2 + EP) * M, case.lengths, axis=0)[:, :, None]
+    close("out", f64(out) * s, o, 2.0 ** -8 * np.abs(o) + 1.01 * case.scale * case.query_size() * token_off)
+    close("state", f64(final) * s, S, 2.0 ** -24 * np.abs(S) + 1.01 * state_off[:, :, None, None])
+
+
+@PATHS
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 20, 2.0 ** 60])
+@pytest.mark.parametrize("step", [2.0 ** -60, 2.0 ** -110, 2.0 ** -125, 2.0 ** -140])
+def test_tiny_steps_beside_a_state(step, size, path):
+    """Step sizes that do next to nothing beside a state: in all chunks, and in a last chunk of a single token."""
+    for lens in ([200, 30], [65, 129]):
+        case = DeltaCase(lens, 2, seed=43, state="dense")
+        case.initial = case.initial * size
+        some = torch.ones(case.T, dtype=torch.bool)
+        if lens[0] == 65:
+            some[:] = False
+            some[[64, 193]] = True
+        case.beta[some] *= step
+        d = case.device()
+        out, final = case.forward(d, path=path)
+        torch.cuda.synchronize()
+        o, S, M = case.oracle()
+        n = np.array(case.lengths, np.float64)[:, None]
+        state_off = 4 * E2 * (1 + np.sqrt(n)) * M
+        token_off = np.repeat(state_off + 4 * (E2 + EP) * M, case.lengths, axis=0)[:, :, None]
+        close("out", f64(out), o, 2.0 ** -8 * np.abs(o) + 1.01 * case.scale * token_off)
+        close("state", f64(final), S, 2.0 ** -24 * np.abs(S) + 1.01 * state_off[:, :, None, None])
