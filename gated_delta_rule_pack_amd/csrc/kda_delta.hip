@@ -48,6 +48,7 @@ struct Slot {
   alignas(16) char t[2 * kTermP];
   alignas(16) char p[kTermP + kRestP];
   alignas(16) Factors factors;
+  alignas(16) float decay[kC];  // e^g
 };
 template <int K, int V>
 struct DeltaShared {
@@ -76,7 +77,7 @@ struct Chain {
   }
 
   // One chunk; passes kBarriers - 1 barriers.
-  __device__ __forceinline__ void step(Slot<K, V>& slot, int wave, int lane_) {
+  __device__ __forceinline__ void step(Slot<K, V>& slot, int wave, int lane_, int count) {
     const int lane = local_copy(lane_), g4 = lane >> 4, l16 = lane & 15;
     constexpr uint32_t kInf = kF16In ? 0x7c00u : 0x7f80u;
     const Factors& fa = slot.factors;
@@ -84,7 +85,9 @@ struct Chain {
     u32x2 raw[VT][4];
     int first_bad[VT];
     bool any_bad = false;
-    const int steps = fa.steps, reach = max(fa.reach, 0);
+    const int steps = fa.steps, reach = fa.reach;
+    int state_top[VT];
+    bool apart = false;
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt) {
       uint32_t most = 0;
@@ -122,12 +125,19 @@ struct Chain {
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(state.S[vt][kt][i]));
-      const int e = channel_max(max(exponent(top) + reach, exponent(token_value<kF16In>(most)) + steps + scale[vt].ex));
-      const bool outside = e > 4 || (e < 1 && e > kNoExponent / 2);
-      if (__ballot(outside)) {  // each channel by itself: none depends on the others of its wave
-        const int by = outside ? min(max(scale[vt].ex + 4 - e, -120), 120) - scale[vt].ex : 0;
-        ldexp_state(vt, by);
-        scale[vt].set(lane, scale[vt].ex + by);
+      Scale& sc = scale[vt];
+      const int own = exponent(top);
+      const i16x2 tops = channel_max(i16x2{(short)own, (short)max(own - sc.ex + reach, exponent(token_value<kF16In>(most)) + steps)});
+      state_top[vt] = tops[0];
+      sc.apart = 0;
+      if (__ballot(!stays(sc.ex, tops[0], tops[1]))) {  // each channel by itself: none depends on the others of its wave
+        const Ranges r = ranges_of(sc.ex, tops[0], tops[1]);
+        ldexp_state(vt, r.s - sc.ex);
+        state_top[vt] += r.s - sc.ex;
+        sc.ex = r.s;
+        sc.apart = r.x - r.s;
+        sc.set(lane, r.x);
+        apart = apart || __ballot(sc.apart != 0);
       }
     }
     barrier_lds();
@@ -161,9 +171,21 @@ struct Chain {
         }
       }
       if (m == KB / 2 - 1) barrier_lds();
+      else __builtin_amdgcn_sched_barrier(0);
     }
     barrier_lds();
     // What is to be learnt, b V - h K' S.
+    if (apart) {
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        const float by = ldexp2(1.f, scale[vt].apart);
+        f32x4 rows;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows[i] = __shfl(by, 4 * g4 + i);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) x[vt][tt] *= by, o[vt][tt] *= rows;
+      }
+    }
     f16x8 xh[VT][2], xl[VT][2];
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
@@ -178,29 +200,53 @@ struct Chain {
           o[vt][tt][i] *= e;
         }
     }
+    uint64_t small[VT], any_small = 0;
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt) {
+      float least = INFINITY;
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) least = fminf(least, fabsf(x[vt][tt][i]));
+      small[vt] = __ballot(least < kLeastShare<kF16In> && !state_lasts(state_top[vt], scale[vt].apart, fa.total));
+      any_small |= small[vt];
+    }
+    if (__builtin_expect(any_small != 0, 0) && __builtin_expect(fades(slot, x, small, state_top, lane), 0)) {
+      by_tokens(slot, wave, lane, count);
+      barrier_lds();
+      barrier_lds();
+      return;
+    }
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         xh[vt][b] = to_f16(x[vt][2 * b], x[vt][2 * b + 1]);
-        xl[vt][b] = rest_f16(x[vt][2 * b], x[vt][2 * b + 1], xh[vt][b]);
+        xl[vt][b] = rest_up(x[vt][2 * b], x[vt][2 * b + 1], xh[vt][b]);
       }
     // D = T x, rows t, column v.
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
+      f16x8 th[2];
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) x[vt][tt] = zero4();
 #pragma unroll
       for (int b = 0; b <= tt / 2; ++b) {
-        const f16x8 th = read_fragment(slot.t, lane, tt, b);
+        th[b] = read_fragment(slot.t, lane, tt, b);
         const f16x8 tl = read_fragment(slot.t + kTermP, lane, tt, b);
 #pragma unroll
         for (int vt = 0; vt < VT; ++vt) {
           x[vt][tt] = mfma(tl, xh[vt][b], x[vt][tt]);
-          x[vt][tt] = mfma(th, xl[vt][b], x[vt][tt]);
-          x[vt][tt] = mfma(th, xh[vt][b], x[vt][tt]);
+          x[vt][tt] = mfma(th[b], xl[vt][b], x[vt][tt]);
         }
       }
+#pragma unroll
+      for (int vt = 0; vt < VT; ++vt) {
+        x[vt][tt] *= kDown;
+#pragma unroll
+        for (int b = 0; b <= tt / 2; ++b) x[vt][tt] = mfma(th[b], xh[vt][b], x[vt][tt]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
     barrier_lds();
     // O^T += D^T P^T, and the outputs, rows v = 4g + i, column t, to V's tile.
@@ -269,28 +315,95 @@ struct Chain {
       }
     barrier_lds();
     // The state.
-    const float total = fa.total;
+    f16x8 dh[VT][2], dl[VT][2];
+    float total[VT];
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt) {
+      total[vt] = ldexp2(fa.total, 12 + scale[vt].apart);
+      scale[vt].ex += scale[vt].apart;
+    }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      f16x8 dh[VT], dl[VT];
       const f32x4 c0 = *reinterpret_cast<const f32x4*>(&fa.c[32 * b + 4 * g4]), c1 = *reinterpret_cast<const f32x4*>(&fa.c[32 * b + 16 + 4 * g4]);
 #pragma unroll
       for (int vt = 0; vt < VT; ++vt) {
         const f32x4 y0 = x[vt][2 * b] * c0, y1 = x[vt][2 * b + 1] * c1;
-        dh[vt] = to_f16(y0, y1);
-        dl[vt] = rest_f16(y0, y1, dh[vt]);
+        dh[vt][b] = to_f16(y0, y1);
+        dl[vt][b] = rest_up(y0, y1, dh[vt][b]);
+      }
+    }
+#pragma unroll
+    for (int kt = 0; kt < KT; kt += 2) {
+      f16x8 k0[2], k1[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        k0[b] = __builtin_bit_cast(f16x8, read_col<K, true>(slot.k, lane, 32 * b, kt));
+        k1[b] = __builtin_bit_cast(f16x8, read_col<K, true>(slot.k, lane, 32 * b, kt + 1));
       }
 #pragma unroll
-      for (int kt = 0; kt < KT; kt += 2) {
-        const f16x8 k0 = __builtin_bit_cast(f16x8, read_col<K, true>(slot.k, lane, 32 * b, kt));
-        const f16x8 k1 = __builtin_bit_cast(f16x8, read_col<K, true>(slot.k, lane, 32 * b, kt + 1));
+      for (int vt = 0; vt < VT; ++vt) {
+        f32x4 &s0 = state.S[vt][kt], &s1 = state.S[vt][kt + 1];
+        s0 *= total[vt], s1 *= total[vt];
 #pragma unroll
-        for (int vt = 0; vt < VT; ++vt) {
-          f32x4 &s0 = state.S[vt][kt], &s1 = state.S[vt][kt + 1];
-          if (b == 0) s0 *= total, s1 *= total;
-          s0 = mfma(k0, dl[vt], s0), s1 = mfma(k1, dl[vt], s1);
-          s0 = mfma(k0, dh[vt], s0), s1 = mfma(k1, dh[vt], s1);
+        for (int b = 0; b < 2; ++b) s0 = mfma(k0[b], dl[vt][b], s0), s1 = mfma(k1[b], dl[vt][b], s1);
+        s0 *= kDown, s1 *= kDown;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) s0 = mfma(k0[b], dh[vt][b], s0), s1 = mfma(k1[b], dh[vt][b], s1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  __device__ __forceinline__ bool fades(const Slot<K, V>& slot, const f32x4 (&x)[VT][4], const uint64_t (&small)[VT], const int (&state_top)[VT],
+                                        int lane) const {
+    bool found = false;
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt) {
+      if (!small[vt]) continue;
+      float through = state_share(state_top[vt], scale[vt].apart);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        Fading f;
+        f.set(*reinterpret_cast<const f32x4*>(&slot.decay[16 * tt + 4 * (lane >> 4)]), x[vt][tt]);
+        const float before = f.before(through, lane);
+        found = found || f.fades(before, kLeastShare<kF16In>);
+      }
+    }
+    return __ballot(found) != 0;
+  }
+  // The chunk token by token in fp32, for this wave's channels.
+  __device__ __forceinline__ void by_tokens(Slot<K, V>& slot, int wave, int lane, int count) {
+    const Factors& fa = slot.factors;
+#pragma unroll
+    for (int vt = 0; vt < VT; ++vt) {
+      f32x4 (&S)[KT] = state.S[vt];
+      ldexp_state(vt, -scale[vt].ex);
+      scale[vt].ex = scale[vt].apart = 0;
+      scale[vt].set(lane, 0);
+      const auto over_keys = [&](const char* row, auto use) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < KB; ++m) {
+          const f16x8 k = *reinterpret_cast<const f16x8*>(row + m * 64 + (lane >> 4) * 16);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) use(2 * m + j / 4, j % 4, (float)k[j]);
         }
+      };
+#pragma unroll 1
+      for (int t = 0; t < count; ++t) {
+        const float decay = slot.decay[t];
+        uint16_t* const at = reinterpret_cast<uint16_t*>(slot.v + row_at<V>(t)) + (wave * VT + vt) * 16 + (lane & 15);
+        float u = 0.f, o = 0.f;
+        over_keys(slot.k + row_at<K>(t), [&](int kt, int i, float k) __attribute__((always_inline)) { u += S[kt][i] * k; });
+        u = add_far(add_far(u, 16), 32);
+        u = fa.b[t] * token_value<kF16In>(*at) - fa.s[t] * (decay * u);
+        over_keys(slot.k + row_at<K>(t), [&](int kt, int i, float k) __attribute__((always_inline)) { S[kt][i] = S[kt][i] * decay + u * k; });
+        over_keys(slot.q + row_at<K>(t), [&](int kt, int i, float q) __attribute__((always_inline)) { o += S[kt][i] * q; });
+        o = fa.f[t] * kTimesP * add_far(add_far(o, 16), 32);
+        if (lane < 16) *at = kF16In ? __builtin_bit_cast(uint16_t, (_Float16)o) : __builtin_bit_cast(uint16_t, to_bf16(o));
+      }
+      if (fa.total != fa.total) {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) S[kt] = zero4() + __builtin_nanf("");
       }
     }
   }
@@ -300,11 +413,7 @@ struct Chain {
 // as 64 tokens: 16 prompts of 256 among 240 single tokens at H = 12 197 instead of 84 us.)
 template <int K, int V>
 __device__ __forceinline__ void one_token(DeltaShared<K, V>& shared, int begin, int h, int v0, Slots slots, int tid) {
-  // The plan read again from the kernel's arguments: with the walk's own copy of it the walk spills scalars (2 %).
-  typedef const __attribute__((address_space(4))) DeltaPlan* Arguments;
-  Arguments arguments = (Arguments)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(arguments));
-  const DeltaPlan& p = *(const DeltaPlan*)arguments;
+  const DeltaPlan& p = plan_again();
   auto& sh = *reinterpret_cast<TokenShared<K, V, kWalkThreads>*>(&shared);
   static_assert(sizeof(TokenShared<K, V, kWalkThreads>) <= sizeof(shared), "fits");
   uint16_t x[kTokenRow<K, V>], k[K / 64];
@@ -342,11 +451,14 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     chain.state.zero();
     if (slots.from >= 0) chain.state.load_plane(p, stage, plane_at(p, slots.from, h), v0, wave, lane);
 #pragma unroll
-    for (int vt = 0; vt < chain.VT; ++vt) chain.scale[vt].set(lane, 0);
+    for (int vt = 0; vt < chain.VT; ++vt) {
+      chain.scale[vt].ex = 0;
+      chain.scale[vt].set(lane, 0);
+    }
     if (chunks > 0) {
       for (int i = 0; i <= kBarriers; ++i) barrier_lds();
       for (int i = 0; i < chunks; ++i) {
-        chain.step(sh.slot[i & 1], wave, lane);
+        chain.step(sh.slot[i & 1], wave, lane, min(len - i * kC, kC));
         barrier_lds();
       }
     }
@@ -417,8 +529,10 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     rq.put(slot.q, sh.info[1], tid);
     barrier_lds();
     const int l = local_copy(lane);
-    if (w == kNumbersWave)
+    if (w == kNumbersWave) {
+      slot.decay[l] = decays.own;
       put_chunk(sh.making, slot.factors, p, decays, sh.info[0][l], sh.info[1][l], bits_value(beta_next, p.beta_bf16), l);
+    }
     TileProducts products;
     by_wave(w, [&](auto W) { tile_products<K, decltype(W)::value>(slot.k, slot.q, l, products); });
     if constexpr (kNext) fetch(i + 1);

@@ -47,15 +47,8 @@ __device__ __forceinline__ f16x8 rest_f16(f32x4 a, f32x4 b, f16x8 hi) {
   return __builtin_bit_cast(f16x8, u32x4{rest_pair(a[0], a[1], h[0]), rest_pair(a[2], a[3], h[1]), rest_pair(b[0], b[1], h[2]),
                                          rest_pair(b[2], b[3], h[3])});
 }
-// One tile (rows 4g + i) as half a fragment, in two terms.
-__device__ __forceinline__ void put_half(char* high, char* low, int at, f32x4 x) {
-  const u32x2 h = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])};
-  *reinterpret_cast<u32x2*>(high + at) = h;
-  *reinterpret_cast<u32x2*>(low + at) = u32x2{rest_pair(x[0], x[1], h[0]), rest_pair(x[2], x[3], h[1])};
-}
-
-// Second terms of outputs' operands, D and P, times 2^12: as large as the first ones, so that fp16's least step is far below
-// them. Their products are summed by themselves and taken back by 2^-12.
+// Second terms times 2^12, as large as the first ones: fp16's least step then stands for 2^-37. Their products are summed by
+// themselves and taken back by 2^-12. (Of the state alone the second term stands as it is: its largest value is kept near 1.)
 constexpr float kUp = 0x1p12f, kDown = 0x1p-12f;
 __device__ __forceinline__ uint32_t rest_up(float a, float b, uint32_t first) {
   return rest_pair(a * kUp, b * kUp, first, -kUp);
@@ -64,17 +57,21 @@ __device__ __forceinline__ f16x8 rest_up(f32x4 a, f32x4 b, f16x8 hi) {
   const u32x4 h = __builtin_bit_cast(u32x4, hi);
   return __builtin_bit_cast(f16x8, u32x4{rest_up(a[0], a[1], h[0]), rest_up(a[2], a[3], h[1]), rest_up(b[0], b[1], h[2]), rest_up(b[2], b[3], h[3])});
 }
-__device__ __forceinline__ void put_half_up(char* high, char* low, int at, f32x4 x) {
+// One tile (rows 4g + i) as half a fragment, in two terms.
+template <bool kRestUp>
+__device__ __forceinline__ void put_half(char* high, char* low, int at, f32x4 x) {
   const u32x2 h = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])};
   *reinterpret_cast<u32x2*>(high + at) = h;
-  *reinterpret_cast<u32x2*>(low + at) = u32x2{rest_up(x[0], x[1], h[0]), rest_up(x[2], x[3], h[1])};
+  *reinterpret_cast<u32x2*>(low + at) = kRestUp ? u32x2{rest_up(x[0], x[1], h[0]), rest_up(x[2], x[3], h[1])}
+                                                : u32x2{rest_pair(x[0], x[1], h[0]), rest_pair(x[2], x[3], h[1])};
 }
-// P's second term has 8 bits, five of exponent and two of fraction, fp16's upper byte: with them P is within 2^-14 of itself,
-// an eighth of the half step of outputs in fp16, and its records keep their size. It is stored times 2^15 (so that its least
-// step, 2^-16, stands for 2^-31), and read times 2^12.
+// P stands 16 times as large as it is (it is at most 2^10, by rows of 2^5). Its second term has 8 bits, five of exponent and two of
+// fraction, fp16's upper byte: with them P is within 2^-14 of itself, an eighth of the half step of outputs in fp16, or within 2^-32, and its
+// records keep their size. It is stored times 2^11, and read times 2^12.
+constexpr float kTimesP = 16.f;
 __device__ __forceinline__ uint32_t p_rest(f32x4 x, u32x2 first) {
   typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-  const float up = 8 * kUp;
+  const float up = kUp / 2;
   uint32_t w[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -86,7 +83,7 @@ __device__ __forceinline__ uint32_t p_rest(f32x4 x, u32x2 first) {
 __device__ __forceinline__ f16x8 p_rest_operand(u32x2 x) {
   const u32x4 w = {__builtin_amdgcn_perm(0, x[0], 0x010c000c), __builtin_amdgcn_perm(0, x[0], 0x030c020c),
                    __builtin_amdgcn_perm(0, x[1], 0x010c000c), __builtin_amdgcn_perm(0, x[1], 0x030c020c)};
-  return __builtin_bit_cast(f16x8, w) * (_Float16)0.125f;
+  return __builtin_bit_cast(f16x8, w) * (_Float16)2.f;
 }
 
 // A token's element of a 16-bit word, by type.
@@ -132,6 +129,19 @@ __device__ __forceinline__ int channel_max(int x) {
   x = max((int)a[0], (int)a[1]);
   const auto b = __builtin_amdgcn_permlane16_swap((unsigned)x, (unsigned)x, false, false);
   return max((int)b[0], (int)b[1]);
+}
+
+// Two exponents in one word, and the larger of each.
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ int pair_max(int a, int b) {
+  return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(i16x2, a), __builtin_bit_cast(i16x2, b)));
+}
+__device__ __forceinline__ i16x2 channel_max(i16x2 of) {
+  unsigned x = __builtin_bit_cast(unsigned, of);
+  const auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  x = pair_max((int)a[0], (int)a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  return __builtin_bit_cast(i16x2, pair_max((int)b[0], (int)b[1]));
 }
 
 constexpr int kBadRow = 1 << 20;  // exponent of a row that is not finite
@@ -285,8 +295,9 @@ struct Factors {
   float b[kC];  // beta rk: the share of V in what is to be learnt
   float h[kC];  // beta rk^2 e^G: that of K' S0
   float c[kC];  // e^{G_C - G}: what of D reaches the chunk's end
-  float e[kC];  // e^G
-  float f[kC];  // scale rq: outputs; NaN from the first bad token on
+  float e[kC];  // e^G times 16, as P
+  float f[kC];  // scale rq / 16: outputs; NaN from the first bad token on
+  float s[kC];  // beta rk^2, for a walk by tokens
   float total;  // e^{G_C}; NaN with a bad token
   int steps;    // |b| < 2^steps
   int reach;    // |h K'| < 2^reach
@@ -307,6 +318,7 @@ __device__ __forceinline__ int wave_max(int x) {
 }
 // A token's decays, one lane for each token: what does not wait for the chunk's rows.
 struct Decays {
+  float own;      // e^g
   float e, c;     // e^G, e^{G_C - G}
   float total;    // e^{G_C}
   uint64_t bad;   // tokens whose log decay is not allowed
@@ -316,7 +328,9 @@ __device__ __forceinline__ Decays put_decays(Making& mk, float g, int lane) {
   const bool bad = !(g <= 0.f);
   d.bad = __ballot(bad);
   if (bad) g = 0.f;
-  const double G = prefix_sum((double)(g < kMinLogDecay ? kMinLogDecay : g));
+  g = g < kMinLogDecay ? kMinLogDecay : g;
+  d.own = __expf(g);
+  const double G = prefix_sum((double)g);
   const uint64_t u = __builtin_bit_cast(uint64_t, G);
   const double end = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
                                                     (uint32_t)__builtin_amdgcn_readlane((int)u, 63));
@@ -354,8 +368,9 @@ __device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPl
   to.b[lane] = share;
   to.h[lane] = h;
   to.c[lane] = d.c;
-  to.e[lane] = d.e;
-  to.f[lane] = wide || lane >= first || q.e == kBadRow ? __builtin_nanf("") : rq;
+  to.e[lane] = d.e * kTimesP;
+  to.s[lane] = step;
+  to.f[lane] = wide || lane >= first || q.e == kBadRow ? __builtin_nanf("") : rq / kTimesP;
   const int steps = wave_max(exponent(fabsf(share))), reach = wave_max(exponent(fabsf(h) * __builtin_amdgcn_sqrtf(k.squares)));
   if (lane == 0) {
     to.total = wide || all_bad ? __builtin_nanf("") : d.total;
@@ -465,7 +480,7 @@ __device__ __forceinline__ void put_tiles(float* blocks, const Making& mk, int l
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float a = p.kk[j][i] * (d.of[j][i] * step[j]);
-      x[i] = p.kq[j][i] * d.of[j][i];
+      x[i] = p.kq[j][i] * (d.of[j][i] * kTimesP);
       to[i * kBlockRow] = diagonal && 4 * g4 + i >= l16 ? 0.f : a;
       if (diagonal && 4 * g4 + i > l16) x[i] = 0.f;
     }
@@ -578,24 +593,117 @@ struct Terms {
   f16x4 hi, lo;
 };
 __device__ __forceinline__ Terms t_terms(f32x4 x) {
-  const u32x2 hi = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}, lo = {rest_pair(x[0], x[1], hi[0]), rest_pair(x[2], x[3], hi[1])};
+  const u32x2 hi = {pair_f16(x[0], x[1]), pair_f16(x[2], x[3])}, lo = {rest_up(x[0], x[1], hi[0]), rest_up(x[2], x[3], hi[1])};
   return Terms{__builtin_bit_cast(f16x4, hi), __builtin_bit_cast(f16x4, lo)};
 }
 
-// The power of two that holds one value channel's state and what is to be learnt in fp16's range: S' = S 2^ex. The larger of
-// both is kept in [1, 16) before products: fp16's least step, 2^-24, is then nothing beside it, and what 64 tokens learn stays
-// below fp16's largest number, 2^16: |b v' - h K' S'| is at most 2^7.6, and no stable rule makes more than 64 times that of it.
+// Powers of two that hold one value channel in fp16's range: the state S' = S 2^s, what is to be learnt X' = X 2^x. X' is
+// kept in [1/2, 16) before the keys' products (|X'| is then at most 2^7.6, and no stable rule makes more than 64 times that of it: below
+// fp16's largest number, 2^16), and so is S' where that leaves it at least 2^-9: else it has a power of its own.
+struct Ranges {
+  int s, x;
+};
+// state: exponent of the largest |S'| at 2^now; learnt: of the largest X. kNoExponent or less: none.
+__device__ __forceinline__ Ranges ranges_of(int now, int state, int learnt) {
+  constexpr int kNone = kNoExponent / 2, kMost = 120, kTop = 3;
+  Ranges r = {now, now};
+  if (learnt > kNone && (learnt + now > 4 || learnt + now < 0)) r.x = min(max(kTop - learnt, -kMost), kMost);
+  const int there = state + r.x - now;
+  r.s = state > kNone && (there > 4 || there < -8) ? min(max(now + kTop - state, -kMost), kMost) : r.x;
+  // What is this far below the other is nothing beside it, or is found too small (fades).
+  r.x = min(r.x, r.s + 60);
+  r.s = min(r.s, r.x + 100);
+  return r;
+}
+// Whether both may stay where they are (a plain sight: some that may stay are not seen).
+__device__ __forceinline__ bool stays(int now, int state, int learnt) { return (unsigned)(learnt + now) <= 4u && (unsigned)(state + 8) <= 12u; }
+// A channel's powers of two.
 struct Scale {
-  int ex;
-  float v;         // 2^ex
-  f32x4 out;       // 2^-ex of the channels 4g + i, for tiles that hold channels as rows
+  int ex;          // of the state
+  int apart;       // X's less the state's; the state takes X's with the chunk
+  float v;         // X's
+  f32x4 out;       // its inverse, of the channels 4g + i, for tiles that hold channels as rows
   __device__ __forceinline__ void set(int lane, int to) {
-    ex = to;
     v = ldexp2(1.f, to);
     const float back = ldexp2(1.f, -to);
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[i] = __shfl(back, 4 * (lane >> 4) + i);
   }
 };
+
+// What a token's output and state are made of: of the state before the chunk and of what it and those before it learn, each as far as
+// it has decayed, the largest, L_t = max(e^{g_t} L_{t-1}, |X'_t|). Beside the share of 2^-22 of itself that a term may be off, T and what is to be
+// learnt may be off by 2^-37 and P by 2^-32, wherever the range's top (2^4) stands: where every L_t is at least kLeastShare, a token's state is
+// within 2^-16 of L_t (at the range's top 2^-22), and its output within 2^-11, or 2^-13 in fp16. A chunk in which some L_t is less (a large
+// value behind small ones, small ones behind a large one that was forgotten) is walked token by token.
+template <bool kF16In>
+constexpr float kLeastShare = kF16In ? 0x1p-15f : 0x1p-17f;
+
+// The plan read again from the kernel's arguments, for what is rare: with one copy of it for all the walk spills scalars (2 %).
+__device__ __forceinline__ const DeltaPlan& plan_again() {
+  typedef const __attribute__((address_space(4))) DeltaPlan* Arguments;
+  Arguments arguments = (Arguments)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(arguments));
+  return *(const DeltaPlan*)arguments;
+}
+// The decays of tokens `first` to first + 3, of which `count` are the chunk's, as the chunks count them.
+__device__ __forceinline__ f32x4 decays_at(const DeltaPlan& p, int64_t first, int count, int h) {
+  f32x4 d = {1.f, 1.f, 1.f, 1.f};
+  if (!p.g || count <= 0) return d;
+  uint32_t bits[4];
+  const int64_t at = p.g_per_token ? first * p.H + h : h, step = p.g_per_token ? p.H : 0;
+  if (p.g_bf16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bits[i] = (uint32_t)reinterpret_cast<const uint16_t*>(p.g)[at + min(i, count - 1) * step] << 16;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bits[i] = reinterpret_cast<const uint32_t*>(p.g)[at + min(i, count - 1) * step];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float g = __uint_as_float(bits[i]);
+    if (i < count && g <= 0.f) d[i] = __expf(fmaxf(g, kMinLogDecay));
+  }
+  return d;
+}
+// L over a run of four tokens: out = max(in * all, own).
+struct Fading {
+  f32x4 decay, x;
+  float all, own;
+  __device__ __forceinline__ void set(f32x4 decays, f32x4 of) {
+    decay = decays;
+    all = 1.f, own = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = of[i] == of[i] ? fabsf(of[i]) : INFINITY;  // not finite: not to be found too small
+      all *= decay[i];
+      own = fmaxf(own * decay[i], x[i]);
+    }
+  }
+  // The four runs of 16 tokens follow each other in the lanes of a channel: L before this lane's, and, in `through`, behind the last.
+  __device__ __forceinline__ float before(float& through, int lane) const {
+    float mine = 0.f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float a = __shfl(all, (lane & 15) + 16 * g), o = __shfl(own, (lane & 15) + 16 * g);
+      if (lane >> 4 == g) mine = through;
+      through = fmaxf(through * a, o);
+    }
+    return mine;
+  }
+  // Whether some L is too small. (Where nothing at all is left the chunk's products are zeros too.)
+  __device__ __forceinline__ bool fades(float L, float least) const {
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      L = fmaxf(L * decay[i], x[i]);
+      found = found || (L > 0.f && L < least);
+    }
+    return found;
+  }
+};
+// A lower bound of L before the chunk, and whether the state alone holds L up to the chunk's end.
+__device__ __forceinline__ float state_share(int state, int apart) { return state > kNoExponent / 2 ? ldexp2(0.5f, state + apart) : 0.f; }
+__device__ __forceinline__ bool state_lasts(int state, int apart, float total) { return state + apart + exponent(total) >= -12; }  // 2^-14
 
 }  // namespace kda

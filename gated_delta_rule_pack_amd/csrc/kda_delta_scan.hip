@@ -125,8 +125,7 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
   far_blocks(sh.blocks, lane, wave, put_t);
 }
 
-constexpr int kBadTop = 1 << 20;  // exponent that stands for a value that is not finite
-
+constexpr int kBadTop = 1 << 14;  // exponent that stands for a value that is not finite
 template <int K>
 struct ScanShared {
   static constexpr int KB = K / 32;
@@ -138,9 +137,14 @@ struct ScanShared {
   alignas(16) char v[2][kC * 32];    // V of this chunk and of the next, 16 channels
   alignas(16) float factors[2][3][kC];  // b, h and c of both
   alignas(16) uint32_t numbers[2][4];   // total, steps, reach
-  alignas(16) int top[16][4];        // largest exponent of a channel, by wave
+  alignas(16) int top[16][4];        // largest exponents of a channel, of its state and of what is to be learnt, by wave
   alignas(16) int bad[16][4];        // its first token whose value is not finite
+  alignas(16) uint32_t small[2][4];  // whether a wave found what is to be learnt too small: at first sight; looked into
   alignas(16) float sum[2][4][16];
+  // For a chunk that is walked token by token.
+  alignas(16) float run[2][4][16];   // what a wave's tokens leave of L before them, and their own L
+  alignas(16) float token[4][kC];    // b, s and f, and the decays
+  alignas(16) char q[kC * kRowBytes<K>];
 };
 
 // A wave's share of a chunk on its way from memory, in the same registers for both kinds of wave.
@@ -197,7 +201,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       }
     }
   }
-  const auto store_state = [&]() {
+  const auto store_state = [&]() __attribute__((always_inline)) {
     if (!chain || slots.to < 0) return;
     const int64_t plane = plane_at(p, slots.to, h);
 #pragma unroll
@@ -274,14 +278,14 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 
   const int chunks = (len + kC - 1) / kC, place = chunk_place(p, n);
   const int H_qk = p.H / p.group, hq = h / p.group;
-  const auto whole = [](const char* at, int bytes) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), (short)0, bytes, kBufWord3); };
+  const auto whole = [](const char* at, int bytes) __attribute__((always_inline)) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), (short)0, bytes, kBufWord3); };
   // Rows of V or the outputs, 16 channels: those behind the sequence's end are out of range.
-  const auto buffer = [&](const uint16_t* at, int64_t stride, int left) {
+  const auto buffer = [&](const uint16_t* at, int64_t stride, int left) __attribute__((always_inline)) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(at), (short)0, ((min(left, kC) - 1) * (int)stride + 16) * 2, kBufWord3);
   };
   constexpr int kAhead = 3;
   Fetch<K> fetched[kAhead];
-  const auto load = [](__amdgpu_buffer_rsrc_t r, int at, int uniform) { return __builtin_amdgcn_raw_buffer_load_b128(r, at, uniform, 0); };
+  const auto load = [](__amdgpu_buffer_rsrc_t r, int at, int uniform) __attribute__((always_inline)) { return __builtin_amdgcn_raw_buffer_load_b128(r, at, uniform, 0); };
   // Where the next chunk to be fetched lies. Behind the last chunk it is fetched again, without a branch, so that a wait can count
   // the loads behind its own.
   const char* next_record = p.records + ((int64_t)place * p.H + h) * kDeltaRecord;
@@ -293,23 +297,23 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   // The last fragment of a row of tiles: with one tile (half_fragment) a lane has 8 bytes of it, and reads 16; what is its neighbour's goes.
   const int last_unit = w & 1 ? 16 : 8;
   const uint32_t keep = w & 1 ? ~0u : 0u;
-  const auto operand = [&](u32x4 x, int b) {
+  const auto operand = [&](u32x4 x, int b) __attribute__((always_inline)) {
     if (b == w >> 1) x[2] &= keep, x[3] &= keep;
     return __builtin_bit_cast(f16x8, x);
   };
-  const auto rest_operand = [&](u32x4 x, int b) { return p_rest_operand(u32x2{x[0], b == w >> 1 ? x[1] & keep : x[1]}); };
-  const auto advance = [&]() {
+  const auto rest_operand = [&](u32x4 x, int b) __attribute__((always_inline)) { return p_rest_operand(u32x2{x[0], b == w >> 1 ? x[1] & keep : x[1]}); };
+  const auto advance = [&]() __attribute__((always_inline)) {
     const bool more = next_left > kC;
     next_record += more ? (int64_t)p.H * kDeltaRecord : 0;
     next_rows += more ? (int64_t)H_qk * (kC * K * 2) : 0;
     next_left -= more ? kC : 0;
   };
-  const auto fetch_rows = [&](Fetch<K>& f) {
+  const auto fetch_rows = [&](Fetch<K>& f) __attribute__((always_inline)) {
     const __amdgpu_buffer_rsrc_t row = whole(next_rows, kC * K * 2);
 #pragma unroll
     for (int m = 0; m < KB; ++m) f.rows[m] = load(row, at16 + m * 1024, w * (KB * 1024));
   };
-  const auto fetch_record = [&](Fetch<K>& f, auto for_chain) {
+  const auto fetch_record = [&](Fetch<K>& f, auto for_chain) __attribute__((always_inline)) {
     const __amdgpu_buffer_rsrc_t rec = whole(next_record, kDeltaRecord);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {  // the first two rows of tiles have one fragment
@@ -329,23 +333,23 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   };
   // V of one chunk, by the outputs' waves: token 16 w + l / 2, channels 8 (l % 2) on, twice. (All of a row's offset is the
   // lane's: the uniform one is not compared with the buffer's end.)
-  const auto fetch_v = [&]() {
+  const auto fetch_v = [&]() __attribute__((always_inline)) {
     const int v_row = (int)p.v_t * 2;
     return load(buffer(next_v, p.v_t, left_v), (16 * w + ((lane & 31) >> 1)) * v_row + (lane & 1) * 16, 0);
   };
-  const auto advance_v = [&]() {
+  const auto advance_v = [&]() __attribute__((always_inline)) {
     const bool more = left_v > kC;
     next_v += more ? p.v_t * kC : 0;
     next_factors += more ? (int64_t)p.H * kDeltaRecord : 0;
     left_v -= more ? kC : 0;
   };
-  const auto put_v = [&](u32x4 x, int i) { *reinterpret_cast<u32x4*>(sh.v[i & 1] + 16 * w * 32 + (lane & 31) * 16) = x; };
+  const auto put_v = [&](u32x4 x, int i) __attribute__((always_inline)) { *reinterpret_cast<u32x4*>(sh.v[i & 1] + 16 * w * 32 + (lane & 31) * 16) = x; };
   // The factors that the chain takes: b, h and c of tokens 16 w + l % 16 in 48 lanes, the chunk's numbers behind them.
   static_assert(offsetof(Factors, b) == 0 && offsetof(Factors, h) == 4 * kC && offsetof(Factors, c) == 8 * kC &&
                 offsetof(Factors, steps) == offsetof(Factors, total) + 4 && offsetof(Factors, reach) == offsetof(Factors, total) + 8, "as they are fetched");
   const int number = min(lane - 48, 2), at_factor = lane < 48 ? 4 * kC * g4 + 64 * w + 4 * l16 : (int)offsetof(Factors, total) + 4 * number;
-  const auto fetch_factor = [&]() { return __builtin_amdgcn_raw_buffer_load_b32(whole(next_factors, kDeltaRecord), at_factor, kRecFactors, 0); };
-  const auto put_factor = [&](uint32_t x, int i) {
+  const auto fetch_factor = [&]() __attribute__((always_inline)) { return __builtin_amdgcn_raw_buffer_load_b32(whole(next_factors, kDeltaRecord), at_factor, kRecFactors, 0); };
+  const auto put_factor = [&](uint32_t x, int i) __attribute__((always_inline)) {
     if (lane < 48) sh.factors[i & 1][g4][16 * w + l16] = __uint_as_float(x);
     else if (w == 0) sh.numbers[i & 1][number] = x;
   };
@@ -353,52 +357,99 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     f32x4 b, h, c;  // of tokens 16 w + 4g + i
     uint32_t total, steps, reach;
   };
-  const auto read_factors = [&](int i) {
-    const auto of = [&](int j) { return *reinterpret_cast<const f32x4*>(&sh.factors[i & 1][j][16 * w + 4 * g4]); };
+  const auto read_factors = [&](int i) __attribute__((always_inline)) {
+    const auto of = [&](int j) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4*>(&sh.factors[i & 1][j][16 * w + 4 * g4]); };
     const u32x4 n = *reinterpret_cast<const u32x4*>(sh.numbers[i & 1]);
     return OwnFactors{of(0), of(1), of(2), n[0], n[1], n[2]};
   };
   // Tokens 16 w + 4g + i of channel l % 16.
-  const auto read_v = [&](int i) {
+  const auto read_v = [&](int i) __attribute__((always_inline)) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sh.v[i & 1] + (16 * w + 4 * g4 + (l16 >> 2)) * 32 + (lane & 3) * 8));
   };
   Scale scale;
+  scale.ex = scale.apart = 0;
   scale.set(lane, 0);
   typedef int i32x4 __attribute__((ext_vector_type(4)));
-  const auto largest = [&](const int (&of)[16][4]) {
-    const i32x4 t = *reinterpret_cast<const i32x4*>(of[l16]);
-    return max(max(t[0], t[1]), max(t[2], t[3]));
+  const auto largest = [&]() __attribute__((always_inline)) {
+    const i32x4 t = *reinterpret_cast<const i32x4*>(sh.top[l16]);
+    return __builtin_bit_cast(i16x2, pair_max(pair_max(t[0], t[1]), pair_max(t[2], t[3])));
   };
-  const auto least = [&](const int (&of)[16][4]) {
-    const i32x4 t = *reinterpret_cast<const i32x4*>(of[l16]);
+  const auto least_bad = [&]() __attribute__((always_inline)) {
+    const i32x4 t = *reinterpret_cast<const i32x4*>(sh.bad[l16]);
     return min(min(t[0], t[1]), min(t[2], t[3]));
   };
-  const auto outside = [](int e) { return e > 4 || (e < 1 && e > kNoExponent / 2); };
-  const auto rescaled = [&](int e) { return outside(e) ? min(max(scale.ex + 4 - e, -120), 120) - scale.ex : 0; };
-  const auto walk_chunks = [&](auto step) {
-    int i = 0;
-    for (; i + kAhead <= chunks; i += kAhead) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) step(fetched[a], i + a);
-    }
-#pragma unroll
-    for (int a = 0; a + 1 < kAhead; ++a)
-      if (i + a < chunks) step(fetched[a], i + a);
+  const auto any_small = [&](int i) __attribute__((always_inline)) {
+    const u32x4 t = *reinterpret_cast<const u32x4*>(sh.small[i]);
+    return __builtin_amdgcn_readfirstlane(t[0] | t[1] | t[2] | t[3]) != 0;
   };
-  // Both kinds of wave take the same barriers: three a chunk, and three more where a channel's scale has to move or a value
-  // is not finite, which all of them see in sh.top.
+  const auto moves = [&](i16x2 tops) __attribute__((always_inline)) { return !stays(scale.ex, tops[0], tops[1]); };
+  // Takes the ranges' powers; how far the state moves.
+  const auto move = [&](i16x2 tops) __attribute__((always_inline)) {
+    const Ranges r = ranges_of(scale.ex, tops[0], tops[1]);
+    const int by = r.s - scale.ex;
+    scale.ex = r.s;
+    scale.apart = r.x - r.s;
+    scale.set(lane, r.x);
+    return by;
+  };
+  const auto walk_chunks = [&](auto step) __attribute__((always_inline)) {
+    static_assert(kAhead == 3, "as written out");
+    for (int i = 0;;) {
+      step(fetched[0], i);
+      if (++i >= chunks) break;
+      step(fetched[1], i);
+      if (++i >= chunks) break;
+      step(fetched[2], i);
+      if (++i >= chunks) break;
+    }
+  };
+  // Both kinds of wave take the same barriers: three a chunk; three more where a channel's scale has to move or a value
+  // is not finite, which all of them see in sh.top; and two more where what is to be learnt is small, which they see in sh.small, with four
+  // instead of the last where it is too small.
+  // A chunk token by token in fp32, by the chain's waves: K / 8 lanes to a channel, 8 keys to a lane. The state is in sh.s, [channel][K].
+  const auto by_tokens = [&](int i, int count, float total) __attribute__((always_inline)) {
+    constexpr int kLanes = K / 8;
+    const int channel = tid / kLanes, j = tid % kLanes;
+    if (channel >= 16) return;
+    float* const plain = reinterpret_cast<float*>(sh.s) + channel * K + 8 * j;
+    f32x4 a = *reinterpret_cast<const f32x4*>(plain), b = *reinterpret_cast<const f32x4*>(plain + 4);
+    const DeltaPlan& p = plan_again();
+    uint16_t* to = reinterpret_cast<uint16_t*>(p.out) + h * p.o_h + v0 + (begin + (int64_t)i * kC) * p.o_t + channel;
+    const auto row = [&](const char* tile, int t, f32x4& x, f32x4& y) __attribute__((always_inline)) {
+      const f16x8 r = *reinterpret_cast<const f16x8*>(tile + row_at<K>(t) + 16 * j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = (float)r[e], y[e] = (float)r[4 + e];
+    };
+    const auto dot = [&](f32x4 x, f32x4 y) __attribute__((always_inline)) {
+      x *= a, y *= b;
+      return lane_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((y[0] + y[1]) + (y[2] + y[3])), kLanes);
+    };
+#pragma unroll 1
+    for (int t = 0; t < count; ++t) {
+      f32x4 k0, k1, q0, q1;
+      row(sh.k, t, k0, k1);
+      row(sh.q, t, q0, q1);
+      const float decay = sh.token[3][t], v = token_value<kF16In>(*reinterpret_cast<const uint16_t*>(sh.v[i & 1] + t * 32 + channel * 2));
+      const float x = sh.token[0][t] * v - sh.token[1][t] * (decay * dot(k0, k1));
+      a = a * decay + k0 * x, b = b * decay + k1 * x;
+      const float o = sh.token[2][t] * kTimesP * dot(q0, q1);
+      if (j == 0) to[t * p.o_t] = kF16In ? __builtin_bit_cast(uint16_t, (_Float16)o) : __builtin_bit_cast(uint16_t, to_bf16(o));
+    }
+    if (total != total) a = b = zero4() + __builtin_nanf("");
+    *reinterpret_cast<f32x4*>(plain) = a, *reinterpret_cast<f32x4*>(plain + 4) = b;
+  };
   if (chain) {
     constexpr uint32_t kInf = kF16In ? 0x7c00u : 0x7f80u;
-    const auto put_state = [&]() {
+    const auto put_state = [&]() __attribute__((always_inline)) {
       if constexpr (KTW == 2) {
         const f16x8 hi = to_f16(S[0], S[1]);
         *reinterpret_cast<f16x8*>(sh.s[w][0] + lane * 16) = hi;
         *reinterpret_cast<f16x8*>(sh.s[w][1] + lane * 16) = rest_f16(S[0], S[1], hi);
       } else {
-        put_half(sh.s[w >> 1][0], sh.s[w >> 1][1], lane * 16 + (w & 1) * 8, S[0]);
+        put_half<false>(sh.s[w >> 1][0], sh.s[w >> 1][1], lane * 16 + (w & 1) * 8, S[0]);
       }
     };
-    const auto state_top = [&]() {
+    const auto state_top = [&]() __attribute__((always_inline)) {
       float m = 0.f;
 #pragma unroll
       for (int kt = 0; kt < KTW; ++kt)
@@ -411,21 +462,24 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     barrier_lds();  // the first chunk's V and factors
     s16x4 values = read_v(0);
     OwnFactors own = read_factors(0);
-    const auto step = [&](Fetch<K>& f, int i) {
+    const auto step = [&](Fetch<K>& f, int i) __attribute__((always_inline)) {
       const int steps = (int)__builtin_amdgcn_readfirstlane(own.steps), reach = max((int)__builtin_amdgcn_readfirstlane(own.reach), 0);
       const float total = __uint_as_float(__builtin_amdgcn_readfirstlane(own.total));
-      // The state's fragments and the channel's largest exponent.
+      // The state's fragments and the channel's largest exponents.
       put_state();
       uint32_t value[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) value[e] = (uint16_t)values[e];
       uint32_t most = max(max(value[0] & 0x7fffu, value[1] & 0x7fffu), max(value[2] & 0x7fffu, value[3] & 0x7fffu));
-      int top = max(state_top() + reach, exponent(token_value<kF16In>(most)) + steps + scale.ex);
-      sh.top[l16][w] = channel_max(most >= kInf ? kBadTop : top);
+      const auto tops_of = [&](uint32_t most) __attribute__((always_inline)) {
+        const int state = state_top(), learnt = max(state - scale.ex + reach, exponent(token_value<kF16In>(most)) + steps);
+        return __builtin_bit_cast(int, channel_max(i16x2{(short)state, (short)(most >= kInf ? kBadTop : learnt)}));
+      };
+      sh.top[l16][w] = tops_of(most);
       barrier_lds();
       f16x8 hi[KB], lo[KB];
-      const int tops = largest(sh.top);
-      const auto read_state = [&]() {
+      i16x2 tops = largest();
+      const auto read_state = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int m = 0; m < KB; ++m) {
           hi[m] = *reinterpret_cast<const f16x8*>(sh.s[m][0] + at16);
@@ -435,7 +489,9 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       read_state();
       __builtin_amdgcn_sched_barrier(0);  // all reads before the first wait
       int first_bad = kC;
-      if (__ballot(outside(tops))) {
+      scale.apart = 0;
+      float by_apart = 1.f;
+      if (__builtin_expect(__ballot(moves(tops)) != 0, 0)) {
         barrier_lds();
         int bad = kC;
         most = 0;
@@ -444,12 +500,14 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           if ((value[x] & 0x7fffu) >= kInf) bad = 16 * w + 4 * g4 + x, value[x] = 0;
           most = max(most, value[x] & 0x7fffu);
         }
-        sh.top[l16][w] = channel_max(max(state_top() + reach, exponent(token_value<kF16In>(most)) + steps + scale.ex));
+        sh.top[l16][w] = tops_of(most);
         sh.bad[l16][w] = -channel_max(-bad);
         barrier_lds();
-        first_bad = least(sh.bad);
-        const int by = rescaled(largest(sh.top));
-        scale.set(lane, scale.ex + by);
+        first_bad = least_bad();
+        tops = largest();
+        const int by = move(tops);
+        tops[0] += by;
+        by_apart = ldexp2(1.f, scale.apart);
 #pragma unroll
         for (int kt = 0; kt < KTW; ++kt)
 #pragma unroll
@@ -471,12 +529,17 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
         for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(k_rows + m * 64) = f.rows[m];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(value[e]) * (own.b[e] * scale.v) - own.h[e] * (a[e] + b[e]);
-        put_half(sh.x[w >> 1][0], sh.x[w >> 1][1], at16 + (w & 1) * 8, x);
+        for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(value[e]) * (own.b[e] * scale.v) - own.h[e] * ((a[e] + b[e]) * by_apart);
+        const float least = fminf(fminf(fabsf(x[0]), fabsf(x[1])), fminf(fabsf(x[2]), fabsf(x[3])));
+        const uint32_t small = __ballot(least < kLeastShare<kF16In> && !state_lasts(tops[0], scale.apart, total)) != 0;
+        if (lane == 0) sh.small[0][w] = small;
+        put_half<true>(sh.x[w >> 1][0], sh.x[w >> 1][1], at16 + (w & 1) * 8, x);
       }
       barrier_lds();
       f16x8 kk[2][KTW];
+      bool found_small;
       {
+        const u32x4 smalls = *reinterpret_cast<const u32x4*>(sh.small[0]);
         f16x8 xh[2], xl[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -497,12 +560,50 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           b = mfma(u1, xh[1], b);
           c = mfma(u0, xl[1], c);
         }
-        f32x4 d = a + (b + c), decayed = d * own.c;
-        put_half(sh.d[w >> 1][0], sh.d[w >> 1][1], at16 + (w & 1) * 8, decayed);
-        put_half_up(sh.dh[w >> 1][0], sh.dh[w >> 1][1], at16 + (w & 1) * 8, d);
-#pragma unroll
-        for (int kt = 0; kt < KTW; ++kt) S[kt] *= total;
+        f32x4 d = a + (b + c) * kDown, decayed = d * own.c;
+        put_half<true>(sh.d[w >> 1][0], sh.d[w >> 1][1], at16 + (w & 1) * 8, decayed);
+        put_half<true>(sh.dh[w >> 1][0], sh.dh[w >> 1][1], at16 + (w & 1) * 8, d);
+        found_small = __builtin_amdgcn_readfirstlane(smalls[0] | smalls[1] | smalls[2] | smalls[3]) != 0;
       }
+      if (__builtin_expect(found_small, 0)) {
+        Fading own_run;
+        const int count = min(len - i * kC, kC), t = 16 * w + 4 * g4;
+        own_run.set(decays_at(plan_again(), begin + (int64_t)i * kC + t, count - t, h), x);
+        float through = 0.f, all = own_run.all;
+        own_run.before(through, lane);
+        all *= __shfl_xor(all, 16), all *= __shfl_xor(all, 32);
+        if (lane < 16) sh.run[0][w][lane] = all, sh.run[1][w][lane] = through;
+        barrier_lds();
+        through = state_share(tops[0], scale.apart);
+        for (int j = 0; j < w; ++j) through = fmaxf(through * sh.run[0][j][l16], sh.run[1][j][l16]);
+        const float before = own_run.before(through, lane);
+        const uint32_t found = __ballot(own_run.fades(before, kLeastShare<kF16In>)) != 0;
+        if (lane == 0) sh.small[1][w] = found;
+        barrier_lds();
+        if (any_small(1)) {
+          float* const plain = reinterpret_cast<float*>(sh.s);  // the state, [channel][K]
+#pragma unroll
+          for (int kt = 0; kt < KTW; ++kt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) plain[l16 * K + k0 + 4 * kt + e] = ldexp2(S[kt][e], -scale.ex);
+          scale.ex = scale.apart = 0;
+          scale.set(lane, 0);
+          barrier_lds();
+          by_tokens(i, count, total);
+          barrier_lds();
+#pragma unroll
+          for (int kt = 0; kt < KTW; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(plain + l16 * K + k0 + 4 * kt);
+          values = read_v(i + 1);
+          own = read_factors(i + 1);
+          fetch_record(f, std::true_type());
+          advance();
+          barrier_lds();
+          return;
+        }
+      }
+#pragma unroll
+      for (int kt = 0; kt < KTW; ++kt) S[kt] *= ldexp2(total, 12 + scale.apart);
+      scale.ex += scale.apart;
       barrier_lds();
       {
         f16x8 dh[2], dl[2];
@@ -517,14 +618,15 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         advance();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int kt = 0; kt < KTW; ++kt) {
-            S[kt] = mfma(kk[s][kt], dl[s], S[kt]);
-          }
+          for (int kt = 0; kt < KTW; ++kt) S[kt] = mfma(kk[s][kt], dl[s], S[kt]);
+#pragma unroll
+        for (int kt = 0; kt < KTW; ++kt) S[kt] *= kDown;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int kt = 0; kt < KTW; ++kt) S[kt] = mfma(kk[s][kt], dh[s], S[kt]);
-        }
       }
       if (first_bad < kC)
 #pragma unroll
@@ -548,14 +650,19 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     put_v(fetch_v(), 0);
     put_factor(fetch_factor(), 0);
     advance_v();
-    const auto step = [&](Fetch<K>& f, int i) {
+    const auto step = [&](Fetch<K>& f, int i) __attribute__((always_inline)) {
       barrier_lds();
       int first_bad = kC;
-      if (__ballot(outside(largest(sh.top)))) {
+      scale.apart = 0;
+      f32x4 by_apart = zero4() + 1.f;
+      if (__builtin_expect(__ballot(moves(largest())) != 0, 0)) {
         barrier_lds();
         barrier_lds();
-        first_bad = least(sh.bad);
-        scale.set(lane, scale.ex + rescaled(largest(sh.top)));
+        first_bad = least_bad();
+        move(largest());
+        const float by = ldexp2(1.f, scale.apart);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) by_apart[e] = __shfl(by, 4 * g4 + e);
         barrier_lds();
       }
       put_v(f.v, i + 1);
@@ -568,8 +675,37 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), q, o);
         o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), q, o);
       }
-      o *= f.e;
+      o *= f.e * by_apart;
+      const auto fetch_next = [&]() __attribute__((always_inline)) {
+        fetch_rows(f);
+        fetch_record(f, std::false_type());
+        advance();
+        f.v = fetch_v();
+        f.factor = fetch_factor();
+        advance_v();
+      };
       barrier_lds();
+      if (__builtin_expect(any_small(0), 0)) {
+        barrier_lds();
+        barrier_lds();
+        if (any_small(1)) {
+          scale.ex = scale.apart = 0;
+          scale.set(lane, 0);
+          // The rows of Q' and the tokens' factors, for the chain's waves.
+#pragma unroll
+          for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(sh.q + 16 * w * kRowBytes<K> + row_at<K>(l16) + g4 * 16 + m * 64) = f.rows[m];
+          const DeltaPlan& p = plan_again();
+          const Factors& fa = *reinterpret_cast<const Factors*>(p.records + (((int64_t)place + i) * p.H + h) * kDeltaRecord + kRecFactors);
+          sh.token[w][lane] = w == 3 ? decays_at(p, begin + (int64_t)i * kC + lane, min(len - i * kC - lane, 1), h)[0]
+                                     : (w == 0 ? fa.b : w == 1 ? fa.s : fa.f)[lane];
+          barrier_lds();
+          fetch_next();
+          barrier_lds();
+          barrier_lds();
+          return;
+        }
+      }
+      scale.ex += scale.apart;
       barrier_lds();
       f32x4 rest = zero4();
 #pragma unroll
@@ -588,12 +724,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         for (int e = 0; e < 4; ++e)
           if (16 * w + l16 >= __shfl(first_bad, 4 * g4 + e)) o[e] = __builtin_nanf("");
       }
-      fetch_rows(f);
-      fetch_record(f, std::false_type());
-      advance();
-      f.v = fetch_v();
-      f.factor = fetch_factor();
-      advance_v();
+      fetch_next();
       u32x2 packed;
       if constexpr (kF16In) packed = __builtin_bit_cast(u32x2, f16x4{(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]});
       else packed = __builtin_bit_cast(u32x2, bf16x4{to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])});

@@ -111,3 +111,129 @@ def test_tiny_steps_beside_a_state(step, size, path):
         token_off = np.repeat(state_off + 4 * (E2 + EP) * M, case.lengths, axis=0)[:, :, None]
         close("out", f64(out), o, 2.0 ** -8 * np.abs(o) + 1.01 * case.scale * token_off)
         close("state", f64(final), S, 2.0 ** -24 * np.abs(S) + 1.01 * state_off[:, :, None, None])
+
+
+# ------------------------------------------------------------------------------ sizes far apart in one sequence
+# L_t of a channel: the largest of what its token t is made of, each as far as it has decayed, max(e^{g_t} L_{t-1}, |beta_t v_t|), from
+# the largest element of its initial state on. The kernels keep every term within EL = 2^-16 of L_t, however large a value stands
+# elsewhere in the chunk, so the harness's bounds hold with EL and L_t in place of e2 and M.
+EL = 2.0 ** -16
+
+
+def _check_reach(case, d, out, final, rows=slice(None)):
+    o, S, _ = case.oracle()
+    v, beta = np.abs(f64(case.v)) * np.abs(f64(case.beta))[:, :, None], f64(case.beta)
+    decay = np.ones((case.T, case.H)) if case.g is None else np.exp(np.broadcast_to(f64(case.g), (case.T, case.H)))
+    start = case.start()
+    L, end, n = np.zeros_like(o), np.zeros((case.N, case.H, case.V)), np.zeros((case.T, 1, 1))
+    for i in range(case.N):
+        l = np.zeros((case.H, case.V)) if start is None else np.abs(start[i]).max(-1)
+        for t in range(int(case.cu[i]), int(case.cu[i + 1])):
+            l = np.maximum(decay[t][:, None] * l, v[t])
+            L[t], n[t] = l, t - int(case.cu[i]) + 1
+        end[i] = l
+    u = HALF[case.dtype]
+    room = u * np.abs(o) + (1 + u) * case.scale * case.query_size() * (4 * EL * (1 + np.sqrt(n)) + 4 * EP) * L + TINY[case.dtype]
+    got = f64(out)
+    close("out", got[rows], o[rows], room[rows])
+    if case.state != "none":
+        got = case.finals(d, final)
+        sdt = d["cache"].dtype if case.state == "paged" else final.dtype
+        m = np.array(case.lengths, np.float64)[:, None, None]
+        close("state", got, S, HALF[sdt] * np.abs(S) + (1 + HALF[sdt]) * (4 * EL * (1 + np.sqrt(m)) * end)[..., None] + 1e-37)
+
+
+@PATHS
+@pytest.mark.parametrize("dtype,small,large", [("bf16", 0.1, 1e8), ("bf16", 1e-10, 1e10), ("bf16", 1.0, 1e4), ("f16", 1e-3, 6e4), ("f16", 1e-2, 6e4),
+                                               ("f16", 1.0, 300.0)])
+@pytest.mark.parametrize("where", [(1, None), (40, None), (40, 5), (63, 77), (70, None)])
+@pytest.mark.parametrize("state", ["none", "dense"])
+def test_a_large_value_behind_small_ones(state, where, dtype, small, large, path):
+    """One token, of all channels or of one, far above those before it: they keep their own accuracy, and so does all else."""
+    case = DeltaCase([150, 70], 2, seed=44, state=state, dtype=dtype, V=128 if where[1] is None else 64, K=64 if where[0] == 63 else 128)
+    case.v = (case.v.float() * small / 4).clamp(-small, small).to(case.dtype)
+    if state == "dense":
+        case.initial *= small
+    at, channel = where
+    if channel is None:
+        case.v[at] = (large * torch.sign(case.v[at].float())).to(case.dtype)
+    else:
+        case.v[at, :, channel % case.V] = large
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
+
+
+@PATHS
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 20, 2.0 ** 60])
+@pytest.mark.parametrize("at", [0, 1, 31, 63, 64, 100])
+@pytest.mark.parametrize("reset", [-float("inf"), -90.0, -18.0])
+def test_a_large_state_that_is_forgotten(reset, at, size, path):
+    case = DeltaCase([150, 30, 64], 2, seed=45, state="dense", decay="none")
+    case.initial *= size
+    case.g = torch.full((case.T, 2), -0.01)
+    case.g[[at, 150 + min(at, 29), 180 + min(at, 63)]] = reset
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
+
+
+@PATHS
+@pytest.mark.parametrize("step", [2.0 ** -14, 2.0 ** -20, 2.0 ** -27, 2.0 ** -60])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("state", ["none", "dense"])
+def test_small_steps_behind_a_reset(state, dtype, step, path):
+    """Step sizes near 1, everything forgotten, then small ones alone: nothing larger is left to hide what they teach."""
+    case = DeltaCase([150, 60, 64], 2, seed=46, state=state, dtype=dtype)
+    for begin, at in ((0, 20), (0, 90), (150, 5), (210, 50)):
+        case.g[begin + at] = -float("inf")
+    for a, b in ((20, 64), (90, 150), (155, 210), (260, 274)):
+        case.beta[a:b] *= step
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
+
+
+@PATHS
+@pytest.mark.parametrize("decay", [-0.1, -1.0, -3.0, -8.0])
+def test_large_values_that_decay_to_the_size_of_later_ones(decay, path):
+    case = DeltaCase([200, 64, 3], 2, seed=47, state="dense", decay="none")
+    case.g = torch.full((case.T, 2), decay)
+    for t in (3, 70, 128, 210):
+        case.v[t] *= 1e7
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
+
+
+@PATHS
+def test_masked_tokens_keep_what_is_left(path):
+    """Values and step sizes of zero for most of a sequence, while the state decays: what is left keeps its accuracy."""
+    case = DeltaCase([200, 100, 40], 2, seed=48, state="dense", decay="none")
+    case.g = torch.full((case.T, 2), -0.3)
+    case.beta[10:150] = 0
+    case.v[205:290] = 0
+    case.v[300:] = 0
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
+
+
+@PATHS
+@pytest.mark.parametrize("kw", [dict(), dict(decay="resets", flags="all"), dict(K=64, V=64, dtype="f16"), dict(unit=True, H=4, H_qk=2), dict(state="none")], ids=str)
+def test_channels_of_all_sizes_and_times(kw, path):
+    """Every value with a size of its own, from 2^-30 to 2^30 (2^-10 to 2^10 in fp16), in order and out of it."""
+    kw = {**dict(H=2), **kw}
+    case = DeltaCase([130, 64, 257, 1, 2], seed=49, **kw)
+    gen = torch.Generator().manual_seed(8)
+    span = 10 if case.dtype == torch.float16 else 30
+    case.v = (case.v.float() * 2.0 ** torch.randint(-span, span + 1, case.v.shape, generator=gen).float()).to(case.dtype)
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
