@@ -529,10 +529,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     rq.put(slot.q, sh.info[1], tid);
     barrier_lds();
     const int l = local_copy(lane);
-    if (w == kNumbersWave) {
-      slot.decay[l] = decays.own;
-      put_chunk(sh.making, slot.factors, p, decays, sh.info[0][l], sh.info[1][l], bits_value(beta_next, p.beta_bf16), l);
-    }
+    Numbers numbers;
+    if (w == kNumbersWave) numbers.put_steps(sh.making, p, decays, sh.info[0][l], sh.info[1][l], bits_value(beta_next, p.beta_bf16), l);
     TileProducts products;
     by_wave(w, [&](auto W) { tile_products<K, decltype(W)::value>(slot.k, slot.q, l, products); });
     if constexpr (kNext) fetch(i + 1);
@@ -543,6 +541,10 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
         put_rest(slot.p + kTermP, l, tt, st, rest);
       });
     });
+    if (w == kNumbersWave) {
+      numbers.put_factors(slot.factors, p, decays, l);
+      slot.decay[l] = decays.own;
+    }
     {
       // The outputs of chunk i - 2; for the first two a buffer of no rows.
       const __amdgpu_buffer_rsrc_t to = i < 2 ? __builtin_amdgcn_make_buffer_rsrc(out, (short)0, 0, kBufWord3)
@@ -551,7 +553,6 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     }
     barrier_lds();
     if (w == 0) invert_diagonal(sh.blocks, l);
-    if (kNext && w == kNumbersWave) make_decays();
     if (kNext && w != 0) scale_rows();  // the first wave's in the next two parts, in which it has none
     barrier_lds();
     const auto put_t = [&](int tt, int st, f32x4 x) {
@@ -563,6 +564,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void delta_walk(const DeltaPlan p)
     rv.put(slot.v, tid);
     if constexpr (kNext) fetch_v(i + 1);
     if (kNext && w == 0) rk.scale();
+    if (kNext && w == kNumbersWave) make_decays();
     barrier_lds();
     far_blocks(sh.blocks, l, w, put_t);
     if (kNext && w == 0) rq.scale();

@@ -341,43 +341,58 @@ __device__ __forceinline__ Decays put_decays(Making& mk, float g, int lane) {
   mk.rest[lane] = (float)(G - (double)(float)G);
   return d;
 }
-__device__ __forceinline__ void put_chunk(Making& mk, Factors& to, const DeltaPlan& p, const Decays& d, RowInfo k, RowInfo q, float beta, int lane) {
-  const bool bad = k.e == kBadRow || !(fabsf(beta) < INFINITY);
-  const uint64_t all_bad = __ballot(bad) | d.bad;
-  const int first = all_bad ? __builtin_ctzll(all_bad) : kC;
-  if (all_bad >> lane & 1) beta = 0.f, k = RowInfo{0, 0.f};
-  if (k.squares == 0.f) beta = 0.f;  // nothing is learnt of a zero key, whatever its step size
-  float share, step, rq;
-  int longest = 0;
-  if (p.normalize) {
-    const float rk = rsqrtf(k.squares + ldexp2(kNormEps, -2 * k.e));
-    rq = p.scale * rsqrtf(q.squares + ldexp2(kNormEps, -2 * q.e));
-    share = beta * rk;
-    step = share * rk;
-  } else {
-    share = ldexp2(beta, k.e);
-    step = ldexp2(beta, 2 * k.e);
-    rq = ldexp2(p.scale, q.e);
-    const int top = wave_max(k.squares > 0.f ? k.e : -1000);
-    longest = top == -1000 ? 0 : top;
+// A token's part of the chunk's numbers, one lane for each token, in two steps: what the making of T waits for, and what the chain does.
+struct Numbers {
+  float share, step, rq, length, beta;
+  int long_by;      // the chunk's longest raw key, as a power of two
+  uint64_t all_bad;
+  bool bad_q;
+  __device__ __forceinline__ void put_steps(Making& mk, const DeltaPlan& p, const Decays& d, RowInfo k, RowInfo q, float of, int lane) {
+    beta = of;
+    const bool bad = k.e == kBadRow || !(fabsf(beta) < INFINITY);
+    all_bad = __ballot(bad) | d.bad;
+    bad_q = q.e == kBadRow;
+    if (all_bad >> lane & 1) beta = 0.f, k = RowInfo{0, 0.f};
+    if (k.squares == 0.f) beta = 0.f;  // nothing is learnt of a zero key, whatever its step size
+    length = k.squares;
+    if (p.normalize) {
+      const float rk = rsqrtf(k.squares + ldexp2(kNormEps, -2 * k.e));
+      rq = p.scale * rsqrtf(q.squares + ldexp2(kNormEps, -2 * q.e));
+      share = beta * rk;
+      step = share * rk;
+      long_by = 0;
+    } else {
+      share = ldexp2(beta, k.e);
+      step = ldexp2(beta, 2 * k.e);
+      rq = ldexp2(p.scale, q.e);
+      long_by = k.squares > 0.f ? k.e : -1000;
+    }
+    mk.step[lane] = step;
   }
-  // Step sizes that break |beta| |k|^2 <= 2 so far that the products' fp16 would: outputs and the final state are not finite.
-  const bool wide = __ballot(!(fabsf(ldexp2(beta, 2 * longest)) < 0x1p28f)) != 0;
-  const float h = step * d.e;
-  mk.step[lane] = step;
-  to.b[lane] = share;
-  to.h[lane] = h;
-  to.c[lane] = d.c;
-  to.e[lane] = d.e * kTimesP;
-  to.s[lane] = step;
-  to.f[lane] = wide || lane >= first || q.e == kBadRow ? __builtin_nanf("") : rq / kTimesP;
-  const int steps = wave_max(exponent(fabsf(share))), reach = wave_max(exponent(fabsf(h) * __builtin_amdgcn_sqrtf(k.squares)));
-  if (lane == 0) {
-    to.total = wide || all_bad ? __builtin_nanf("") : d.total;
-    to.steps = steps;
-    to.reach = reach;
+  __device__ __forceinline__ void put_factors(Factors& to, const DeltaPlan& p, const Decays& d, int lane) const {
+    int longest = 0;
+    if (!p.normalize) {
+      const int top = wave_max(long_by);
+      longest = top == -1000 ? 0 : top;
+    }
+    // Step sizes that break |beta| |k|^2 <= 2 so far that the products' fp16 would: outputs and the final state are not finite.
+    const bool wide = __ballot(!(fabsf(ldexp2(beta, 2 * longest)) < 0x1p28f)) != 0;
+    const int first = all_bad ? __builtin_ctzll(all_bad) : kC;
+    const float h = step * d.e;
+    to.b[lane] = share;
+    to.h[lane] = h;
+    to.c[lane] = d.c;
+    to.e[lane] = d.e * kTimesP;
+    to.s[lane] = step;
+    to.f[lane] = wide || lane >= first || bad_q ? __builtin_nanf("") : rq / kTimesP;
+    const int steps = wave_max(exponent(fabsf(share))), reach = wave_max(exponent(fabsf(h) * __builtin_amdgcn_sqrtf(length)));
+    if (lane == 0) {
+      to.total = wide || all_bad ? __builtin_nanf("") : d.total;
+      to.steps = steps;
+      to.reach = reach;
+    }
   }
-}
+};
 
 // A's ten causal 16 x 16 blocks in fp32, each as [s][t] with rows of 20 floats; T's take their places.
 constexpr int kBlockRow = 20, kBlock = 16 * kBlockRow;
@@ -598,8 +613,8 @@ __device__ __forceinline__ Terms t_terms(f32x4 x) {
 }
 
 // Powers of two that hold one value channel in fp16's range: the state S' = S 2^s, what is to be learnt X' = X 2^x. X' is
-// kept in [1/2, 16) before the keys' products (|X'| is then at most 2^7.6, and no stable rule makes more than 64 times that of it: below
-// fp16's largest number, 2^16), and so is S' where that leaves it at least 2^-9: else it has a power of its own.
+// kept in [1, 16) before the keys' products (|X'| is then at most 2^7.6, and no stable rule makes more than 64 times that of it: below
+// fp16's largest number, 2^16), and S' at the same power where that leaves it in [2^-9, 2^12): else it has a power of its own.
 struct Ranges {
   int s, x;
 };
@@ -607,16 +622,16 @@ struct Ranges {
 __device__ __forceinline__ Ranges ranges_of(int now, int state, int learnt) {
   constexpr int kNone = kNoExponent / 2, kMost = 120, kTop = 3;
   Ranges r = {now, now};
-  if (learnt > kNone && (learnt + now > 4 || learnt + now < 0)) r.x = min(max(kTop - learnt, -kMost), kMost);
+  if (learnt > kNone && (learnt + now > 4 || learnt + now < 1)) r.x = min(max(kTop - learnt, -kMost), kMost);
   const int there = state + r.x - now;
-  r.s = state > kNone && (there > 4 || there < -8) ? min(max(now + kTop - state, -kMost), kMost) : r.x;
+  r.s = state > kNone && (there > 12 || there < -8) ? min(max(now + kTop - state, -kMost), kMost) : r.x;
   // What is this far below the other is nothing beside it, or is found too small (fades).
   r.x = min(r.x, r.s + 60);
   r.s = min(r.s, r.x + 100);
   return r;
 }
 // Whether both may stay where they are (a plain sight: some that may stay are not seen).
-__device__ __forceinline__ bool stays(int now, int state, int learnt) { return (unsigned)(learnt + now) <= 4u && (unsigned)(state + 8) <= 12u; }
+__device__ __forceinline__ bool stays(int now, int state, int learnt) { return (unsigned)(learnt + now - 1) <= 3u && (unsigned)(state + 8) <= 20u; }
 // A channel's powers of two.
 struct Scale {
   int ex;          // of the state

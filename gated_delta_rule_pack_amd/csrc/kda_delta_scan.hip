@@ -98,7 +98,11 @@ __global__ __launch_bounds__(256, 3) void delta_prep(const DeltaPlan p) {
     store_fragments<K, kThreads>(sh.k, p.keys + at, tid);
     store_fragments<K, kThreads>(sh.q, p.queries + at, tid);
   }
-  if (wave == 0) put_chunk(sh.making, *reinterpret_cast<Factors*>(rec + kRecFactors), p, decays, sh.info[0][lane], sh.info[1][lane], beta, lane);
+  if (wave == 0) {
+    Numbers numbers;
+    numbers.put_steps(sh.making, p, decays, sh.info[0][lane], sh.info[1][lane], beta, lane);
+    numbers.put_factors(*reinterpret_cast<Factors*>(rec + kRecFactors), p, decays, lane);
+  }
   TileDecays between;
   TileProducts products;
   by_wave(wave, [&](auto W) {
@@ -296,12 +300,12 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
   const int at16 = lane * 16, at_row = l16 * 4;
   // The last fragment of a row of tiles: with one tile (half_fragment) a lane has 8 bytes of it, and reads 16; what is its neighbour's goes.
   const int last_unit = w & 1 ? 16 : 8;
-  const uint32_t keep = w & 1 ? ~0u : 0u;
+  const uint32_t keep[2] = {w == 0 ? 0u : ~0u, w == 2 ? 0u : ~0u};
   const auto operand = [&](u32x4 x, int b) __attribute__((always_inline)) {
-    if (b == w >> 1) x[2] &= keep, x[3] &= keep;
+    x[2] &= keep[b], x[3] &= keep[b];
     return __builtin_bit_cast(f16x8, x);
   };
-  const auto rest_operand = [&](u32x4 x, int b) __attribute__((always_inline)) { return p_rest_operand(u32x2{x[0], b == w >> 1 ? x[1] & keep : x[1]}); };
+  const auto rest_operand = [&](u32x4 x, int b) __attribute__((always_inline)) { return p_rest_operand(u32x2{x[0], x[1] & keep[b]}); };
   const auto advance = [&]() __attribute__((always_inline)) {
     const bool more = next_left > kC;
     next_record += more ? (int64_t)p.H * kDeltaRecord : 0;
@@ -392,20 +396,21 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     scale.set(lane, r.x);
     return by;
   };
+  // (One way out of the loop: from each of its steps the compiler would see a way back to the first, and wait there for all loads.)
   const auto walk_chunks = [&](auto step) __attribute__((always_inline)) {
     static_assert(kAhead == 3, "as written out");
-    for (int i = 0;;) {
+    int i = 0;
+    for (; i + 3 <= chunks; i += 3) {
       step(fetched[0], i);
-      if (++i >= chunks) break;
-      step(fetched[1], i);
-      if (++i >= chunks) break;
-      step(fetched[2], i);
-      if (++i >= chunks) break;
+      step(fetched[1], i + 1);
+      step(fetched[2], i + 2);
     }
+    if (i < chunks) step(fetched[0], i);
+    if (i + 1 < chunks) step(fetched[1], i + 1);
   };
   // Both kinds of wave take the same barriers: three a chunk; three more where a channel's scale has to move or a value
-  // is not finite, which all of them see in sh.top; and two more where what is to be learnt is small, which they see in sh.small, with four
-  // instead of the last where it is too small.
+  // is not finite, which all of them see in sh.top; and two more where what is to be learnt is small, which they see in sh.small, and
+  // three where it is too small.
   // A chunk token by token in fp32, by the chain's waves: K / 8 lanes to a channel, 8 keys to a lane. The state is in sh.s, [channel][K].
   const auto by_tokens = [&](int i, int count, float total) __attribute__((always_inline)) {
     constexpr int kLanes = K / 8;
@@ -463,7 +468,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     s16x4 values = read_v(0);
     OwnFactors own = read_factors(0);
     const auto step = [&](Fetch<K>& f, int i) __attribute__((always_inline)) {
-      const int steps = (int)__builtin_amdgcn_readfirstlane(own.steps), reach = max((int)__builtin_amdgcn_readfirstlane(own.reach), 0);
+      const int steps = (int)__builtin_amdgcn_readfirstlane(own.steps), reach = (int)__builtin_amdgcn_readfirstlane(own.reach);
       const float total = __uint_as_float(__builtin_amdgcn_readfirstlane(own.total));
       // The state's fragments and the channel's largest exponents.
       put_state();
@@ -486,11 +491,32 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           lo[m] = *reinterpret_cast<const f16x8*>(sh.s[m][1] + at16);
         }
       };
+      // K' S0, tokens 4g + i, channel l % 16.
+      f32x4 a, b;
+      const auto products = [&]() __attribute__((always_inline)) {
+        a = b = zero4();
+#pragma unroll
+        for (int m = 0; m < KB; ++m) {
+          const f16x8 k = __builtin_bit_cast(f16x8, f.rows[m]);
+          a = mfma(k, hi[m], a);
+          b = mfma(k, lo[m], b);
+        }
+      };
       read_state();
       __builtin_amdgcn_sched_barrier(0);  // all reads before the first wait
+      products();
+#pragma unroll
+      for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(k_rows + m * 64) = f.rows[m];
       int first_bad = kC;
       scale.apart = 0;
-      float by_apart = 1.f;
+      f32x4 x;  // what is to be learnt, b V - h K' S
+      bool lasts;
+      const auto own_part = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(value[e]) * (own.b[e] * scale.v);
+        lasts = state_lasts(tops[0], scale.apart, total);
+      };
+      own_part();
       if (__builtin_expect(__ballot(moves(tops)) != 0, 0)) {
         barrier_lds();
         int bad = kC;
@@ -507,7 +533,6 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         tops = largest();
         const int by = move(tops);
         tops[0] += by;
-        by_apart = ldexp2(1.f, scale.apart);
 #pragma unroll
         for (int kt = 0; kt < KTW; ++kt)
 #pragma unroll
@@ -515,31 +540,25 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         put_state();
         barrier_lds();
         read_state();
+        products();
+        const float apart = ldexp2(1.f, scale.apart);
+        a *= apart, b *= apart;
+        own_part();
       }
-      f32x4 x;
       {
-        // K' S0, tokens 4g + i, channel l % 16, and what is to be learnt.
-        f32x4 a = zero4(), b = zero4();
 #pragma unroll
-        for (int m = 0; m < KB; ++m) {
-          const f16x8 k = __builtin_bit_cast(f16x8, f.rows[m]);
-          a = mfma(k, hi[m], a);
-          b = mfma(k, lo[m], b);
-        }
-#pragma unroll
-        for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(k_rows + m * 64) = f.rows[m];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = token_value<kF16In>(value[e]) * (own.b[e] * scale.v) - own.h[e] * ((a[e] + b[e]) * by_apart);
+        for (int e = 0; e < 4; ++e) x[e] -= own.h[e] * (a[e] + b[e]);
         const float least = fminf(fminf(fabsf(x[0]), fabsf(x[1])), fminf(fabsf(x[2]), fabsf(x[3])));
-        const uint32_t small = __ballot(least < kLeastShare<kF16In> && !state_lasts(tops[0], scale.apart, total)) != 0;
-        if (lane == 0) sh.small[0][w] = small;
+        const uint32_t small = __ballot(least < kLeastShare<kF16In> && !lasts) != 0;
         put_half<true>(sh.x[w >> 1][0], sh.x[w >> 1][1], at16 + (w & 1) * 8, x);
+        sh.small[0][w] = small;
       }
+      const f16x8 t0 = operand(f.frag[0][0], 0), t1 = operand(f.frag[1][0], 0), u0 = operand(f.frag[0][1], 1), u1 = operand(f.frag[1][1], 1);
       barrier_lds();
       f16x8 kk[2][KTW];
-      bool found_small;
+      u32x4 smalls;
       {
-        const u32x4 smalls = *reinterpret_cast<const u32x4*>(sh.small[0]);
+        smalls = *reinterpret_cast<const u32x4*>(sh.small[0]);
         f16x8 xh[2], xl[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -552,10 +571,8 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           for (int kt = 0; kt < KTW; ++kt) kk[s][kt] = __builtin_bit_cast(f16x8, read_col<K, true>(sh.k, lane, 32 * s, w * KTW + kt));
         fetch_rows(f);
         __builtin_amdgcn_sched_barrier(0);
-        const f16x8 t0 = operand(f.frag[0][0], 0), t1 = operand(f.frag[1][0], 0);
         f32x4 a = mfma(t0, xh[0], zero4()), b = mfma(t1, xh[0], zero4()), c = mfma(t0, xl[0], zero4());
         if (w >= 2) {
-          const f16x8 u0 = operand(f.frag[0][1], 1), u1 = operand(f.frag[1][1], 1);
           a = mfma(u0, xh[1], a);
           b = mfma(u1, xh[1], b);
           c = mfma(u0, xl[1], c);
@@ -563,8 +580,10 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         f32x4 d = a + (b + c) * kDown, decayed = d * own.c;
         put_half<true>(sh.d[w >> 1][0], sh.d[w >> 1][1], at16 + (w & 1) * 8, decayed);
         put_half<true>(sh.dh[w >> 1][0], sh.dh[w >> 1][1], at16 + (w & 1) * 8, d);
-        found_small = __builtin_amdgcn_readfirstlane(smalls[0] | smalls[1] | smalls[2] | smalls[3]) != 0;
       }
+      barrier_lds();
+      const bool found_small = __builtin_amdgcn_readfirstlane(smalls[0] | smalls[1] | smalls[2] | smalls[3]) != 0;
+      bool walked = false;  // the next chunk's loads stand behind both ways, which then have the same loads behind each other
       if (__builtin_expect(found_small, 0)) {
         Fading own_run;
         const int count = min(len - i * kC, kC), t = 16 * w + 4 * g4;
@@ -593,18 +612,15 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
           barrier_lds();
 #pragma unroll
           for (int kt = 0; kt < KTW; ++kt) S[kt] = *reinterpret_cast<const f32x4*>(plain + l16 * K + k0 + 4 * kt);
-          values = read_v(i + 1);
-          own = read_factors(i + 1);
-          fetch_record(f, std::true_type());
-          advance();
           barrier_lds();
-          return;
+          walked = true;
         }
       }
+      if (__builtin_expect(!walked, 1)) {
 #pragma unroll
-      for (int kt = 0; kt < KTW; ++kt) S[kt] *= ldexp2(total, 12 + scale.apart);
-      scale.ex += scale.apart;
-      barrier_lds();
+        for (int kt = 0; kt < KTW; ++kt) S[kt] *= ldexp2(total, scale.apart);
+        scale.ex += scale.apart;
+      }
       {
         f16x8 dh[2], dl[2];
 #pragma unroll
@@ -617,20 +633,23 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
         fetch_record(f, std::true_type());
         advance();
         __builtin_amdgcn_sched_barrier(0);
+        if (__builtin_expect(!walked, 1)) {
+          f32x4 rest[KTW];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+          for (int kt = 0; kt < KTW; ++kt) rest[kt] = mfma(kk[0][kt], dl[0], zero4());
 #pragma unroll
-          for (int kt = 0; kt < KTW; ++kt) S[kt] = mfma(kk[s][kt], dl[s], S[kt]);
+          for (int kt = 0; kt < KTW; ++kt) S[kt] = mfma(kk[0][kt], dh[0], S[kt]);
 #pragma unroll
-        for (int kt = 0; kt < KTW; ++kt) S[kt] *= kDown;
+          for (int kt = 0; kt < KTW; ++kt) rest[kt] = mfma(kk[1][kt], dl[1], rest[kt]);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+          for (int kt = 0; kt < KTW; ++kt) S[kt] = mfma(kk[1][kt], dh[1], S[kt]);
 #pragma unroll
-          for (int kt = 0; kt < KTW; ++kt) S[kt] = mfma(kk[s][kt], dh[s], S[kt]);
+          for (int kt = 0; kt < KTW; ++kt) S[kt] += rest[kt] * kDown;
+          if (first_bad < kC)
+#pragma unroll
+            for (int kt = 0; kt < KTW; ++kt) S[kt] = zero4() + __builtin_nanf("");
+        }
       }
-      if (first_bad < kC)
-#pragma unroll
-        for (int kt = 0; kt < KTW; ++kt) S[kt] = zero4() + __builtin_nanf("");
     };
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
@@ -652,10 +671,25 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
     advance_v();
     const auto step = [&](Fetch<K>& f, int i) __attribute__((always_inline)) {
       barrier_lds();
+      // S0 Q', channels 4g + i, token l % 16.
+      f32x4 o, low;
+      const auto products = [&]() __attribute__((always_inline)) {
+        o = low = zero4();
+#pragma unroll
+        for (int m = 0; m < KB; ++m) {
+          const f16x8 q = __builtin_bit_cast(f16x8, f.rows[m]);
+          o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), q, o);
+          low = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), q, low);
+        }
+      };
+      const i16x2 tops = largest();
+      products();
+      put_v(f.v, i + 1);
+      put_factor(f.factor, i + 1);
       int first_bad = kC;
       scale.apart = 0;
       f32x4 by_apart = zero4() + 1.f;
-      if (__builtin_expect(__ballot(moves(largest())) != 0, 0)) {
+      if (__builtin_expect(__ballot(moves(tops)) != 0, 0)) {
         barrier_lds();
         barrier_lds();
         first_bad = least_bad();
@@ -664,71 +698,67 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) by_apart[e] = __shfl(by, 4 * g4 + e);
         barrier_lds();
+        products();
       }
-      put_v(f.v, i + 1);
-      put_factor(f.factor, i + 1);
-      // S0 Q', channels 4g + i, token l % 16.
-      f32x4 o = zero4();
-#pragma unroll
-      for (int m = 0; m < KB; ++m) {
-        const f16x8 q = __builtin_bit_cast(f16x8, f.rows[m]);
-        o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][1] + lane * 16), q, o);
-        o = mfma(*reinterpret_cast<const f16x8*>(sh.s[m][0] + lane * 16), q, o);
-      }
-      o *= f.e * by_apart;
-      const auto fetch_next = [&]() __attribute__((always_inline)) {
-        fetch_rows(f);
-        fetch_record(f, std::false_type());
-        advance();
-        f.v = fetch_v();
-        f.factor = fetch_factor();
-        advance_v();
-      };
+      o = (o + low) * (f.e * by_apart);
       barrier_lds();
-      if (__builtin_expect(any_small(0), 0)) {
+      const bool found_small = any_small(0);
+      const f16x8 p0 = operand(f.frag[0][0], 0), p1 = operand(f.frag[0][1], 1), rest0 = rest_operand(f.frag[1][0], 0), rest1 = rest_operand(f.frag[1][1], 1);
+      fetch_rows(f);
+      barrier_lds();
+      bool walked = false;
+      if (__builtin_expect(found_small, 0)) {
         barrier_lds();
         barrier_lds();
         if (any_small(1)) {
           scale.ex = scale.apart = 0;
           scale.set(lane, 0);
           // The rows of Q' and the tokens' factors, for the chain's waves.
-#pragma unroll
-          for (int m = 0; m < KB; ++m) *reinterpret_cast<u32x4*>(sh.q + 16 * w * kRowBytes<K> + row_at<K>(l16) + g4 * 16 + m * 64) = f.rows[m];
           const DeltaPlan& p = plan_again();
+          const char* rows = p.queries + (((int64_t)place + i) * H_qk + hq) * (kC * K * 2) + w * (KB * 1024) + at16;
+#pragma unroll
+          for (int m = 0; m < KB; ++m)
+            *reinterpret_cast<u32x4*>(sh.q + 16 * w * kRowBytes<K> + row_at<K>(l16) + g4 * 16 + m * 64) = *reinterpret_cast<const u32x4*>(rows + m * 1024);
           const Factors& fa = *reinterpret_cast<const Factors*>(p.records + (((int64_t)place + i) * p.H + h) * kDeltaRecord + kRecFactors);
           sh.token[w][lane] = w == 3 ? decays_at(p, begin + (int64_t)i * kC + lane, min(len - i * kC - lane, 1), h)[0]
                                      : (w == 0 ? fa.b : w == 1 ? fa.s : fa.f)[lane];
           barrier_lds();
-          fetch_next();
           barrier_lds();
           barrier_lds();
-          return;
+          walked = true;
         }
       }
-      scale.ex += scale.apart;
-      barrier_lds();
-      f32x4 rest = zero4();
+      u32x2 packed = {0, 0};
+      if (__builtin_expect(!walked, 1)) {
+        scale.ex += scale.apart;
+        const auto d = [&](int s, int term) __attribute__((always_inline)) { return *reinterpret_cast<const f16x8*>(sh.dh[s][term] + lane * 16); };
+        const f16x8 d0 = d(0, 0);
+        o = mfma(d0, p0, o);
+        f32x4 rest = mfma(d(0, 1), p0, zero4()), other = mfma(d0, rest0, zero4());
+        if (w >= 2) {
+          const f16x8 d1 = d(1, 0);
+          o = mfma(d1, p1, o);
+          rest = mfma(d(1, 1), p1, rest);
+          other = mfma(d1, rest1, other);
+        }
+        o += (rest + other) * kDown;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s > 0 && w < 2) break;
-        const f16x8 high = *reinterpret_cast<const f16x8*>(sh.dh[s][0] + lane * 16), pp = operand(f.frag[0][s], s);
-        rest = mfma(*reinterpret_cast<const f16x8*>(sh.dh[s][1] + lane * 16), pp, rest);
-        rest = mfma(high, rest_operand(f.frag[1][s], s), rest);
-        o = mfma(high, pp, o);
+        for (int e = 0; e < 4; ++e) o[e] *= f.f * scale.out[e];
+        if (__ballot(first_bad < kC)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * w + l16 >= __shfl(first_bad, 4 * g4 + e)) o[e] = __builtin_nanf("");
+        }
+        if constexpr (kF16In) packed = __builtin_bit_cast(u32x2, f16x4{(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]});
+        else packed = __builtin_bit_cast(u32x2, bf16x4{to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])});
       }
-      o += rest * kDown;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] *= f.f * scale.out[e];
-      if (__ballot(first_bad < kC)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (16 * w + l16 >= __shfl(first_bad, 4 * g4 + e)) o[e] = __builtin_nanf("");
-      }
-      fetch_next();
-      u32x2 packed;
-      if constexpr (kF16In) packed = __builtin_bit_cast(u32x2, f16x4{(_Float16)o[0], (_Float16)o[1], (_Float16)o[2], (_Float16)o[3]});
-      else packed = __builtin_bit_cast(u32x2, bf16x4{to_bf16(o[0]), to_bf16(o[1]), to_bf16(o[2]), to_bf16(o[3])});
-      __builtin_amdgcn_raw_buffer_store_b64(packed, buffer(out + (begin + (int64_t)i * kC) * p.o_t, p.o_t, len - i * kC), at_out, 0, 0);
+      fetch_record(f, std::false_type());
+      advance();
+      f.v = fetch_v();
+      f.factor = fetch_factor();
+      advance_v();
+      // (Of no row where the chunk was walked.)
+      __builtin_amdgcn_raw_buffer_store_b64(packed, walked ? whole(reinterpret_cast<const char*>(out), 0) : buffer(out + (begin + (int64_t)i * kC) * p.o_t, p.o_t, len - i * kC), at_out, 0, 0);
     };
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
