@@ -3,7 +3,8 @@
 ``gated_delta_fwd`` (prompts) and ``gated_delta_step`` (single tokens) serve beside ``linear_fwd`` and
 ``linear_step`` with the same packed bounds, state pool, slots, checks and errors. They enqueue the kernels of
 ``libkda.so`` on the current torch stream; nothing synchronises and no metadata is built, so every call can be
-captured. They record no gradient, and refuse inputs that require one while gradients are enabled.
+captured. They record no gradient, and refuse inputs that require one while gradients are enabled, or that carry a
+forward-mode tangent.
 """
 from __future__ import annotations
 
@@ -12,7 +13,8 @@ import ctypes
 import torch
 
 from . import _lib
-from .linear import _BF16, _Call, _check, _context, _fill_linear, _grads_on, _like, _on, _packed, _refuse_gradient
+from .linear import (_BF16, _Call, _check, _context, _fill_linear, _grads_on, _like, _on, _packed, _refuse_gradient, _refuse_tangents,
+                     _tangents_on)
 
 __all__ = ["gated_delta_fwd", "gated_delta_step"]
 
@@ -28,6 +30,8 @@ def make_gated_delta_args(q, k, v, g, beta, *, N=None, cu_seqlens=None, cu_seqle
         raise ValueError("beta is required")
     if beta.requires_grad and _grads_on():
         _refuse_gradient()
+    if _tangents_on():
+        _refuse_tangents(beta)
     a = _lib.GatedDeltaArgs()
     dtype = q.dtype
     if dtype == _BF16:

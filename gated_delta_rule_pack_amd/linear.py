@@ -4,7 +4,7 @@
 same packed bounds, state pool and slots; ``rotary`` turns q and k by their positions. All three
 marshal tensors into the C ABI of ``libkda.so`` and enqueue its kernels on the current torch
 stream; nothing synchronises and no metadata is built, so every call can be captured. They record no
-gradient, and refuse inputs that require one while gradients are enabled.
+gradient, and refuse inputs that require one while gradients are enabled, or that carry a forward-mode tangent.
 """
 from __future__ import annotations
 
@@ -12,6 +12,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import _lib
 
@@ -74,6 +75,17 @@ def _refuse_gradient(advice=""):
     raise ValueError("an input requires a gradient, and the call records none: use torch.no_grad() or detach()" + advice)
 
 
+# Nor do they carry tangents of forward-mode derivatives on, which no_grad leaves in force.
+def _tangents_on():
+    return _forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled()
+
+
+def _refuse_tangents(*tensors):
+    for t in tensors:
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("an input carries a tangent, and the call computes no forward-mode gradient: use detach()")
+
+
 _I32 = (torch.int32,)
 _INTS = (torch.int32, torch.int64)
 _BOOLS = (torch.bool, torch.uint8)
@@ -121,6 +133,8 @@ def _fill_linear(a, q, k, v, g, dtype, N, cu_seqlens, cu_seqlens_cpu, scale, ini
                         (state_cache is not None and state_cache.requires_grad) or (out is not None and out.requires_grad) or
                         (initial_state is not None and initial_state.requires_grad)):
         _refuse_gradient()
+    if _tangents_on():
+        _refuse_tangents(q, k, v, g, state_cache, initial_state, out)
     q, k, v = _packed("q", q), _packed("k", k), _packed("v", v)
     T, H_qk, K = q.shape
     Tv, H, V = v.shape
@@ -360,6 +374,8 @@ def make_rotary_args(q, k, positions, inv_freq, out_q, out_k, *, interleaved=Fal
     if _grads_on() and (q.requires_grad or out_q.requires_grad or (k is not None and k.requires_grad) or
                         (out_k is not None and out_k.requires_grad)):
         _refuse_gradient(" (the gradient is the call with inverse=True)")
+    if _tangents_on():
+        _refuse_tangents(q, k, out_q, out_k)
     q, out_q = _packed("q", q), _packed("out_q", out_q)
     T, H, D = q.shape
     dtype = q.dtype

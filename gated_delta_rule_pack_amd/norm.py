@@ -3,7 +3,7 @@
 ``qk_norm`` stands in front of ``linear_fwd``, ``gated_delta_fwd`` or any attention; ``qk_norm_backward`` is its gradient as a
 call of its own, as ``rotary(..., inverse=True)`` is the rotation's. Both enqueue kernels of ``libkda.so`` on the current
 torch stream, synchronise nothing and can be captured; they record no gradient, and refuse inputs that require one while
-gradients are enabled.
+gradients are enabled, or that carry a forward-mode tangent.
 """
 from __future__ import annotations
 
@@ -12,7 +12,8 @@ import ctypes
 import torch
 
 from . import _lib
-from .linear import _STATE_DT, _Call, _check, _context, _fill_rotation, _grads_on, _like, _on, _packed, _refuse_gradient, _strides
+from .linear import (_STATE_DT, _Call, _check, _context, _fill_rotation, _grads_on, _like, _on, _packed, _refuse_gradient,
+                     _refuse_tangents, _strides, _tangents_on)
 
 __all__ = ["qk_norm", "qk_norm_backward"]
 
@@ -43,6 +44,8 @@ def make_qk_norm_args(q, k, q_weight, k_weight, positions, inv_freq, out_q, out_
                         (k_weight is not None and k_weight.requires_grad) or (grad_q is not None and grad_q.requires_grad) or
                         (grad_k is not None and grad_k.requires_grad)):
         _refuse_gradient(_ADVICE)
+    if _tangents_on():
+        _refuse_tangents(q, k, q_weight, k_weight, out_q, out_k, grad_q, grad_k)
     q, out_q = _packed("q", q), _packed("out_q", out_q)
     shape, dtype = q.shape, q.dtype
     T, H, D = shape
