@@ -78,7 +78,10 @@ def gated_delta_fwd(q, k, v, g, beta, cu_seqlens, *, cu_seqlens_cpu=None, scale=
     2^-12, and from about 2^13 apart on nothing finite.)
     scale defaults to ``K ** -0.5``.
 
-    cu_seqlens, states, ``out``, ``workspace``, ``stream`` and ``context`` as in :func:`linear_fwd`. ``path`` overrides the
+    cu_seqlens, states, ``out``, ``stream`` and ``context`` as in :func:`linear_fwd`. ``workspace``: a contiguous uint8 tensor at
+    a 256-byte address, made here where none is given; one that is too small or lies elsewhere is refused with KDAError. "walk"
+    needs none; "scan" keeps a record of every chunk in it, 308 bytes for each token and value head and 4 K for each token and q/k
+    head (a chunk more for each sequence): 593 MB for 32768 tokens of 32 heads that share 16. ``path`` overrides the
     choice between one kernel that walks every sequence of a head ("walk") and two that split the work further
     ("scan"), which agree within rounding. The choice looks at the shapes and, where ``cu_seqlens_cpu`` is given, at the
     lengths: give it where a batch mixes long prompts with single tokens. Returns ``(out, final_state)``, final_state
@@ -104,9 +107,10 @@ def gated_delta_fwd(q, k, v, g, beta, cu_seqlens, *, cu_seqlens_cpu=None, scale=
             raise TypeError("workspace must be a contiguous uint8 tensor")
         lib, ref, context = _lib.load(), ctypes.byref(a), _context(context, call.index)
         given = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
-        # Short calls need no workspace: it is asked for where the call says so, which has enqueued nothing then.
+        # Short calls need no workspace: it is asked for where the call says so, which has enqueued nothing then. (One that is given and
+        # does not serve is the caller's to mend.)
         rc = lib.kda_gated_delta_fwd(context, ref, *given, call.handle)
-        if rc == _lib.KDA_ERR_WORKSPACE:
+        if rc == _lib.KDA_ERR_WORKSPACE and workspace is None:
             workspace = torch.empty(lib.kda_gated_delta_fwd_workspace_bytes(ref), dtype=torch.uint8, device=call.device)
             rc = lib.kda_gated_delta_fwd(context, ref, workspace.data_ptr(), workspace.numel(), call.handle)
         _check(rc, "kda_gated_delta_fwd")

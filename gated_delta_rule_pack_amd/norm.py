@@ -145,7 +145,7 @@ def qk_norm_backward(grad_q, grad_k, q, k, q_weight=None, k_weight=None, positio
     """The gradient of :func:`qk_norm`: given the results' gradients and the call's inputs, ``(dq, dk, dq_weight,
     dk_weight)``, of the inputs' types (None for an input that is None). Weight gradients are summed over all
     rows in fp32 and rounded once. ``out_q`` / ``out_k`` may be grad_q / grad_k themselves, or share no element with any
-    input. A training program calls both under ``torch.no_grad()``, or in the two halves of an autograd function."""
+    input. ``workspace``, for weight gradients: as in :func:`gated_delta_fwd`, at most 4096 bytes for each channel. A training program calls both under ``torch.no_grad()``, or in the two halves of an autograd function."""
     with _Call(q, stream) as call:
         _on(call.index, "grad_q grad_k k q_weight k_weight positions inv_freq out_q out_k workspace", grad_q, grad_k, k, q_weight,
             k_weight, positions, inv_freq, out_q, out_k, workspace)
@@ -165,8 +165,8 @@ def qk_norm_backward(grad_q, grad_k, q, k, q_weight=None, k_weight=None, positio
         need = lib.kda_qk_norm_backward_workspace_bytes(ref)  # 0 for a refused call too: the call says why
         if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
             raise TypeError("workspace must be a contiguous uint8 tensor")
-        if need and (workspace is None or workspace.numel() < need):
+        if need and workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=call.device)
-        _check(lib.kda_qk_norm_backward(_context(context, call.index), ref, workspace.data_ptr() if need else None, need, call.handle),
-               "kda_qk_norm_backward")
+        given = (workspace.data_ptr(), workspace.numel()) if need else (None, 0)
+        _check(lib.kda_qk_norm_backward(_context(context, call.index), ref, *given, call.handle), "kda_qk_norm_backward")
     return out_q, out_k, dqw, dkw

@@ -526,7 +526,9 @@ kda_status kda_gated_delta_fwd(kda_ctx* ctx, const kda_gated_delta_args* args, v
 /* Host-only, pure: every argument check of kda_gated_delta_fwd. */
 kda_status kda_gated_delta_fwd_validate(const kda_gated_delta_args* args);
 /* Host-only, pure: bytes of caller workspace (256-byte aligned) of the path that the call takes (0 for the walk, and
- * for invalid arguments); path = KDA_DELTA_SCAN gives what a call of these shapes needs at most. */
+ * for invalid arguments); path = KDA_DELTA_SCAN gives what a call of these shapes needs at most. It grows with the tokens: with
+ * T / 64 + N places for chunks, 19712 H + 256 K H_qk bytes for each (593 MB for 32768 tokens at H = 32, H_qk = 16, K = 128;
+ * 18 GB for a million). The walk needs none. */
 size_t kda_gated_delta_fwd_workspace_bytes(const kda_gated_delta_args* args);
 
 /* Single tokens, as kda_linear_step: one kernel, no workspace, capturable; padding rows are left as they were. */

@@ -611,3 +611,23 @@ def test_refused_calls_on_the_device():
         case.forward(d, workspace=torch.empty(4, device="cuda"))
     with pytest.raises(ValueError):
         case.forward(dict(d, beta=d["beta"].cpu()))
+
+
+def test_a_given_workspace_that_does_not_serve_is_refused():
+    case = DeltaCase([200, 90], H=2, seed=97)
+    d = case.device()
+    before = d["store"].clone()
+    out = torch.full_like(d["v"], 7.0)
+    big = torch.empty(4 << 20, dtype=torch.uint8, device="cuda")
+    for ws in (big[:0], big[:1000], big[128:], big[1:]):
+        with pytest.raises(kda.KDAError, match="workspace"):
+            case.forward(d, out=out, path="scan", workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7.0) and same_bits(d["store"], before)
+    case.forward(d, out=out, path="scan", workspace=big)
+    torch.cuda.synchronize()
+    check(case, out, d, None)
+    e = case.device()
+    case.forward(e, out=out, path="walk", workspace=big[1:3])  # which needs none
+    torch.cuda.synchronize()
+    check(case, out, e, None)

@@ -310,3 +310,17 @@ def test_refused_calls_on_the_device():
         backward(d, kw, workspace=torch.empty(4, device="cuda"))
     with pytest.raises(ValueError):
         forward(dict(d, q=d["q"].float().requires_grad_()), kw)
+
+
+def test_a_given_workspace_that_does_not_serve_is_refused():
+    q = torch.randn(600, 3, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    big = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for ws in (big[:1000], big[128:]):
+        with pytest.raises(kda.KDAError, match="workspace"):
+            kda.qk_norm_backward(q, None, q, None, w, workspace=ws)
+    got = kda.qk_norm_backward(q, None, q, None, w, workspace=big)
+    want = kda.qk_norm_backward(q, None, q, None, w)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    assert kda.qk_norm_backward(q, None, q, None, workspace=big[:1])[2] is None  # no weights: none is needed
