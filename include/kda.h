@@ -546,8 +546,8 @@ kda_status kda_gated_delta_step_validate(const kda_gated_delta_args* args);
  * fp32, rounded once.
  *
  * The gradient, with z = R^T dy:  dweight = sum over rows of z x r;  with u = z (weight_offset + weight):
- * dx = r (u - m x r^2 sum(u x)). Weight gradients are summed in fp32, in an order that depends on the shapes
- * alone. */
+ * dx = r (u - m x r^2 sum(u x)). Weight gradients are summed in fp32, in an order that depends on the shapes, and on
+ * what vectors the tensors' addresses and strides allow: a call repeats bit for bit, rows at another alignment may not. */
 typedef enum kda_norm_kind { KDA_NORM_RMS = 0, KDA_NORM_L2 = 1 } kda_norm_kind;
 typedef struct kda_qk_norm_args {
   int32_t T;              /* tokens, may be 0 */

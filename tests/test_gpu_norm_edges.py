@@ -324,3 +324,21 @@ def test_a_given_workspace_that_does_not_serve_is_refused():
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     assert kda.qk_norm_backward(q, None, q, None, workspace=big[:1])[2] is None  # no weights: none is needed
+
+
+@pytest.mark.parametrize("T,H,D,rot,interleaved", [(1001, 12, 72, 36, True), (1001, 12, 72, 36, False), (513, 3, 65, 64, False), (4096, 8, 128, 128, False)])
+def test_weight_gradients_sum_in_pairs(T, H, D, rot, interleaved):
+    """n terms of one size and random signs: with e = 0.735 2^-24 (the half step's share of a value is 2^-24 at its lowest, 0.735 of that in
+    the mean square over all values) a chain of m partial sums is off by e sqrt(m / 6) of its result, rms, pairs of pairs by e sqrt(log2(m) /
+    3). The terms carry five roundings each, 1.3 e. Here chains hold at most 16 rows of a lane (1.6) and 8 in each four of a workgroup's
+    groups (1.1 and 0.8), then two in each four of a channel's 8 workgroups (0.6 and 0.8), and pairs of 64 (1.4): 3.1 e = 2.3 2^-24 in all at
+    most. One chain of 64 (3.3) instead of pairs makes 2.8 2^-24 and more."""
+    gen = torch.Generator().manual_seed(12)
+    q, gq = (torch.randn(T, H, D, generator=gen) for _ in range(2))
+    w = 1 + 0.2 * torch.randn(D, generator=gen)
+    pos, freq = torch.arange(T), 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    _, _, got, _ = kda.qk_norm_backward(gq.cuda(), None, q.cuda(), None, w.cuda(), None, pos.cuda(), freq.cuda(), interleaved=interleaved)
+    _, want = qk_norm_gradient(f64(gq), f64(q), f64(w), positions=f64(pos), inv_freq=f64(freq), interleaved=interleaved)
+    rel = np.linalg.norm(f64(got) - want) / np.linalg.norm(want)
+    print(f"  dw: rel-L2 {rel * 2 ** 24:.2f} 2^-24", flush=True)
+    assert rel < 2.5 * 2.0 ** -24
