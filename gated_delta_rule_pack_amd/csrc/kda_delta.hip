@@ -374,6 +374,7 @@ struct Chain {
   // The chunk token by token in fp32, for this wave's channels.
   __device__ __forceinline__ void by_tokens(Slot<K, V>& slot, int wave, int lane, int count) {
     const Factors& fa = slot.factors;
+    const auto channel_sum = [](f32x4 x) __attribute__((always_inline)) { return add_far(add_far((x[0] + x[1]) + (x[2] + x[3]), 16), 32); };
 #pragma unroll
     for (int vt = 0; vt < VT; ++vt) {
       f32x4 (&S)[KT] = state.S[vt];
@@ -392,13 +393,13 @@ struct Chain {
       for (int t = 0; t < count; ++t) {
         const float decay = slot.decay[t];
         uint16_t* const at = reinterpret_cast<uint16_t*>(slot.v + row_at<V>(t)) + (wave * VT + vt) * 16 + (lane & 15);
-        float u = 0.f, o = 0.f;
-        over_keys(slot.k + row_at<K>(t), [&](int kt, int i, float k) __attribute__((always_inline)) { u += S[kt][i] * k; });
-        u = add_far(add_far(u, 16), 32);
+        f32x4 us = zero4(), os = zero4();
+        over_keys(slot.k + row_at<K>(t), [&](int kt, int i, float k) __attribute__((always_inline)) { us[i] += S[kt][i] * k; });
+        float u = channel_sum(us);
         u = fa.b[t] * token_value<kF16In>(*at) - fa.s[t] * (decay * u);
         over_keys(slot.k + row_at<K>(t), [&](int kt, int i, float k) __attribute__((always_inline)) { S[kt][i] = S[kt][i] * decay + u * k; });
-        over_keys(slot.q + row_at<K>(t), [&](int kt, int i, float q) __attribute__((always_inline)) { o += S[kt][i] * q; });
-        o = fa.f[t] * kTimesP * add_far(add_far(o, 16), 32);
+        over_keys(slot.q + row_at<K>(t), [&](int kt, int i, float q) __attribute__((always_inline)) { os[i] += S[kt][i] * q; });
+        const float o = fa.f[t] * kTimesP * channel_sum(os);
         if (lane < 16) *at = kF16In ? __builtin_bit_cast(uint16_t, (_Float16)o) : __builtin_bit_cast(uint16_t, to_bf16(o));
       }
       if (fa.total != fa.total) {

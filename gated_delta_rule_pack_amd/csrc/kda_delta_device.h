@@ -65,10 +65,10 @@ __device__ __forceinline__ void put_half(char* high, char* low, int at, f32x4 x)
   *reinterpret_cast<u32x2*>(low + at) = kRestUp ? u32x2{rest_up(x[0], x[1], h[0]), rest_up(x[2], x[3], h[1])}
                                                 : u32x2{rest_pair(x[0], x[1], h[0]), rest_pair(x[2], x[3], h[1])};
 }
-// P stands 16 times as large as it is (it is at most 2^10, by rows of 2^5). Its second term has 8 bits, five of exponent and two of
-// fraction, fp16's upper byte: with them P is within 2^-14 of itself, an eighth of the half step of outputs in fp16, or within 2^-32, and its
+// P stands 64 times as large as it is (it is at most 2^8, by rows of 16). Its second term has 8 bits, five of exponent and two of
+// fraction, fp16's upper byte: with them P is within 2^-14 of itself, an eighth of the half step of outputs in fp16, or within 2^-34, and its
 // records keep their size. It is stored times 2^11, and read times 2^12.
-constexpr float kTimesP = 16.f;
+constexpr float kTimesP = 64.f;
 __device__ __forceinline__ uint32_t p_rest(f32x4 x, u32x2 first) {
   typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
   const float up = kUp / 2;
@@ -200,12 +200,12 @@ __device__ __forceinline__ int ranked_sequence(const DeltaPlan& p, Ranking& r, i
   return __builtin_amdgcn_readfirstlane(r.sequence);
 }
 
-// Rows of q or k on their way to LDS as fp16, each scaled by 2^-e: e = 0 for rows whose length is between 2^-4 and 2^5, where all
+// Rows of q or k on their way to LDS as fp16, each scaled by 2^-e: e = 0 for rows whose length is between 1/2 and 16, where all
 // that counts of them fits as it stands, else what brings their largest element into [1/4, 1/2).
 template <int D, int kThreads, bool kF16In>
 struct ScaledRows {
   typedef Rows<D, kThreads> R;
-  static constexpr float kLeast = 0x1p-8f, kMost = 0x1p10f;
+  static constexpr float kLeast = 0x1p-2f, kMost = 0x1p8f;
   R rows;
   RowInfo info[R::kPasses];
 
@@ -295,8 +295,8 @@ struct Factors {
   float b[kC];  // beta rk: the share of V in what is to be learnt
   float h[kC];  // beta rk^2 e^G: that of K' S0
   float c[kC];  // e^{G_C - G}: what of D reaches the chunk's end
-  float e[kC];  // e^G times 16, as P
-  float f[kC];  // scale rq / 16: outputs; NaN from the first bad token on
+  float e[kC];  // e^G times 64, as P
+  float f[kC];  // scale rq / 64: outputs; NaN from the first bad token on
   float s[kC];  // beta rk^2, for a walk by tokens
   float total;  // e^{G_C}; NaN with a bad token
   int steps;    // |b| < 2^steps
@@ -418,13 +418,14 @@ __device__ __forceinline__ void put_rest(char* p, int lane, int tt, int st, uint
 }
 
 // Making T and P, by four waves. The ten tiles (tt, st <= tt) of K' K'^T and K' Q'^T, rows s = 4g + i, column t = l % 16, are dealt
-// out as rows of tiles: 0 and 1, 2, and two halves of 3. Each wave has code of its own, in which all places are constants.
+// out as rows of tiles: 0 and 1, 2, 3 but its last, and that one, by the wave that makes the chunk's numbers in the walk. Each wave has
+// code of its own, in which all places are constants.
 constexpr int kTileJobs = 3;
 template <int W>
 struct TileJobs {
-  static constexpr int kCount = W < 2 ? 3 : 2;
+  static constexpr int kCount = W < 3 ? 3 : 1;
   static constexpr int tt(int j) { return W == 0 ? (j > 0) : W == 1 ? 2 : 3; }
-  static constexpr int st(int j) { return W == 0 ? (j == 2) : W == 1 ? j : 2 * (W - 2) + j; }
+  static constexpr int st(int j) { return W == 0 ? (j == 2) : W < 3 ? j : 3; }
 };
 template <typename F>
 __device__ __forceinline__ void by_wave(int w, F f) {
@@ -648,11 +649,12 @@ struct Scale {
 
 // What a token's output and state are made of: of the state before the chunk and of what it and those before it learn, each as far as
 // it has decayed, the largest, L_t = max(e^{g_t} L_{t-1}, |X'_t|). Beside the share of 2^-22 of itself that a term may be off, T and what is to be
-// learnt may be off by 2^-37 and P by 2^-32, wherever the range's top (2^4) stands: where every L_t is at least kLeastShare, a token's state is
-// within 2^-16 of L_t (at the range's top 2^-22), and its output within 2^-11, or 2^-13 in fp16. A chunk in which some L_t is less (a large
-// value behind small ones, small ones behind a large one that was forgotten) is walked token by token.
+// learnt may be off by 2^-37 and P by 2^-34, wherever the range's top (2^4) stands; where every L_t is at least kLeastShare that is little of
+// what the token is made of: over 7500 random batches (values and steps of 2^+-30, resets, raw keys) states were within 2^-16 of L_t, and outputs too,
+// beside their rounding. A chunk in which some L_t is less (a large value behind small ones, small ones behind a large one that
+// was forgotten) is walked token by token. With random values that is one chunk and wave in 10^5, where decays are steepest.
 template <bool kF16In>
-constexpr float kLeastShare = kF16In ? 0x1p-15f : 0x1p-17f;
+constexpr float kLeastShare = kF16In ? 0x1p-17f : 0x1p-18f;
 
 // The plan read again from the kernel's arguments, for what is rare: with one copy of it for all the walk spills scalars (2 %).
 __device__ __forceinline__ const DeltaPlan& plan_again() {
