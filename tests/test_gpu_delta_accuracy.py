@@ -8,6 +8,8 @@ Relative to all outputs, e_p is spread over the terms of an output and adds in q
 r = 2.1e-4 in fp16 and 1.66e-3 in bf16: sqrt(r^2 + e_p^2) is 1.042 r and 1.0007 r. One term anywhere (2^-11) is 1.28 r and more
 than 1.01 r.
 """
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -114,15 +116,18 @@ def test_tiny_steps_beside_a_state(step, size, path):
 
 
 # ------------------------------------------------------------------------------ sizes far apart in one sequence
-# L_t of a channel: the largest of what its token t is made of, each as far as it has decayed, max(e^{g_t} L_{t-1}, |beta_t v_t|), from
-# the largest element of its initial state on. The kernels keep every term within EL = 2^-16 of L_t, however large a value stands
+# L_t of a channel: the largest of what its token t is made of, each as far as it has decayed, max(e^{g_t} L_{t-1}, |beta_t v_t| |k_t|),
+# from the largest element of its initial state on. The kernels keep every term within EL = 2^-16 of L_t, however large a value stands
 # elsewhere in the chunk, so the harness's bounds hold with EL and L_t in place of e2 and M.
 EL = 2.0 ** -16
 
 
 def _check_reach(case, d, out, final, rows=slice(None)):
     o, S, _ = case.oracle()
-    v, beta = np.abs(f64(case.v)) * np.abs(f64(case.beta))[:, :, None], f64(case.beta)
+    length = 1.0
+    if not case.normalize:
+        length = np.repeat(np.sqrt((f64(case.k) ** 2).sum(-1)), case.H // case.H_qk, axis=1)
+    v = np.abs(f64(case.v)) * (np.abs(f64(case.beta)) * length)[:, :, None]
     decay = np.ones((case.T, case.H)) if case.g is None else np.exp(np.broadcast_to(f64(case.g), (case.T, case.H)))
     start = case.start()
     L, end, n = np.zeros_like(o), np.zeros((case.N, case.H, case.V)), np.zeros((case.T, 1, 1))
@@ -233,6 +238,40 @@ def test_channels_of_all_sizes_and_times(kw, path):
     gen = torch.Generator().manual_seed(8)
     span = 10 if case.dtype == torch.float16 else 30
     case.v = (case.v.float() * 2.0 ** torch.randint(-span, span + 1, case.v.shape, generator=gen).float()).to(case.dtype)
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
+
+
+@PATHS
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed, path):
+    """Types, head sizes, decays, sizes of values, steps and states, and lengths of raw keys, drawn by the seed."""
+    rng = random.Random(seed)
+    dtype, unit = rng.choice(["bf16", "bf16", "f16"]), rng.random() < 0.6
+    lens = [rng.choice([1, 2, 40, 64, 65, 100, 150, 200]) for _ in range(rng.choice([1, 2, 3]))]
+    case = DeltaCase(lens, H=rng.choice([1, 2, 3]), K=rng.choice([64, 128]), V=rng.choice([64, 128]), dtype=dtype, unit=unit,
+                     state=rng.choice(["none", "dense"]), decay=rng.choice(["token", "none", "resets", "head"]), k_first=rng.random() < 0.3, seed=seed)
+    gen = torch.Generator().manual_seed(seed)
+
+    def powers(low, high, *shape):
+        return 2.0 ** torch.randint(low, high + 1, shape, generator=gen).float()
+
+    if case.g is not None and case.g.dim() == 2:
+        # Beyond e^-60 what is left of a state falls below fp32's range, where nothing keeps its accuracy.
+        case.g = torch.where(case.g > -20, (case.g * 10 ** rng.uniform(-2, 1)).clamp(min=-20), torch.full_like(case.g, -float("inf")))
+    span = rng.choice([0, 3, 10, 30]) if dtype == "bf16" else rng.choice([0, 3, 8])
+    shape = rng.choice([(case.T, case.H, case.V), (case.T, case.H, 1), (1, case.H, case.V)])
+    case.v = (case.v.float() * powers(-span, span, *shape)).to(case.dtype)
+    if case.state == "dense":
+        case.initial *= 2.0 ** rng.choice([0, 0, -10, 10] + [-30, 30] * (dtype == "bf16"))
+    case.beta = case.beta / powers(0, rng.choice([0, 0, 5, 30]), *case.beta.shape)
+    case.beta[torch.rand(case.beta.shape, generator=gen) < rng.choice([0, 0, 0.2])] = 0
+    if unit:
+        low, high = rng.choice([(0, 0), (-4, 4), (-2, 3)] + [(-20, -18), (5, 9)] * (dtype == "bf16"))
+        case.k = (case.k.float() * powers(low, high, case.T, case.H_qk, 1)).to(case.dtype)
+        case.beta = case.beta / case.k.float().norm(dim=-1) ** 2
     d = case.device()
     out, final = case.forward(d, path=path)
     torch.cuda.synchronize()
