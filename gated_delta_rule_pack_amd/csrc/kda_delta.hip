@@ -11,11 +11,12 @@
 // sums: nothing is divided, so no decay is too steep. T is made of 16 x 16 blocks: those on the diagonal by forward
 // substitution, those below it by products of blocks, all in fp32.
 //
-// Number formats. MFMA operands are fp16, whose 11 bits make two terms 22: the state keeps nearly fp32's accuracy in two
-// products where bf16 would take three. Keys and queries are exact in one term: each row is scaled by the power of two
-// that brings its largest element into [1/4, 1/2), near unit length, and 8 bits of bf16 (11 of fp16) fit. The state and what is
-// to be learnt of one value channel are held in a range by a power of two of that channel's own (Scale); step sizes and
-// what the keys' scaling left of their lengths stay in fp32 (Factors), so that T's diagonal is 1. P's second term has 8 bits (p_rest).
+// Number formats. MFMA operands are fp16, whose 11 bits make two terms 22: every operand but keys and queries enters in two,
+// where bf16 would take three. Keys and queries are exact in one: 8 bits of bf16 (11 of fp16) fit, and rows far from unit length
+// are scaled by a power of two of their own (ScaledRows). The state and what is to be learnt of one value channel are held in a range
+// by powers of two of that channel's own (Scale); step sizes and what the keys' scaling left of their lengths stay in
+// fp32 (Factors), so that T's diagonal is 1. P's second term has 8 bits (p_rest). What decays further within a chunk
+// than two terms reach is walked token by token in fp32 (by_tokens).
 //
 // A workgroup walks one sequence of one value head, or a slice of 64 of its state rows, with four chain waves and four
 // making waves. The chain waves hold the state as S^T[k][v] in fp32 MFMA accumulators, 32 or 16 value channels each. Lanes
@@ -24,10 +25,12 @@
 // and no chain wave waits for another's values. Meanwhile the making waves turn the next chunk's rows into operands, T and P in
 // the other half of LDS.
 //
-// Measured: a turn takes 14900 cycles, 6.2 us. The making waves' longest parts come to 13600 of them with six meetings, and the
-// chain waves work for 10000, each beside one of the others on its SIMD. 128 ragged prompts (135060 tokens) at H = 12 with bf16
-// states take 664 us: vector instructions 36 % of the time, the matrix unit 18 %, LDS 28 %, memory 1.15 GB at 1.7 TB/s; what is
-// left is one part waiting for the next. With all eight waves making and walking in turn they took 1507.
+// Measured: a turn takes 16500 cycles at V = 128 (12750 for slices of 64). The making waves work for up to 14200 of them and the
+// chain waves, each beside one of those on its SIMD, for 13300 to 13900 (12100 and 9300); the longest of each of the six parts come to
+// 16100 and 12500. 128 ragged prompts (135060 tokens) at H = 12 with bf16 states take 805 us: vector instructions 46 % of the time, the matrix
+// unit 27 %, LDS 25 %, memory 1.16 GB at 1.4 TB/s; what is left is one part waiting for the next. (With one term of what is learnt
+// and of the state they took 664, and with all eight waves making and walking in turn 1507.) A chunk that is walked by tokens adds
+// 32 us at 64 channels and 110 at 128.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -411,7 +414,7 @@ struct Chain {
 };
 
 // A sequence of one token, in fp32 as a step of its own. (As a chunk it would take as long
-// as 64 tokens: 16 prompts of 256 among 240 single tokens at H = 12 197 instead of 84 us.)
+// as 64 tokens: 16 prompts of 256 among 240 single tokens at H = 12, with fp32 states, 226 instead of 127 us.)
 template <int K, int V>
 __device__ __forceinline__ void one_token(DeltaShared<K, V>& shared, int begin, int h, int v0, Slots slots, int tid) {
   const DeltaPlan& p = plan_again();

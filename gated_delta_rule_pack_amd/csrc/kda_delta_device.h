@@ -152,8 +152,8 @@ struct RowInfo {
 };
 
 // The sequence of a rank, the longest first: where workgroups wait for a place on the chip, those of long sequences start
-// early, so that none of them runs alone at the end (128 prompts of 0 to 2016 tokens at H = 12: 790 us in the call's order,
-// 671 ranked). Lengths count by their half octave of chunks, and the call's order inside one: with 8 waves' ballots
+// early, so that none of them runs alone at the end (128 prompts of 0 to 2048 tokens at H = 12: 930 us in the call's order,
+// 810 ranked). Lengths count by their half octave of chunks, and the call's order inside one: with 8 waves' ballots
 // that takes 0.7 us of a workgroup, where ranks by comparison with every length took 7 for 256 sequences.
 constexpr int kRankWaves = kMostRanked / 64, kRankClasses = 32;
 struct Ranking {

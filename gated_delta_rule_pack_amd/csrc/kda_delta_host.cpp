@@ -43,16 +43,16 @@ bool fits_scan(const kda_gated_delta_args* a) {
   return (int64_t)places_of(a) * l.H <= kMaxGroups && ((int64_t)l.N * l.H + 7) * (l.V / 16) <= kMaxGroups / 2;
 }
 // Whether a call makes its chunks' records in one kernel and scans them with workgroups of 16 value channels, or
-// walks every sequence of a head in one workgroup. Times in turns of the scan (about 1.2 us with its start); a chunk of the walk takes four.
+// walks every sequence of a head in one workgroup. Times in turns of the scan (1.4 us); a chunk of the walk takes four.
 // Both wait for the longest sequence, or for all of them where there are more workgroups than 256: the walk has one for
 // each sequence and head, whose start takes about a chunk; the scan V / 16, whose start takes about two turns,
 // and its records are made 75 to a turn. Tokens that are their sequence's only one are a step in both. Without bounds on
 // the host all sequences count as equally long.
 //
-// Measured at K = V = 128 with 32-bit states, walk and scan: prompts of 1024 tokens at 12, 48, 64, 96, 128, 192 sequences and
-// heads 83 and 31, 84 and 59, 84 and 64, 85 and 91, 86 and 119, 105 and 194 us; one prompt of 64, 128, 192 at H = 12 13.4
-// and 18.2, 15.3 and 18.3, 20.0 and 18.3; one of 4096 among 31 single tokens 390 and 98, one of 512 among 127 at
-// H = 24 69 and 384; eight from 64 to 8192 628 and 201. K = V = 64, 1024 tokens at 96, 128, 144: 72 and 57, 72 and 61, 72 and 80.
+// Measured at K = V = 128 with 32-bit states, in a graph, walk and scan: prompts of 1024 tokens at 12, 48, 64, 96, 128, 192 sequences
+// and heads 92 and 43, 93 and 80, 93 and 89, 94 and 121, 97 and 155, 125 and 228 us; one prompt of 64, 128, 192 at H = 12 17.3
+// and 18.3, 22.3 and 20.4, 27.5 and 22.4; one of 4096 among 31 single tokens 437 and 122, one of 512 among 127 at
+// H = 24 102 and 451; eight from 64 to 8192 644 and 231. K = V = 64, 1024 tokens at 96, 128, 144: 82 and 79, 83 and 89, 83 and 112.
 bool scans(const kda_gated_delta_args* a) {
   const kda_linear_args& l = a->lin;
   if (a->path != KDA_DELTA_POLICY) return a->path == KDA_DELTA_SCAN;

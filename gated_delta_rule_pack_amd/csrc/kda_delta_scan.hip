@@ -9,10 +9,11 @@
 // three times a chunk in LDS, where every value passes as an operand fragment. Four more waves make the outputs behind them.
 // All read their fragments straight from memory, a few chunks ahead, each fragment in one wave alone.
 //
-// Measured: delta_prep is bound by memory, 0.87 GB in 190 us for 32768 tokens at H = 32 (4.6 TB/s) and 50 us for 16384 at
-// H = 12; a chunk of delta_scan takes 1.07 us, 2600 cycles, most of it its three dependent products with what lies between
-// them: 274 us for 16384 tokens at H = 12, where the walk took 1232 for all. V comes by the outputs' waves, through LDS and a
-// transposing read; by the chain's own, two bytes a lane, it took 308. K' by the outputs' waves too: 300.
+// Measured: delta_prep is bound by memory, 0.87 GB in 195 us for 32768 tokens at H = 32 (4.5 TB/s) and 50 us for 16384 at
+// H = 12; a chunk of delta_scan takes 1.33 us, 3200 cycles, most of it its three dependent products with what lies between
+// them: 342 us for 16384 tokens at H = 12, where the walk takes 1270 for all. V comes by the outputs' waves, through LDS and a
+// transposing read: by the chain's own, two bytes a lane, the scan took 308 us where it took 274, and with K' by the outputs'
+// waves too 300. A chunk that is walked by tokens adds 20 us.
 #include <hip/hip_runtime.h>
 
 #include <cstddef>

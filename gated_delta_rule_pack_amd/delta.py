@@ -73,9 +73,8 @@ def gated_delta_fwd(q, k, v, g, beta, cu_seqlens, *, cu_seqlens_cpu=None, scale=
     dividing H; rows may be strided. g: log decays, at most 0, fp32 or bf16, ``[H]`` or ``[T, H]``, or None for no decay.
     beta: step sizes, fp32 or bf16 ``[T, H]``, as they are used (any sigmoid has been applied). ``normalize`` takes q and k
     to unit length first (``x / sqrt(sum x^2 + 1e-6)``, in fp32); without it keys have to be near unit length
-    themselves, or at least keep ``|beta| |k|^2 <= 2``, beyond which a step grows the state. (Raw keys of one length
-    keep fp32's accuracy; lengths more than 2^5 apart within 64 tokens, with step sizes to match, leave states within
-    2^-12, and from about 2^13 apart on nothing finite.)
+    themselves, or at least keep ``|beta| |k|^2 <= 2``, beyond which a step grows the state. (Raw keys may differ
+    in length, with step sizes to match; lengths more than 2^12 apart within 64 tokens may leave nothing finite.)
     scale defaults to ``K ** -0.5``.
 
     cu_seqlens, states, ``out``, ``stream`` and ``context`` as in :func:`linear_fwd`. ``workspace``: a contiguous uint8 tensor at

@@ -500,9 +500,10 @@ size_t kda_rotary_args_size(void);
  * Rules for the data. g <= 0 (-inf forgets everything before the token; anything below -120 counts as
  * -inf). A step is stable for |beta| |k|^2 <= 2, which normalised keys and 0 <= beta <= 2 satisfy; keys that
  * break it may overflow the products' fp16 terms within 64 tokens, which gives values that are not finite.
- * Raw keys of one length, whatever it is, keep fp32's accuracy; where the longest of 64 tokens is more than 2^5 times as long
- * as the shortest and has a step size to match, 1 / |k|^2, states are within 2^-12 of their largest value, and from about
- * 2^13 on the 64 tokens' outputs, and what follows in their sequence and head, are not finite.
+ * Raw keys may have any lengths, with step sizes to match, 1 / |k|^2; but where the shortest of 64 tokens' keys is less than 2^-12 of
+ * the longest, the 64 tokens' outputs, and what follows in their sequence and head, may be not finite.
+ * A prompt's states are within about 2^-16, and outputs within that times |scale q| and their rounding, of the largest that a
+ * token's channel is made of, L_t = max(e^g_t L_{t-1}, |beta_t v_t| |k_t|), whatever the sizes of other tokens and channels.
  * What is not finite stays causal in its own sequence and head: a row of q takes its own output; a row of k, a
  * beta, and a log decay that is NaN or above 0 every output from its token on and the final state; a value of v
  * or of a state row the same of its own channel. A token with k = 0 or beta = 0 only decays. */
