@@ -4,7 +4,7 @@
 //   forward   y = R (x r w)
 //   backward  z = R^T dy;  dw = sum over rows of z x r;  u = z w;  dx = r (u - m x r sum(u x r)).
 // Every element is read and written once, so in vectors both are bound by memory: bf16 tokens of 32 + 8 heads of 128,
-// 16384 forward in 67 us, 5.0 TB/s, and 8192 backward in 54, 4.7 TB/s with the weight gradients' sums; a few tokens wait
+// 16384 forward in 67 us, 5.0 TB/s, and 8192 backward in 54 to 57, 4.5 TB/s with the weight gradients' sums; a few tokens wait
 // for their angles, 6 us. A row's sums are taken over the lanes that hold it before anything of it is
 // written, so a result may take its input's place. Squares are summed in 64 bits: their sum overflows in 32 from
 // |x| = 1.8e19 on, and these kernels wait for memory anyway.
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void norm_narrow(const NormPlan p) {
 }
 
 // The workgroups' sums of weight gradients, joined: 16 channels to a workgroup, 64 threads to a channel, four loads in
-// flight at a time (512 workgroups' sums of 128 channels: 4.6 us; 16 threads to a channel and one load at a time took 20 for 1024),
+// flight at a time (512 workgroups' sums of 128 channels: 4.1 us; 16 threads to a channel and one load at a time took 20 for 1024),
 // summed in pairs: the 64 threads' sums one after another would add 3.3 2^-24 to a gradient's error, pairs of pairs 1.4.
 template <int DT>
 __global__ __launch_bounds__(1024) void norm_sums(const NormPlan p) {
