@@ -402,7 +402,7 @@ struct Chain {
         u = fa.b[t] * token_value<kF16In>(*at) - fa.s[t] * (decay * u);
         over_keys(slot.k + row_at<K>(t), [&](int kt, int i, float k) __attribute__((always_inline)) { S[kt][i] = S[kt][i] * decay + u * k; });
         over_keys(slot.q + row_at<K>(t), [&](int kt, int i, float q) __attribute__((always_inline)) { os[i] += S[kt][i] * q; });
-        const float o = fa.f[t] * kTimesP * channel_sum(os);
+        const float o = fa.f[t] * channel_sum(os) * kTimesP;
         if (lane < 16) *at = kF16In ? __builtin_bit_cast(uint16_t, (_Float16)o) : __builtin_bit_cast(uint16_t, to_bf16(o));
       }
       if (fa.total != fa.total) {

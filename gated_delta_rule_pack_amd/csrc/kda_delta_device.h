@@ -65,7 +65,7 @@ __device__ __forceinline__ void put_half(char* high, char* low, int at, f32x4 x)
   *reinterpret_cast<u32x2*>(low + at) = kRestUp ? u32x2{rest_up(x[0], x[1], h[0]), rest_up(x[2], x[3], h[1])}
                                                 : u32x2{rest_pair(x[0], x[1], h[0]), rest_pair(x[2], x[3], h[1])};
 }
-// P stands 64 times as large as it is (it is at most 2^8, by rows of 16). Its second term has 8 bits, five of exponent and two of
+// P stands 64 times as large as it is (it is at most 2^9, by the longest rows). Its second term has 8 bits, five of exponent and two of
 // fraction, fp16's upper byte: with them P is within 2^-14 of itself, an eighth of the half step of outputs in fp16, or within 2^-34, and its
 // records keep their size. It is stored times 2^11, and read times 2^12.
 constexpr float kTimesP = 64.f;
@@ -201,7 +201,8 @@ __device__ __forceinline__ int ranked_sequence(const DeltaPlan& p, Ranking& r, i
 }
 
 // Rows of q or k on their way to LDS as fp16, each scaled by 2^-e: e = 0 for rows whose length is between 1/2 and 16, where all
-// that counts of them fits as it stands, else what brings their largest element into [1/4, 1/2).
+// that counts of them fits as it stands, else what brings their largest element into [1/4, 1/2), or below 2 at bf16's end: 2^e has to be finite.
+// (Two rows of the largest length, 2 sqrt(128), make P 2^15 at most.)
 template <int D, int kThreads, bool kF16In>
 struct ScaledRows {
   typedef Rows<D, kThreads> R;
@@ -263,7 +264,7 @@ struct ScaledRows {
         for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, rows.w[i][j] & 0x7fff7fffu));
         const uint32_t largest = row_max<R::kUnits>(max((uint32_t)top[0], (uint32_t)top[1]));
         const bool bad = largest >= (kF16In ? 0x7c00u : 0x7f80u);
-        const int e = largest == 0 || bad || plain ? 0 : min(__builtin_amdgcn_frexp_expf(token_value<kF16In>(largest)) + 1, 126);
+        const int e = largest == 0 || bad || plain ? 0 : min(__builtin_amdgcn_frexp_expf(token_value<kF16In>(largest)) + 1, 127);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t word = bad ? 0u : rows.w[i][j];
@@ -343,7 +344,7 @@ __device__ __forceinline__ Decays put_decays(Making& mk, float g, int lane) {
 }
 // A token's part of the chunk's numbers, one lane for each token, in two steps: what the making of T waits for, and what the chain does.
 struct Numbers {
-  float share, step, rq, length, beta;
+  float share, step, rq, length, beta;  // rq: f without its NaN
   int long_by;      // the chunk's longest raw key, as a power of two
   uint64_t all_bad;
   bool bad_q;
@@ -357,14 +358,14 @@ struct Numbers {
     length = k.squares;
     if (p.normalize) {
       const float rk = rsqrtf(k.squares + ldexp2(kNormEps, -2 * k.e));
-      rq = p.scale * rsqrtf(q.squares + ldexp2(kNormEps, -2 * q.e));
+      rq = p.scale / kTimesP * rsqrtf(q.squares + ldexp2(kNormEps, -2 * q.e));
       share = beta * rk;
       step = share * rk;
       long_by = 0;
     } else {
       share = ldexp2(beta, k.e);
       step = ldexp2(beta, 2 * k.e);
-      rq = ldexp2(p.scale, q.e);
+      rq = ldexp2(p.scale / kTimesP, q.e);
       long_by = k.squares > 0.f ? k.e : -1000;
     }
     mk.step[lane] = step;
@@ -384,7 +385,7 @@ struct Numbers {
     to.c[lane] = d.c;
     to.e[lane] = d.e * kTimesP;
     to.s[lane] = step;
-    to.f[lane] = wide || lane >= first || bad_q ? __builtin_nanf("") : rq / kTimesP;
+    to.f[lane] = wide || lane >= first || bad_q ? __builtin_nanf("") : rq;
     const int steps = wave_max(exponent(fabsf(share))), reach = wave_max(exponent(fabsf(h) * __builtin_amdgcn_sqrtf(length)));
     if (lane == 0) {
       to.total = wide || all_bad ? __builtin_nanf("") : d.total;

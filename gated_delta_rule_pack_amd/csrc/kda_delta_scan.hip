@@ -438,7 +438,7 @@ __global__ __launch_bounds__(512, 2) void delta_scan(const DeltaPlan p) {
       const float decay = sh.token[3][t], v = token_value<kF16In>(*reinterpret_cast<const uint16_t*>(sh.v[i & 1] + t * 32 + channel * 2));
       const float x = sh.token[0][t] * v - sh.token[1][t] * (decay * dot(k0, k1));
       a = a * decay + k0 * x, b = b * decay + k1 * x;
-      const float o = sh.token[2][t] * kTimesP * dot(q0, q1);
+      const float o = sh.token[2][t] * dot(q0, q1) * kTimesP;
       if (j == 0) to[t * p.o_t] = kF16In ? __builtin_bit_cast(uint16_t, (_Float16)o) : __builtin_bit_cast(uint16_t, to_bf16(o));
     }
     if (total != total) a = b = zero4() + __builtin_nanf("");

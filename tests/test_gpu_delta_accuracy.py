@@ -276,3 +276,34 @@ def test_random_batches(seed, path):
     out, final = case.forward(d, path=path)
     torch.cuda.synchronize()
     _check_reach(case, d, out, final)
+
+
+# ------------------------------------------------------------------------------ rows at the end of bf16's range
+LARGEST = torch.finfo(torch.bfloat16).max
+
+
+@PATHS
+@pytest.mark.parametrize("kw", [dict(), dict(K=64, V=64, decay="none", state="none")])
+def test_parallel_rows_of_the_largest_elements(kw, path):
+    """Normalised q and k in one direction, every element bf16's largest: the products of the rows as they are scaled have to fit fp16."""
+    case = DeltaCase([70, 64], H=2, seed=61, **kw)
+    signs = torch.randn(case.K, generator=torch.Generator().manual_seed(61)).sign()
+    case.q, case.k = ((LARGEST * signs).expand_as(x).to(x.dtype).contiguous() for x in (case.q, case.k))
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
+
+
+@PATHS
+@pytest.mark.parametrize("scale", [1.0, 4.0])
+def test_raw_queries_of_the_largest_elements(scale, path):
+    """Values are as small as bring the outputs back into range."""
+    case = DeltaCase([70, 64], H=2, seed=62, unit=True, state="none")
+    case.scale = scale
+    case.q = (LARGEST * case.q.float().sign()).to(case.dtype)
+    case.v = (case.v.float() * 2.0 ** -60).to(case.dtype)
+    d = case.device()
+    out, final = case.forward(d, path=path)
+    torch.cuda.synchronize()
+    _check_reach(case, d, out, final)
